@@ -368,6 +368,206 @@ int s6_scan_1d(int64_t batch, int64_t dim, int64_t dstate, int64_t seqlen, int d
                const void* C, const float* A, const float* Dskip, const float* dt_bias,
                int delta_softplus, void* y, void* stream);
 
+/*
+ * ---- The causal mixer: short causal convolution and causal scan
+ *
+ * The S6 operator of this header in the direction a language model needs:
+ * tokens 0..len-1 in order, each row with its own length, with the state that
+ * earlier text left behind going in and the state after the last token coming
+ * out. A block computes u = s6_causal_conv(x), takes delta, B and C from u by
+ * its projections, and calls s6_causal_scan; one token at a time it calls
+ * s6_conv_step and s6_scan_step on pools of states.
+ *
+ * Beside the conventions at the top of this file:
+ *   - Layout is channel-major, [batch][dim][L], token stride 1. `strides`
+ *     gives the batch and the channel stride (elements, host memory) of each
+ *     activation input in the order the entry point names; NULL means all are
+ *     contiguous. Inputs may therefore be the halves of one projection's
+ *     output or a span of tokens of a longer tensor. Strides are >= 0, channel
+ *     strides below 2^27; a tensor may span any number of elements (offsets
+ *     are 64 bit). Outputs are contiguous.
+ *   - lengths [batch] int32 (device), or NULL when every row has L tokens.
+ *     Row b's tokens 0..lengths[b]-1 are real, the others are padding: their
+ *     inputs are never used (they may hold anything, NaN included), their
+ *     outputs and gradients are zero, and states are those after the last
+ *     real token. Values are clamped to 0..L; a row of length 0 passes its
+ *     incoming state on.
+ *   - 1 <= L < 2^27, batch at most 65535, dim below 2^20, dstate 1..16,
+ *     width 2..8.
+ *   - No output may overlap an input or another output (VS_ERR_ALIAS).
+ */
+#define VS_MAX_CONV_WIDTH 8
+#define VS_CONV_SILU 1   /* flags of the convolution: apply SiLU to its result */
+
+/* Bytes of the buffers of the causal entry points; 0 for sizes they refuse.
+ * VS_S6_SCAN: workspace of s6_causal_scan (0 where it needs none);
+ * VS_S6_SAVED: the saved-state buffer of s6_causal_scan_saved, 4 bytes for
+ * each token and channel and 4 dstate for each 16 tokens;
+ * VS_S6_GRAD: workspace of s6_causal_scan_grad;
+ * VS_S6_CONV_GRAD: workspace of s6_causal_conv_grad (`dstate` is the width). */
+enum { VS_S6_SCAN = 0, VS_S6_SAVED = 1, VS_S6_GRAD = 2, VS_S6_CONV_GRAD = 3 };
+size_t s6_workspace_bytes(int op, int64_t batch, int64_t dim, int64_t dstate, int64_t seqlen);
+
+/*
+ * Depthwise causal convolution with its state:
+ *   line = [window | x],  pre[t] = bias + sum_j w[j] line[t + j],
+ *   y[t] = silu(pre[t]) (VS_CONV_SILU) or pre[t], sums in fp32
+ * so tap width-1 multiplies the token itself.
+ *   x           [batch][dim][L] (strides: x)
+ *   w, bias     [dim][width], [dim] fp32; bias may be NULL
+ *   window      [batch][dim][width-1], dtype, oldest first: the tokens before
+ *               x; NULL for zeros
+ *   y           [batch][dim][L]
+ *   window_out  [batch][dim][width-1] or NULL: the last width-1 entries of
+ *               the row's line, i.e. the window of the text that follows
+ */
+int s6_causal_conv(int64_t batch, int64_t dim, int64_t width, int64_t seqlen, int dtype, int flags,
+                   const void* x, const int64_t* strides, const float* w, const float* bias,
+                   const void* window, const int32_t* lengths, void* y, void* window_out,
+                   void* stream);
+
+/*
+ * Gradient of s6_causal_conv.
+ *   dy          [batch][dim][L] (strides: x, dy)
+ *   dwindow_out [batch][dim][width-1] or NULL: dL/d window_out
+ *   dx          [batch][dim][L]; dw [dim][width], dbias [dim] fp32
+ *   dwindow     [batch][dim][width-1] or NULL: dL/d window
+ *   workspace   s6_workspace_bytes(VS_S6_CONV_GRAD, batch, dim, width, L)
+ * Sums over tokens and rows are taken in a fixed order: every output repeats
+ * bit for bit.
+ */
+int s6_causal_conv_grad(int64_t batch, int64_t dim, int64_t width, int64_t seqlen, int dtype,
+                        int flags, const void* x, const void* dy, const int64_t* strides,
+                        const float* w, const float* bias, const void* window,
+                        const int32_t* lengths, const void* dwindow_out, void* dx, float* dw,
+                        float* dbias, void* dwindow, void* workspace, size_t workspace_bytes,
+                        void* stream);
+
+/*
+ * One token of the convolution for each row, on a pool of windows.
+ *   x           [batch][dim], row stride x_stride (0: dim)
+ *   window      [slots][dim][width-1], read at slot_in[b], written at slot_out[b]
+ *   slot_in, slot_out [batch] int32 (device) or NULL (row b uses slot b). A
+ *               row with a slot outside 0..slots-1 is empty: its output is
+ *               zero and it touches no state. Several rows may read one slot.
+ *               A slot written by one row must not be read or written by
+ *               another row of the call.
+ *   y           [batch][dim]
+ */
+int s6_conv_step(int64_t batch, int64_t dim, int64_t width, int dtype, int flags, const void* x,
+                 int64_t x_stride, const float* w, const float* bias, void* window, int64_t slots,
+                 const int32_t* slot_in, const int32_t* slot_out, void* y, void* stream);
+
+/*
+ * The causal scan of prompts: with delta = softplus(delta_raw + dt_bias)
+ * (VS_FLAG_SOFTPLUS) or delta_raw + dt_bias,
+ *   h_t = exp(delta_t A) h_{t-1} + delta_t B_t u_t
+ *   y_t = (C_t . h_t + Dskip u_t) silu(z_t)       (no gate when z is NULL)
+ *   strides     u, delta, z, B, C
+ *   B, C        [batch][dstate][L], shared by the channels
+ *   A           [dim][dstate] fp32; Dskip, dt_bias [dim] fp32 or NULL
+ *   h0          [batch][dim][dstate] fp32, the state before token 0; NULL for
+ *               zeros
+ *   y           [batch][dim][L]
+ *   h_out       [batch][dim][dstate] fp32 or NULL: the state after the row's
+ *               last token
+ *   workspace   s6_workspace_bytes(VS_S6_SCAN, ...) bytes, used where the
+ *               rows are too few to fill the chip and the sequence is cut
+ *               into pieces; may be NULL when that is 0
+ */
+int s6_causal_scan(int64_t batch, int64_t dim, int64_t dstate, int64_t seqlen, int dtype, int flags,
+                   const void* u, const void* delta, const void* z, const void* B, const void* C,
+                   const int64_t* strides, const float* A, const float* Dskip, const float* dt_bias,
+                   const float* h0, const int32_t* lengths, void* y, float* h_out, void* workspace,
+                   size_t workspace_bytes, void* stream);
+
+/* s6_causal_scan for training: the same y and h_out, and into `saved`
+ * (s6_workspace_bytes(VS_S6_SAVED, ...) bytes, layout private to the library)
+ * what s6_causal_scan_grad reads instead of running the forward pass again. */
+int s6_causal_scan_saved(int64_t batch, int64_t dim, int64_t dstate, int64_t seqlen, int dtype,
+                         int flags, const void* u, const void* delta, const void* z, const void* B,
+                         const void* C, const int64_t* strides, const float* A, const float* Dskip,
+                         const float* dt_bias, const float* h0, const int32_t* lengths, void* y,
+                         float* h_out, void* saved, size_t saved_bytes, void* workspace,
+                         size_t workspace_bytes, void* stream);
+
+/*
+ * Gradient of s6_causal_scan from the saved buffer of a
+ * s6_causal_scan_saved call on the same inputs (not checked).
+ *   strides     u, delta, z, B, C, dy
+ *   dh_out      [batch][dim][dstate] fp32 or NULL: dL/d h_out
+ *   du, ddelta, dz [batch][dim][L], dtype (dz NULL when z is)
+ *   dB, dC      [batch][dstate][L] fp32, summed over the channels
+ *   dA [dim][dstate], dD [dim], ddt_bias [dim] fp32, summed over rows and tokens
+ *   dh0         [batch][dim][dstate] fp32 or NULL
+ *   workspace   s6_workspace_bytes(VS_S6_GRAD, ...)
+ * Every output is overwritten and repeats bit for bit (no atomics).
+ */
+int s6_causal_scan_grad(int64_t batch, int64_t dim, int64_t dstate, int64_t seqlen, int dtype,
+                        int flags, const void* u, const void* delta, const void* z, const void* B,
+                        const void* C, const void* dy, const int64_t* strides, const float* A,
+                        const float* Dskip, const float* dt_bias, const int32_t* lengths,
+                        const void* saved, size_t saved_bytes, const float* dh_out, void* du,
+                        void* ddelta, void* dz, float* dB, float* dC, float* dA, float* dD,
+                        float* ddt_bias, float* dh0, void* workspace, size_t workspace_bytes,
+                        void* stream);
+
+/*
+ * One token of the causal scan for each row, on a pool of states.
+ *   u, delta, z [batch][dim]; B, C [batch][dstate]; strides: their row strides
+ *               (u, delta, z, B, C; NULL: contiguous)
+ *   h           [slots][dim][dstate] fp32; slot_in, slot_out as for s6_conv_step
+ *   y           [batch][dim]
+ */
+int s6_scan_step(int64_t batch, int64_t dim, int64_t dstate, int dtype, int flags, const void* u,
+                 const void* delta, const void* z, const void* B, const void* C,
+                 const int64_t* strides, const float* A, const float* Dskip, const float* dt_bias,
+                 float* h, int64_t slots, const int32_t* slot_in, const int32_t* slot_out, void* y,
+                 void* stream);
+
+/*
+ * ---- Beam search over the states above
+ *
+ * beam_select: the `beams` best of the beams x vocab candidates of each
+ * sequence, candidate (k, v) scoring scores[k] + log softmax(logits[k])[v].
+ *   logits      [batch][beams][vocab], dtype; row (b, k) starts at element
+ *               b * strides[0] + k * strides[1] (NULL: contiguous)
+ *   scores      [batch][beams] fp32, the beams' sums so far
+ *   done        [batch][beams] uint8 or NULL: a finished beam offers its `eos`
+ *               token at its unchanged score, its other tokens score -inf
+ *   eos         0..vocab-1, used where done is given
+ *   out_scores  [batch][beams] fp32, best first
+ *   out_parent  [batch][beams] int32: the row b * beams + k that was chosen
+ *               (the slot to read in the next step)
+ *   out_token   [batch][beams] int32
+ * A logit of NaN or -inf scores -inf; a row of nothing else scores -inf
+ * throughout; logits of +inf share the row's probability. A score that is NaN
+ * ranks as -inf. Within a beam candidates are ordered by their logits and
+ * equal ones by the lowest token; across beams by their scores and equal ones
+ * by the lowest beam. Sums are fp32.
+ * beams 1..VS_MAX_BEAMS, vocab < 2^30, batch at most 65535.
+ * workspace: beam_workspace_bytes(batch, beams, vocab) bytes.
+ */
+#define VS_MAX_BEAMS 32
+size_t beam_workspace_bytes(int64_t batch, int64_t beams, int64_t vocab);
+int beam_select(int64_t batch, int64_t beams, int64_t vocab, int dtype, const void* logits,
+                const int64_t* strides, const float* scores, const uint8_t* done, int64_t eos,
+                float* out_scores, int32_t* out_parent, int32_t* out_token, void* workspace,
+                size_t workspace_bytes, void* stream);
+
+/*
+ * beam_reorder: out[l][row] = state[l][parent[row]] for `layers` states of
+ * batch * beams rows of row_bytes bytes; consecutive layers are layer_bytes
+ * apart (in state and out alike, 0: dense).
+ *   parent      [batch * beams] int32; an entry that is not one of its own
+ *               sequence's rows counts as the row itself
+ *   out         may be state itself: rows that keep their own parent are then
+ *               not touched; any other overlap is refused
+ */
+int beam_reorder(int64_t layers, int64_t batch, int64_t beams, int64_t row_bytes,
+                 int64_t layer_bytes, const void* state, const int32_t* parent, void* out,
+                 void* stream);
+
 /* Static name of a status code ("VS_OK", ...). Never NULL. */
 const char* vs_strerror(int status);
 

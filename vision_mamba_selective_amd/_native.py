@@ -17,6 +17,9 @@ VS_F32, VS_BF16 = 0, 1
 VS_OP_VIM_BIDIR, VS_OP_CROSS4, VS_OP_1D, VS_OP_VIM_GRAD = 0, 1, 2, 3
 VS_OP_VIM_SAVED, VS_OP_VIM_GRAD_SAVED = 4, 5
 VS_NOALLOC_MAX_ELEMS = 1 << 25
+VS_S6_SCAN, VS_S6_SAVED, VS_S6_GRAD, VS_S6_CONV_GRAD = 0, 1, 2, 3
+VS_MAX_CONV_WIDTH = 8
+VS_MAX_BEAMS = 32
 
 # names and argument types of every entry point declared in include/vimscan.h
 _I64 = ctypes.c_int64
@@ -48,6 +51,18 @@ SIGNATURES = {
     "vim_x_proj": (_I, [_I64, _I64, _I64, _I64, _I, _P, _P, _P, _P, _P, _P]),
     "vim_dt_proj": (_I, [_I64, _I64, _I64, _I, _P, _P, _P, _P]),
     "vim_out_proj": (_I, [_I64, _I64, _I64, _I64, _I, _P, _P, _P, _P, _P, _P]),
+    "s6_workspace_bytes": (_SZ, [_I, _I64, _I64, _I64, _I64]),
+    "s6_causal_conv": (_I, [_I64, _I64, _I64, _I64, _I, _I] + [_P] * 9),
+    "s6_causal_conv_grad": (_I, [_I64, _I64, _I64, _I64, _I, _I] + [_P] * 13 + [_SZ, _P]),
+    "s6_conv_step": (_I, [_I64, _I64, _I64, _I, _I, _P, _I64, _P, _P, _P, _I64, _P, _P, _P, _P]),
+    "s6_causal_scan": (_I, [_I64, _I64, _I64, _I64, _I, _I] + [_P] * 14 + [_SZ, _P]),
+    "s6_causal_scan_saved": (_I, [_I64, _I64, _I64, _I64, _I, _I] + [_P] * 14 + [_SZ, _P, _SZ, _P]),
+    "s6_causal_scan_grad": (_I, [_I64, _I64, _I64, _I64, _I, _I] + [_P] * 12 + [_SZ] + [_P] * 11 +
+                            [_SZ, _P]),
+    "s6_scan_step": (_I, [_I64, _I64, _I64, _I, _I] + [_P] * 10 + [_I64, _P, _P, _P, _P]),
+    "beam_workspace_bytes": (_SZ, [_I64, _I64, _I64]),
+    "beam_select": (_I, [_I64, _I64, _I64, _I] + [_P] * 4 + [_I64] + [_P] * 4 + [_SZ, _P]),
+    "beam_reorder": (_I, [_I64, _I64, _I64, _I64, _I64, _P, _P, _P, _P]),
     "vs_strerror": (ctypes.c_char_p, [_I]),
     "vs_last_error": (ctypes.c_char_p, []),
     "vs_abi_version": (_I, []),

@@ -5,16 +5,20 @@ import os
 import re
 import subprocess
 import sys
+import tempfile
+from concurrent.futures import ThreadPoolExecutor
 
 PKG = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(PKG)
 SRC = os.path.join(PKG, "csrc", "vimscan.hip")
-SRCS = [SRC, os.path.join(PKG, "csrc", "proj.hip"), os.path.join(PKG, "csrc", "host.cpp")]
+SRCS = [SRC] + [os.path.join(PKG, "csrc", f) for f in
+                ("proj.hip", "causal.hip", "causal_grad.hip", "beam.hip", "host.cpp",
+                 "host_causal.cpp")]
 LIB = os.path.join(PKG, "libvimscan.so")
 INCLUDE = os.path.join(ROOT, "include")
 
 HIPCC_FLAGS = [
-    "-O3", "-std=c++17", "-fPIC", "-shared", "--offload-arch=gfx950",
+    "-O3", "-std=c++17", "-fPIC", "--offload-arch=gfx950",
     # packed-fp32 VALU forms are kept out of every kernel
     "-Xclang", "-target-feature", "-Xclang", "-packed-fp32-ops",
     "-Wall", "-Wno-unused-function",
@@ -44,18 +48,32 @@ def scratch_kernels(log: str):
 
 
 def build(out: str = LIB, extra=()) -> str:
+    """Compile every source for itself, at most one compiler per CPU at a
+    time, and link the objects."""
     tmp = out + ".tmp%d" % os.getpid()
-    cmd = [hipcc(), *HIPCC_FLAGS, "-Rpass-analysis=kernel-resource-usage", *extra, "-I", INCLUDE,
-           *SRCS, "-o", tmp]
-    r = subprocess.run(cmd, capture_output=True, text=True)
-    if r.returncode != 0:
-        sys.stderr.write(r.stdout + r.stderr)
-        raise RuntimeError("hipcc failed building %s" % out)
-    bad = scratch_kernels(r.stderr)
-    if bad:
-        os.remove(tmp)
-        raise RuntimeError("kernels use scratch memory: " +
-                           ", ".join("%s (%d B/lane)" % b for b in bad))
+    flags = [*HIPCC_FLAGS, "-Rpass-analysis=kernel-resource-usage", *extra, "-I", INCLUDE]
+    with tempfile.TemporaryDirectory() as d:
+        objs = [os.path.join(d, "%d.o" % i) for i in range(len(SRCS))]
+
+        def compile_one(i):
+            return subprocess.run([hipcc(), *flags, "-c", SRCS[i], "-o", objs[i]],
+                                  capture_output=True, text=True)
+
+        with ThreadPoolExecutor(min(len(SRCS), os.cpu_count() or 1)) as pool:
+            done = list(pool.map(compile_one, range(len(SRCS))))
+        for src, r in zip(SRCS, done):
+            if r.returncode != 0:
+                sys.stderr.write(r.stdout + r.stderr)
+                raise RuntimeError("hipcc failed compiling %s" % src)
+        bad = scratch_kernels("\n".join(r.stderr for r in done))
+        if bad:
+            raise RuntimeError("kernels use scratch memory: " +
+                               ", ".join("%s (%d B/lane)" % b for b in bad))
+        r = subprocess.run([hipcc(), "-shared", "--offload-arch=gfx950", *objs, "-o", tmp],
+                           capture_output=True, text=True)
+        if r.returncode != 0:
+            sys.stderr.write(r.stdout + r.stderr)
+            raise RuntimeError("hipcc failed linking %s" % out)
     os.replace(tmp, out)
     return out
 

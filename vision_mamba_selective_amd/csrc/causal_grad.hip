@@ -1,0 +1,484 @@
+// causal_grad.hip -- gfx950 kernels of the causal mixer's gradients: the short
+// causal convolution's and the selective scan's (include/vimscan.h has the
+// contract).
+#include <hip/hip_runtime.h>
+
+#include <cstdint>
+#include <string>
+
+#include "vimscan.h"
+#include "vs_causal.h"
+#include "vs_device.h"
+#include "vs_internal.h"
+
+namespace {
+
+using vs::fail;
+using vs::Strides;
+
+constexpr int kThreads = 256;
+constexpr int kWaves = kThreads / 64;
+
+// 1 / (1 + e^{-x}); e^{-x} = inf gives 0
+__device__ __forceinline__ float sigmoid_f(float x) {
+    return __builtin_amdgcn_rcpf(1.f + __builtin_amdgcn_exp2f(-x * kLog2e));
+}
+
+// ------------------------------------------------------------ convolution
+struct ConvGradArgs {
+    const void *x, *dy, *window, *dwindow_out;
+    const float *w, *bias;
+    const int32_t* lengths;
+    void *dx, *dwindow;
+    float* part;            // [batch][segs][dim][W + 1]: dw, dbias of each segment
+    Strides sx, sdy;
+    int64_t dim;
+    int L, silu, segs, seg_len;
+};
+
+// A wave takes one segment of one row in strides of 64 - (W - 1) tokens: every
+// lane forms dpre of its token, and dx[t] = sum_j w[j] dpre[t + W-1 - j] takes
+// the W - 1 later ones from the lanes above, so the last W - 1 lanes only
+// supply theirs and the next stride forms them again. Each lane sums dw and
+// dbias of its tokens; the wave's sums go to the segment's partial row.
+template <typename T, int W>
+__global__ __launch_bounds__(kThreads) void causal_conv_grad_kernel(const ConvGradArgs a) {
+    constexpr int kStep = 64 - (W - 1);
+    const int lane = threadIdx.x & 63;
+    const int64_t b = blockIdx.y;
+    const int64_t item = static_cast<int64_t>(blockIdx.x) * kWaves + (threadIdx.x >> 6);
+    const int seg = static_cast<int>(item % a.segs);
+    const int64_t d = item / a.segs;
+    if (d >= a.dim) return;                          // whole waves
+    const int len = row_length(a.lengths, b, a.L);
+    const T* x = static_cast<const T*>(a.x) + b * a.sx.b + d * a.sx.d;
+    const T* dy = static_cast<const T*>(a.dy) + b * a.sdy.b + d * a.sdy.d;
+    const size_t wrow = static_cast<size_t>(b * a.dim + d) * (W - 1);
+    const T* win = a.window ? static_cast<const T*>(a.window) + wrow : nullptr;
+    const T* dwo = a.dwindow_out ? static_cast<const T*>(a.dwindow_out) + wrow : nullptr;
+    T* dx = static_cast<T*>(a.dx) + static_cast<size_t>(b * a.dim + d) * a.L;
+    float w[W];
+#pragma unroll
+    for (int j = 0; j < W; ++j) w[j] = a.w[d * W + j];
+    const float bias = a.bias ? a.bias[d] : 0.f;
+    float dw[W], db = 0.f;
+#pragma unroll
+    for (int j = 0; j < W; ++j) dw[j] = 0.f;
+    const int s0 = seg * a.seg_len, s1 = min(s0 + a.seg_len, a.L);
+    for (int t0 = s0; t0 < s1; t0 += kStep) {
+        const int t = t0 + lane;
+        float line[W], dpre = 0.f;
+#pragma unroll
+        for (int j = 0; j < W; ++j) line[j] = 0.f;
+        if (t < len) {
+            float pre = bias;
+#pragma unroll
+            for (int j = 0; j < W; ++j) {
+                const int p = t + j - (W - 1);
+                line[j] = p >= 0 ? ld(x, p) : (win ? ld(win, p + W - 1) : 0.f);
+                pre = fmaf(w[j], line[j], pre);
+            }
+            dpre = ld(dy, t);
+            if (a.silu) {
+                const float sg = sigmoid_f(pre);
+                dpre *= sg * fmaf(pre, 1.f - sg, 1.f);
+            }
+        }
+        const bool mine = lane < kStep && t < s1;
+        float g = w[W - 1] * dpre;
+#pragma unroll
+        for (int k = 1; k < W; ++k) g = fmaf(w[W - 1 - k], __shfl_down(dpre, k), g);
+        if (mine) {
+            float v = 0.f;
+            if (t < len) {
+                v = g;
+                const int k = t + W - 1 - len;       // the token's place in the outgoing window
+                if (dwo && k >= 0) v += ld(dwo, k);
+            }
+            st(dx, t, v);
+            db += dpre;
+#pragma unroll
+            for (int j = 0; j < W; ++j) dw[j] = fmaf(dpre, line[j], dw[j]);
+        }
+        // the incoming window's entry p = lane feeds pre[p - j], j <= p
+        if (a.dwindow && seg == 0 && t0 == 0) {
+            float v = 0.f;
+#pragma unroll
+            for (int j = 0; j < W - 1; ++j) {
+                const float other = __shfl(dpre, (lane - j) & 63);
+                if (j <= lane) v = fmaf(w[j], other, v);
+            }
+            if (lane < W - 1) {
+                const int k = lane - len;            // short rows hand it on
+                if (dwo && k >= 0) v += ld(dwo, k);
+                st(static_cast<T*>(a.dwindow) + wrow, lane, v);
+            }
+        }
+    }
+    float* part = a.part + ((static_cast<size_t>(b) * a.segs + seg) * a.dim + d) * (W + 1);
+#pragma unroll
+    for (int j = 0; j <= W; ++j) {
+        float v = j < W ? dw[j < W ? j : 0] : db;
+#pragma unroll
+        for (int m = 32; m > 0; m >>= 1) v += __shfl_xor(v, m);
+        if (lane == 0) part[j] = v;
+    }
+}
+
+// dw and dbias: the segments' partial sums added in order, one thread per output
+__global__ __launch_bounds__(kThreads) void conv_grad_reduce_kernel(const float* part, float* dw, float* dbias,
+                                                                    int64_t n, int64_t parts, int width) {
+    const int64_t i = static_cast<int64_t>(blockIdx.x) * kThreads + threadIdx.x;
+    if (i >= n) return;
+    float s = 0.f;
+    for (int64_t p = 0; p < parts; ++p) s += part[p * n + i];
+    const int64_t d = i / (width + 1);
+    const int j = static_cast<int>(i % (width + 1));
+    if (j < width) dw[d * width + j] = s;
+    else dbias[d] = s;
+}
+
+// ------------------------------------------------------------------- scan
+struct ScanGradArgs {
+    const void *u, *delta, *z, *B, *C, *dy;
+    Strides su, sdl, sz, sB, sC, sdy;
+    const float *A, *Dskip, *dt_bias;
+    const int32_t* lengths;
+    const float *ckpt, *s, *dh_out;
+    void *du, *ddelta, *dz;
+    float *dh0;
+    float* bc_part;         // [batch][group][nblk][2][16 tokens][16 states]
+    float* stat;            // [batch][dim][dstate + 2]: dA, dD, dt_bias of each row
+    int64_t dim;
+    int L, dstate, nblk;
+};
+
+// Lanes 0-31 return a[l] + a[l + 32]; lanes 32-63 return b[l - 32] + b[l].
+__device__ __forceinline__ float swap32_sum(float a, float b) {
+    const auto r = __builtin_amdgcn_permlane32_swap(__float_as_uint(a), __float_as_uint(b), false, false);
+    return __uint_as_float(r[0]) + __uint_as_float(r[1]);
+}
+// Of the four 16-lane rows, rows 0 and 2 return a's sum over themselves and
+// the row above, rows 1 and 3 return b's sum over the row below and themselves.
+__device__ __forceinline__ float swap16_sum(float a, float b) {
+    const auto r = __builtin_amdgcn_permlane16_swap(__float_as_uint(a), __float_as_uint(b), false, false);
+    return __uint_as_float(r[0]) + __uint_as_float(r[1]);
+}
+
+// Reverse mode, on the forward kernel's layout (a 16-lane row per channel,
+// lane n = state n, 16 channels per workgroup), blocks of 16 tokens taken from
+// the row's end. Per block the states are formed again from the one stored at
+// its start, keeping h_t and e_t = exp(delta_t A); then the adjoint runs back,
+//   lam_t = gy_t C_t + e_{t+1} lam_{t+1},  gy = dy silu(z),
+// and with q_t = e_t lam_t h_{t-1}: dA += q delta, dC_t = gy h_t,
+// dB_t = lam_t delta u; the sums over states W = sum lam B, V = sum q A are
+// transpose reductions inside the row and give du = delta W + gy D and
+// dDelta = V + u W. dB and dC are sums over channels: the wave's four rows are
+// added by two rounds of lane swaps, the workgroup's waves in LDS, and the
+// workgroups' chunks by bc_reduce_kernel, all in a fixed order.
+template <typename T, bool GATE, bool SOFTPLUS>
+__global__ __launch_bounds__(kThreads) void causal_grad_kernel(const ScanGradArgs a) {
+    __shared__ __attribute__((aligned(16))) float tile[2][2][kRowLanes][kTilePad];
+    __shared__ __attribute__((aligned(16))) float red[2][kWaves][8][64];
+    const int tid = threadIdx.x;
+    const int lane = tid & 63;
+    const int wave = tid >> 6;
+    const int n = lane & 15;
+    uint32_t cg, bb;
+    xcd_block(cg, bb);
+    const int64_t b = bb;
+    const int64_t d0 = static_cast<int64_t>(cg) * vs::kCausalCh + (tid >> 4);
+    const bool active = d0 < a.dim;
+    const int64_t d = active ? d0 : a.dim - 1;
+    const int L = a.L;
+    const int len = row_length(a.lengths, b, L);
+    const bool n_ok = n < a.dstate;
+    const float An = n_ok ? a.A[d * a.dstate + n] : 0.f;
+    const float A2 = An * kLog2e;
+    const float Dk = a.Dskip ? a.Dskip[d] : 0.f;
+    const float bias = a.dt_bias ? a.dt_bias[d] : 0.f;
+    const T* u = static_cast<const T*>(a.u) + b * a.su.b + d * a.su.d;
+    const T* dl = static_cast<const T*>(a.delta) + b * a.sdl.b + d * a.sdl.d;
+    const T* z = static_cast<const T*>(a.z) + b * a.sz.b + d * a.sz.d;
+    const T* dy = static_cast<const T*>(a.dy) + b * a.sdy.b + d * a.sdy.d;
+    const size_t row = static_cast<size_t>(b * a.dim + d);
+    const size_t at = row * static_cast<size_t>(L);
+    T* du = static_cast<T*>(a.du) + at;
+    T* dd = static_cast<T*>(a.ddelta) + at;
+    T* dz = static_cast<T*>(a.dz) + (GATE ? at : 0);
+    const float* s = a.s + at;
+    const float* ck = a.ckpt + row * static_cast<size_t>(a.nblk) * a.dstate;
+    float* chunk = a.bc_part + (static_cast<size_t>(b) * gridDim.x + cg) * static_cast<size_t>(a.nblk) * 512;
+
+    BcStage<T> stage(a, b, tid, len);
+    const int nblk = (len + 15) / 16;
+    const int ntile = (len + kTileTok - 1) / kTileTok;
+    float lamE = a.dh_out && n_ok ? a.dh_out[row * a.dstate + n] : 0.f;
+    float dA = 0.f, dD = 0.f, db = 0.f;
+    if (ntile > 0) {
+        stage.load(ntile - 1);
+        stage.store(tile[(ntile - 1) & 1]);
+    }
+    lds_barrier();
+    for (int blk = nblk - 1; blk >= 0; --blk) {
+        const int it = blk >> 1, half = blk & 1;
+        // the tile below goes to the other buffer while this one is used
+        const bool stages = it > 0 && (half == 1 || blk == nblk - 1);
+        if (stages) stage.load(it - 1);
+        const int t = blk * 16 + n;
+        const bool ok = t < len;
+        const int tc = ok ? t : len - 1;
+        const float x = ld(dl, tc) + bias;
+        const float dlt = ok ? (SOFTPLUS ? softplus_f(x) : x) : 0.f;
+        const float cu = ok ? ld(u, tc) : 0.f;
+        const float du_ = dlt * cu;
+        const float g = ok ? ld(dy, tc) : 0.f;
+        float gs = g;
+        if (GATE) {
+            const float zz = ld(z, tc), sg = sigmoid_f(zz);
+            gs = ok ? g * (zz * sg) : 0.f;
+            const float v = g * s[tc] * sg * fmaf(zz, 1.f - sg, 1.f);
+            if (active && t < L) st(dz, t, ok ? v : 0.f);
+        }
+        const float4* Bt = reinterpret_cast<const float4*>(&tile[it & 1][0][n][half * 16]);
+        const float4* Ct = reinterpret_cast<const float4*>(&tile[it & 1][1][n][half * 16]);
+        float Bv[16], Cv[16], hs[16], es[16], wv[16], vv[16], sbc[16];
+#pragma unroll
+        for (int q = 0; q < 4; ++q) {
+            const float4 bq = Bt[q], cq = Ct[q];
+            Bv[4 * q] = bq.x; Bv[4 * q + 1] = bq.y; Bv[4 * q + 2] = bq.z; Bv[4 * q + 3] = bq.w;
+            Cv[4 * q] = cq.x; Cv[4 * q + 1] = cq.y; Cv[4 * q + 2] = cq.z; Cv[4 * q + 3] = cq.w;
+        }
+        const float h_in = n_ok ? ck[static_cast<size_t>(blk) * a.dstate + n] : 0.f;
+        float h = h_in;
+        Unroll<16>::run([&](auto ic) VS_INLINE {
+            constexpr int i = decltype(ic)::value;
+            es[i] = __builtin_amdgcn_exp2f(row_bcast<i>(dlt) * A2);
+            h = fmaf(es[i], h, row_bcast<i>(du_) * Bv[i]);
+            hs[i] = h;
+        });
+        // lanes of channels past dim hold another channel's values: they
+        // count for nothing in the sums over channels
+        const float du_m = active ? du_ : 0.f, gs_m = active ? gs : 0.f;
+        Unroll<16>::run([&](auto ic) VS_INLINE {
+            constexpr int i = 15 - decltype(ic)::value;
+            const float lam = fmaf(row_bcast<i>(gs), Cv[i], lamE);
+            lamE = lam * es[i];
+            const float q = lamE * (i > 0 ? hs[i > 0 ? i - 1 : 0] : h_in);
+            dA = fmaf(row_bcast<i>(dlt), q, dA);
+            wv[i] = lam * Bv[i];
+            vv[i] = q * An;
+            sbc[i] = swap32_sum(row_bcast<i>(du_m) * lam, row_bcast<i>(gs_m) * hs[i]);
+        });
+        const float Rw = row_transpose_sum(wv, lane);
+        const float Rv = row_transpose_sum(vv, lane);
+        const float ddl = fmaf(cu, Rw, Rv);
+        const float dx = ok ? (SOFTPLUS ? ddl * sigmoid_f(x) : ddl) : 0.f;
+        if (active && t < L) {
+            st(du, t, ok ? fmaf(dlt, Rw, gs * Dk) : 0.f);
+            st(dd, t, dx);
+        }
+        db += dx;
+        dD = fmaf(gs, cu, dD);
+        // steps i and i + 8 of the block share a register: row 0 of a wave
+        // then holds dB of step i, row 1 dB of i + 8, rows 2 and 3 dC
+#pragma unroll
+        for (int i = 0; i < 8; ++i) red[blk & 1][wave][i][lane] = swap16_sum(sbc[i], sbc[i + 8]);
+        if (stages) stage.store(tile[(it - 1) & 1]);
+        lds_barrier();
+        // thread (i, l) of two rounds: the waves' sums of step i (or i + 8)
+#pragma unroll
+        for (int r = 0; r < 2; ++r) {
+            const int i = (tid >> 6) + 4 * r;
+            float v = 0.f;
+#pragma unroll
+            for (int w = 0; w < kWaves; ++w) v += red[blk & 1][w][i][lane];
+            const int which = lane >> 5, tok = i + ((lane >> 4) & 1) * 8;
+            chunk[static_cast<size_t>(blk) * 512 + which * 256 + tok * 16 + n] = v;
+        }
+    }
+    if (active) {
+        float* stat = a.stat + row * (a.dstate + 2);
+        if (n_ok) {
+            stat[n] = dA;
+            if (a.dh0) a.dh0[row * a.dstate + n] = lamE;
+        }
+    }
+    // dD and dt_bias: the row's lanes hold its tokens' shares
+#pragma unroll
+    for (int m = 8; m > 0; m >>= 1) {
+        dD += __shfl_xor(dD, m);
+        db += __shfl_xor(db, m);
+    }
+    if (active && n == 0) {
+        float* stat = a.stat + row * (a.dstate + 2);
+        stat[a.dstate] = dD;
+        stat[a.dstate + 1] = db;
+    }
+    // the gradients of the padding
+    if (active)
+        for (int t = nblk * 16 + n; t < L; t += 16) {
+            st(du, t, 0.f);
+            st(dd, t, 0.f);
+            if (GATE) st(dz, t, 0.f);
+        }
+}
+
+struct BcReduceArgs {
+    const float *part, *stat;
+    const int32_t* lengths;
+    float *dB, *dC, *dA, *dD, *dbias;
+    int64_t batch, dim;
+    int L, dstate, nblk, groups;
+    int tok_wgs;            // workgroups over the tokens of a batch row
+};
+
+// dB and dC: the workgroups' chunks added in order; a thread takes four
+// states of one token. The workgroups past tok_wgs of batch row 0 add dA, dD
+// and dt_bias over the batch rows, one thread per output.
+__global__ __launch_bounds__(kThreads) void bc_reduce_kernel(const BcReduceArgs a) {
+    const int tid = threadIdx.x;
+    const int64_t b = blockIdx.y;
+    if (static_cast<int>(blockIdx.x) >= a.tok_wgs) {
+        const int per = a.dstate + 2;
+        const int64_t n = a.dim * per;
+        const int64_t i = static_cast<int64_t>(blockIdx.x - a.tok_wgs) * kThreads + tid;
+        if (b != 0 || i >= n) return;
+        float s = 0.f;
+        for (int64_t r = 0; r < a.batch; ++r) s += a.stat[r * n + i];
+        const int64_t d = i / per;
+        const int k = static_cast<int>(i % per);
+        if (k < a.dstate) a.dA[d * a.dstate + k] = s;
+        else if (k == a.dstate) a.dD[d] = s;
+        else a.dbias[d] = s;
+        return;
+    }
+    // 256 threads: 2 (dB, dC) x 4 (quads of states) x 32 tokens
+    const int which = tid >> 7, quad = tid & 3, tok = (tid >> 2) & 31;
+    const int t = static_cast<int>(blockIdx.x) * 32 + tok;
+    if (t >= a.L) return;
+    const int len = row_length(a.lengths, b, a.L);
+    float4 s = make_float4(0.f, 0.f, 0.f, 0.f);
+    if (t < len) {
+        const float* p = a.part + (static_cast<size_t>(b) * a.groups * a.nblk + (t >> 4)) * 512 + which * 256 + (t & 15) * 16 + quad * 4;
+        for (int g = 0; g < a.groups; ++g) {
+            const float4 v = *reinterpret_cast<const float4*>(p + static_cast<size_t>(g) * a.nblk * 512);
+            s.x += v.x; s.y += v.y; s.z += v.z; s.w += v.w;
+        }
+    }
+    float* out = which ? a.dC : a.dB;
+    const float v[4] = {s.x, s.y, s.z, s.w};
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+        const int n = quad * 4 + k;
+        if (n < a.dstate) out[(b * a.dstate + n) * static_cast<int64_t>(a.L) + t] = v[k];
+    }
+}
+
+// -------------------------------------------------------------- launching
+int launched() {
+    const hipError_t e = hipGetLastError();
+    if (e != hipSuccess) return fail(VS_ERR_HIP, std::string("kernel launch: ") + hipGetErrorString(e));
+    return VS_OK;
+}
+
+template <typename T>
+int launch_conv_grad(const vs::ConvCall& c) {
+    ConvGradArgs a{};
+    a.x = c.x; a.dy = c.dy; a.window = c.window; a.dwindow_out = c.dwindow_out; a.w = c.w; a.bias = c.bias;
+    a.lengths = c.lengths; a.dx = c.dx; a.dwindow = c.dwindow; a.part = static_cast<float*>(c.ws);
+    a.sx = c.st[0]; a.sdy = c.st[1]; a.dim = c.dim; a.L = static_cast<int>(c.L); a.silu = c.flags & VS_CONV_SILU;
+    a.seg_len = static_cast<int>(vs::conv_grad_segment(c.batch, c.dim, c.L));
+    a.segs = static_cast<int>((c.L + a.seg_len - 1) / a.seg_len);
+    const int64_t wgs = (c.dim * a.segs + kWaves - 1) / kWaves;
+    if (wgs >= (int64_t(1) << 31)) return fail(VS_ERR_UNSUPPORTED, "too many tokens and channels for one launch");
+    const dim3 grid(static_cast<unsigned>(wgs), static_cast<unsigned>(c.batch));
+    const hipStream_t st = static_cast<hipStream_t>(c.stream);
+    switch (c.width) {
+#define VS_CASE(w) case w: hipLaunchKernelGGL((causal_conv_grad_kernel<T, w>), grid, dim3(kThreads), 0, st, a); break;
+    VS_CASE(2) VS_CASE(3) VS_CASE(4) VS_CASE(5) VS_CASE(6) VS_CASE(7) VS_CASE(8)
+#undef VS_CASE
+    }
+    if (int rc = launched()) return rc;
+    const int64_t n = c.dim * (c.width + 1);
+    hipLaunchKernelGGL(conv_grad_reduce_kernel, dim3(static_cast<unsigned>((n + kThreads - 1) / kThreads)), dim3(kThreads), 0, st,
+                       static_cast<const float*>(c.ws), c.dw, c.dbias, n, c.batch * a.segs, static_cast<int>(c.width));
+    return launched();
+}
+
+template <typename T>
+int launch_scan_grad(const vs::CausalCall& c) {
+    size_t so[2], wo[4];
+    vs::causal_saved_layout(c.batch, c.dim, c.dstate, c.L, so);
+    vs::causal_grad_layout(c.batch, c.dim, c.dstate, c.L, wo);
+    ScanGradArgs a{};
+    a.u = c.u; a.delta = c.delta; a.z = c.z; a.B = c.B; a.C = c.C; a.dy = c.dy;
+    a.su = c.st[0]; a.sdl = c.st[1]; a.sz = c.st[2]; a.sB = c.st[3]; a.sC = c.st[4]; a.sdy = c.st[5];
+    a.A = c.A; a.Dskip = c.Dskip; a.dt_bias = c.dt_bias; a.lengths = c.lengths;
+    a.ckpt = reinterpret_cast<const float*>(static_cast<const char*>(c.saved) + so[0]);
+    a.s = reinterpret_cast<const float*>(static_cast<const char*>(c.saved) + so[1]);
+    a.dh_out = c.dh_out; a.du = c.du; a.ddelta = c.ddelta; a.dz = c.dz; a.dh0 = c.dh0;
+    a.bc_part = reinterpret_cast<float*>(static_cast<char*>(c.ws) + wo[0]);
+    a.stat = reinterpret_cast<float*>(static_cast<char*>(c.ws) + wo[1]);
+    a.dim = c.dim; a.L = static_cast<int>(c.L); a.dstate = static_cast<int>(c.dstate);
+    a.nblk = static_cast<int>((c.L + vs::kBlockTok - 1) / vs::kBlockTok);
+    const unsigned groups = static_cast<unsigned>((c.dim + vs::kCausalCh - 1) / vs::kCausalCh);
+    const dim3 grid(groups, static_cast<unsigned>(c.batch)), blk(kThreads);
+    const hipStream_t st = static_cast<hipStream_t>(c.stream);
+    const bool sp = c.flags & VS_FLAG_SOFTPLUS;
+    if (c.z && sp) hipLaunchKernelGGL((causal_grad_kernel<T, true, true>), grid, blk, 0, st, a);
+    else if (c.z) hipLaunchKernelGGL((causal_grad_kernel<T, true, false>), grid, blk, 0, st, a);
+    else if (sp) hipLaunchKernelGGL((causal_grad_kernel<T, false, true>), grid, blk, 0, st, a);
+    else hipLaunchKernelGGL((causal_grad_kernel<T, false, false>), grid, blk, 0, st, a);
+    if (int rc = launched()) return rc;
+    BcReduceArgs r{};
+    r.part = a.bc_part; r.stat = a.stat; r.lengths = c.lengths; r.dB = c.dB; r.dC = c.dC; r.dA = c.dA; r.dD = c.dD;
+    r.dbias = c.dbias; r.batch = c.batch; r.dim = c.dim; r.L = a.L; r.dstate = a.dstate; r.nblk = a.nblk;
+    r.groups = static_cast<int>(groups);
+    r.tok_wgs = (a.L + 31) / 32;
+    const int64_t stat_wgs = (c.dim * (c.dstate + 2) + kThreads - 1) / kThreads;
+    hipLaunchKernelGGL(bc_reduce_kernel, dim3(static_cast<unsigned>(r.tok_wgs + stat_wgs), static_cast<unsigned>(c.batch)),
+                       blk, 0, st, r);
+    return launched();
+}
+
+}  // namespace
+
+// ---------------------------------------------------------------- C ABI
+extern "C" {
+
+int s6_causal_conv_grad(int64_t batch, int64_t dim, int64_t width, int64_t seqlen, int dtype,
+                        int flags, const void* x, const void* dy, const int64_t* strides,
+                        const float* w, const float* bias, const void* window,
+                        const int32_t* lengths, const void* dwindow_out, void* dx, float* dw,
+                        float* dbias, void* dwindow, void* workspace, size_t workspace_bytes,
+                        void* stream) {
+    vs::ConvCall c{};
+    c.batch = batch; c.dim = dim; c.width = width; c.L = seqlen; c.dtype = dtype; c.flags = flags;
+    c.x = x; c.dy = dy; c.strides = strides; c.w = w; c.bias = bias; c.window = window; c.lengths = lengths;
+    c.grad = true; c.dwindow_out = dwindow_out; c.dx = dx; c.dw = dw; c.dbias = dbias; c.dwindow = dwindow;
+    c.ws = workspace; c.ws_bytes = workspace_bytes; c.stream = stream;
+    if (int rc = vs::prepare_conv(c)) return rc;
+    return dtype == VS_BF16 ? launch_conv_grad<uint16_t>(c) : launch_conv_grad<float>(c);
+}
+
+int s6_causal_scan_grad(int64_t batch, int64_t dim, int64_t dstate, int64_t seqlen, int dtype,
+                        int flags, const void* u, const void* delta, const void* z, const void* B,
+                        const void* C, const void* dy, const int64_t* strides, const float* A,
+                        const float* Dskip, const float* dt_bias, const int32_t* lengths,
+                        const void* saved, size_t saved_bytes, const float* dh_out, void* du,
+                        void* ddelta, void* dz, float* dB, float* dC, float* dA, float* dD,
+                        float* ddt_bias, float* dh0, void* workspace, size_t workspace_bytes,
+                        void* stream) {
+    vs::CausalCall c{};
+    c.batch = batch; c.dim = dim; c.dstate = dstate; c.L = seqlen; c.dtype = dtype; c.flags = flags;
+    c.u = u; c.delta = delta; c.z = z; c.B = B; c.C = C; c.dy = dy; c.strides = strides; c.A = A;
+    c.Dskip = Dskip; c.dt_bias = dt_bias; c.lengths = lengths; c.saved = const_cast<void*>(saved);
+    c.saved_bytes = saved_bytes; c.dh_out = dh_out; c.du = du; c.ddelta = ddelta; c.dz = dz; c.dB = dB;
+    c.dC = dC; c.dA = dA; c.dD = dD; c.dbias = ddt_bias; c.dh0 = dh0; c.ws = workspace;
+    c.ws_bytes = workspace_bytes; c.stream = stream; c.grad = true;
+    if (int rc = vs::prepare_causal(c)) return rc;
+    return dtype == VS_BF16 ? launch_scan_grad<uint16_t>(c) : launch_scan_grad<float>(c);
+}
+
+}  // extern "C"

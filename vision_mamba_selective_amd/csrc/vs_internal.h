@@ -122,4 +122,93 @@ int validate_out_proj(int64_t batch, int64_t dim_in, int64_t dim_out, int64_t se
                       const void* y, const void* W, const float* bias, const void* residual,
                       const void* out);
 
+// ---- the causal mixer and beam search (host_causal.cpp)
+constexpr int64_t kCausalMaxL = int64_t(1) << 27;    // tokens and channel strides: 4 rows of a wave
+                                                     // stay below 2^32 bytes
+constexpr int64_t kCausalMaxDim = int64_t(1) << 20;
+constexpr int kCausalCh = 16;                        // channels per workgroup of the scan kernels
+
+struct Strides { int64_t b, d; };                    // batch and channel stride, elements
+
+struct CausalCall {
+    int64_t batch, dim, dstate, L;
+    int dtype, flags;
+    const void *u, *delta, *z, *B, *C, *dy;
+    const int64_t* strides;                          // as the caller gave them (may be NULL)
+    const float *A, *Dskip, *dt_bias, *h0;
+    const int32_t* lengths;
+    void* y;
+    float* h_out;
+    void* saved;                                     // the saving forward's, or the gradient's (read)
+    size_t saved_bytes;
+    void* ws;
+    size_t ws_bytes;
+    void* stream;
+    // gradient
+    const float* dh_out;
+    void *du, *ddelta, *dz;
+    float *dB, *dC, *dA, *dD, *dbias, *dh0;
+    bool save = false, grad = false;
+    // filled by the validation: strides of u, delta, z, B, C, dy
+    Strides st[6];
+};
+
+struct ConvCall {
+    int64_t batch, dim, width, L;
+    int dtype, flags;
+    const void *x, *dy;
+    const int64_t* strides;
+    const float *w, *bias;
+    const void* window;
+    const int32_t* lengths;
+    void *y, *window_out;
+    void* stream;
+    // gradient
+    bool grad = false;
+    const void* dwindow_out;
+    void *dx, *dwindow;
+    float *dw, *dbias;
+    void* ws;
+    size_t ws_bytes;
+    Strides st[2];
+};
+
+struct StepCall {
+    int64_t batch, dim, inner;                       // inner: dstate, or the window's width
+    int dtype, flags;
+    const void *u, *delta, *z, *B, *C;               // conv: u is x, the others NULL
+    const int64_t* strides;
+    const float *A, *Dskip, *dt_bias;                // conv: A is w, dt_bias the bias
+    void* pool;
+    int64_t slots;
+    const int32_t *slot_in, *slot_out;
+    void* y;
+    void* stream;
+    int64_t st[5];                                   // row strides
+};
+
+// pieces a causal scan's sequence is cut into (1: not cut)
+int causal_pieces(int64_t batch, int64_t dim, int64_t L);
+int causal_grad_pieces(int64_t batch, int64_t dim, int64_t L);
+// tokens of one wave's part of a row in the convolution's gradient
+int64_t conv_grad_segment(int64_t batch, int64_t dim, int64_t L);
+size_t causal_ws_bytes(int op, int64_t batch, int64_t dim, int64_t dstate, int64_t L);
+// saved buffer: [checkpoints: fp32 [batch][dim][nblk][dstate]][s: fp32 batch*dim*L]
+size_t causal_saved_layout(int64_t batch, int64_t dim, int64_t dstate, int64_t L, size_t offs[2]);
+// gradient workspace: [dB/dC chunks][per row dA, dD, dt_bias][pieces' adjoints][pieces' sums of delta]
+size_t causal_grad_layout(int64_t batch, int64_t dim, int64_t dstate, int64_t L, size_t offs[4]);
+
+int prepare_causal(CausalCall& c);
+int prepare_conv(ConvCall& c);
+int prepare_conv_step(StepCall& c);
+int prepare_scan_step(StepCall& c);
+int validate_beam_select(int64_t batch, int64_t beams, int64_t vocab, int dtype, const void* logits,
+                         const int64_t* strides, const float* scores, const uint8_t* done, int64_t eos,
+                         const float* out_scores, const int32_t* out_parent, const int32_t* out_token,
+                         const void* ws, size_t ws_bytes, int64_t st[2]);
+int validate_beam_reorder(int64_t layers, int64_t batch, int64_t beams, int64_t row_bytes,
+                          int64_t& layer_bytes, const void* state, const int32_t* parent, const void* out);
+// beam_select: vocabulary entries of one workgroup's part of a row, and the parts of a row
+int64_t beam_part(int64_t batch, int64_t beams, int64_t vocab);
+
 }  // namespace vs
