@@ -31,12 +31,10 @@ struct ConvArgs {
     int segs;               // workgroups along a row
 };
 
-constexpr int kConvTok = 4;     // tokens of one thread, tw apart
-
-// y = silu(bias + sum_j w[j] line[t + j]): a thread takes kConvTok tokens of
-// one row, tw apart, so that loads and stores of a wave are contiguous; short
-// rows share a workgroup. Bound by memory: each entry of x comes from HBM
-// once, the taps' repeats from the caches.
+// y = silu(bias + sum_j w[j] line[t + j]): a lane takes eight consecutive
+// tokens of a row (one or two 16-byte loads, and a second load of the W - 1
+// entries before them, which the caches hold); short rows share a workgroup.
+// Bound by memory: each entry of x comes from HBM once.
 template <typename T, int W>
 __global__ __launch_bounds__(kThreads) void causal_conv_kernel(const ConvArgs a) {
     const int tid = threadIdx.x;
@@ -48,29 +46,29 @@ __global__ __launch_bounds__(kThreads) void causal_conv_kernel(const ConvArgs a)
     const int len = row_length(a.lengths, b, a.L);
     const T* x = static_cast<const T*>(a.x) + b * a.sx.b + d * a.sx.d;
     const T* win = a.window ? static_cast<const T*>(a.window) + (b * a.dim + d) * (W - 1) : nullptr;
-    // entry p of the row's line [window | x]
-    auto line = [&](int p) {
-        if (p >= W - 1) return ld(x, p - (W - 1));
-        return win ? ld(win, p) : 0.f;
-    };
     float w[W];
 #pragma unroll
     for (int j = 0; j < W; ++j) w[j] = a.w[d * W + j];
     const float bias = a.bias ? a.bias[d] : 0.f;
     T* y = static_cast<T*>(a.y) + (b * a.dim + d) * a.L;
-    const int t0 = seg * a.tw * kConvTok + tid % a.tw;
+    const int t0 = (seg * a.tw + tid % a.tw) * vs::kConvVec;
+    if (t0 < a.L) {
+        float f[W + 7], v[8];
+        conv_line<T, W>(x, win, t0, len, f);
 #pragma unroll
-    for (int i = 0; i < kConvTok; ++i) {
-        const int t = t0 + i * a.tw;
-        if (t >= a.L) break;
-        float v = 0.f;
-        if (t < len) {
-            v = bias;
+        for (int i = 0; i < 8; ++i) {
+            v[i] = bias;
 #pragma unroll
-            for (int j = 0; j < W; ++j) v = fmaf(w[j], line(t + j), v);
-            if (a.silu) v = silu_f(v);
+            for (int j = 0; j < W; ++j) v[i] = fmaf(w[j], f[i + j], v[i]);
+            if (a.silu) v[i] = silu_f(v[i]);
         }
-        st(y, t, v);
+        if (t0 + 8 <= len) {
+            store_eight(y + t0, v);
+        } else {
+#pragma unroll
+            for (int i = 0; i < 8; ++i)
+                if (t0 + i < a.L) st(y, t0 + i, t0 + i < len ? v[i] : 0.f);
+        }
     }
     // the row's last W - 1 line entries, unchanged in their type
     const int j = tid % a.tw;
@@ -146,35 +144,67 @@ __global__ __launch_bounds__(kThreads) void causal_scan_kernel(const ScanFwdArgs
     const float A2 = n_ok ? a.A[d * a.dstate + n] * kLog2e : 0.f;
     const float Dk = a.Dskip ? a.Dskip[d] : 0.f;
     const float bias = a.dt_bias ? a.dt_bias[d] : 0.f;
-    const T* u = static_cast<const T*>(a.u) + b * a.su.b + d * a.su.d;
-    const T* dl = static_cast<const T*>(a.delta) + b * a.sdl.b + d * a.sdl.d;
-    const T* z = static_cast<const T*>(a.z) + b * a.sz.b + d * a.sz.d;
     const size_t row = static_cast<size_t>(b * a.dim + d);
-    T* y = static_cast<T*>(a.y) + row * static_cast<size_t>(L);
-    float* s = SAVE ? a.s + row * static_cast<size_t>(L) : nullptr;
     float* ck = SAVE ? a.ckpt + row * static_cast<size_t>(a.nblk) * a.dstate : nullptr;
+
+    // The wave's four rows of a tensor are read and written through a buffer
+    // descriptor: a lane holds one running byte offset per tensor, reads past
+    // the rows return zero and writes there are dropped, so nothing in the
+    // loop branches around memory.
+    const int64_t w0 = static_cast<int64_t>(cg) * vs::kCausalCh + __builtin_amdgcn_readfirstlane(tid >> 6) * 4;
+    const int64_t wd = w0 < a.dim ? w0 : a.dim - 1;
+    const int64_t wrows = w0 < a.dim ? (a.dim - w0 < 4 ? a.dim - w0 : 4) : 1;
+    const uint32_t wr = static_cast<uint32_t>(d - wd);
+    const Rows<T> u(a.u, b * a.su.b + wd * a.su.d, wrows, a.su.d, L), dl(a.delta, b * a.sdl.b + wd * a.sdl.d, wrows, a.sdl.d, L);
+    const Rows<T> z(a.z, GATE ? b * a.sz.b + wd * a.sz.d : 0, GATE ? wrows : 0, a.sz.d, L);
+    const int64_t orow = (b * a.dim + wd) * L;
+    const Rows<T> y(a.y, orow, wrows, L, L);
+    const Rows<float> s(a.s, SAVE ? orow : 0, SAVE && GATE ? wrows : 0, L, L);
+    uint32_t ou = u.at(wr, n), od = dl.at(wr, n), oz = z.at(wr, n);
+    uint32_t oy = y.at(wr, n), os = s.at(wr, n);
+    const int t_lim = active ? L : 0;           // tokens whose outputs this lane may write
 
     BcStage<T> stage(a, b, tid, len);
     float h = a.h0 && n_ok ? a.h0[row * a.dstate + n] : 0.f;
     const int ntile = (len + kTileTok - 1) / kTileTok;
+    Raw<T> ru[2], rd[2], rz[2];
+    auto tok_load = [&]() VS_INLINE {
+#pragma unroll
+        for (int k = 0; k < 2; ++k) {
+            ru[k] = u.load(ou + k * 16 * sizeof(T));
+            rd[k] = dl.load(od + k * 16 * sizeof(T));
+            if (GATE) rz[k] = z.load(oz + k * 16 * sizeof(T));
+        }
+        ou += kTileTok * sizeof(T);
+        od += kTileTok * sizeof(T);
+        oz += kTileTok * sizeof(T);
+    };
     if (ntile > 0) {
         stage.load(0);
+        tok_load();
         stage.store(tile[0]);
     }
     for (int it = 0; it < ntile; ++it) {
         lds_barrier();
         if (it + 1 < ntile) stage.load(it + 1);
+        Raw<T> cu_[2], cd_[2], cz_[2];
+#pragma unroll
+        for (int k = 0; k < 2; ++k) { cu_[k] = ru[k]; cd_[k] = rd[k]; cz_[k] = rz[k]; }
+        tok_load();                             // past the row: zero, or another row's, unused
 #pragma unroll
         for (int half = 0; half < 2; ++half) {
-            const int blk = it * 2 + half;
-            const int t = blk * 16 + n;
+            const int t = it * kTileTok + half * 16 + n;
+            if (half == 1 && it * kTileTok + 16 >= len) {          // uniform: nothing but padding
+                y.store(t < t_lim ? oy + 16 * static_cast<uint32_t>(sizeof(T)) : kDropped, 0.f);
+                break;
+            }
             const bool ok = t < len;
-            const int tc = ok ? t : len - 1;
-            const float x = ld(dl, tc) + bias;
+            const float x = from_raw<T>(cd_[half]) + bias;
             const float dlt = ok ? (SOFTPLUS ? softplus_f(x) : x) : 0.f;
-            const float cu = ok ? ld(u, tc) : 0.f;
+            const float cu = ok ? from_raw<T>(cu_[half]) : 0.f;
             const float du = dlt * cu;
-            if (SAVE && active && n_ok && blk < a.nblk) ck[static_cast<size_t>(blk) * a.dstate + n] = h;
+            if (SAVE && active && n_ok && it * 2 + half < a.nblk)
+                ck[static_cast<size_t>(it * 2 + half) * a.dstate + n] = h;
             const float4* Bt = reinterpret_cast<const float4*>(&tile[it & 1][0][n][half * 16]);
             const float4* Ct = reinterpret_cast<const float4*>(&tile[it & 1][1][n][half * 16]);
             float Bv[16], Cv[16], c[16];
@@ -191,19 +221,254 @@ __global__ __launch_bounds__(kThreads) void causal_scan_kernel(const ScanFwdArgs
                 c[i] = h * Cv[i];
             });
             const float sum = fmaf(Dk, cu, row_transpose_sum(c, lane));
-            if (active && t < L) {
-                if (SAVE && GATE) s[t] = sum;
-                float v = sum;
-                if (GATE) v *= silu_f(ld(z, tc));
-                st(y, t, ok ? v : 0.f);
-            }
+            float v = sum;
+            if (GATE) v *= silu_f(from_raw<T>(cz_[half]));
+            const bool wr_ok = t < t_lim;
+            if (SAVE && GATE) s.store(wr_ok ? os + half * 16 * 4 : kDropped, sum);
+            y.store(wr_ok ? oy + half * 16 * static_cast<uint32_t>(sizeof(T)) : kDropped, ok ? v : 0.f);
         }
+        oy += kTileTok * sizeof(T);
+        if (SAVE) os += kTileTok * 4;
         if (it + 1 < ntile) stage.store(tile[(it + 1) & 1]);
     }
     if (a.h_out && active && n_ok) a.h_out[row * a.dstate + n] = h;
     // the outputs of the padding past the last tile
-    if (active)
-        for (int t = ntile * kTileTok + n; t < L; t += 16) st(y, t, 0.f);
+    for (int t = ntile * kTileTok + n; t < t_lim; t += 16) {
+        y.store(oy, 0.f);
+        oy += 16 * sizeof(T);
+    }
+}
+
+// The same scan with four states in a lane: a wave holds 16 channels, lane q
+// of a channel's quad states 4q..4q+3, a workgroup 64 channels of one piece
+// of one batch row's tokens. Lane q loads the block's tokens 4q..4q+3 (one
+// wide load per tensor), forms their delta and delta u, and the quad
+// broadcasts them into the multiplications as DPP operands; the read-out sums
+// four states in the lane and finishes in the quad (9 instructions for four
+// tokens). B and C of 32 tokens stand in LDS as [token][B | C].
+//
+// Against one state per lane this takes about a fifth fewer instruction slots
+// per state update, but a quarter of the waves: it is the form for sequences
+// cut into pieces. A piece's effect on the state is h -> P h + h_loc with P =
+// exp(A sum of delta), so a first launch (CARRY) scans every piece but the
+// last from zero, with no read-out, and stores h_loc and the sum of delta;
+// the second folds those of the earlier pieces into its own starting state
+// and scans its tokens in full.
+constexpr int kWideCh = vs::kCausalWideCh; // channels per workgroup
+constexpr int kWidePad = 2 * kRowLanes + 4; // floats per token of the LDS tile
+
+template <int Q>
+__device__ __forceinline__ float quad_bcast(float v) { return dpp<Q * 0x55>(v); }
+
+// four values of each lane summed over the quad: lane q returns sum of p_q
+__device__ __forceinline__ float quad_transpose_sum(float p0, float p1, float p2, float p3, int lane) {
+    const bool odd = (lane & 1) != 0, high = (lane & 2) != 0;
+    const float a = p0 + dpp<0xb1>(p0), b = p1 + dpp<0xb1>(p1);      // quad_perm [1,0,3,2]
+    const float c = p2 + dpp<0xb1>(p2), d = p3 + dpp<0xb1>(p3);
+    const float ab = odd ? b : a, cd = odd ? d : c;
+    const float s = ab + dpp<0x4e>(ab), t = cd + dpp<0x4e>(cd);      // quad_perm [2,3,0,1]
+    return high ? t : s;
+}
+
+template <typename T, bool GATE, bool SOFTPLUS, bool SAVE, bool CARRY>
+__global__ __launch_bounds__(kThreads) void causal_scan4_kernel(const ScanFwdArgs a) {
+    __shared__ __attribute__((aligned(16))) float tile[2][kTileTok][kWidePad];
+    const int tid = threadIdx.x;
+    const int lane = tid & 63;
+    const int q = lane & 3;
+    uint32_t cg, bb;
+    xcd_block(cg, bb);
+    // grid.y enumerates (batch, piece), piece fastest; the carry launch leaves the last piece out
+    const uint32_t np = static_cast<uint32_t>(CARRY ? a.pieces - 1 : a.pieces);
+    const int piece = static_cast<int>(bb % np);
+    const int64_t b = bb / np;
+    const int64_t d0 = static_cast<int64_t>(cg) * kWideCh + (tid >> 2);
+    const bool active = d0 < a.dim;
+    const int64_t d = active ? d0 : a.dim - 1;
+    const int L = a.L;
+    const int len = row_length(a.lengths, b, L);
+    // this piece's tokens [s0, s1) and, of those, the real ones [s0, e)
+    const int s0 = piece * a.piece_len, s1 = min(s0 + a.piece_len, L), e = min(s1, len);
+    const size_t row = static_cast<size_t>(b * a.dim + d);
+    float A2[4], h[4];
+#pragma unroll
+    for (int r = 0; r < 4; ++r) {
+        const int n = 4 * q + r;
+        A2[r] = n < a.dstate ? a.A[d * a.dstate + n] * kLog2e : 0.f;
+        h[r] = 0.f;
+    }
+    const float Dk = !CARRY && a.Dskip ? a.Dskip[d] : 0.f;
+    const float bias = a.dt_bias ? a.dt_bias[d] : 0.f;
+    const T* u = static_cast<const T*>(a.u) + b * a.su.b + d * a.su.d;
+    const T* dl = static_cast<const T*>(a.delta) + b * a.sdl.b + d * a.sdl.d;
+    const T* z = static_cast<const T*>(a.z) + b * a.sz.b + d * a.sz.d;
+    T* y = static_cast<T*>(a.y) + row * static_cast<size_t>(L);
+    float* s = SAVE ? a.s + row * static_cast<size_t>(L) : nullptr;
+    float* ck = SAVE ? a.ckpt + row * static_cast<size_t>(a.nblk) * a.dstate : nullptr;
+    // pieces' end states [batch][piece][dim][dstate] and sums of delta [batch][piece][dim]
+    const int64_t np1 = a.pieces - 1;
+    auto piece_row = [&](int p) { return static_cast<size_t>((b * np1 + p) * a.dim + d); };
+
+    // ---- staging: thread (row r of B | C, tokens 4k..4k+3)
+    const int sr = tid >> 3, sk = (tid & 7) * 4;
+    const bool s_ok = (sr & 15) < a.dstate;
+    const int64_t sn = s_ok ? sr & 15 : 0;
+    const T* ssrc = sr < 16 ? static_cast<const T*>(a.B) + b * a.sB.b + sn * a.sB.d
+                            : static_cast<const T*>(a.C) + b * a.sC.b + sn * a.sC.d;
+    Four<T> sraw;
+    auto stage_load = [&](int t0) VS_INLINE {
+        const int t = t0 + sk;
+        if (t + 4 <= len) sraw.load(ssrc + t);
+        else sraw.load_some(ssrc, t, len);
+    };
+    auto stage_store = [&](float (&dst)[kTileTok][kWidePad]) VS_INLINE {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) dst[sk + i][sr] = s_ok ? sraw.get(i) : 0.f;
+    };
+    Four<T> ru, rd, rz;
+    auto tok_load = [&](int t0) VS_INLINE {
+        const int t = t0 + 4 * q;
+        if (t0 + 16 <= len) {                                  // uniform
+            ru.load(u + t);
+            rd.load(dl + t);
+            if (GATE && !CARRY) rz.load(z + t);
+        } else {
+            ru.load_some(u, t, len);
+            rd.load_some(dl, t, len);
+            if (GATE && !CARRY) rz.load_some(z, t, len);
+        }
+    };
+    const int ntile = e > s0 ? (e - s0 + kTileTok - 1) / kTileTok : 0;
+    if (ntile > 0) {
+        stage_load(s0);
+        tok_load(s0);
+        stage_store(tile[0]);
+    }
+    // ---- the state that the earlier pieces leave
+    if (!CARRY) {
+        if (a.h0) {
+#pragma unroll
+            for (int r = 0; r < 4; ++r)
+                if (4 * q + r < a.dstate) h[r] = a.h0[row * a.dstate + 4 * q + r];
+        }
+        const int before = min(piece, (len + a.piece_len - 1) / a.piece_len);
+        for (int p = 0; p < before; ++p) {
+            const float sd = a.piece_sum[piece_row(p)];
+            const float* hp = a.piece_h + piece_row(p) * a.dstate;
+#pragma unroll
+            for (int r = 0; r < 4; ++r) {
+                const float loc = 4 * q + r < a.dstate ? hp[4 * q + r] : 0.f;
+                h[r] = fmaf(__builtin_amdgcn_exp2f(sd * A2[r]), h[r], loc);
+            }
+        }
+    }
+    float sdl = 0.f;
+    for (int it = 0; it < ntile; ++it) {
+        const int t_tile = s0 + it * kTileTok;
+        lds_barrier();
+        const bool more = it + 1 < ntile;
+        if (more) stage_load(t_tile + kTileTok);
+#pragma unroll
+        for (int half = 0; half < 2; ++half) {
+            const int t0 = t_tile + half * 16;
+            if (t0 >= e) break;                                // uniform
+            float dlt[4], du[4], uu[4], zz[4];
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                const float x = rd.get(i) + bias;
+                dlt[i] = SOFTPLUS ? softplus_f(x) : x;
+                uu[i] = ru.get(i);
+                zz[i] = GATE && !CARRY ? rz.get(i) : 0.f;
+            }
+            if (t0 + 16 > e) {                                 // uniform: the row's last block
+#pragma unroll
+                for (int i = 0; i < 4; ++i) dlt[i] = t0 + 4 * q + i < e ? dlt[i] : 0.f;
+            }
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                du[i] = dlt[i] * uu[i];
+                if (CARRY) sdl += dlt[i];
+            }
+            if (t0 + 16 < e) tok_load(t0 + 16);
+            if (SAVE) {
+                if (active)
+#pragma unroll
+                    for (int r = 0; r < 4; ++r)
+                        if (4 * q + r < a.dstate) ck[static_cast<size_t>(t0 >> 4) * a.dstate + 4 * q + r] = h[r];
+            }
+            float p[16];
+            Unroll<16>::run([&](auto ic) VS_INLINE {
+                constexpr int i = decltype(ic)::value;
+                const float* row_bc = tile[it & 1][half * 16 + i];
+                const float4 Bv = *reinterpret_cast<const float4*>(row_bc + 4 * q);
+                const float dt = quad_bcast<i / 4>(dlt[i % 4]), dx = quad_bcast<i / 4>(du[i % 4]);
+                h[0] = fmaf(__builtin_amdgcn_exp2f(dt * A2[0]), h[0], dx * Bv.x);
+                h[1] = fmaf(__builtin_amdgcn_exp2f(dt * A2[1]), h[1], dx * Bv.y);
+                h[2] = fmaf(__builtin_amdgcn_exp2f(dt * A2[2]), h[2], dx * Bv.z);
+                h[3] = fmaf(__builtin_amdgcn_exp2f(dt * A2[3]), h[3], dx * Bv.w);
+                if (!CARRY) {
+                    const float4 Cv = *reinterpret_cast<const float4*>(row_bc + kRowLanes + 4 * q);
+                    p[i] = fmaf(h[3], Cv.w, fmaf(h[2], Cv.z, fmaf(h[1], Cv.y, h[0] * Cv.x)));
+                }
+                // the exponentials do not wait for the states: unbounded, the
+                // scheduler moves all 64 of a block to its start
+                if (i % 4 == 3) __builtin_amdgcn_sched_barrier(0);
+            });
+            if (!CARRY) {
+                float v[4];
+#pragma unroll
+                for (int i = 0; i < 4; ++i)
+                    v[i] = fmaf(Dk, uu[i], quad_transpose_sum(p[i], p[4 + i], p[8 + i], p[12 + i], lane));
+                const int t = t0 + 4 * q;
+                if (active) {
+                    if (SAVE && GATE) {
+                        if (t0 + 16 <= e) store_four(s + t, v);
+                        else
+#pragma unroll
+                            for (int i = 0; i < 4; ++i)
+                                if (t + i < e) s[t + i] = v[i];
+                    }
+                    if (GATE) {
+#pragma unroll
+                        for (int i = 0; i < 4; ++i) v[i] *= silu_f(zz[i]);
+                    }
+                    if (t0 + 16 <= e) store_four(y + t, v);
+                    else
+#pragma unroll
+                        for (int i = 0; i < 4; ++i)
+                            if (t + i < s1) st(y, t + i, t + i < e ? v[i] : 0.f);
+                }
+            }
+        }
+        if (more) stage_store(tile[(it + 1) & 1]);
+    }
+    if (CARRY) {
+        sdl += dpp<0xb1>(sdl);
+        sdl += dpp<0x4e>(sdl);
+        if (active) {
+            if (q == 0) a.piece_sum[piece_row(piece)] = sdl;
+#pragma unroll
+            for (int r = 0; r < 4; ++r)
+                if (4 * q + r < a.dstate) a.piece_h[piece_row(piece) * a.dstate + 4 * q + r] = h[r];
+        }
+        return;
+    }
+    // the piece with the row's last token (the first one for an empty row) has its final state
+    if (a.h_out && active && (len > 0 ? s0 < len && len <= s1 : piece == 0)) {
+#pragma unroll
+        for (int r = 0; r < 4; ++r)
+            if (4 * q + r < a.dstate) a.h_out[row * a.dstate + 4 * q + r] = h[r];
+    }
+    // outputs of the padding past the last block: lanes along the tokens of
+    // the wave's 16 channels
+    const int zf = e > s0 ? s0 + (e - s0 + 15) / 16 * 16 : s0;
+    if (zf < s1) {
+        const int64_t w0 = static_cast<int64_t>(cg) * kWideCh + (tid >> 6) * 16;
+        for (int c = 0; c < 16 && w0 + c < a.dim; ++c) {
+            T* yr = static_cast<T*>(a.y) + static_cast<size_t>(b * a.dim + w0 + c) * L;
+            for (int t = zf + lane; t < s1; t += 64) st(yr, t, 0.f);
+        }
+    }
 }
 
 // one token of each row on the pool: four lanes per channel, lane q of a quad
@@ -285,9 +550,9 @@ int launch_conv(const vs::ConvCall& c) {
     a.x = c.x; a.window = c.window; a.w = c.w; a.bias = c.bias; a.lengths = c.lengths;
     a.y = c.y; a.window_out = c.window_out; a.sx = c.st[0]; a.dim = c.dim;
     a.L = static_cast<int>(c.L); a.silu = c.flags & VS_CONV_SILU;
-    a.tw = 4;
-    while (a.tw < kThreads && a.tw < c.L) a.tw *= 2;
-    const int64_t per = static_cast<int64_t>(a.tw) * kConvTok;
+    a.tw = 1;
+    while (a.tw < kThreads && a.tw * vs::kConvVec < c.L) a.tw *= 2;
+    const int64_t per = static_cast<int64_t>(a.tw) * vs::kConvVec;
     a.segs = static_cast<int>((c.L + per - 1) / per);
     const int64_t rows = kThreads / a.tw, groups = (c.dim + rows - 1) / rows * a.segs;
     if (groups >= (int64_t(1) << 31)) return fail(VS_ERR_UNSUPPORTED, "too many tokens and channels for one launch");
@@ -343,10 +608,30 @@ int launch_scan(const vs::CausalCall& c) {
         a.ckpt = reinterpret_cast<float*>(static_cast<char*>(c.saved) + offs[0]);
         a.s = reinterpret_cast<float*>(static_cast<char*>(c.saved) + offs[1]);
     }
-    const dim3 grid(static_cast<unsigned>((c.dim + vs::kCausalCh - 1) / vs::kCausalCh), static_cast<unsigned>(c.batch));
     const dim3 blk(kThreads);
     const hipStream_t st = static_cast<hipStream_t>(c.stream);
     const bool sp = c.flags & VS_FLAG_SOFTPLUS;
+    a.pieces = vs::causal_pieces(c.batch, c.dim, c.L);
+    if (a.pieces > 0) {
+        const int64_t tiles = (c.L + kTileTok - 1) / kTileTok;
+        a.piece_len = static_cast<int>((tiles + a.pieces - 1) / a.pieces * kTileTok);
+        a.piece_h = static_cast<float*>(c.ws);
+        a.piece_sum = a.piece_h + c.batch * (a.pieces - 1) * c.dim * c.dstate;
+        const unsigned groups = static_cast<unsigned>((c.dim + kWideCh - 1) / kWideCh);
+        const dim3 fgrid(groups, static_cast<unsigned>(c.batch * a.pieces));
+        if (a.pieces > 1) {
+            const dim3 cgrid(groups, static_cast<unsigned>(c.batch * (a.pieces - 1)));
+            if (sp) hipLaunchKernelGGL((causal_scan4_kernel<T, false, true, false, true>), cgrid, blk, 0, st, a);
+            else hipLaunchKernelGGL((causal_scan4_kernel<T, false, false, false, true>), cgrid, blk, 0, st, a);
+            if (int rc = launched()) return rc;
+        }
+        if (c.z && sp) hipLaunchKernelGGL((causal_scan4_kernel<T, true, true, SAVE, false>), fgrid, blk, 0, st, a);
+        else if (c.z) hipLaunchKernelGGL((causal_scan4_kernel<T, true, false, SAVE, false>), fgrid, blk, 0, st, a);
+        else if (sp) hipLaunchKernelGGL((causal_scan4_kernel<T, false, true, SAVE, false>), fgrid, blk, 0, st, a);
+        else hipLaunchKernelGGL((causal_scan4_kernel<T, false, false, SAVE, false>), fgrid, blk, 0, st, a);
+        return launched();
+    }
+    const dim3 grid(static_cast<unsigned>((c.dim + vs::kCausalCh - 1) / vs::kCausalCh), static_cast<unsigned>(c.batch));
     if (c.z && sp) hipLaunchKernelGGL((causal_scan_kernel<T, true, true, SAVE>), grid, blk, 0, st, a);
     else if (c.z) hipLaunchKernelGGL((causal_scan_kernel<T, true, false, SAVE>), grid, blk, 0, st, a);
     else if (sp) hipLaunchKernelGGL((causal_scan_kernel<T, false, true, SAVE>), grid, blk, 0, st, a);

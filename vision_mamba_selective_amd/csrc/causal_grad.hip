@@ -36,14 +36,14 @@ struct ConvGradArgs {
     int L, silu, segs, seg_len;
 };
 
-// A wave takes one segment of one row in strides of 64 - (W - 1) tokens: every
-// lane forms dpre of its token, and dx[t] = sum_j w[j] dpre[t + W-1 - j] takes
-// the W - 1 later ones from the lanes above, so the last W - 1 lanes only
-// supply theirs and the next stride forms them again. Each lane sums dw and
-// dbias of its tokens; the wave's sums go to the segment's partial row.
+// A wave takes one segment of one row, 63 x 8 tokens at a time: every lane
+// forms dpre of its eight consecutive tokens, and dx[t] = sum_j w[j] dpre[t +
+// W-1 - j] takes up to W - 1 later ones from the lane above, so lane 63 only
+// supplies its own and lane 0 of the next stride forms them again. Each lane
+// sums dw and dbias of its tokens; the wave's sums go to the segment's partial
+// row. Bound by memory (x and dy read, dx written once).
 template <typename T, int W>
 __global__ __launch_bounds__(kThreads) void causal_conv_grad_kernel(const ConvGradArgs a) {
-    constexpr int kStep = 64 - (W - 1);
     const int lane = threadIdx.x & 63;
     const int64_t b = blockIdx.y;
     const int64_t item = static_cast<int64_t>(blockIdx.x) * kWaves + (threadIdx.x >> 6);
@@ -65,53 +65,65 @@ __global__ __launch_bounds__(kThreads) void causal_conv_grad_kernel(const ConvGr
 #pragma unroll
     for (int j = 0; j < W; ++j) dw[j] = 0.f;
     const int s0 = seg * a.seg_len, s1 = min(s0 + a.seg_len, a.L);
-    for (int t0 = s0; t0 < s1; t0 += kStep) {
-        const int t = t0 + lane;
-        float line[W], dpre = 0.f;
+    for (int base = s0; base < s1; base += vs::kConvGradStep) {
+        const int t0 = base + lane * 8;
+        float dpre[8 + W - 1];
 #pragma unroll
-        for (int j = 0; j < W; ++j) line[j] = 0.f;
-        if (t < len) {
-            float pre = bias;
+        for (int i = 0; i < 8 + W - 1; ++i) dpre[i] = 0.f;
+        if (t0 < len) {
+            float f[W + 7];
+            conv_line<T, W>(x, win, t0, len, f);
+            Eight<T> g;
+            if (t0 + 8 <= len) g.load(dy + t0);
+            else g.load_some(dy, t0, len);
 #pragma unroll
-            for (int j = 0; j < W; ++j) {
-                const int p = t + j - (W - 1);
-                line[j] = p >= 0 ? ld(x, p) : (win ? ld(win, p + W - 1) : 0.f);
-                pre = fmaf(w[j], line[j], pre);
-            }
-            dpre = ld(dy, t);
-            if (a.silu) {
-                const float sg = sigmoid_f(pre);
-                dpre *= sg * fmaf(pre, 1.f - sg, 1.f);
+            for (int i = 0; i < 8; ++i) {
+                float pre = bias, v = g.get(i);
+#pragma unroll
+                for (int j = 0; j < W; ++j) pre = fmaf(w[j], f[i + j], pre);
+                if (a.silu) {
+                    const float sg = sigmoid_f(pre);
+                    v *= sg * fmaf(pre, 1.f - sg, 1.f);
+                }
+                dpre[i] = t0 + i < len ? v : 0.f;
+                if (lane < 63) {
+                    db += dpre[i];
+#pragma unroll
+                    for (int j = 0; j < W; ++j) dw[j] = fmaf(dpre[i], f[i + j], dw[j]);
+                }
             }
         }
-        const bool mine = lane < kStep && t < s1;
-        float g = w[W - 1] * dpre;
 #pragma unroll
-        for (int k = 1; k < W; ++k) g = fmaf(w[W - 1 - k], __shfl_down(dpre, k), g);
-        if (mine) {
-            float v = 0.f;
-            if (t < len) {
-                v = g;
-                const int k = t + W - 1 - len;       // the token's place in the outgoing window
-                if (dwo && k >= 0) v += ld(dwo, k);
+        for (int k = 0; k < W - 1; ++k) dpre[8 + k] = __shfl_down(dpre[k], 1);
+        if (lane < 63 && t0 < s1) {
+            float v[8];
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+                v[i] = 0.f;
+#pragma unroll
+                for (int k = 0; k < W; ++k) v[i] = fmaf(w[W - 1 - k], dpre[i + k], v[i]);
+                const int k = t0 + i + W - 1 - len;     // the token's place in the outgoing window
+                if (dwo && k >= 0 && t0 + i < len) v[i] += ld(dwo, k);
+                if (t0 + i >= len) v[i] = 0.f;
             }
-            st(dx, t, v);
-            db += dpre;
+            if (t0 + 8 <= a.L) {
+                store_eight(dx + t0, v);
+            } else {
 #pragma unroll
-            for (int j = 0; j < W; ++j) dw[j] = fmaf(dpre, line[j], dw[j]);
+                for (int i = 0; i < 8; ++i)
+                    if (t0 + i < a.L) st(dx, t0 + i, v[i]);
+            }
         }
-        // the incoming window's entry p = lane feeds pre[p - j], j <= p
-        if (a.dwindow && seg == 0 && t0 == 0) {
-            float v = 0.f;
+        // entry p of the incoming window feeds pre[p - j], j <= p
+        if (a.dwindow && base == 0 && lane == 0) {
 #pragma unroll
-            for (int j = 0; j < W - 1; ++j) {
-                const float other = __shfl(dpre, (lane - j) & 63);
-                if (j <= lane) v = fmaf(w[j], other, v);
-            }
-            if (lane < W - 1) {
-                const int k = lane - len;            // short rows hand it on
+            for (int p = 0; p < W - 1; ++p) {
+                float v = 0.f;
+#pragma unroll
+                for (int j = 0; j <= p; ++j) v = fmaf(w[j], dpre[p - j], v);
+                const int k = p - len;                  // short rows hand it on
                 if (dwo && k >= 0) v += ld(dwo, k);
-                st(static_cast<T*>(a.dwindow) + wrow, lane, v);
+                st(static_cast<T*>(a.dwindow) + wrow, p, v);
             }
         }
     }

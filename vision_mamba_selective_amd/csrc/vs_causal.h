@@ -26,8 +26,10 @@ struct ScanFwdArgs {
     void* y;
     float* h_out;
     float *ckpt, *s;        // the saving forward: states at block starts, ungated output
+    float *piece_h, *piece_sum;   // the pieces' end states from zero and sums of delta
     int64_t dim;
     int L, dstate, nblk;
+    int pieces, piece_len;
 };
 
 __device__ __forceinline__ int row_length(const int32_t* lengths, int64_t b, int L) {
@@ -41,6 +43,141 @@ __device__ __forceinline__ void lds_barrier() {
     __builtin_amdgcn_fence(__ATOMIC_RELEASE, "workgroup", "local");
     __builtin_amdgcn_s_barrier();
     __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "workgroup", "local");
+}
+
+// A few rows of a tensor behind a buffer descriptor: 32-bit byte offsets from
+// the first row; reads outside return zero, writes outside are dropped. The
+// rows span under 2^31 bytes (4 rows of at most 2^27 entries).
+constexpr uint32_t kDropped = 0xfffffff0u;          // an offset past every descriptor
+template <typename T>
+using Raw = std::conditional_t<sizeof(T) == 2, uint16_t, uint32_t>;
+template <typename T>
+struct Rows {
+    __amdgpu_buffer_rsrc_t rsrc;
+    uint32_t stride;
+    __device__ __forceinline__ Rows(const void* p, int64_t first, int64_t rows, int64_t d, int L) {
+        const int64_t n = rows > 0 ? (rows - 1) * d + L : 0;
+        rsrc = __builtin_amdgcn_make_buffer_rsrc(const_cast<T*>(static_cast<const T*>(p) + (rows > 0 ? first : 0)), 0,
+                                                 static_cast<int>(static_cast<uint32_t>(n * static_cast<int64_t>(sizeof(T)))),
+                                                 0x00020000);
+        stride = static_cast<uint32_t>(d);
+    }
+    __device__ __forceinline__ uint32_t at(uint32_t row, int t) const {
+        return (row * stride + static_cast<uint32_t>(t)) * static_cast<uint32_t>(sizeof(T));
+    }
+    __device__ __forceinline__ Raw<T> load(uint32_t off) const {
+        if constexpr (sizeof(T) == 2) return __builtin_amdgcn_raw_buffer_load_b16(rsrc, static_cast<int>(off), 0, 0);
+        else return __builtin_amdgcn_raw_buffer_load_b32(rsrc, static_cast<int>(off), 0, 0);
+    }
+    __device__ __forceinline__ void store(uint32_t off, float v) const {
+        if constexpr (sizeof(T) == 2)
+            __builtin_amdgcn_raw_buffer_store_b16(__builtin_bit_cast(uint16_t, static_cast<__bf16>(v)), rsrc, static_cast<int>(off), 0, 0);
+        else
+            __builtin_amdgcn_raw_buffer_store_b32(__float_as_uint(v), rsrc, static_cast<int>(off), 0, 0);
+    }
+};
+
+// Four consecutive entries of a row, kept as loaded until they are used.
+// Rows start at any element: the accesses are only as aligned as one element.
+template <typename T>
+struct Four;
+template <>
+struct Four<float> {
+    float v[4];
+    __device__ __forceinline__ void load(const float* p) { __builtin_memcpy(v, p, sizeof(v)); }
+    // entries first.. of a row of n; zeros past its end
+    __device__ __forceinline__ void load_some(const float* p, int first, int n) {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) v[i] = first + i < n ? p[first + i] : 0.f;
+    }
+    __device__ __forceinline__ float get(int i) const { return v[i]; }
+};
+template <>
+struct Four<uint16_t> {
+    uint32_t v[2];
+    __device__ __forceinline__ void load(const uint16_t* p) { __builtin_memcpy(v, p, sizeof(v)); }
+    __device__ __forceinline__ void load_some(const uint16_t* p, int first, int n) {
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+            const uint32_t lo = first + 2 * i < n ? p[first + 2 * i] : 0u;
+            const uint32_t hi = first + 2 * i + 1 < n ? p[first + 2 * i + 1] : 0u;
+            v[i] = lo | (hi << 16);
+        }
+    }
+    __device__ __forceinline__ float get(int i) const {
+        return __uint_as_float(i & 1 ? v[i / 2] & 0xffff0000u : v[i / 2] << 16);
+    }
+};
+__device__ __forceinline__ void store_four(float* p, const float (&f)[4]) { __builtin_memcpy(p, f, sizeof(f)); }
+__device__ __forceinline__ void store_four(uint16_t* p, const float (&f)[4]) {
+    typedef __bf16 Vec4 __attribute__((ext_vector_type(4)));
+    const Vec4 v = {static_cast<__bf16>(f[0]), static_cast<__bf16>(f[1]), static_cast<__bf16>(f[2]), static_cast<__bf16>(f[3])};
+    __builtin_memcpy(p, &v, sizeof(v));
+}
+
+// eight of them
+template <typename T>
+struct Eight {
+    Four<T> a, b;
+    __device__ __forceinline__ void load(const T* p) {
+        if constexpr (sizeof(T) == 2) {
+            uint32_t w[4];
+            __builtin_memcpy(w, p, sizeof(w));
+            a.v[0] = w[0]; a.v[1] = w[1]; b.v[0] = w[2]; b.v[1] = w[3];
+        } else {
+            a.load(p);
+            b.load(p + 4);
+        }
+    }
+    __device__ __forceinline__ void load_some(const T* p, int first, int n) {
+        a.load_some(p, first, n);
+        b.load_some(p, first + 4, n);
+    }
+    __device__ __forceinline__ float get(int i) const { return i < 4 ? a.get(i) : b.get(i - 4); }
+};
+__device__ __forceinline__ void store_eight(float* p, const float (&f)[8]) { __builtin_memcpy(p, f, sizeof(f)); }
+__device__ __forceinline__ void store_eight(uint16_t* p, const float (&f)[8]) {
+    typedef __bf16 Vec8 __attribute__((ext_vector_type(8)));
+    const Vec8 v = {static_cast<__bf16>(f[0]), static_cast<__bf16>(f[1]), static_cast<__bf16>(f[2]), static_cast<__bf16>(f[3]),
+                    static_cast<__bf16>(f[4]), static_cast<__bf16>(f[5]), static_cast<__bf16>(f[6]), static_cast<__bf16>(f[7])};
+    __builtin_memcpy(p, &v, sizeof(v));
+}
+
+// The convolution's view of one lane's eight tokens t0..t0+7: the W - 1 entries
+// of the row's line before them and the tokens themselves, zero past the
+// row's length. x starts at token 0; win (or NULL) holds the W - 1 entries
+// before it.
+template <typename T, int W>
+__device__ __forceinline__ void conv_line(const T* x, const T* win, int t0, int len, float (&f)[W + 7]) {
+    constexpr int P = W - 1;
+    if (t0 + 8 <= len) {
+        Eight<T> e;
+        e.load(x + t0);
+#pragma unroll
+        for (int i = 0; i < 8; ++i) f[P + i] = e.get(i);
+    } else {
+#pragma unroll
+        for (int i = 0; i < 8; ++i) f[P + i] = t0 + i < len ? ld(x, t0 + i) : 0.f;
+    }
+    if (t0 >= 8 && t0 <= len) {
+        if constexpr (P <= 4) {
+            Four<T> e;
+            e.load(x + t0 - 4);
+#pragma unroll
+            for (int i = 0; i < P; ++i) f[i] = e.get(4 - P + i);
+        } else {
+            Eight<T> e;
+            e.load(x + t0 - 8);
+#pragma unroll
+            for (int i = 0; i < P; ++i) f[i] = e.get(8 - P + i);
+        }
+    } else {
+#pragma unroll
+        for (int i = 0; i < P; ++i) {
+            const int t = t0 - P + i;
+            f[i] = t >= 0 ? (t < len ? ld(x, t) : 0.f) : (win ? ld(win, t + P) : 0.f);
+        }
+    }
 }
 
 // B and C of one 32-token tile into tile[which][state][token], fp32: 256

@@ -126,7 +126,11 @@ int validate_out_proj(int64_t batch, int64_t dim_in, int64_t dim_out, int64_t se
 constexpr int64_t kCausalMaxL = int64_t(1) << 27;    // tokens and channel strides: 4 rows of a wave
                                                      // stay below 2^32 bytes
 constexpr int64_t kCausalMaxDim = int64_t(1) << 20;
-constexpr int kCausalCh = 16;                        // channels per workgroup of the scan kernels
+constexpr int kCausalCh = 16;                        // channels per workgroup of the narrow scan kernels
+constexpr int kCausalWideCh = 64;                    // and of the wide ones
+constexpr int kCausalMaxPieces = 64;
+constexpr int kConvVec = 8;                          // convolution: consecutive tokens of one lane
+constexpr int kConvGradStep = 63 * kConvVec;         // its gradient: tokens of one wave at a time
 
 struct Strides { int64_t b, d; };                    // batch and channel stride, elements
 
@@ -187,7 +191,8 @@ struct StepCall {
     int64_t st[5];                                   // row strides
 };
 
-// pieces a causal scan's sequence is cut into (1: not cut)
+// pieces the wide form of a causal scan cuts the sequence into (1: not cut);
+// 0: the narrow form
 int causal_pieces(int64_t batch, int64_t dim, int64_t L);
 int causal_grad_pieces(int64_t batch, int64_t dim, int64_t L);
 // tokens of one wave's part of a row in the convolution's gradient
