@@ -254,22 +254,6 @@ __global__ __launch_bounds__(kThreads) void causal_scan_kernel(const ScanFwdArgs
 // last from zero, with no read-out, and stores h_loc and the sum of delta;
 // the second folds those of the earlier pieces into its own starting state
 // and scans its tokens in full.
-constexpr int kWideCh = vs::kCausalWideCh; // channels per workgroup
-constexpr int kWidePad = 2 * kRowLanes + 4; // floats per token of the LDS tile
-
-template <int Q>
-__device__ __forceinline__ float quad_bcast(float v) { return dpp<Q * 0x55>(v); }
-
-// four values of each lane summed over the quad: lane q returns sum of p_q
-__device__ __forceinline__ float quad_transpose_sum(float p0, float p1, float p2, float p3, int lane) {
-    const bool odd = (lane & 1) != 0, high = (lane & 2) != 0;
-    const float a = p0 + dpp<0xb1>(p0), b = p1 + dpp<0xb1>(p1);      // quad_perm [1,0,3,2]
-    const float c = p2 + dpp<0xb1>(p2), d = p3 + dpp<0xb1>(p3);
-    const float ab = odd ? b : a, cd = odd ? d : c;
-    const float s = ab + dpp<0x4e>(ab), t = cd + dpp<0x4e>(cd);      // quad_perm [2,3,0,1]
-    return high ? t : s;
-}
-
 template <typename T, bool GATE, bool SOFTPLUS, bool SAVE, bool CARRY>
 __global__ __launch_bounds__(kThreads) void causal_scan4_kernel(const ScanFwdArgs a) {
     __shared__ __attribute__((aligned(16))) float tile[2][kTileTok][kWidePad];
@@ -352,13 +336,26 @@ __global__ __launch_bounds__(kThreads) void causal_scan4_kernel(const ScanFwdArg
                 if (4 * q + r < a.dstate) h[r] = a.h0[row * a.dstate + 4 * q + r];
         }
         const int before = min(piece, (len + a.piece_len - 1) / a.piece_len);
-        for (int p = 0; p < before; ++p) {
-            const float sd = a.piece_sum[piece_row(p)];
-            const float* hp = a.piece_h + piece_row(p) * a.dstate;
+        // eight pieces' aggregates in flight at a time; past the last, P = 1 and h_loc = 0
+        constexpr int kFold = 8;
+        for (int p0 = 0; p0 < before; p0 += kFold) {
+            float sd[kFold], loc[kFold][4];
 #pragma unroll
-            for (int r = 0; r < 4; ++r) {
-                const float loc = 4 * q + r < a.dstate ? hp[4 * q + r] : 0.f;
-                h[r] = fmaf(__builtin_amdgcn_exp2f(sd * A2[r]), h[r], loc);
+            for (int k = 0; k < kFold; ++k) {
+                const int p = min(p0 + k, before - 1);
+                sd[k] = a.piece_sum[piece_row(p)];
+                const float* hp = a.piece_h + piece_row(p) * a.dstate;
+#pragma unroll
+                for (int r = 0; r < 4; ++r) loc[k][r] = hp[min(4 * q + r, a.dstate - 1)];
+            }
+#pragma unroll
+            for (int k = 0; k < kFold; ++k) {
+                const bool on = p0 + k < before;
+#pragma unroll
+                for (int r = 0; r < 4; ++r) {
+                    const float l = on && 4 * q + r < a.dstate ? loc[k][r] : 0.f;
+                    h[r] = fmaf(__builtin_amdgcn_exp2f((on ? sd[k] : 0.f) * A2[r]), h[r], l);
+                }
             }
         }
     }
@@ -390,15 +387,24 @@ __global__ __launch_bounds__(kThreads) void causal_scan4_kernel(const ScanFwdArg
                 if (CARRY) sdl += dlt[i];
             }
             if (t0 + 16 < e) tok_load(t0 + 16);
-            if (SAVE) {
-                if (active)
+            if (SAVE && active) {
+                float* c = ck + static_cast<size_t>(t0 >> 4) * a.dstate + 4 * q;
+                if ((a.dstate & 3) == 0) {                     // uniform; rows of 16-byte multiples
+                    if (4 * q < a.dstate) __builtin_memcpy(c, h, sizeof(h));
+                } else {
 #pragma unroll
                     for (int r = 0; r < 4; ++r)
-                        if (4 * q + r < a.dstate) ck[static_cast<size_t>(t0 >> 4) * a.dstate + 4 * q + r] = h[r];
+                        if (4 * q + r < a.dstate) c[r] = h[r];
+                }
             }
             float p[16];
             Unroll<16>::run([&](auto ic) VS_INLINE {
                 constexpr int i = decltype(ic)::value;
+                // the exponentials do not wait for the states: left free, all
+                // 64 of a block are formed at its start and held in
+                // registers, so each four tokens' steps are tied to the state
+                // that the tokens before them left
+                if (i % 4 == 0) asm volatile("" : "+v"(dlt[0]), "+v"(dlt[1]), "+v"(dlt[2]), "+v"(dlt[3]), "+v"(h[0]));
                 const float* row_bc = tile[it & 1][half * 16 + i];
                 const float4 Bv = *reinterpret_cast<const float4*>(row_bc + 4 * q);
                 const float dt = quad_bcast<i / 4>(dlt[i % 4]), dx = quad_bcast<i / 4>(du[i % 4]);
@@ -410,9 +416,6 @@ __global__ __launch_bounds__(kThreads) void causal_scan4_kernel(const ScanFwdArg
                     const float4 Cv = *reinterpret_cast<const float4*>(row_bc + kRowLanes + 4 * q);
                     p[i] = fmaf(h[3], Cv.w, fmaf(h[2], Cv.z, fmaf(h[1], Cv.y, h[0] * Cv.x)));
                 }
-                // the exponentials do not wait for the states: unbounded, the
-                // scheduler moves all 64 of a block to its start
-                if (i % 4 == 3) __builtin_amdgcn_sched_barrier(0);
             });
             if (!CARRY) {
                 float v[4];

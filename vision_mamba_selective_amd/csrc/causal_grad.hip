@@ -34,22 +34,26 @@ struct ConvGradArgs {
     Strides sx, sdy;
     int64_t dim;
     int L, silu, segs, seg_len;
+    int tw;                 // lanes along a row: 64, or fewer where a whole row fits
 };
 
 // A wave takes one segment of one row, 63 x 8 tokens at a time: every lane
 // forms dpre of its eight consecutive tokens, and dx[t] = sum_j w[j] dpre[t +
 // W-1 - j] takes up to W - 1 later ones from the lane above, so lane 63 only
-// supplies its own and lane 0 of the next stride forms them again. Each lane
-// sums dw and dbias of its tokens; the wave's sums go to the segment's partial
-// row. Bound by memory (x and dy read, dx written once).
+// supplies its own and lane 0 of the next stride forms them again. Rows of up
+// to 248 tokens share a wave (tw lanes each). Each lane sums dw and dbias of
+// its tokens; the segment's sums go to its partial row. Bound by memory (x
+// and dy read, dx written once).
 template <typename T, int W>
 __global__ __launch_bounds__(kThreads) void causal_conv_grad_kernel(const ConvGradArgs a) {
-    const int lane = threadIdx.x & 63;
+    const int last = a.tw - 1;                       // the lane that only supplies its dpre
+    const int lane = threadIdx.x & last;
     const int64_t b = blockIdx.y;
-    const int64_t item = static_cast<int64_t>(blockIdx.x) * kWaves + (threadIdx.x >> 6);
+    const int64_t item = static_cast<int64_t>(blockIdx.x) * (kThreads / a.tw) + threadIdx.x / a.tw;
     const int seg = static_cast<int>(item % a.segs);
-    const int64_t d = item / a.segs;
-    if (d >= a.dim) return;                          // whole waves
+    const int64_t d0 = item / a.segs;
+    const bool real = d0 < a.dim;                    // lanes past the last row load, and write nothing
+    const int64_t d = real ? d0 : a.dim - 1;
     const int len = row_length(a.lengths, b, a.L);
     const T* x = static_cast<const T*>(a.x) + b * a.sx.b + d * a.sx.d;
     const T* dy = static_cast<const T*>(a.dy) + b * a.sdy.b + d * a.sdy.d;
@@ -65,7 +69,7 @@ __global__ __launch_bounds__(kThreads) void causal_conv_grad_kernel(const ConvGr
 #pragma unroll
     for (int j = 0; j < W; ++j) dw[j] = 0.f;
     const int s0 = seg * a.seg_len, s1 = min(s0 + a.seg_len, a.L);
-    for (int base = s0; base < s1; base += vs::kConvGradStep) {
+    for (int base = s0; base < s1; base += vs::kConvGradStep) {     // once where tw < 64
         const int t0 = base + lane * 8;
         float dpre[8 + W - 1];
 #pragma unroll
@@ -86,7 +90,7 @@ __global__ __launch_bounds__(kThreads) void causal_conv_grad_kernel(const ConvGr
                     v *= sg * fmaf(pre, 1.f - sg, 1.f);
                 }
                 dpre[i] = t0 + i < len ? v : 0.f;
-                if (lane < 63) {
+                if (lane < last) {
                     db += dpre[i];
 #pragma unroll
                     for (int j = 0; j < W; ++j) dw[j] = fmaf(dpre[i], f[i + j], dw[j]);
@@ -95,7 +99,7 @@ __global__ __launch_bounds__(kThreads) void causal_conv_grad_kernel(const ConvGr
         }
 #pragma unroll
         for (int k = 0; k < W - 1; ++k) dpre[8 + k] = __shfl_down(dpre[k], 1);
-        if (lane < 63 && t0 < s1) {
+        if (real && lane < last && t0 < s1) {
             float v[8];
 #pragma unroll
             for (int i = 0; i < 8; ++i) {
@@ -115,7 +119,7 @@ __global__ __launch_bounds__(kThreads) void causal_conv_grad_kernel(const ConvGr
             }
         }
         // entry p of the incoming window feeds pre[p - j], j <= p
-        if (a.dwindow && base == 0 && lane == 0) {
+        if (a.dwindow && base == 0 && lane == 0 && real) {
 #pragma unroll
             for (int p = 0; p < W - 1; ++p) {
                 float v = 0.f;
@@ -132,8 +136,9 @@ __global__ __launch_bounds__(kThreads) void causal_conv_grad_kernel(const ConvGr
     for (int j = 0; j <= W; ++j) {
         float v = j < W ? dw[j < W ? j : 0] : db;
 #pragma unroll
-        for (int m = 32; m > 0; m >>= 1) v += __shfl_xor(v, m);
-        if (lane == 0) part[j] = v;
+        for (int m = 32; m > 0; m >>= 1)
+            if (m < a.tw) v += __shfl_xor(v, m);
+        if (lane == 0 && real) part[j] = v;
     }
 }
 
@@ -160,9 +165,11 @@ struct ScanGradArgs {
     void *du, *ddelta, *dz;
     float *dh0;
     float* bc_part;         // [batch][group][nblk][2][16 tokens][16 states]
-    float* stat;            // [batch][dim][dstate + 2]: dA, dD, dt_bias of each row
+    float* stat;            // [batch][piece][dim][dstate + 2]: dA, dD, dt_bias of each row
+    float *piece_lam, *piece_sum;   // the pieces' adjoints from zero and sums of delta
     int64_t dim;
     int L, dstate, nblk;
+    int pieces, piece_len;  // piece_len a multiple of kTileTok
 };
 
 // Lanes 0-31 return a[l] + a[l + 32]; lanes 32-63 return b[l - 32] + b[l].
@@ -188,6 +195,12 @@ __device__ __forceinline__ float swap16_sum(float a, float b) {
 // dDelta = V + u W. dB and dC are sums over channels: the wave's four rows are
 // added by two rounds of lane swaps, the workgroup's waves in LDS, and the
 // workgroups' chunks by bc_reduce_kernel, all in a fixed order.
+//
+// Where the rows are too few to fill the chip the sequence is cut into pieces
+// as in the forward pass: the adjoint that leaves a piece at its start is P
+// lam + lam_loc, lam the one that enters at its end, so a first launch
+// (adjoint_carry_kernel) forms lam_loc and the sum of delta of every piece but
+// the first, and each workgroup here folds those of the later pieces.
 template <typename T, bool GATE, bool SOFTPLUS>
 __global__ __launch_bounds__(kThreads) void causal_grad_kernel(const ScanGradArgs a) {
     __shared__ __attribute__((aligned(16))) float tile[2][2][kRowLanes][kTilePad];
@@ -198,7 +211,8 @@ __global__ __launch_bounds__(kThreads) void causal_grad_kernel(const ScanGradArg
     const int n = lane & 15;
     uint32_t cg, bb;
     xcd_block(cg, bb);
-    const int64_t b = bb;
+    const int piece = static_cast<int>(bb % static_cast<uint32_t>(a.pieces));     // piece fastest
+    const int64_t b = bb / static_cast<uint32_t>(a.pieces);
     const int64_t d0 = static_cast<int64_t>(cg) * vs::kCausalCh + (tid >> 4);
     const bool active = d0 < a.dim;
     const int64_t d = active ? d0 : a.dim - 1;
@@ -209,49 +223,96 @@ __global__ __launch_bounds__(kThreads) void causal_grad_kernel(const ScanGradArg
     const float A2 = An * kLog2e;
     const float Dk = a.Dskip ? a.Dskip[d] : 0.f;
     const float bias = a.dt_bias ? a.dt_bias[d] : 0.f;
-    const T* u = static_cast<const T*>(a.u) + b * a.su.b + d * a.su.d;
-    const T* dl = static_cast<const T*>(a.delta) + b * a.sdl.b + d * a.sdl.d;
-    const T* z = static_cast<const T*>(a.z) + b * a.sz.b + d * a.sz.d;
-    const T* dy = static_cast<const T*>(a.dy) + b * a.sdy.b + d * a.sdy.d;
     const size_t row = static_cast<size_t>(b * a.dim + d);
-    const size_t at = row * static_cast<size_t>(L);
-    T* du = static_cast<T*>(a.du) + at;
-    T* dd = static_cast<T*>(a.ddelta) + at;
-    T* dz = static_cast<T*>(a.dz) + (GATE ? at : 0);
-    const float* s = a.s + at;
-    const float* ck = a.ckpt + row * static_cast<size_t>(a.nblk) * a.dstate;
+    // the wave's four rows of each tensor behind a buffer descriptor, as in
+    // the forward kernel: no branches around memory in the loop
+    const int64_t w0 = static_cast<int64_t>(cg) * vs::kCausalCh + __builtin_amdgcn_readfirstlane(wave) * 4;
+    const int64_t wd = w0 < a.dim ? w0 : a.dim - 1;
+    const int64_t wrows = w0 < a.dim ? (a.dim - w0 < 4 ? a.dim - w0 : 4) : 1;
+    const uint32_t wr = static_cast<uint32_t>(d - wd);
+    const Rows<T> u(a.u, b * a.su.b + wd * a.su.d, wrows, a.su.d, L), dl(a.delta, b * a.sdl.b + wd * a.sdl.d, wrows, a.sdl.d, L);
+    const Rows<T> z(a.z, GATE ? b * a.sz.b + wd * a.sz.d : 0, GATE ? wrows : 0, a.sz.d, L);
+    const Rows<T> dy(a.dy, b * a.sdy.b + wd * a.sdy.d, wrows, a.sdy.d, L);
+    const int64_t orow = (b * a.dim + wd) * L;
+    const Rows<T> du(a.du, orow, wrows, L, L), dd(a.ddelta, orow, wrows, L, L), dz(a.dz, orow, GATE ? wrows : 0, L, L);
+    const Rows<float> s(a.s, orow, GATE ? wrows : 0, L, L);
+    const int64_t crow = static_cast<int64_t>(a.nblk) * a.dstate;
+    const Rows<float> ck(a.ckpt, (b * a.dim + wd) * crow, wrows, crow, static_cast<int>(crow));
     float* chunk = a.bc_part + (static_cast<size_t>(b) * gridDim.x + cg) * static_cast<size_t>(a.nblk) * 512;
+    // this piece's tokens [s0, s1), of which [s0, e) are real
+    const int s0 = piece * a.piece_len, s1 = min(s0 + a.piece_len, L), e = min(s1, len);
+    const int t_lim = active ? s1 : 0;               // tokens whose outputs this lane may write
 
     BcStage<T> stage(a, b, tid, len);
-    const int nblk = (len + 15) / 16;
-    const int ntile = (len + kTileTok - 1) / kTileTok;
+    const int blk0 = s0 / 16;
+    const int nblk = e > s0 ? (e + 15) / 16 : blk0;  // blocks [blk0, nblk)
+    const int tile0 = s0 / kTileTok;
+    const int ntile = e > s0 ? (e + kTileTok - 1) / kTileTok : tile0;
     float lamE = a.dh_out && n_ok ? a.dh_out[row * a.dstate + n] : 0.f;
-    float dA = 0.f, dD = 0.f, db = 0.f;
-    if (ntile > 0) {
+    // the adjoint that enters at the piece's end: those of the later pieces
+    // that hold tokens, the last of them first, eight in flight at a time
+    const int nonempty = (len + a.piece_len - 1) / a.piece_len;
+    constexpr int kFold = 8;
+    for (int p1 = nonempty - 1; p1 > piece; p1 -= kFold) {
+        float sd[kFold], loc[kFold];
+#pragma unroll
+        for (int k = 0; k < kFold; ++k) {
+            const int p = max(p1 - k, piece + 1);
+            const size_t pr = static_cast<size_t>((b * (a.pieces - 1) + p - 1) * a.dim + d);
+            sd[k] = a.piece_sum[pr];
+            loc[k] = a.piece_lam[pr * a.dstate + (n_ok ? n : 0)];
+        }
+#pragma unroll
+        for (int k = 0; k < kFold; ++k) {
+            const bool on = p1 - k > piece;
+            lamE = fmaf(__builtin_amdgcn_exp2f((on ? sd[k] : 0.f) * A2), lamE, on && n_ok ? loc[k] : 0.f);
+        }
+    }
+    // dA adds up all of a row's tokens in one lane: in fp64, a block's sum at a time
+    double dA = 0.;
+    float dD = 0.f, db = 0.f;
+    struct Tok { Raw<T> u, d, z, g; uint32_t s, h; };
+    auto tok_load = [&](int blk, Tok& k) VS_INLINE {
+        const int t = blk * 16 + n;
+        k.u = u.load(u.at(wr, t));
+        k.d = dl.load(dl.at(wr, t));
+        k.g = dy.load(dy.at(wr, t));
+        if (GATE) {
+            k.z = z.load(z.at(wr, t));
+            k.s = s.load(s.at(wr, t));
+        }
+        k.h = ck.load(n_ok ? ck.at(wr, blk * a.dstate + n) : kDropped);
+    };
+    Tok nxt{};
+    if (ntile > tile0) {
         stage.load(ntile - 1);
+        tok_load(nblk - 1, nxt);
         stage.store(tile[(ntile - 1) & 1]);
     }
     lds_barrier();
-    for (int blk = nblk - 1; blk >= 0; --blk) {
+    for (int blk = nblk - 1; blk >= blk0; --blk) {
         const int it = blk >> 1, half = blk & 1;
         // the tile below goes to the other buffer while this one is used
-        const bool stages = it > 0 && (half == 1 || blk == nblk - 1);
+        const bool stages = it > tile0 && (half == 1 || blk == nblk - 1);
         if (stages) stage.load(it - 1);
+        const Tok cur = nxt;
+        tok_load(blk > blk0 ? blk - 1 : blk0, nxt);
         const int t = blk * 16 + n;
         const bool ok = t < len;
-        const int tc = ok ? t : len - 1;
-        const float x = ld(dl, tc) + bias;
+        const bool wr_ok = t < t_lim;
+        const float x = from_raw<T>(cur.d) + bias;
         const float dlt = ok ? (SOFTPLUS ? softplus_f(x) : x) : 0.f;
-        const float cu = ok ? ld(u, tc) : 0.f;
+        const float cu = ok ? from_raw<T>(cur.u) : 0.f;
         const float du_ = dlt * cu;
-        const float g = ok ? ld(dy, tc) : 0.f;
+        const float g = from_raw<T>(cur.g);
         float gs = g;
         if (GATE) {
-            const float zz = ld(z, tc), sg = sigmoid_f(zz);
-            gs = ok ? g * (zz * sg) : 0.f;
-            const float v = g * s[tc] * sg * fmaf(zz, 1.f - sg, 1.f);
-            if (active && t < L) st(dz, t, ok ? v : 0.f);
+            const float zz = from_raw<T>(cur.z), sg = sigmoid_f(zz);
+            gs = g * (zz * sg);
+            const float v = g * __uint_as_float(cur.s) * sg * fmaf(zz, 1.f - sg, 1.f);
+            dz.store(wr_ok ? dz.at(wr, t) : kDropped, ok ? v : 0.f);
         }
+        gs = ok ? gs : 0.f;
         const float4* Bt = reinterpret_cast<const float4*>(&tile[it & 1][0][n][half * 16]);
         const float4* Ct = reinterpret_cast<const float4*>(&tile[it & 1][1][n][half * 16]);
         float Bv[16], Cv[16], hs[16], es[16], wv[16], vv[16], sbc[16];
@@ -261,7 +322,7 @@ __global__ __launch_bounds__(kThreads) void causal_grad_kernel(const ScanGradArg
             Bv[4 * q] = bq.x; Bv[4 * q + 1] = bq.y; Bv[4 * q + 2] = bq.z; Bv[4 * q + 3] = bq.w;
             Cv[4 * q] = cq.x; Cv[4 * q + 1] = cq.y; Cv[4 * q + 2] = cq.z; Cv[4 * q + 3] = cq.w;
         }
-        const float h_in = n_ok ? ck[static_cast<size_t>(blk) * a.dstate + n] : 0.f;
+        const float h_in = __uint_as_float(cur.h);
         float h = h_in;
         Unroll<16>::run([&](auto ic) VS_INLINE {
             constexpr int i = decltype(ic)::value;
@@ -270,26 +331,29 @@ __global__ __launch_bounds__(kThreads) void causal_grad_kernel(const ScanGradArg
             hs[i] = h;
         });
         // lanes of channels past dim hold another channel's values: they
-        // count for nothing in the sums over channels
-        const float du_m = active ? du_ : 0.f, gs_m = active ? gs : 0.f;
+        // count for nothing in the sums over channels. Second copies of the
+        // broadcast sources, opaque to the compiler, give every broadcast one
+        // use, which folds it into that use as a DPP operand
+        float du_m = active ? du_ : 0.f, gs_m = active ? gs : 0.f;
+        asm volatile("" : "+v"(du_m), "+v"(gs_m));
+        float dA_blk = 0.f;
         Unroll<16>::run([&](auto ic) VS_INLINE {
             constexpr int i = 15 - decltype(ic)::value;
-            const float lam = fmaf(row_bcast<i>(gs), Cv[i], lamE);
+            const float lam = row_bcast_fmac<i, i == 15>(lamE, gs, Cv[i]);
             lamE = lam * es[i];
             const float q = lamE * (i > 0 ? hs[i > 0 ? i - 1 : 0] : h_in);
-            dA = fmaf(row_bcast<i>(dlt), q, dA);
+            dA_blk = row_bcast_fmac<i, i == 15>(dA_blk, dlt, q);
             wv[i] = lam * Bv[i];
             vv[i] = q * An;
             sbc[i] = swap32_sum(row_bcast<i>(du_m) * lam, row_bcast<i>(gs_m) * hs[i]);
         });
+        dA += static_cast<double>(dA_blk);
         const float Rw = row_transpose_sum(wv, lane);
         const float Rv = row_transpose_sum(vv, lane);
         const float ddl = fmaf(cu, Rw, Rv);
         const float dx = ok ? (SOFTPLUS ? ddl * sigmoid_f(x) : ddl) : 0.f;
-        if (active && t < L) {
-            st(du, t, ok ? fmaf(dlt, Rw, gs * Dk) : 0.f);
-            st(dd, t, dx);
-        }
+        du.store(wr_ok ? du.at(wr, t) : kDropped, ok ? fmaf(dlt, Rw, gs * Dk) : 0.f);
+        dd.store(wr_ok ? dd.at(wr, t) : kDropped, dx);
         db += dx;
         dD = fmaf(gs, cu, dD);
         // steps i and i + 8 of the block share a register: row 0 of a wave
@@ -309,12 +373,10 @@ __global__ __launch_bounds__(kThreads) void causal_grad_kernel(const ScanGradArg
             chunk[static_cast<size_t>(blk) * 512 + which * 256 + tok * 16 + n] = v;
         }
     }
-    if (active) {
-        float* stat = a.stat + row * (a.dstate + 2);
-        if (n_ok) {
-            stat[n] = dA;
-            if (a.dh0) a.dh0[row * a.dstate + n] = lamE;
-        }
+    float* stat = a.stat + (static_cast<size_t>(b * a.pieces + piece) * a.dim + d) * (a.dstate + 2);
+    if (active && n_ok) {
+        stat[n] = static_cast<float>(dA);
+        if (a.dh0 && piece == 0) a.dh0[row * a.dstate + n] = lamE;
     }
     // dD and dt_bias: the row's lanes hold its tokens' shares
 #pragma unroll
@@ -323,31 +385,141 @@ __global__ __launch_bounds__(kThreads) void causal_grad_kernel(const ScanGradArg
         db += __shfl_xor(db, m);
     }
     if (active && n == 0) {
-        float* stat = a.stat + row * (a.dstate + 2);
         stat[a.dstate] = dD;
         stat[a.dstate + 1] = db;
     }
     // the gradients of the padding
-    if (active)
-        for (int t = nblk * 16 + n; t < L; t += 16) {
-            st(du, t, 0.f);
-            st(dd, t, 0.f);
-            if (GATE) st(dz, t, 0.f);
+    for (int t = nblk * 16 + n; t < t_lim; t += 16) {
+        du.store(du.at(wr, t), 0.f);
+        dd.store(dd.at(wr, t), 0.f);
+        if (GATE) dz.store(dz.at(wr, t), 0.f);
+    }
+}
+
+// The adjoint that a piece's tokens leave at its start from zero at its end,
+// and their sum of delta: lamE <- exp(delta_t A) (lamE + gy_t C_t) from the
+// piece's last token to its first. The wide form of the forward scan (four
+// states a lane, 64 channels a workgroup), without a read-out.
+template <typename T, bool GATE, bool SOFTPLUS>
+__global__ __launch_bounds__(kThreads) void adjoint_carry_kernel(const ScanGradArgs a) {
+    constexpr int kPad = kRowLanes + 4;
+    __shared__ __attribute__((aligned(16))) float tile[2][kTileTok][kPad];
+    const int tid = threadIdx.x;
+    const int q = tid & 3;
+    uint32_t cg, bb;
+    xcd_block(cg, bb);
+    const uint32_t np = static_cast<uint32_t>(a.pieces - 1);
+    const int slot = static_cast<int>(bb % np);          // piece slot + 1
+    const int64_t b = bb / np;
+    const int64_t d0 = static_cast<int64_t>(cg) * kWideCh + (tid >> 2);
+    const bool active = d0 < a.dim;
+    const int64_t d = active ? d0 : a.dim - 1;
+    const int len = row_length(a.lengths, b, a.L);
+    const int s0 = (slot + 1) * a.piece_len, e = min(min(s0 + a.piece_len, a.L), len);
+    if (e <= s0) return;                                 // no later piece is folded either
+    float A2[4], lam[4];
+#pragma unroll
+    for (int r = 0; r < 4; ++r) {
+        const int n = 4 * q + r;
+        A2[r] = n < a.dstate ? a.A[d * a.dstate + n] * kLog2e : 0.f;
+        lam[r] = 0.f;
+    }
+    const float bias = a.dt_bias ? a.dt_bias[d] : 0.f;
+    const T* dl = static_cast<const T*>(a.delta) + b * a.sdl.b + d * a.sdl.d;
+    const T* z = static_cast<const T*>(a.z) + b * a.sz.b + d * a.sz.d;
+    const T* dy = static_cast<const T*>(a.dy) + b * a.sdy.b + d * a.sdy.d;
+    // C: thread (state tid / 8, tokens 4k..4k+3) of the first 128
+    const int sr = (tid >> 3) & 15, sk = (tid & 7) * 4;
+    const bool s_ok = sr < a.dstate, stager = tid < 128;
+    const T* ssrc = static_cast<const T*>(a.C) + b * a.sC.b + (s_ok ? sr : 0) * a.sC.d;
+    Four<T> sraw, rd, rz, rg;
+    auto stage_load = [&](int t0) VS_INLINE {
+        const int t = t0 + sk;
+        if (t + 4 <= len) sraw.load(ssrc + t);
+        else sraw.load_some(ssrc, t, len);
+    };
+    auto stage_store = [&](float (&dst)[kTileTok][kPad]) VS_INLINE {
+        if (stager)
+#pragma unroll
+            for (int i = 0; i < 4; ++i) dst[sk + i][sr] = s_ok ? sraw.get(i) : 0.f;
+    };
+    auto tok_load = [&](int t0) VS_INLINE {
+        const int t = t0 + 4 * q;
+        if (t0 + 16 <= len) {                            // uniform
+            rd.load(dl + t);
+            rg.load(dy + t);
+            if (GATE) rz.load(z + t);
+        } else {
+            rd.load_some(dl, t, len);
+            rg.load_some(dy, t, len);
+            if (GATE) rz.load_some(z, t, len);
         }
+    };
+    const int ntile = (e - s0 + kTileTok - 1) / kTileTok;
+    stage_load(s0 + (ntile - 1) * kTileTok);
+    tok_load(s0 + (e - s0 - 1) / 16 * 16);
+    stage_store(tile[(ntile - 1) & 1]);
+    float sdl = 0.f;
+    for (int it = ntile - 1; it >= 0; --it) {
+        const int t_tile = s0 + it * kTileTok;
+        lds_barrier();
+        if (it > 0) stage_load(t_tile - kTileTok);
+#pragma unroll
+        for (int half = 1; half >= 0; --half) {
+            const int t0 = t_tile + half * 16;
+            if (t0 >= e) continue;                       // uniform
+            float dlt[4], gs[4];
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                const bool ok = t0 + 4 * q + i < e;
+                const float x = rd.get(i) + bias;
+                dlt[i] = ok ? (SOFTPLUS ? softplus_f(x) : x) : 0.f;
+                gs[i] = rg.get(i);
+                if (GATE) {
+                    const float zz = rz.get(i);
+                    gs[i] *= zz * sigmoid_f(zz);
+                }
+                gs[i] = ok ? gs[i] : 0.f;
+                sdl += dlt[i];
+            }
+            if (t0 > s0) tok_load(t0 - 16);
+            Unroll<16>::run([&](auto ic) VS_INLINE {
+                constexpr int i = 15 - decltype(ic)::value;
+                // as in the forward form: keep the exponentials of later tokens from moving up
+                if (i % 4 == 3) asm volatile("" : "+v"(dlt[0]), "+v"(dlt[1]), "+v"(dlt[2]), "+v"(dlt[3]), "+v"(lam[0]));
+                const float4 Cv = *reinterpret_cast<const float4*>(&tile[it & 1][half * 16 + i][4 * q]);
+                const float dt = quad_bcast<i / 4>(dlt[i % 4]), g = quad_bcast<i / 4>(gs[i % 4]);
+                lam[0] = __builtin_amdgcn_exp2f(dt * A2[0]) * fmaf(g, Cv.x, lam[0]);
+                lam[1] = __builtin_amdgcn_exp2f(dt * A2[1]) * fmaf(g, Cv.y, lam[1]);
+                lam[2] = __builtin_amdgcn_exp2f(dt * A2[2]) * fmaf(g, Cv.z, lam[2]);
+                lam[3] = __builtin_amdgcn_exp2f(dt * A2[3]) * fmaf(g, Cv.w, lam[3]);
+            });
+        }
+        if (it > 0) stage_store(tile[(it - 1) & 1]);
+    }
+    sdl += dpp<0xb1>(sdl);
+    sdl += dpp<0x4e>(sdl);
+    if (active) {
+        const size_t pr = static_cast<size_t>((b * (a.pieces - 1) + slot) * a.dim + d);
+        if (q == 0) a.piece_sum[pr] = sdl;
+#pragma unroll
+        for (int r = 0; r < 4; ++r)
+            if (4 * q + r < a.dstate) a.piece_lam[pr * a.dstate + 4 * q + r] = lam[r];
+    }
 }
 
 struct BcReduceArgs {
     const float *part, *stat;
     const int32_t* lengths;
     float *dB, *dC, *dA, *dD, *dbias;
-    int64_t batch, dim;
+    int64_t stat_rows, dim;  // stat_rows: batch rows times pieces
     int L, dstate, nblk, groups;
     int tok_wgs;            // workgroups over the tokens of a batch row
 };
 
 // dB and dC: the workgroups' chunks added in order; a thread takes four
 // states of one token. The workgroups past tok_wgs of batch row 0 add dA, dD
-// and dt_bias over the batch rows, one thread per output.
+// and dt_bias over the batch rows and their pieces, one thread per output.
 __global__ __launch_bounds__(kThreads) void bc_reduce_kernel(const BcReduceArgs a) {
     const int tid = threadIdx.x;
     const int64_t b = blockIdx.y;
@@ -357,7 +529,7 @@ __global__ __launch_bounds__(kThreads) void bc_reduce_kernel(const BcReduceArgs 
         const int64_t i = static_cast<int64_t>(blockIdx.x - a.tok_wgs) * kThreads + tid;
         if (b != 0 || i >= n) return;
         float s = 0.f;
-        for (int64_t r = 0; r < a.batch; ++r) s += a.stat[r * n + i];
+        for (int64_t r = 0; r < a.stat_rows; ++r) s += a.stat[r * n + i];
         const int64_t d = i / per;
         const int k = static_cast<int>(i % per);
         if (k < a.dstate) a.dA[d * a.dstate + k] = s;
@@ -402,7 +574,10 @@ int launch_conv_grad(const vs::ConvCall& c) {
     a.sx = c.st[0]; a.sdy = c.st[1]; a.dim = c.dim; a.L = static_cast<int>(c.L); a.silu = c.flags & VS_CONV_SILU;
     a.seg_len = static_cast<int>(vs::conv_grad_segment(c.batch, c.dim, c.L));
     a.segs = static_cast<int>((c.L + a.seg_len - 1) / a.seg_len);
-    const int64_t wgs = (c.dim * a.segs + kWaves - 1) / kWaves;
+    a.tw = 2;
+    while (a.tw < 64 && (a.tw - 1) * vs::kConvVec < c.L) a.tw *= 2;
+    const int64_t per = kThreads / a.tw;
+    const int64_t wgs = (c.dim * a.segs + per - 1) / per;
     if (wgs >= (int64_t(1) << 31)) return fail(VS_ERR_UNSUPPORTED, "too many tokens and channels for one launch");
     const dim3 grid(static_cast<unsigned>(wgs), static_cast<unsigned>(c.batch));
     const hipStream_t st = static_cast<hipStream_t>(c.stream);
@@ -435,9 +610,22 @@ int launch_scan_grad(const vs::CausalCall& c) {
     a.dim = c.dim; a.L = static_cast<int>(c.L); a.dstate = static_cast<int>(c.dstate);
     a.nblk = static_cast<int>((c.L + vs::kBlockTok - 1) / vs::kBlockTok);
     const unsigned groups = static_cast<unsigned>((c.dim + vs::kCausalCh - 1) / vs::kCausalCh);
-    const dim3 grid(groups, static_cast<unsigned>(c.batch)), blk(kThreads);
+    a.pieces = vs::causal_grad_pieces(c.batch, c.dim, c.L);
+    const int64_t tiles = (c.L + kTileTok - 1) / kTileTok;
+    a.piece_len = static_cast<int>((tiles + a.pieces - 1) / a.pieces * kTileTok);
+    const dim3 grid(groups, static_cast<unsigned>(c.batch * a.pieces)), blk(kThreads);
     const hipStream_t st = static_cast<hipStream_t>(c.stream);
     const bool sp = c.flags & VS_FLAG_SOFTPLUS;
+    if (a.pieces > 1) {
+        a.piece_lam = reinterpret_cast<float*>(static_cast<char*>(c.ws) + wo[2]);
+        a.piece_sum = reinterpret_cast<float*>(static_cast<char*>(c.ws) + wo[3]);
+        const dim3 cgrid(static_cast<unsigned>((c.dim + kWideCh - 1) / kWideCh), static_cast<unsigned>(c.batch * (a.pieces - 1)));
+        if (c.z && sp) hipLaunchKernelGGL((adjoint_carry_kernel<T, true, true>), cgrid, blk, 0, st, a);
+        else if (c.z) hipLaunchKernelGGL((adjoint_carry_kernel<T, true, false>), cgrid, blk, 0, st, a);
+        else if (sp) hipLaunchKernelGGL((adjoint_carry_kernel<T, false, true>), cgrid, blk, 0, st, a);
+        else hipLaunchKernelGGL((adjoint_carry_kernel<T, false, false>), cgrid, blk, 0, st, a);
+        if (int rc = launched()) return rc;
+    }
     if (c.z && sp) hipLaunchKernelGGL((causal_grad_kernel<T, true, true>), grid, blk, 0, st, a);
     else if (c.z) hipLaunchKernelGGL((causal_grad_kernel<T, true, false>), grid, blk, 0, st, a);
     else if (sp) hipLaunchKernelGGL((causal_grad_kernel<T, false, true>), grid, blk, 0, st, a);
@@ -445,7 +633,7 @@ int launch_scan_grad(const vs::CausalCall& c) {
     if (int rc = launched()) return rc;
     BcReduceArgs r{};
     r.part = a.bc_part; r.stat = a.stat; r.lengths = c.lengths; r.dB = c.dB; r.dC = c.dC; r.dA = c.dA; r.dD = c.dD;
-    r.dbias = c.dbias; r.batch = c.batch; r.dim = c.dim; r.L = a.L; r.dstate = a.dstate; r.nblk = a.nblk;
+    r.dbias = c.dbias; r.stat_rows = c.batch * a.pieces; r.dim = c.dim; r.L = a.L; r.dstate = a.dstate; r.nblk = a.nblk;
     r.groups = static_cast<int>(groups);
     r.tok_wgs = (a.L + 31) / 32;
     const int64_t stat_wgs = (c.dim * (c.dstate + 2) + kThreads - 1) / kThreads;

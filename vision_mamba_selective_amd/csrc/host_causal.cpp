@@ -72,41 +72,68 @@ int check_overlaps(const Span* in, int ni, const Span* out, int no) {
 // The form of a causal scan by an estimate of its time in shader cycles, from
 // the kernels' measured cycles per block of 16 tokens with w workgroups on a
 // compute unit (of the 256):
-//   narrow (16 channels a workgroup)  1,070 for w = 1, then 200 + 770 w
-//   wide (64 channels), last launch   3,450 for w = 1, then 2,750 w
-//   wide, carry launch                2,500 for w = 1, then 2,000 w
-// and about 20,000 cycles for the wide form's second launch and its start.
-// Measured at 768 channels, bf16: 8 rows of 4,097 tokens 204 us narrow, 195 us
-// in 8 pieces; one row 125 us narrow, 56 us in 32 pieces; 1 x 1,536 x 16,385
-// 530 us narrow, 209 us in 32 pieces.
+//   narrow (16 channels a workgroup)  max(1070, 200 + 770 w)
+//   wide (64 channels), last launch   max(3300, 2600 w)
+//   wide, carry launch                max(2450, 1950 w)
+// and what the second launch, its start and its folding of p pieces add,
+// 9,000 + 6,000 w + (500 + 150 w) p. Measured, bf16: 8 x 768 x 4,097 tokens
+// 205 us narrow, 200 us in 8 pieces; 1 x 768 x 4,097 137 us narrow, 49 us in 21
+// pieces; 1 x 1,536 x 16,385 563 us narrow, 211 us in 21 pieces; 64 x 1,536 x
+// 197 110 us narrow, 101 us wide and not cut.
 int causal_pieces(int64_t batch, int64_t dim, int64_t L) {
-    const int64_t tiles = ceil_div(L, kTileTok);
+    const int64_t tiles = ceil_div(L, kTileTok), blocks = ceil_div(L, kBlockTok);
+    auto least = [](int64_t a, int64_t b) { return a > b ? a : b; };
     const int64_t wn = ceil_div(batch * ceil_div(dim, kCausalCh), kNumCUs);
-    const int64_t narrow = ceil_div(L, kBlockTok) * (wn == 1 ? 1070 : 200 + 770 * wn);
     const int64_t wgs = batch * ceil_div(dim, kCausalWideCh);
-    int64_t best = narrow;
+    const int64_t w1 = ceil_div(wgs, kNumCUs);
+    int64_t best = blocks * least(1070, 200 + 770 * wn);
     int pieces = 0;
+    if (blocks * least(3300, 2600 * w1) < best) {
+        best = blocks * least(3300, 2600 * w1);
+        pieces = 1;
+    }
     // for each w the most pieces that w workgroups a compute unit hold
-    for (int64_t w = 1; w <= 6; ++w) {
+    for (int64_t w = 1; w <= 4; ++w) {
         int64_t p = kNumCUs * w / wgs;
         p = p > kCausalMaxPieces ? kCausalMaxPieces : p;
         p = p > tiles ? tiles : p;
-        if (p < 1) continue;
+        if (p < 2) continue;
         p = ceil_div(tiles, ceil_div(tiles, p));        // no empty pieces
-        const int64_t per = (w == 1 ? 3450 : 2750 * w) + (p == 1 ? 0 : (w == 1 ? 2500 : 2000 * w));
-        const int64_t t = ceil_div(tiles, p) * 2 * per + (p == 1 ? 0 : 20000 + 100 * p);
+        const int64_t t = ceil_div(tiles, p) * 2 * (least(3300, 2600 * w) + least(2450, 1950 * w)) +
+                          9000 + 6000 * w + (500 + 150 * w) * p;
         if (t < best && batch * p <= 65535) {
             best = t;
             pieces = static_cast<int>(p);
         }
     }
-    // rows enough for more than that are not cut
-    const int64_t w1 = ceil_div(wgs, kNumCUs);
-    if (w1 > 6 && ceil_div(L, kBlockTok) * 2750 * w1 < best) pieces = 1;
     return pieces;
 }
 
-int causal_grad_pieces(int64_t, int64_t, int64_t) { return 1; }
+// The gradient's pieces, by the same kind of estimate: the adjoint kernel (16
+// channels a workgroup) takes max(2900, 2100 w) cycles per block, the carry
+// launch max(2450, 1950 w) with 64 channels a workgroup. Measured, bf16: 1 x
+// 768 x 4,097 tokens 342 us uncut.
+int causal_grad_pieces(int64_t batch, int64_t dim, int64_t L) {
+    const int64_t tiles = ceil_div(L, kTileTok);
+    auto least = [](int64_t a, int64_t b) { return a > b ? a : b; };
+    const int64_t wgs = batch * ceil_div(dim, kCausalCh), wide = batch * ceil_div(dim, kCausalWideCh);
+    int64_t best = ceil_div(L, kBlockTok) * least(2900, 2100 * ceil_div(wgs, kNumCUs));
+    int pieces = 1;
+    for (int64_t w = 1; w <= 4; ++w) {
+        int64_t p = kNumCUs * w / wgs;
+        p = p > kCausalMaxPieces ? kCausalMaxPieces : p;
+        p = p > tiles ? tiles : p;
+        if (p < 2) continue;
+        p = ceil_div(tiles, ceil_div(tiles, p));
+        const int64_t t = ceil_div(tiles, p) * 2 * (least(2900, 2100 * w) + least(2450, 1950 * ceil_div(wide * p, kNumCUs))) +
+                          9000 + 6000 * w + (500 + 150 * w) * p;
+        if (t < best && batch * p <= 65535) {
+            best = t;
+            pieces = static_cast<int>(p);
+        }
+    }
+    return pieces;
+}
 
 // A wave covers kConvGradStep tokens at a time; it takes up to 8 such steps of
 // a row where that leaves 16 waves for each of the 1,024 SIMDs.

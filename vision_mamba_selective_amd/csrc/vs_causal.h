@@ -220,4 +220,21 @@ struct BcStage {
     }
 };
 
+// ---- the wide form: four states a lane, a quad of lanes per channel
+constexpr int kWideCh = vs::kCausalWideCh; // channels per workgroup
+constexpr int kWidePad = 2 * kRowLanes + 4; // floats per token of the LDS tile
+
+template <int Q>
+__device__ __forceinline__ float quad_bcast(float v) { return dpp<Q * 0x55>(v); }
+
+// four values of each lane summed over the quad: lane q returns sum of p_q
+__device__ __forceinline__ float quad_transpose_sum(float p0, float p1, float p2, float p3, int lane) {
+    const bool odd = (lane & 1) != 0, high = (lane & 2) != 0;
+    const float a = p0 + dpp<0xb1>(p0), b = p1 + dpp<0xb1>(p1);      // quad_perm [1,0,3,2]
+    const float c = p2 + dpp<0xb1>(p2), d = p3 + dpp<0xb1>(p3);
+    const float ab = odd ? b : a, cd = odd ? d : c;
+    const float s = ab + dpp<0x4e>(ab), t = cd + dpp<0x4e>(cd);      // quad_perm [2,3,0,1]
+    return high ? t : s;
+}
+
 }  // namespace
