@@ -475,54 +475,101 @@ __global__ __launch_bounds__(kThreads) void causal_scan4_kernel(const ScanFwdArg
 }
 
 // one token of each row on the pool: four lanes per channel, lane q of a quad
-// holds states q, q + 4, ... (vector loads where dstate is 16)
+// holds states 4q..4q+3
 struct ScanStepArgs {
     const void *u, *delta, *z, *B, *C;
     const float *A, *Dskip, *dt_bias;
     float* h;
     const int32_t *slot_in, *slot_out;
     void* y;
-    int64_t st[5], slots, dim;
+    int64_t st[5], slots, dim, batch;
     int dstate;
 };
 
-template <typename T, bool GATE, bool SOFTPLUS>
+// ROWS batch rows per thread keep several rows' states in flight and read A
+// once for them; it is 4 where that still leaves every compute unit 4
+// workgroups. VEC: dstate a multiple of 4 (16-byte accesses of the states).
+// Bound by memory: each state is read and written once.
+template <typename T, bool GATE, bool SOFTPLUS, bool VEC, int ROWS>
 __global__ __launch_bounds__(kThreads) void scan_step_kernel(const ScanStepArgs a) {
     const int64_t d = static_cast<int64_t>(blockIdx.x) * (kThreads / 4) + (threadIdx.x >> 2);
     const int q = threadIdx.x & 3;
-    const int64_t b = blockIdx.y;
     if (d >= a.dim) return;                          // whole quads
-    T* y = static_cast<T*>(a.y) + b * a.dim + d;
-    const int64_t si = a.slot_in ? a.slot_in[b] : b, so = a.slot_out ? a.slot_out[b] : b;
-    if (si < 0 || so < 0 || si >= a.slots || so >= a.slots) {
-        if (q == 0) st(y, 0, 0.f);
-        return;
-    }
-    const float cu = ld(static_cast<const T*>(a.u), b * a.st[0] + d);
-    const float x = ld(static_cast<const T*>(a.delta), b * a.st[1] + d) + (a.dt_bias ? a.dt_bias[d] : 0.f);
-    const float dlt = SOFTPLUS ? softplus_f(x) : x;
-    const float du = dlt * cu;
-    const T* B = static_cast<const T*>(a.B) + b * a.st[3];
-    const T* C = static_cast<const T*>(a.C) + b * a.st[4];
-    const float* hi = a.h + (si * a.dim + d) * a.dstate;
-    float* ho = a.h + (so * a.dim + d) * a.dstate;
-    const float* A = a.A + d * a.dstate;
-    float sum = 0.f;
+    float A2[4];
+    const float* A = a.A + d * a.dstate + 4 * q;
 #pragma unroll
-    for (int r = 0; r < 4; ++r) {
-        const int n = 4 * q + r;
-        if (n < a.dstate) {
-            const float v = fmaf(__builtin_amdgcn_exp2f(dlt * (A[n] * kLog2e)), hi[n], du * ld(B, n));
-            ho[n] = v;
-            sum = fmaf(v, ld(C, n), sum);
+    for (int r = 0; r < 4; ++r) A2[r] = 4 * q + r < a.dstate ? A[r] * kLog2e : 0.f;
+    const float bias = a.dt_bias ? a.dt_bias[d] : 0.f;
+    const float Dk = a.Dskip ? a.Dskip[d] : 0.f;
+    // states past dstate: read as zero, never written
+    const bool lane_ok = 4 * q < a.dstate;
+    int64_t so[ROWS];
+    bool live[ROWS];
+    float h[ROWS][4], Bv[ROWS][4], Cv[ROWS][4], u[ROWS], x[ROWS], z[ROWS];
+#pragma unroll
+    for (int k = 0; k < ROWS; ++k) {
+        const int64_t b0 = static_cast<int64_t>(blockIdx.y) * ROWS + k;
+        const bool row = b0 < a.batch;
+        const int64_t b = row ? b0 : a.batch - 1;
+        const int64_t si = a.slot_in ? a.slot_in[b] : b;
+        so[k] = a.slot_out ? a.slot_out[b] : b;
+        live[k] = row && si >= 0 && si < a.slots && so[k] >= 0 && so[k] < a.slots;
+        const float* hi = a.h + ((live[k] ? si : 0) * a.dim + d) * a.dstate + 4 * q;
+        const T* B = static_cast<const T*>(a.B) + b * a.st[3] + 4 * q;
+        const T* C = static_cast<const T*>(a.C) + b * a.st[4] + 4 * q;
+        if (VEC) {
+            Four<T> fb, fc;
+#pragma unroll
+            for (int r = 0; r < 4; ++r) h[k][r] = Bv[k][r] = Cv[k][r] = 0.f;
+            if (lane_ok) {
+                __builtin_memcpy(h[k], hi, sizeof(h[k]));
+                fb.load(B);
+                fc.load(C);
+#pragma unroll
+                for (int r = 0; r < 4; ++r) {
+                    Bv[k][r] = fb.get(r);
+                    Cv[k][r] = fc.get(r);
+                }
+            }
+        } else {
+#pragma unroll
+            for (int r = 0; r < 4; ++r) {
+                const bool ok = 4 * q + r < a.dstate;
+                h[k][r] = ok ? hi[r] : 0.f;
+                Bv[k][r] = ok ? ld(B, r) : 0.f;
+                Cv[k][r] = ok ? ld(C, r) : 0.f;
+            }
         }
+        u[k] = ld(static_cast<const T*>(a.u), b * a.st[0] + d);
+        x[k] = ld(static_cast<const T*>(a.delta), b * a.st[1] + d) + bias;
+        z[k] = GATE ? ld(static_cast<const T*>(a.z), b * a.st[2] + d) : 0.f;
     }
-    sum += dpp<0xb1>(sum);                           // quad_perm [1,0,3,2]
-    sum += dpp<0x4e>(sum);                           // quad_perm [2,3,0,1]
-    if (q == 0) {
-        float v = fmaf(a.Dskip ? a.Dskip[d] : 0.f, cu, sum);
-        if (GATE) v *= silu_f(ld(static_cast<const T*>(a.z), b * a.st[2] + d));
-        st(y, 0, v);
+#pragma unroll
+    for (int k = 0; k < ROWS; ++k) {
+        const int64_t b = static_cast<int64_t>(blockIdx.y) * ROWS + k;
+        const float dlt = SOFTPLUS ? softplus_f(x[k]) : x[k];
+        const float du = dlt * u[k];
+        float sum = 0.f;
+#pragma unroll
+        for (int r = 0; r < 4; ++r) {
+            h[k][r] = fmaf(__builtin_amdgcn_exp2f(dlt * A2[r]), h[k][r], du * Bv[k][r]);
+            sum = fmaf(h[k][r], Cv[k][r], sum);
+        }
+        sum += dpp<0xb1>(sum);                       // quad_perm [1,0,3,2]
+        sum += dpp<0x4e>(sum);                       // quad_perm [2,3,0,1]
+        if (live[k]) {
+            float* ho = a.h + (so[k] * a.dim + d) * a.dstate + 4 * q;
+            if (VEC) {
+                if (lane_ok) __builtin_memcpy(ho, h[k], sizeof(h[k]));
+            } else {
+#pragma unroll
+                for (int r = 0; r < 4; ++r)
+                    if (4 * q + r < a.dstate) ho[r] = h[k][r];
+            }
+        }
+        float v = fmaf(Dk, u[k], sum);
+        if (GATE) v *= silu_f(z[k]);
+        if (q == 0 && b < a.batch) st(static_cast<T*>(a.y) + b * a.dim + d, 0, live[k] ? v : 0.f);
     }
 }
 
@@ -578,6 +625,17 @@ int launch_conv_step(const vs::StepCall& c) {
     });
 }
 
+template <typename T, bool VEC, int ROWS>
+void launch_step(const ScanStepArgs& a, dim3 grid, const vs::StepCall& c) {
+    const dim3 blk(kThreads);
+    const hipStream_t st = static_cast<hipStream_t>(c.stream);
+    const bool sp = c.flags & VS_FLAG_SOFTPLUS;
+    if (c.z && sp) hipLaunchKernelGGL((scan_step_kernel<T, true, true, VEC, ROWS>), grid, blk, 0, st, a);
+    else if (c.z) hipLaunchKernelGGL((scan_step_kernel<T, true, false, VEC, ROWS>), grid, blk, 0, st, a);
+    else if (sp) hipLaunchKernelGGL((scan_step_kernel<T, false, true, VEC, ROWS>), grid, blk, 0, st, a);
+    else hipLaunchKernelGGL((scan_step_kernel<T, false, false, VEC, ROWS>), grid, blk, 0, st, a);
+}
+
 template <typename T>
 int launch_scan_step(const vs::StepCall& c) {
     ScanStepArgs a{};
@@ -585,14 +643,18 @@ int launch_scan_step(const vs::StepCall& c) {
     a.h = static_cast<float*>(c.pool); a.slot_in = c.slot_in; a.slot_out = c.slot_out; a.y = c.y;
     for (int i = 0; i < 5; ++i) a.st[i] = c.st[i];
     a.slots = c.slots; a.dim = c.dim; a.dstate = static_cast<int>(c.inner);
-    const dim3 grid(static_cast<unsigned>((c.dim + kThreads / 4 - 1) / (kThreads / 4)), static_cast<unsigned>(c.batch));
-    const dim3 blk(kThreads);
-    const hipStream_t st = static_cast<hipStream_t>(c.stream);
-    const bool sp = c.flags & VS_FLAG_SOFTPLUS;
-    if (c.z && sp) hipLaunchKernelGGL((scan_step_kernel<T, true, true>), grid, blk, 0, st, a);
-    else if (c.z) hipLaunchKernelGGL((scan_step_kernel<T, true, false>), grid, blk, 0, st, a);
-    else if (sp) hipLaunchKernelGGL((scan_step_kernel<T, false, true>), grid, blk, 0, st, a);
-    else hipLaunchKernelGGL((scan_step_kernel<T, false, false>), grid, blk, 0, st, a);
+    a.batch = c.batch;
+    const int64_t groups = (c.dim + kThreads / 4 - 1) / (kThreads / 4);
+    const bool vec = c.inner % 4 == 0 && vs::aligned(c.pool, 16);
+    if (groups * ((c.batch + 3) / 4) >= 4 * vs::kNumCUs) {
+        const dim3 grid(static_cast<unsigned>(groups), static_cast<unsigned>((c.batch + 3) / 4));
+        if (vec) launch_step<T, true, 4>(a, grid, c);
+        else launch_step<T, false, 4>(a, grid, c);
+    } else {
+        const dim3 grid(static_cast<unsigned>(groups), static_cast<unsigned>(c.batch));
+        if (vec) launch_step<T, true, 1>(a, grid, c);
+        else launch_step<T, false, 1>(a, grid, c);
+    }
     return launched();
 }
 
