@@ -23,12 +23,12 @@ __all__ += _CAUSAL + _BEAM
 
 def __getattr__(name):
     if name in _CAUSAL:
-        from . import causal
-        return getattr(causal, name)
-    if name in _BEAM:
-        from . import beam
-        return getattr(beam, name)
-    if name in __all__:
-        from . import scan
-        return getattr(scan, name)
-    raise AttributeError(name)
+        from . import causal as module
+    elif name in _BEAM:
+        from . import beam as module
+    elif name in __all__:
+        from . import scan as module
+    else:
+        raise AttributeError(name)
+    value = globals()[name] = getattr(module, name)     # the next use finds it here
+    return value

@@ -7,8 +7,8 @@ import ctypes
 import torch
 
 from . import _native as nat
-from .causal import _dense, _input, _out, _start
-from .scan import _DTYPES, _ptr, _stream
+from .causal import _dense, _input, _out, _start, _stream
+from .scan import _DTYPES, _ptr
 
 _lib = nat.lib
 _F32 = torch.float32

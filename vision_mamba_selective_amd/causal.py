@@ -15,10 +15,17 @@ import ctypes
 import torch
 
 from . import _native as nat
-from .scan import _DTYPES, _ptr, _stream
+from .scan import _DTYPES, _ptr
 
 _lib = nat.lib
 _F32 = torch.float32
+_raw_stream = torch._C._cuda_getCurrentRawStream
+
+
+def _stream(device):
+    """The current stream's handle on a device (of a tensor, so with an index):
+    as torch.cuda.current_stream(device).cuda_stream, without making an object."""
+    return _raw_stream(device.index)
 
 
 def _fail(name, t, shape, dtype, device):
