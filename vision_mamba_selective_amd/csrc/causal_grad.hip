@@ -148,7 +148,8 @@ __global__ __launch_bounds__(kThreads) void conv_grad_reduce_kernel(const float*
     const int64_t i = static_cast<int64_t>(blockIdx.x) * kThreads + threadIdx.x;
     if (i >= n) return;
     float s = 0.f;
-    for (int64_t p = 0; p < parts; ++p) s += part[p * n + i];
+#pragma unroll 8
+    for (int64_t p = 0; p < parts; ++p) s += part[p * n + i];        // eight loads in flight
     const int64_t d = i / (width + 1);
     const int j = static_cast<int>(i % (width + 1));
     if (j < width) dw[d * width + j] = s;
@@ -164,12 +165,13 @@ struct ScanGradArgs {
     const float *ckpt, *s, *dh_out;
     void *du, *ddelta, *dz;
     float *dh0;
-    float* bc_part;         // [batch][group][nblk][2][16 tokens][16 states]
+    float* bc_part;         // [batch][group][nblk][512]: the sums of dB and dC over the group
     float* stat;            // [batch][piece][dim][dstate + 2]: dA, dD, dt_bias of each row
     float *piece_lam, *piece_sum;   // the pieces' adjoints from zero and sums of delta
     int64_t dim;
     int L, dstate, nblk;
-    int pieces, piece_len;  // piece_len a multiple of kTileTok
+    int pieces, piece_len;  // piece_len = sub * fine_len, a multiple of kTileTok
+    int sub, fine_len;      // the carry launch cuts every piece into `sub` finer ones
 };
 
 // Lanes 0-31 return a[l] + a[l + 32]; lanes 32-63 return b[l - 32] + b[l].
@@ -200,11 +202,13 @@ __device__ __forceinline__ float swap16_sum(float a, float b) {
 // as in the forward pass: the adjoint that leaves a piece at its start is P
 // lam + lam_loc, lam the one that enters at its end, so a first launch
 // (adjoint_carry_kernel) forms lam_loc and the sum of delta of every piece but
-// the first, and each workgroup here folds those of the later pieces.
+// the first, and each workgroup here folds those of the later pieces. That
+// launch has a quarter of this one's workgroups per piece, so it cuts the
+// pieces into finer ones.
 template <typename T, bool GATE, bool SOFTPLUS>
 __global__ __launch_bounds__(kThreads) void causal_grad_kernel(const ScanGradArgs a) {
     __shared__ __attribute__((aligned(16))) float tile[2][2][kRowLanes][kTilePad];
-    __shared__ __attribute__((aligned(16))) float red[2][kWaves][8][64];
+    __shared__ float4 red[2][kWaves][2][64];
     const int tid = threadIdx.x;
     const int lane = tid & 63;
     const int wave = tid >> 6;
@@ -251,20 +255,20 @@ __global__ __launch_bounds__(kThreads) void causal_grad_kernel(const ScanGradArg
     float lamE = a.dh_out && n_ok ? a.dh_out[row * a.dstate + n] : 0.f;
     // the adjoint that enters at the piece's end: those of the later pieces
     // that hold tokens, the last of them first, eight in flight at a time
-    const int nonempty = (len + a.piece_len - 1) / a.piece_len;
+    const int later = (piece + 1) * a.sub;           // the first finer piece after this one
     constexpr int kFold = 8;
-    for (int p1 = nonempty - 1; p1 > piece; p1 -= kFold) {
+    for (int p1 = (len + a.fine_len - 1) / a.fine_len - 1; p1 >= later; p1 -= kFold) {
         float sd[kFold], loc[kFold];
 #pragma unroll
         for (int k = 0; k < kFold; ++k) {
-            const int p = max(p1 - k, piece + 1);
-            const size_t pr = static_cast<size_t>((b * (a.pieces - 1) + p - 1) * a.dim + d);
+            const int p = max(p1 - k, later);
+            const size_t pr = static_cast<size_t>((b * ((a.pieces - 1) * a.sub) + p - a.sub) * a.dim + d);
             sd[k] = a.piece_sum[pr];
             loc[k] = a.piece_lam[pr * a.dstate + (n_ok ? n : 0)];
         }
 #pragma unroll
         for (int k = 0; k < kFold; ++k) {
-            const bool on = p1 - k > piece;
+            const bool on = p1 - k >= later;
             lamE = fmaf(__builtin_amdgcn_exp2f((on ? sd[k] : 0.f) * A2), lamE, on && n_ok ? loc[k] : 0.f);
         }
     }
@@ -272,16 +276,21 @@ __global__ __launch_bounds__(kThreads) void causal_grad_kernel(const ScanGradArg
     double dA = 0.;
     float dD = 0.f, db = 0.f;
     struct Tok { Raw<T> u, d, z, g; uint32_t s, h; };
+    // each lane's byte offset of token n of block 0 in every tensor; the block
+    // comes in as a scalar
+    constexpr int kEs = sizeof(T);
+    const uint32_t ou = u.at(wr, n), od = dl.at(wr, n), og = dy.at(wr, n), oz = z.at(wr, n), os = s.at(wr, n);
+    const uint32_t oh = n_ok ? ck.at(wr, n) : kDropped, oo = du.at(wr, n);
     auto tok_load = [&](int blk, Tok& k) VS_INLINE {
-        const int t = blk * 16 + n;
-        k.u = u.load(u.at(wr, t));
-        k.d = dl.load(dl.at(wr, t));
-        k.g = dy.load(dy.at(wr, t));
+        const int t0 = blk * 16 * kEs;
+        k.u = u.load(ou, t0);
+        k.d = dl.load(od, t0);
+        k.g = dy.load(og, t0);
         if (GATE) {
-            k.z = z.load(z.at(wr, t));
-            k.s = s.load(s.at(wr, t));
+            k.z = z.load(oz, t0);
+            k.s = s.load(os, blk * 64);
         }
-        k.h = ck.load(n_ok ? ck.at(wr, blk * a.dstate + n) : kDropped);
+        k.h = ck.load(oh, blk * a.dstate * 4);
     };
     Tok nxt{};
     if (ntile > tile0) {
@@ -299,7 +308,8 @@ __global__ __launch_bounds__(kThreads) void causal_grad_kernel(const ScanGradArg
         tok_load(blk > blk0 ? blk - 1 : blk0, nxt);
         const int t = blk * 16 + n;
         const bool ok = t < len;
-        const bool wr_ok = t < t_lim;
+        const uint32_t out = t < t_lim ? oo : kDropped;
+        const int out0 = blk * 16 * kEs;
         const float x = from_raw<T>(cur.d) + bias;
         const float dlt = ok ? (SOFTPLUS ? softplus_f(x) : x) : 0.f;
         const float cu = ok ? from_raw<T>(cur.u) : 0.f;
@@ -310,7 +320,7 @@ __global__ __launch_bounds__(kThreads) void causal_grad_kernel(const ScanGradArg
             const float zz = from_raw<T>(cur.z), sg = sigmoid_f(zz);
             gs = g * (zz * sg);
             const float v = g * __uint_as_float(cur.s) * sg * fmaf(zz, 1.f - sg, 1.f);
-            dz.store(wr_ok ? dz.at(wr, t) : kDropped, ok ? v : 0.f);
+            dz.store(out, ok ? v : 0.f, out0);
         }
         gs = ok ? gs : 0.f;
         const float4* Bt = reinterpret_cast<const float4*>(&tile[it & 1][0][n][half * 16]);
@@ -336,7 +346,7 @@ __global__ __launch_bounds__(kThreads) void causal_grad_kernel(const ScanGradArg
         // use, which folds it into that use as a DPP operand
         float du_m = active ? du_ : 0.f, gs_m = active ? gs : 0.f;
         asm volatile("" : "+v"(du_m), "+v"(gs_m));
-        float dA_blk = 0.f;
+        float dA_blk = 0.f, pb[8], pc[8];
         Unroll<16>::run([&](auto ic) VS_INLINE {
             constexpr int i = 15 - decltype(ic)::value;
             const float lam = row_bcast_fmac<i, i == 15>(lamE, gs, Cv[i]);
@@ -345,32 +355,42 @@ __global__ __launch_bounds__(kThreads) void causal_grad_kernel(const ScanGradArg
             dA_blk = row_bcast_fmac<i, i == 15>(dA_blk, dlt, q);
             wv[i] = lam * Bv[i];
             vv[i] = q * An;
-            sbc[i] = swap32_sum(row_bcast<i>(du_m) * lam, row_bcast<i>(gs_m) * hs[i]);
+            pb[i & 7] = row_bcast<i>(du_m) * lam;
+            pc[i & 7] = row_bcast<i>(gs_m) * hs[i];
+            // eight steps' products stand before their swaps: a swap that
+            // follows its operands' writes at once would wait for them
+            if (i % 8 == 0) {
+#pragma unroll
+                for (int k = 0; k < 8; ++k) sbc[i + k] = swap32_sum(pb[k], pc[k]);
+            }
         });
         dA += static_cast<double>(dA_blk);
         const float Rw = row_transpose_sum(wv, lane);
         const float Rv = row_transpose_sum(vv, lane);
         const float ddl = fmaf(cu, Rw, Rv);
         const float dx = ok ? (SOFTPLUS ? ddl * sigmoid_f(x) : ddl) : 0.f;
-        du.store(wr_ok ? du.at(wr, t) : kDropped, ok ? fmaf(dlt, Rw, gs * Dk) : 0.f);
-        dd.store(wr_ok ? dd.at(wr, t) : kDropped, dx);
+        du.store(out, ok ? fmaf(dlt, Rw, gs * Dk) : 0.f, out0);
+        dd.store(out, dx, out0);
         db += dx;
         dD = fmaf(gs, cu, dD);
         // steps i and i + 8 of the block share a register: row 0 of a wave
         // then holds dB of step i, row 1 dB of i + 8, rows 2 and 3 dC
 #pragma unroll
-        for (int i = 0; i < 8; ++i) red[blk & 1][wave][i][lane] = swap16_sum(sbc[i], sbc[i + 8]);
+        for (int k = 0; k < 2; ++k)
+            red[blk & 1][wave][k][lane] = make_float4(swap16_sum(sbc[4 * k], sbc[4 * k + 8]), swap16_sum(sbc[4 * k + 1], sbc[4 * k + 9]),
+                                                      swap16_sum(sbc[4 * k + 2], sbc[4 * k + 10]), swap16_sum(sbc[4 * k + 3], sbc[4 * k + 11]));
         if (stages) stage.store(tile[(it - 1) & 1]);
         lds_barrier();
-        // thread (i, l) of two rounds: the waves' sums of step i (or i + 8)
+        // a thread adds two of the waves' sums: the chunk is [i / 4][lane][i % 4]
+        {
+            const int k = wave >> 1, part = wave & 1;
+            float2 v = reinterpret_cast<const float2*>(&red[blk & 1][0][k][lane])[part];
 #pragma unroll
-        for (int r = 0; r < 2; ++r) {
-            const int i = (tid >> 6) + 4 * r;
-            float v = 0.f;
-#pragma unroll
-            for (int w = 0; w < kWaves; ++w) v += red[blk & 1][w][i][lane];
-            const int which = lane >> 5, tok = i + ((lane >> 4) & 1) * 8;
-            chunk[static_cast<size_t>(blk) * 512 + which * 256 + tok * 16 + n] = v;
+            for (int w = 1; w < kWaves; ++w) {
+                const float2 o = reinterpret_cast<const float2*>(&red[blk & 1][w][k][lane])[part];
+                v.x += o.x; v.y += o.y;
+            }
+            *reinterpret_cast<float2*>(chunk + static_cast<size_t>(blk) * 512 + (k * 64 + lane) * 4 + part * 2) = v;
         }
     }
     float* stat = a.stat + (static_cast<size_t>(b * a.pieces + piece) * a.dim + d) * (a.dstate + 2);
@@ -408,14 +428,14 @@ __global__ __launch_bounds__(kThreads) void adjoint_carry_kernel(const ScanGradA
     const int q = tid & 3;
     uint32_t cg, bb;
     xcd_block(cg, bb);
-    const uint32_t np = static_cast<uint32_t>(a.pieces - 1);
-    const int slot = static_cast<int>(bb % np);          // piece slot + 1
+    const uint32_t np = static_cast<uint32_t>((a.pieces - 1) * a.sub);
+    const int slot = static_cast<int>(bb % np);          // finer piece slot + sub
     const int64_t b = bb / np;
     const int64_t d0 = static_cast<int64_t>(cg) * kWideCh + (tid >> 2);
     const bool active = d0 < a.dim;
     const int64_t d = active ? d0 : a.dim - 1;
     const int len = row_length(a.lengths, b, a.L);
-    const int s0 = (slot + 1) * a.piece_len, e = min(min(s0 + a.piece_len, a.L), len);
+    const int s0 = (slot + a.sub) * a.fine_len, e = min(min(s0 + a.fine_len, a.L), len);
     if (e <= s0) return;                                 // no later piece is folded either
     float A2[4], lam[4];
 #pragma unroll
@@ -500,7 +520,7 @@ __global__ __launch_bounds__(kThreads) void adjoint_carry_kernel(const ScanGradA
     sdl += dpp<0xb1>(sdl);
     sdl += dpp<0x4e>(sdl);
     if (active) {
-        const size_t pr = static_cast<size_t>((b * (a.pieces - 1) + slot) * a.dim + d);
+        const size_t pr = static_cast<size_t>((b * static_cast<int64_t>(np) + slot) * a.dim + d);
         if (q == 0) a.piece_sum[pr] = sdl;
 #pragma unroll
         for (int r = 0; r < 4; ++r)
@@ -518,7 +538,7 @@ struct BcReduceArgs {
 };
 
 // dB and dC: the workgroups' chunks added in order; a thread takes four
-// states of one token. The workgroups past tok_wgs of batch row 0 add dA, dD
+// tokens of one state. The workgroups past tok_wgs of batch row 0 add dA, dD
 // and dt_bias over the batch rows and their pieces, one thread per output.
 __global__ __launch_bounds__(kThreads) void bc_reduce_kernel(const BcReduceArgs a) {
     const int tid = threadIdx.x;
@@ -529,6 +549,7 @@ __global__ __launch_bounds__(kThreads) void bc_reduce_kernel(const BcReduceArgs 
         const int64_t i = static_cast<int64_t>(blockIdx.x - a.tok_wgs) * kThreads + tid;
         if (b != 0 || i >= n) return;
         float s = 0.f;
+#pragma unroll 8
         for (int64_t r = 0; r < a.stat_rows; ++r) s += a.stat[r * n + i];
         const int64_t d = i / per;
         const int k = static_cast<int>(i % per);
@@ -537,25 +558,30 @@ __global__ __launch_bounds__(kThreads) void bc_reduce_kernel(const BcReduceArgs 
         else a.dbias[d] = s;
         return;
     }
-    // 256 threads: 2 (dB, dC) x 4 (quads of states) x 32 tokens
-    const int which = tid >> 7, quad = tid & 3, tok = (tid >> 2) & 31;
-    const int t = static_cast<int>(blockIdx.x) * 32 + tok;
-    if (t >= a.L) return;
+    // a block of 16 tokens takes 128 threads, thread (k, l) the four tokens
+    // 4 k + 8 ((l / 16) % 2).. of dB (l < 32) or dC, state l % 16
+    const int lane = tid & 63, n = lane & 15;
+    const int blk = static_cast<int>(blockIdx.x) * 2 + (tid >> 7);
+    const int t = blk * 16 + ((lane >> 4) & 1) * 8 + ((tid >> 6) & 1) * 4;
+    if (t >= a.L || n >= a.dstate) return;
     const int len = row_length(a.lengths, b, a.L);
-    float4 s = make_float4(0.f, 0.f, 0.f, 0.f);
+    float v[4] = {0.f, 0.f, 0.f, 0.f};
     if (t < len) {
-        const float* p = a.part + (static_cast<size_t>(b) * a.groups * a.nblk + (t >> 4)) * 512 + which * 256 + (t & 15) * 16 + quad * 4;
+        const float* p = a.part + (static_cast<size_t>(b) * a.groups * a.nblk + blk) * 512 + (tid & 127) * 4;
+#pragma unroll 4
         for (int g = 0; g < a.groups; ++g) {
-            const float4 v = *reinterpret_cast<const float4*>(p + static_cast<size_t>(g) * a.nblk * 512);
-            s.x += v.x; s.y += v.y; s.z += v.z; s.w += v.w;
+            const float4 o = *reinterpret_cast<const float4*>(p + static_cast<size_t>(g) * a.nblk * 512);
+            v[0] += o.x; v[1] += o.y; v[2] += o.z; v[3] += o.w;
         }
     }
-    float* out = which ? a.dC : a.dB;
-    const float v[4] = {s.x, s.y, s.z, s.w};
+    float* out = (lane >> 5 ? a.dC : a.dB) + (b * a.dstate + n) * static_cast<int64_t>(a.L) + t;
+    // tokens of the block past the length hold zero sums
+    if (t + 4 <= a.L) {
+        store_four(out, v);
+    } else {
 #pragma unroll
-    for (int k = 0; k < 4; ++k) {
-        const int n = quad * 4 + k;
-        if (n < a.dstate) out[(b * a.dstate + n) * static_cast<int64_t>(a.L) + t] = v[k];
+        for (int k = 0; k < 4; ++k)
+            if (t + k < a.L) out[k] = v[k];
     }
 }
 
@@ -610,16 +636,18 @@ int launch_scan_grad(const vs::CausalCall& c) {
     a.dim = c.dim; a.L = static_cast<int>(c.L); a.dstate = static_cast<int>(c.dstate);
     a.nblk = static_cast<int>((c.L + vs::kBlockTok - 1) / vs::kBlockTok);
     const unsigned groups = static_cast<unsigned>((c.dim + vs::kCausalCh - 1) / vs::kCausalCh);
-    a.pieces = vs::causal_grad_pieces(c.batch, c.dim, c.L);
-    const int64_t tiles = (c.L + kTileTok - 1) / kTileTok;
-    a.piece_len = static_cast<int>((tiles + a.pieces - 1) / a.pieces * kTileTok);
+    const vs::GradCut cut = vs::causal_grad_cut(c.batch, c.dim, c.L);
+    a.pieces = cut.pieces;
+    a.sub = cut.sub;
+    a.fine_len = static_cast<int>(cut.fine_tiles * kTileTok);
+    a.piece_len = a.fine_len * a.sub;
     const dim3 grid(groups, static_cast<unsigned>(c.batch * a.pieces)), blk(kThreads);
     const hipStream_t st = static_cast<hipStream_t>(c.stream);
     const bool sp = c.flags & VS_FLAG_SOFTPLUS;
     if (a.pieces > 1) {
         a.piece_lam = reinterpret_cast<float*>(static_cast<char*>(c.ws) + wo[2]);
         a.piece_sum = reinterpret_cast<float*>(static_cast<char*>(c.ws) + wo[3]);
-        const dim3 cgrid(static_cast<unsigned>((c.dim + kWideCh - 1) / kWideCh), static_cast<unsigned>(c.batch * (a.pieces - 1)));
+        const dim3 cgrid(static_cast<unsigned>((c.dim + kWideCh - 1) / kWideCh), static_cast<unsigned>(c.batch * (a.pieces - 1) * a.sub));
         if (c.z && sp) hipLaunchKernelGGL((adjoint_carry_kernel<T, true, true>), cgrid, blk, 0, st, a);
         else if (c.z) hipLaunchKernelGGL((adjoint_carry_kernel<T, true, false>), cgrid, blk, 0, st, a);
         else if (sp) hipLaunchKernelGGL((adjoint_carry_kernel<T, false, true>), cgrid, blk, 0, st, a);

@@ -111,28 +111,34 @@ int causal_pieces(int64_t batch, int64_t dim, int64_t L) {
 
 // The gradient's pieces, by the same kind of estimate: the adjoint kernel (16
 // channels a workgroup) takes max(2900, 2100 w) cycles per block, the carry
-// launch max(2450, 1950 w) with 64 channels a workgroup. Measured, bf16: 1 x
-// 768 x 4,097 tokens 342 us uncut.
-int causal_grad_pieces(int64_t batch, int64_t dim, int64_t L) {
+// launch max(2450, 1950 w) with 64 channels a workgroup, and it may cut the
+// pieces finer. Measured, bf16, with the reduction: 1 x 768 x 4,097 tokens 342
+// us uncut, 97 us in 16 pieces; 8 x 768 x 4,097 545 us uncut.
+GradCut causal_grad_cut(int64_t batch, int64_t dim, int64_t L) {
     const int64_t tiles = ceil_div(L, kTileTok);
     auto least = [](int64_t a, int64_t b) { return a > b ? a : b; };
     const int64_t wgs = batch * ceil_div(dim, kCausalCh), wide = batch * ceil_div(dim, kCausalWideCh);
-    int64_t best = ceil_div(L, kBlockTok) * least(2900, 2100 * ceil_div(wgs, kNumCUs));
-    int pieces = 1;
+    GradCut best{1, 1, tiles};
+    int64_t least_t = ceil_div(L, kBlockTok) * least(2900, 2100 * ceil_div(wgs, kNumCUs));
     for (int64_t w = 1; w <= 4; ++w) {
         int64_t p = kNumCUs * w / wgs;
         p = p > kCausalMaxPieces ? kCausalMaxPieces : p;
         p = p > tiles ? tiles : p;
         if (p < 2) continue;
-        p = ceil_div(tiles, ceil_div(tiles, p));
-        const int64_t t = ceil_div(tiles, p) * 2 * (least(2900, 2100 * w) + least(2450, 1950 * ceil_div(wide * p, kNumCUs))) +
-                          9000 + 6000 * w + (500 + 150 * w) * p;
-        if (t < best && batch * p <= 65535) {
-            best = t;
-            pieces = static_cast<int>(p);
+        for (int64_t sub = 1; sub <= 8 && p * sub <= tiles && p * sub <= 2 * kCausalMaxPieces; sub *= 2) {
+            const int64_t fine = ceil_div(tiles, p * sub);
+            const int64_t pieces = ceil_div(tiles, fine * sub);             // no empty pieces
+            if (pieces < 2 || batch * pieces * sub > 65535) continue;
+            const int64_t t = 2 * (fine * sub * least(2900, 2100 * ceil_div(wgs * pieces, kNumCUs)) +
+                                   fine * least(2450, 1950 * ceil_div(wide * (pieces - 1) * sub, kNumCUs))) +
+                              9000 + 6000 * w + (500 + 150 * w) * pieces * sub;
+            if (t < least_t) {
+                least_t = t;
+                best = GradCut{static_cast<int>(pieces), static_cast<int>(sub), fine};
+            }
         }
     }
-    return pieces;
+    return best;
 }
 
 // A wave covers kConvGradStep tokens at a time; it takes up to 8 such steps of
@@ -155,12 +161,13 @@ size_t causal_grad_layout(int64_t batch, int64_t dim, int64_t dstate, int64_t L,
     const size_t rows = static_cast<size_t>(batch * dim);
     const size_t nblk = static_cast<size_t>(ceil_div(L, kBlockTok));
     const size_t groups = static_cast<size_t>(ceil_div(dim, kCausalCh));
-    const size_t pieces = static_cast<size_t>(causal_grad_pieces(batch, dim, L));
+    const GradCut cut = causal_grad_cut(batch, dim, L);
+    const size_t pieces = static_cast<size_t>(cut.pieces), carry = (pieces - 1) * static_cast<size_t>(cut.sub);
     size_t off = 0;
     offs[0] = off; off += al256(static_cast<size_t>(batch) * groups * nblk * 2 * kBlockTok * kRowLanes * kF);
     offs[1] = off; off += al256(rows * pieces * static_cast<size_t>(dstate + 2) * kF);
-    offs[2] = off; off += pieces > 1 ? al256(rows * pieces * static_cast<size_t>(dstate) * kF) : 0;
-    offs[3] = off; off += pieces > 1 ? al256(rows * pieces * kF) : 0;
+    offs[2] = off; off += al256(rows * carry * static_cast<size_t>(dstate) * kF);
+    offs[3] = off; off += al256(rows * carry * kF);
     return off;
 }
 

@@ -65,15 +65,17 @@ struct Rows {
     __device__ __forceinline__ uint32_t at(uint32_t row, int t) const {
         return (row * stride + static_cast<uint32_t>(t)) * static_cast<uint32_t>(sizeof(T));
     }
-    __device__ __forceinline__ Raw<T> load(uint32_t off) const {
-        if constexpr (sizeof(T) == 2) return __builtin_amdgcn_raw_buffer_load_b16(rsrc, static_cast<int>(off), 0, 0);
-        else return __builtin_amdgcn_raw_buffer_load_b32(rsrc, static_cast<int>(off), 0, 0);
+    // `more` bytes further on, the same for the whole wave (a scalar; the range
+    // check takes it in)
+    __device__ __forceinline__ Raw<T> load(uint32_t off, int more = 0) const {
+        if constexpr (sizeof(T) == 2) return __builtin_amdgcn_raw_buffer_load_b16(rsrc, static_cast<int>(off), more, 0);
+        else return __builtin_amdgcn_raw_buffer_load_b32(rsrc, static_cast<int>(off), more, 0);
     }
-    __device__ __forceinline__ void store(uint32_t off, float v) const {
+    __device__ __forceinline__ void store(uint32_t off, float v, int more = 0) const {
         if constexpr (sizeof(T) == 2)
-            __builtin_amdgcn_raw_buffer_store_b16(__builtin_bit_cast(uint16_t, static_cast<__bf16>(v)), rsrc, static_cast<int>(off), 0, 0);
+            __builtin_amdgcn_raw_buffer_store_b16(__builtin_bit_cast(uint16_t, static_cast<__bf16>(v)), rsrc, static_cast<int>(off), more, 0);
         else
-            __builtin_amdgcn_raw_buffer_store_b32(__float_as_uint(v), rsrc, static_cast<int>(off), 0, 0);
+            __builtin_amdgcn_raw_buffer_store_b32(__float_as_uint(v), rsrc, static_cast<int>(off), more, 0);
     }
 };
 

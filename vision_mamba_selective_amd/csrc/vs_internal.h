@@ -194,7 +194,9 @@ struct StepCall {
 // pieces the wide form of a causal scan cuts the sequence into (1: not cut);
 // 0: the narrow form
 int causal_pieces(int64_t batch, int64_t dim, int64_t L);
-int causal_grad_pieces(int64_t batch, int64_t dim, int64_t L);
+// the gradient's pieces, each of `sub` finer ones of fine_tiles 32-token tiles
+struct GradCut { int pieces, sub; int64_t fine_tiles; };
+GradCut causal_grad_cut(int64_t batch, int64_t dim, int64_t L);
 // tokens of one wave's part of a row in the convolution's gradient
 int64_t conv_grad_segment(int64_t batch, int64_t dim, int64_t L);
 size_t causal_ws_bytes(int op, int64_t batch, int64_t dim, int64_t dstate, int64_t L);
