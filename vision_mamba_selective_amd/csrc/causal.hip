@@ -125,7 +125,8 @@ __global__ __launch_bounds__(kThreads) void conv_step_kernel(const ConvStepArgs 
 // B and C of 32 tokens (a tile) are staged in LDS for the workgroup's
 // channels, double-buffered, one barrier per tile. Padding (t >= length)
 // enters as delta = 0 and zero u, B: it leaves the state as it is whatever
-// the padded memory holds.
+// the padded memory holds. Where that evens out the load of the compute units
+// the sequence is cut into a few pieces, as described for the wide form below.
 template <typename T, bool GATE, bool SOFTPLUS, bool SAVE>
 __global__ __launch_bounds__(kThreads) void causal_scan_kernel(const ScanFwdArgs a) {
     __shared__ __attribute__((aligned(16))) float tile[2][2][kRowLanes][kTilePad];
@@ -134,7 +135,8 @@ __global__ __launch_bounds__(kThreads) void causal_scan_kernel(const ScanFwdArgs
     const int n = lane & 15;
     uint32_t cg, bb;
     xcd_block(cg, bb);
-    const int64_t b = bb;
+    const int piece = static_cast<int>(bb % static_cast<uint32_t>(a.pieces));     // piece fastest
+    const int64_t b = bb / static_cast<uint32_t>(a.pieces);
     const int64_t d0 = static_cast<int64_t>(cg) * vs::kCausalCh + (tid >> 4);
     const bool active = d0 < a.dim;
     const int64_t d = active ? d0 : a.dim - 1;
@@ -160,13 +162,16 @@ __global__ __launch_bounds__(kThreads) void causal_scan_kernel(const ScanFwdArgs
     const int64_t orow = (b * a.dim + wd) * L;
     const Rows<T> y(a.y, orow, wrows, L, L);
     const Rows<float> s(a.s, SAVE ? orow : 0, SAVE && GATE ? wrows : 0, L, L);
-    uint32_t ou = u.at(wr, n), od = dl.at(wr, n), oz = z.at(wr, n);
-    uint32_t oy = y.at(wr, n), os = s.at(wr, n);
-    const int t_lim = active ? L : 0;           // tokens whose outputs this lane may write
+    // this piece's tokens [s0, s1), of which [s0, e) are real
+    const int s0 = piece * a.piece_len, s1 = min(s0 + a.piece_len, L), e = min(s1, len);
+    uint32_t ou = u.at(wr, s0 + n), od = dl.at(wr, s0 + n), oz = z.at(wr, s0 + n);
+    uint32_t oy = y.at(wr, s0 + n), os = s.at(wr, s0 + n);
+    const int t_lim = active ? s1 : 0;          // tokens whose outputs this lane may write
 
     BcStage<T> stage(a, b, tid, len);
     float h = a.h0 && n_ok ? a.h0[row * a.dstate + n] : 0.f;
-    const int ntile = (len + kTileTok - 1) / kTileTok;
+    const int tile0 = s0 / kTileTok;
+    const int ntile = e > s0 ? (e + kTileTok - 1) / kTileTok : tile0;      // tiles [tile0, ntile)
     Raw<T> ru[2], rd[2], rz[2];
     auto tok_load = [&]() VS_INLINE {
 #pragma unroll
@@ -179,12 +184,18 @@ __global__ __launch_bounds__(kThreads) void causal_scan_kernel(const ScanFwdArgs
         od += kTileTok * sizeof(T);
         oz += kTileTok * sizeof(T);
     };
-    if (ntile > 0) {
-        stage.load(0);
+    if (ntile > tile0) {
+        stage.load(tile0);
         tok_load();
-        stage.store(tile[0]);
+        stage.store(tile[tile0 & 1]);
     }
-    for (int it = 0; it < ntile; ++it) {
+    if (piece > 0) {
+        const float A1[1] = {A2};
+        float h1[1] = {h};
+        fold_pieces<1>(a, b, d, piece, len, n, A1, h1);
+        h = n_ok ? h1[0] : 0.f;
+    }
+    for (int it = tile0; it < ntile; ++it) {
         lds_barrier();
         if (it + 1 < ntile) stage.load(it + 1);
         Raw<T> cu_[2], cd_[2], cz_[2];
@@ -231,7 +242,8 @@ __global__ __launch_bounds__(kThreads) void causal_scan_kernel(const ScanFwdArgs
         if (SAVE) os += kTileTok * 4;
         if (it + 1 < ntile) stage.store(tile[(it + 1) & 1]);
     }
-    if (a.h_out && active && n_ok) a.h_out[row * a.dstate + n] = h;
+    // the piece with the row's last token (the first one for an empty row) has its final state
+    if (a.h_out && active && n_ok && (len > 0 ? s0 < len && len <= s1 : piece == 0)) a.h_out[row * a.dstate + n] = h;
     // the outputs of the padding past the last tile
     for (int t = ntile * kTileTok + n; t < t_lim; t += 16) {
         y.store(oy, 0.f);
@@ -263,7 +275,7 @@ __global__ __launch_bounds__(kThreads) void causal_scan4_kernel(const ScanFwdArg
     uint32_t cg, bb;
     xcd_block(cg, bb);
     // grid.y enumerates (batch, piece), piece fastest; the carry launch leaves the last piece out
-    const uint32_t np = static_cast<uint32_t>(CARRY ? a.pieces - 1 : a.pieces);
+    const uint32_t np = static_cast<uint32_t>(CARRY ? (a.pieces - 1) * a.sub : a.pieces);
     const int piece = static_cast<int>(bb % np);
     const int64_t b = bb / np;
     const int64_t d0 = static_cast<int64_t>(cg) * kWideCh + (tid >> 2);
@@ -272,7 +284,8 @@ __global__ __launch_bounds__(kThreads) void causal_scan4_kernel(const ScanFwdArg
     const int L = a.L;
     const int len = row_length(a.lengths, b, L);
     // this piece's tokens [s0, s1) and, of those, the real ones [s0, e)
-    const int s0 = piece * a.piece_len, s1 = min(s0 + a.piece_len, L), e = min(s1, len);
+    const int plen = CARRY ? a.fine_len : a.piece_len;
+    const int s0 = min(piece * plen, L), s1 = min(s0 + plen, L), e = min(s1, len);
     const size_t row = static_cast<size_t>(b * a.dim + d);
     float A2[4], h[4];
 #pragma unroll
@@ -289,9 +302,6 @@ __global__ __launch_bounds__(kThreads) void causal_scan4_kernel(const ScanFwdArg
     T* y = static_cast<T*>(a.y) + row * static_cast<size_t>(L);
     float* s = SAVE ? a.s + row * static_cast<size_t>(L) : nullptr;
     float* ck = SAVE ? a.ckpt + row * static_cast<size_t>(a.nblk) * a.dstate : nullptr;
-    // pieces' end states [batch][piece][dim][dstate] and sums of delta [batch][piece][dim]
-    const int64_t np1 = a.pieces - 1;
-    auto piece_row = [&](int p) { return static_cast<size_t>((b * np1 + p) * a.dim + d); };
 
     // ---- staging: thread (row r of B | C, tokens 4k..4k+3)
     const int sr = tid >> 3, sk = (tid & 7) * 4;
@@ -335,29 +345,7 @@ __global__ __launch_bounds__(kThreads) void causal_scan4_kernel(const ScanFwdArg
             for (int r = 0; r < 4; ++r)
                 if (4 * q + r < a.dstate) h[r] = a.h0[row * a.dstate + 4 * q + r];
         }
-        const int before = min(piece, (len + a.piece_len - 1) / a.piece_len);
-        // eight pieces' aggregates in flight at a time; past the last, P = 1 and h_loc = 0
-        constexpr int kFold = 8;
-        for (int p0 = 0; p0 < before; p0 += kFold) {
-            float sd[kFold], loc[kFold][4];
-#pragma unroll
-            for (int k = 0; k < kFold; ++k) {
-                const int p = min(p0 + k, before - 1);
-                sd[k] = a.piece_sum[piece_row(p)];
-                const float* hp = a.piece_h + piece_row(p) * a.dstate;
-#pragma unroll
-                for (int r = 0; r < 4; ++r) loc[k][r] = hp[min(4 * q + r, a.dstate - 1)];
-            }
-#pragma unroll
-            for (int k = 0; k < kFold; ++k) {
-                const bool on = p0 + k < before;
-#pragma unroll
-                for (int r = 0; r < 4; ++r) {
-                    const float l = on && 4 * q + r < a.dstate ? loc[k][r] : 0.f;
-                    h[r] = fmaf(__builtin_amdgcn_exp2f((on ? sd[k] : 0.f) * A2[r]), h[r], l);
-                }
-            }
-        }
+        fold_pieces<4>(a, b, d, piece, len, 4 * q, A2, h);
     }
     float sdl = 0.f;
     for (int it = 0; it < ntile; ++it) {
@@ -449,10 +437,12 @@ __global__ __launch_bounds__(kThreads) void causal_scan4_kernel(const ScanFwdArg
         sdl += dpp<0xb1>(sdl);
         sdl += dpp<0x4e>(sdl);
         if (active) {
-            if (q == 0) a.piece_sum[piece_row(piece)] = sdl;
+            // [batch][finer piece][dim]: sums of delta, and end states [...][dstate]
+            const size_t pr = static_cast<size_t>((b * static_cast<int64_t>(np) + piece) * a.dim + d);
+            if (q == 0) a.piece_sum[pr] = sdl;
 #pragma unroll
             for (int r = 0; r < 4; ++r)
-                if (4 * q + r < a.dstate) a.piece_h[piece_row(piece) * a.dstate + 4 * q + r] = h[r];
+                if (4 * q + r < a.dstate) a.piece_h[pr * a.dstate + 4 * q + r] = h[r];
         }
         return;
     }
@@ -676,31 +666,35 @@ int launch_scan(const vs::CausalCall& c) {
     const dim3 blk(kThreads);
     const hipStream_t st = static_cast<hipStream_t>(c.stream);
     const bool sp = c.flags & VS_FLAG_SOFTPLUS;
-    a.pieces = vs::causal_pieces(c.batch, c.dim, c.L);
-    if (a.pieces > 0) {
-        const int64_t tiles = (c.L + kTileTok - 1) / kTileTok;
-        a.piece_len = static_cast<int>((tiles + a.pieces - 1) / a.pieces * kTileTok);
+    const vs::ScanCut cut = vs::causal_cut(c.batch, c.dim, c.L);
+    a.pieces = cut.pieces;
+    a.sub = cut.sub;
+    a.fine_len = static_cast<int>(cut.fine_tiles * kTileTok);
+    a.piece_len = a.fine_len * a.sub;
+    const unsigned wide = static_cast<unsigned>((c.dim + kWideCh - 1) / kWideCh);
+    if (a.pieces > 1) {
+        const int64_t carry = static_cast<int64_t>(a.pieces - 1) * a.sub;
         a.piece_h = static_cast<float*>(c.ws);
-        a.piece_sum = a.piece_h + c.batch * (a.pieces - 1) * c.dim * c.dstate;
-        const unsigned groups = static_cast<unsigned>((c.dim + kWideCh - 1) / kWideCh);
-        const dim3 fgrid(groups, static_cast<unsigned>(c.batch * a.pieces));
-        if (a.pieces > 1) {
-            const dim3 cgrid(groups, static_cast<unsigned>(c.batch * (a.pieces - 1)));
-            if (sp) hipLaunchKernelGGL((causal_scan4_kernel<T, false, true, false, true>), cgrid, blk, 0, st, a);
-            else hipLaunchKernelGGL((causal_scan4_kernel<T, false, false, false, true>), cgrid, blk, 0, st, a);
-            if (int rc = launched()) return rc;
-        }
-        if (c.z && sp) hipLaunchKernelGGL((causal_scan4_kernel<T, true, true, SAVE, false>), fgrid, blk, 0, st, a);
-        else if (c.z) hipLaunchKernelGGL((causal_scan4_kernel<T, true, false, SAVE, false>), fgrid, blk, 0, st, a);
-        else if (sp) hipLaunchKernelGGL((causal_scan4_kernel<T, false, true, SAVE, false>), fgrid, blk, 0, st, a);
-        else hipLaunchKernelGGL((causal_scan4_kernel<T, false, false, SAVE, false>), fgrid, blk, 0, st, a);
-        return launched();
+        a.piece_sum = a.piece_h + c.batch * carry * c.dim * c.dstate;
+        const dim3 cgrid(wide, static_cast<unsigned>(c.batch * carry));
+        if (sp) hipLaunchKernelGGL((causal_scan4_kernel<T, false, true, false, true>), cgrid, blk, 0, st, a);
+        else hipLaunchKernelGGL((causal_scan4_kernel<T, false, false, false, true>), cgrid, blk, 0, st, a);
+        if (int rc = launched()) return rc;
     }
-    const dim3 grid(static_cast<unsigned>((c.dim + vs::kCausalCh - 1) / vs::kCausalCh), static_cast<unsigned>(c.batch));
-    if (c.z && sp) hipLaunchKernelGGL((causal_scan_kernel<T, true, true, SAVE>), grid, blk, 0, st, a);
-    else if (c.z) hipLaunchKernelGGL((causal_scan_kernel<T, true, false, SAVE>), grid, blk, 0, st, a);
-    else if (sp) hipLaunchKernelGGL((causal_scan_kernel<T, false, true, SAVE>), grid, blk, 0, st, a);
-    else hipLaunchKernelGGL((causal_scan_kernel<T, false, false, SAVE>), grid, blk, 0, st, a);
+    const unsigned rows = static_cast<unsigned>(c.batch * a.pieces);
+    if (cut.wide) {
+        const dim3 grid(wide, rows);
+        if (c.z && sp) hipLaunchKernelGGL((causal_scan4_kernel<T, true, true, SAVE, false>), grid, blk, 0, st, a);
+        else if (c.z) hipLaunchKernelGGL((causal_scan4_kernel<T, true, false, SAVE, false>), grid, blk, 0, st, a);
+        else if (sp) hipLaunchKernelGGL((causal_scan4_kernel<T, false, true, SAVE, false>), grid, blk, 0, st, a);
+        else hipLaunchKernelGGL((causal_scan4_kernel<T, false, false, SAVE, false>), grid, blk, 0, st, a);
+    } else {
+        const dim3 grid(static_cast<unsigned>((c.dim + vs::kCausalCh - 1) / vs::kCausalCh), rows);
+        if (c.z && sp) hipLaunchKernelGGL((causal_scan_kernel<T, true, true, SAVE>), grid, blk, 0, st, a);
+        else if (c.z) hipLaunchKernelGGL((causal_scan_kernel<T, true, false, SAVE>), grid, blk, 0, st, a);
+        else if (sp) hipLaunchKernelGGL((causal_scan_kernel<T, false, true, SAVE>), grid, blk, 0, st, a);
+        else hipLaunchKernelGGL((causal_scan_kernel<T, false, false, SAVE>), grid, blk, 0, st, a);
+    }
     return launched();
 }
 

@@ -636,7 +636,7 @@ int launch_scan_grad(const vs::CausalCall& c) {
     a.dim = c.dim; a.L = static_cast<int>(c.L); a.dstate = static_cast<int>(c.dstate);
     a.nblk = static_cast<int>((c.L + vs::kBlockTok - 1) / vs::kBlockTok);
     const unsigned groups = static_cast<unsigned>((c.dim + vs::kCausalCh - 1) / vs::kCausalCh);
-    const vs::GradCut cut = vs::causal_grad_cut(c.batch, c.dim, c.L);
+    const vs::ScanCut cut = vs::causal_grad_cut(c.batch, c.dim, c.L);
     a.pieces = cut.pieces;
     a.sub = cut.sub;
     a.fine_len = static_cast<int>(cut.fine_tiles * kTileTok);

@@ -69,75 +69,79 @@ int check_overlaps(const Span* in, int ni, const Span* out, int no) {
 
 }  // namespace
 
-// The form of a causal scan by an estimate of its time in shader cycles, from
-// the kernels' measured cycles per block of 16 tokens with w workgroups on a
+// The forms are chosen by an estimate of their time in shader cycles, from the
+// kernels' measured cycles per block of 16 tokens with w workgroups on a
 // compute unit (of the 256):
-//   narrow (16 channels a workgroup)  max(1070, 200 + 770 w)
-//   wide (64 channels), last launch   max(3300, 2600 w)
-//   wide, carry launch                max(2450, 1950 w)
-// and what the second launch, its start and its folding of p pieces add,
-// 9,000 + 6,000 w + (500 + 150 w) p. Measured, bf16: 8 x 768 x 4,097 tokens
-// 205 us narrow, 200 us in 8 pieces; 1 x 768 x 4,097 137 us narrow, 49 us in 21
-// pieces; 1 x 1,536 x 16,385 563 us narrow, 211 us in 21 pieces; 64 x 1,536 x
-// 197 110 us narrow, 101 us wide and not cut.
-int causal_pieces(int64_t batch, int64_t dim, int64_t L) {
+//   narrow scan (16 channels a workgroup)  max(1250, 260 + 750 w)
+//   wide scan (64 channels)                max(3300, 2600 w)
+//   adjoint (16 channels)                  max(2900, 2100 w)
+//   carry launches (64 channels)           max(2450, 1950 w)
+// and what the second launch and the folding of p finer pieces add. Measured,
+// bf16: 8 x 768 x 4,097 tokens narrow 210 us uncut, 189 us in 2 pieces of 8;
+// 1 x 768 x 4,097 132 us narrow, 48 us wide in 19 pieces; 1 x 1,536 x 16,385
+// 570 us narrow, 210 us wide in 21 pieces; 64 x 1,536 x 197 110 us narrow, 101
+// us wide and uncut. Gradient: 8 x 768 x 4,097 553 us uncut, 469 us in 2 pieces
+// of 8; 1 x 768 x 4,097 335 us uncut, 87 us in 16 pieces.
+namespace {
+
+int64_t most(int64_t a, int64_t b) { return a > b ? a : b; }
+
+struct Form {
+    int64_t channels;
+    int64_t least, base, per_wg;        // cycles per block: max(least, base + per_wg w)
+    int64_t start, fold;                // a cut adds start (4 + w) and fold (4 + w) for each finer piece
+    int64_t max_w;                      // the fullest compute unit that is tried
+};
+constexpr Form kNarrow{kCausalCh, 1250, 260, 750, 2000, 50, 4}, kWide{kCausalWideCh, 3300, 0, 2600, 3500, 140, 4},
+    kAdjoint{kCausalCh, 2900, 0, 2100, 2000, 50, 8};
+
+// the best cut of one form, if it beats `cycles`
+void try_form(const Form& f, bool wide, int64_t batch, int64_t dim, int64_t L, ScanCut& best, int64_t& cycles) {
     const int64_t tiles = ceil_div(L, kTileTok), blocks = ceil_div(L, kBlockTok);
-    auto least = [](int64_t a, int64_t b) { return a > b ? a : b; };
-    const int64_t wn = ceil_div(batch * ceil_div(dim, kCausalCh), kNumCUs);
-    const int64_t wgs = batch * ceil_div(dim, kCausalWideCh);
-    const int64_t w1 = ceil_div(wgs, kNumCUs);
-    int64_t best = blocks * least(1070, 200 + 770 * wn);
-    int pieces = 0;
-    if (blocks * least(3300, 2600 * w1) < best) {
-        best = blocks * least(3300, 2600 * w1);
-        pieces = 1;
+    const int64_t wgs = batch * ceil_div(dim, f.channels), carry_wgs = batch * ceil_div(dim, kCausalWideCh);
+    auto per_block = [&](int64_t w) { return most(f.least, f.base + f.per_wg * w); };
+    const int64_t whole = blocks * per_block(ceil_div(wgs, kNumCUs));
+    if (whole < cycles) {
+        cycles = whole;
+        best = ScanCut{wide, 1, 1, tiles};
     }
     // for each w the most pieces that w workgroups a compute unit hold
-    for (int64_t w = 1; w <= 4; ++w) {
-        int64_t p = kNumCUs * w / wgs;
-        p = p > kCausalMaxPieces ? kCausalMaxPieces : p;
-        p = p > tiles ? tiles : p;
-        if (p < 2) continue;
-        p = ceil_div(tiles, ceil_div(tiles, p));        // no empty pieces
-        const int64_t t = ceil_div(tiles, p) * 2 * (least(3300, 2600 * w) + least(2450, 1950 * w)) +
-                          9000 + 6000 * w + (500 + 150 * w) * p;
-        if (t < best && batch * p <= 65535) {
-            best = t;
-            pieces = static_cast<int>(p);
-        }
-    }
-    return pieces;
-}
-
-// The gradient's pieces, by the same kind of estimate: the adjoint kernel (16
-// channels a workgroup) takes max(2900, 2100 w) cycles per block, the carry
-// launch max(2450, 1950 w) with 64 channels a workgroup, and it may cut the
-// pieces finer. Measured, bf16, with the reduction: 1 x 768 x 4,097 tokens 342
-// us uncut, 97 us in 16 pieces; 8 x 768 x 4,097 545 us uncut.
-GradCut causal_grad_cut(int64_t batch, int64_t dim, int64_t L) {
-    const int64_t tiles = ceil_div(L, kTileTok);
-    auto least = [](int64_t a, int64_t b) { return a > b ? a : b; };
-    const int64_t wgs = batch * ceil_div(dim, kCausalCh), wide = batch * ceil_div(dim, kCausalWideCh);
-    GradCut best{1, 1, tiles};
-    int64_t least_t = ceil_div(L, kBlockTok) * least(2900, 2100 * ceil_div(wgs, kNumCUs));
-    for (int64_t w = 1; w <= 4; ++w) {
+    for (int64_t w = 1; w <= f.max_w; ++w) {
         int64_t p = kNumCUs * w / wgs;
         p = p > kCausalMaxPieces ? kCausalMaxPieces : p;
         p = p > tiles ? tiles : p;
         if (p < 2) continue;
         for (int64_t sub = 1; sub <= 8 && p * sub <= tiles && p * sub <= 2 * kCausalMaxPieces; sub *= 2) {
             const int64_t fine = ceil_div(tiles, p * sub);
-            const int64_t pieces = ceil_div(tiles, fine * sub);             // no empty pieces
+            const int64_t pieces = ceil_div(tiles, fine * sub);              // no empty pieces
             if (pieces < 2 || batch * pieces * sub > 65535) continue;
-            const int64_t t = 2 * (fine * sub * least(2900, 2100 * ceil_div(wgs * pieces, kNumCUs)) +
-                                   fine * least(2450, 1950 * ceil_div(wide * (pieces - 1) * sub, kNumCUs))) +
-                              9000 + 6000 * w + (500 + 150 * w) * pieces * sub;
-            if (t < least_t) {
-                least_t = t;
-                best = GradCut{static_cast<int>(pieces), static_cast<int>(sub), fine};
+            const int64_t wm = ceil_div(wgs * pieces, kNumCUs), wc = ceil_div(carry_wgs * (pieces - 1) * sub, kNumCUs);
+            // alone on its compute unit the longest piece counts, else their mean
+            const int64_t main = wm == 1 ? 2 * fine * sub : ceil_div(blocks, pieces);
+            const int64_t t = main * per_block(wm) + 2 * fine * most(2450, 1950 * wc) +
+                              f.start * (4 + w) + f.fold * (4 + w) * pieces * sub;
+            if (t < cycles) {
+                cycles = t;
+                best = ScanCut{wide, static_cast<int>(pieces), static_cast<int>(sub), fine};
             }
         }
     }
+}
+
+}  // namespace
+
+ScanCut causal_cut(int64_t batch, int64_t dim, int64_t L) {
+    ScanCut best{};
+    int64_t cycles = INT64_MAX;
+    try_form(kNarrow, false, batch, dim, L, best, cycles);
+    try_form(kWide, true, batch, dim, L, best, cycles);
+    return best;
+}
+
+ScanCut causal_grad_cut(int64_t batch, int64_t dim, int64_t L) {
+    ScanCut best{};
+    int64_t cycles = INT64_MAX;
+    try_form(kAdjoint, false, batch, dim, L, best, cycles);
     return best;
 }
 
@@ -161,7 +165,7 @@ size_t causal_grad_layout(int64_t batch, int64_t dim, int64_t dstate, int64_t L,
     const size_t rows = static_cast<size_t>(batch * dim);
     const size_t nblk = static_cast<size_t>(ceil_div(L, kBlockTok));
     const size_t groups = static_cast<size_t>(ceil_div(dim, kCausalCh));
-    const GradCut cut = causal_grad_cut(batch, dim, L);
+    const ScanCut cut = causal_grad_cut(batch, dim, L);
     const size_t pieces = static_cast<size_t>(cut.pieces), carry = (pieces - 1) * static_cast<size_t>(cut.sub);
     size_t off = 0;
     offs[0] = off; off += al256(static_cast<size_t>(batch) * groups * nblk * 2 * kBlockTok * kRowLanes * kF);
@@ -178,9 +182,9 @@ size_t causal_ws_bytes(int op, int64_t batch, int64_t dim, int64_t dstate, int64
     size_t offs[4];
     const size_t rows = static_cast<size_t>(batch * dim);
     if (op == VS_S6_SCAN) {
-        // per piece but the last: its end state from zero and its sum of delta
-        const size_t p = static_cast<size_t>(causal_pieces(batch, dim, L));
-        return p > 1 ? rows * (p - 1) * static_cast<size_t>(dstate + 1) * kF : 0;
+        // per finer piece but those of the last: its end state from zero and its sum of delta
+        const ScanCut cut = causal_cut(batch, dim, L);
+        return rows * static_cast<size_t>((cut.pieces - 1) * cut.sub) * static_cast<size_t>(dstate + 1) * kF;
     }
     if (op == VS_S6_SAVED) return causal_saved_layout(batch, dim, dstate, L, offs);
     if (op == VS_S6_GRAD) return causal_grad_layout(batch, dim, dstate, L, offs);

@@ -29,7 +29,8 @@ struct ScanFwdArgs {
     float *piece_h, *piece_sum;   // the pieces' end states from zero and sums of delta
     int64_t dim;
     int L, dstate, nblk;
-    int pieces, piece_len;
+    int pieces, piece_len;  // piece_len = sub * fine_len, a multiple of kTileTok
+    int sub, fine_len;      // the carry launch cuts every piece into `sub` finer ones
 };
 
 __device__ __forceinline__ int row_length(const int32_t* lengths, int64_t b, int L) {
@@ -221,6 +222,37 @@ struct BcStage {
             dst[i >> 1][(r0 + 8 * i) & 15][col] = ok[i] && in ? from_raw<T>(raw[i]) : 0.f;
     }
 };
+
+// The state that the pieces before `piece` leave behind, folded into h: eight
+// of the finer pieces' aggregates are in flight at a time; past the last, P = 1
+// and h_loc = 0. N states a lane from n0 on, A2 their A log2(e).
+template <int N>
+__device__ __forceinline__ void fold_pieces(const ScanFwdArgs& a, int64_t b, int64_t d, int piece, int len, int n0,
+                                            const float (&A2)[N], float (&h)[N]) {
+    constexpr int kFold = 8;
+    const int before = min(piece * a.sub, (len + a.fine_len - 1) / a.fine_len);
+    const int64_t carry = static_cast<int64_t>(a.pieces - 1) * a.sub;
+    for (int p0 = 0; p0 < before; p0 += kFold) {
+        float sd[kFold], loc[kFold][N];
+#pragma unroll
+        for (int k = 0; k < kFold; ++k) {
+            const size_t pr = static_cast<size_t>((b * carry + min(p0 + k, before - 1)) * a.dim + d);
+            sd[k] = a.piece_sum[pr];
+            const float* hp = a.piece_h + pr * a.dstate;
+#pragma unroll
+            for (int r = 0; r < N; ++r) loc[k][r] = hp[min(n0 + r, a.dstate - 1)];
+        }
+#pragma unroll
+        for (int k = 0; k < kFold; ++k) {
+            const bool on = p0 + k < before;
+#pragma unroll
+            for (int r = 0; r < N; ++r) {
+                const float l = on && n0 + r < a.dstate ? loc[k][r] : 0.f;
+                h[r] = fmaf(__builtin_amdgcn_exp2f((on ? sd[k] : 0.f) * A2[r]), h[r], l);
+            }
+        }
+    }
+}
 
 // ---- the wide form: four states a lane, a quad of lanes per channel
 constexpr int kWideCh = vs::kCausalWideCh; // channels per workgroup

@@ -191,12 +191,12 @@ struct StepCall {
     int64_t st[5];                                   // row strides
 };
 
-// pieces the wide form of a causal scan cuts the sequence into (1: not cut);
-// 0: the narrow form
-int causal_pieces(int64_t batch, int64_t dim, int64_t L);
-// the gradient's pieces, each of `sub` finer ones of fine_tiles 32-token tiles
-struct GradCut { int pieces, sub; int64_t fine_tiles; };
-GradCut causal_grad_cut(int64_t batch, int64_t dim, int64_t L);
+// How a causal scan or its gradient is cut: the sequence into `pieces` (1: not
+// cut), each of `sub` finer ones of fine_tiles 32-token tiles, which the carry
+// launch takes; wide: the scan's form with four states a lane.
+struct ScanCut { bool wide; int pieces, sub; int64_t fine_tiles; };
+ScanCut causal_cut(int64_t batch, int64_t dim, int64_t L);
+ScanCut causal_grad_cut(int64_t batch, int64_t dim, int64_t L);
 // tokens of one wave's part of a row in the convolution's gradient
 int64_t conv_grad_segment(int64_t batch, int64_t dim, int64_t L);
 size_t causal_ws_bytes(int op, int64_t batch, int64_t dim, int64_t dstate, int64_t L);
