@@ -89,8 +89,15 @@ __global__ __launch_bounds__(kThreads) void causal_conv_grad_kernel(const ConvGr
                     const float sg = sigmoid_f(pre);
                     v *= sg * fmaf(pre, 1.f - sg, 1.f);
                 }
-                dpre[i] = t0 + i < len ? v : 0.f;
-                if (lane < last) {
+                dpre[i] = v;
+            }
+            if (t0 + 8 > len) {
+#pragma unroll
+                for (int i = 0; i < 8; ++i) dpre[i] = t0 + i < len ? dpre[i] : 0.f;
+            }
+            if (lane < last) {
+#pragma unroll
+                for (int i = 0; i < 8; ++i) {
                     db += dpre[i];
 #pragma unroll
                     for (int j = 0; j < W; ++j) dw[j] = fmaf(dpre[i], f[i + j], dw[j]);
@@ -106,9 +113,14 @@ __global__ __launch_bounds__(kThreads) void causal_conv_grad_kernel(const ConvGr
                 v[i] = 0.f;
 #pragma unroll
                 for (int k = 0; k < W; ++k) v[i] = fmaf(w[W - 1 - k], dpre[i + k], v[i]);
-                const int k = t0 + i + W - 1 - len;     // the token's place in the outgoing window
-                if (dwo && k >= 0 && t0 + i < len) v[i] += ld(dwo, k);
-                if (t0 + i >= len) v[i] = 0.f;
+            }
+            if (t0 + 8 + W - 1 > len) {                 // the row's last tokens, and the padding
+#pragma unroll
+                for (int i = 0; i < 8; ++i) {
+                    const int k = t0 + i + W - 1 - len; // the token's place in the outgoing window
+                    if (dwo && k >= 0 && t0 + i < len) v[i] += ld(dwo, k);
+                    if (t0 + i >= len) v[i] = 0.f;
+                }
             }
             if (t0 + 8 <= a.L) {
                 store_eight(dx + t0, v);
