@@ -26,8 +26,8 @@ struct ConvArgs {
     void *y, *window_out;
     Strides sx;
     int64_t dim;
-    int L, silu;
-    int tw;                 // threads along the tokens of a row: a power of two, at most kThreads
+    int L;
+    int tw_log2;            // 1 << tw_log2 threads along the tokens of a row, at most kThreads
     int segs;               // workgroups along a row
 };
 
@@ -35,13 +35,15 @@ struct ConvArgs {
 // tokens of a row (one or two 16-byte loads, and a second load of the W - 1
 // entries before them, which the caches hold); short rows share a workgroup.
 // Bound by memory: each entry of x comes from HBM once.
-template <typename T, int W>
+template <typename T, int W, bool SILU>
 __global__ __launch_bounds__(kThreads) void causal_conv_kernel(const ConvArgs a) {
     const int tid = threadIdx.x;
-    const int rows = kThreads / a.tw;
+    const int tw = 1 << a.tw_log2, rows = kThreads >> a.tw_log2;
     const int64_t b = blockIdx.y;
-    const int seg = static_cast<int>(blockIdx.x % static_cast<unsigned>(a.segs));
-    const int64_t d = static_cast<int64_t>(blockIdx.x / static_cast<unsigned>(a.segs)) * rows + tid / a.tw;
+    const unsigned group = blockIdx.x / static_cast<unsigned>(a.segs);
+    const int seg = static_cast<int>(blockIdx.x - group * static_cast<unsigned>(a.segs));
+    const int j = tid & (tw - 1);
+    const int64_t d = static_cast<int64_t>(group) * rows + (tid >> a.tw_log2);
     if (d >= a.dim) return;
     const int len = row_length(a.lengths, b, a.L);
     const T* x = static_cast<const T*>(a.x) + b * a.sx.b + d * a.sx.d;
@@ -51,7 +53,7 @@ __global__ __launch_bounds__(kThreads) void causal_conv_kernel(const ConvArgs a)
     for (int j = 0; j < W; ++j) w[j] = a.w[d * W + j];
     const float bias = a.bias ? a.bias[d] : 0.f;
     T* y = static_cast<T*>(a.y) + (b * a.dim + d) * a.L;
-    const int t0 = (seg * a.tw + tid % a.tw) * vs::kConvVec;
+    const int t0 = (seg * tw + j) * vs::kConvVec;
     if (t0 < a.L) {
         float f[W + 7], v[8];
         conv_line<T, W>(x, win, t0, len, f);
@@ -60,7 +62,7 @@ __global__ __launch_bounds__(kThreads) void causal_conv_kernel(const ConvArgs a)
             v[i] = bias;
 #pragma unroll
             for (int j = 0; j < W; ++j) v[i] = fmaf(w[j], f[i + j], v[i]);
-            if (a.silu) v[i] = silu_f(v[i]);
+            if (SILU) v[i] = silu_f(v[i]);
         }
         if (t0 + 8 <= len) {
             store_eight(y + t0, v);
@@ -71,10 +73,9 @@ __global__ __launch_bounds__(kThreads) void causal_conv_kernel(const ConvArgs a)
         }
     }
     // the row's last W - 1 line entries, unchanged in their type
-    const int j = tid % a.tw;
     if (a.window_out && seg == 0) {
         T* wo = static_cast<T*>(a.window_out) + (b * a.dim + d) * (W - 1);
-        for (int k = j; k < W - 1; k += a.tw) {
+        for (int k = j; k < W - 1; k += tw) {
             const int p = len + k;
             wo[k] = p >= W - 1 ? x[p - (W - 1)] : (win ? win[p] : static_cast<T>(0));
         }
@@ -589,17 +590,18 @@ int launch_conv(const vs::ConvCall& c) {
     ConvArgs a{};
     a.x = c.x; a.window = c.window; a.w = c.w; a.bias = c.bias; a.lengths = c.lengths;
     a.y = c.y; a.window_out = c.window_out; a.sx = c.st[0]; a.dim = c.dim;
-    a.L = static_cast<int>(c.L); a.silu = c.flags & VS_CONV_SILU;
-    a.tw = 1;
-    while (a.tw < kThreads && a.tw * vs::kConvVec < c.L) a.tw *= 2;
-    const int64_t per = static_cast<int64_t>(a.tw) * vs::kConvVec;
+    a.L = static_cast<int>(c.L);
+    while ((1 << a.tw_log2) < kThreads && (vs::kConvVec << a.tw_log2) < c.L) ++a.tw_log2;
+    const int64_t per = vs::kConvVec << a.tw_log2;
     a.segs = static_cast<int>((c.L + per - 1) / per);
-    const int64_t rows = kThreads / a.tw, groups = (c.dim + rows - 1) / rows * a.segs;
+    const int64_t rows = kThreads >> a.tw_log2, groups = (c.dim + rows - 1) / rows * a.segs;
     if (groups >= (int64_t(1) << 31)) return fail(VS_ERR_UNSUPPORTED, "too many tokens and channels for one launch");
     const dim3 grid(static_cast<unsigned>(groups), static_cast<unsigned>(c.batch));
     return with_width(c.width, [&](auto w) {
-        hipLaunchKernelGGL((causal_conv_kernel<T, decltype(w)::value>), grid, dim3(kThreads), 0,
-                           static_cast<hipStream_t>(c.stream), a);
+        constexpr int W = decltype(w)::value;
+        const hipStream_t st = static_cast<hipStream_t>(c.stream);
+        if (c.flags & VS_CONV_SILU) hipLaunchKernelGGL((causal_conv_kernel<T, W, true>), grid, dim3(kThreads), 0, st, a);
+        else hipLaunchKernelGGL((causal_conv_kernel<T, W, false>), grid, dim3(kThreads), 0, st, a);
     });
 }
 

@@ -33,8 +33,8 @@ struct ConvGradArgs {
     float* part;            // [batch][segs][dim][W + 1]: dw, dbias of each segment
     Strides sx, sdy;
     int64_t dim;
-    int L, silu, segs, seg_len;
-    int tw;                 // lanes along a row: 64, or fewer where a whole row fits
+    int L, segs, seg_len;
+    int tw_log2;            // 1 << tw_log2 lanes along a row: 64, or fewer where a whole row fits
 };
 
 // A wave takes one segment of one row, 63 x 8 tokens at a time: every lane
@@ -44,14 +44,19 @@ struct ConvGradArgs {
 // to 248 tokens share a wave (tw lanes each). Each lane sums dw and dbias of
 // its tokens; the segment's sums go to its partial row. Bound by memory (x
 // and dy read, dx written once).
-template <typename T, int W>
+template <typename T, int W, bool SILU>
 __global__ __launch_bounds__(kThreads) void causal_conv_grad_kernel(const ConvGradArgs a) {
-    const int last = a.tw - 1;                       // the lane that only supplies its dpre
+    const int tw = 1 << a.tw_log2;
+    const int last = tw - 1;                         // the lane that only supplies its dpre
     const int lane = threadIdx.x & last;
     const int64_t b = blockIdx.y;
-    const int64_t item = static_cast<int64_t>(blockIdx.x) * (kThreads / a.tw) + threadIdx.x / a.tw;
-    const int seg = static_cast<int>(item % a.segs);
-    const int64_t d0 = item / a.segs;
+    int64_t d0 = static_cast<int64_t>(blockIdx.x) * (kThreads >> a.tw_log2) + (threadIdx.x >> a.tw_log2);
+    int seg = 0;
+    if (a.segs > 1) {                                // uniform; a whole wave to a segment then
+        const uint32_t item = blockIdx.x * kWaves + __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+        d0 = item / static_cast<uint32_t>(a.segs);
+        seg = static_cast<int>(item - static_cast<uint32_t>(d0) * static_cast<uint32_t>(a.segs));
+    }
     const bool real = d0 < a.dim;                    // lanes past the last row load, and write nothing
     const int64_t d = real ? d0 : a.dim - 1;
     const int len = row_length(a.lengths, b, a.L);
@@ -85,7 +90,7 @@ __global__ __launch_bounds__(kThreads) void causal_conv_grad_kernel(const ConvGr
                 float pre = bias, v = g.get(i);
 #pragma unroll
                 for (int j = 0; j < W; ++j) pre = fmaf(w[j], f[i + j], pre);
-                if (a.silu) {
+                if (SILU) {
                     const float sg = sigmoid_f(pre);
                     v *= sg * fmaf(pre, 1.f - sg, 1.f);
                 }
@@ -149,7 +154,7 @@ __global__ __launch_bounds__(kThreads) void causal_conv_grad_kernel(const ConvGr
         float v = j < W ? dw[j < W ? j : 0] : db;
 #pragma unroll
         for (int m = 32; m > 0; m >>= 1)
-            if (m < a.tw) v += __shfl_xor(v, m);
+            if (m < tw) v += __shfl_xor(v, m);
         if (lane == 0 && real) part[j] = v;
     }
 }
@@ -609,18 +614,25 @@ int launch_conv_grad(const vs::ConvCall& c) {
     ConvGradArgs a{};
     a.x = c.x; a.dy = c.dy; a.window = c.window; a.dwindow_out = c.dwindow_out; a.w = c.w; a.bias = c.bias;
     a.lengths = c.lengths; a.dx = c.dx; a.dwindow = c.dwindow; a.part = static_cast<float*>(c.ws);
-    a.sx = c.st[0]; a.sdy = c.st[1]; a.dim = c.dim; a.L = static_cast<int>(c.L); a.silu = c.flags & VS_CONV_SILU;
+    a.sx = c.st[0]; a.sdy = c.st[1]; a.dim = c.dim; a.L = static_cast<int>(c.L);
     a.seg_len = static_cast<int>(vs::conv_grad_segment(c.batch, c.dim, c.L));
     a.segs = static_cast<int>((c.L + a.seg_len - 1) / a.seg_len);
-    a.tw = 2;
-    while (a.tw < 64 && (a.tw - 1) * vs::kConvVec < c.L) a.tw *= 2;
-    const int64_t per = kThreads / a.tw;
+    a.tw_log2 = 1;
+    while (a.tw_log2 < 6 && ((1 << a.tw_log2) - 1) * vs::kConvVec < c.L) ++a.tw_log2;
+    const int64_t per = kThreads >> a.tw_log2;
     const int64_t wgs = (c.dim * a.segs + per - 1) / per;
-    if (wgs >= (int64_t(1) << 31)) return fail(VS_ERR_UNSUPPORTED, "too many tokens and channels for one launch");
+    // rows cut into segments are counted in 32 bits
+    if (wgs >= (int64_t(1) << 31) || (a.segs > 1 && c.dim * a.segs >= (int64_t(1) << 31) - kWaves)) return fail(VS_ERR_UNSUPPORTED, "too many tokens and channels for one launch");
     const dim3 grid(static_cast<unsigned>(wgs), static_cast<unsigned>(c.batch));
     const hipStream_t st = static_cast<hipStream_t>(c.stream);
     switch (c.width) {
-#define VS_CASE(w) case w: hipLaunchKernelGGL((causal_conv_grad_kernel<T, w>), grid, dim3(kThreads), 0, st, a); break;
+#define VS_CASE(w)                                                                                                       \
+    case w:                                                                                                              \
+        if (c.flags & VS_CONV_SILU)                                                                                      \
+            hipLaunchKernelGGL((causal_conv_grad_kernel<T, w, true>), grid, dim3(kThreads), 0, st, a);                   \
+        else                                                                                                             \
+            hipLaunchKernelGGL((causal_conv_grad_kernel<T, w, false>), grid, dim3(kThreads), 0, st, a);                  \
+        break;
     VS_CASE(2) VS_CASE(3) VS_CASE(4) VS_CASE(5) VS_CASE(6) VS_CASE(7) VS_CASE(8)
 #undef VS_CASE
     }
