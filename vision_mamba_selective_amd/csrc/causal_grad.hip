@@ -43,7 +43,8 @@ struct ConvGradArgs {
 // supplies its own and lane 0 of the next stride forms them again. Rows of up
 // to 248 tokens share a wave (tw lanes each). Each lane sums dw and dbias of
 // its tokens; the segment's sums go to its partial row. Bound by memory (x
-// and dy read, dx written once).
+// and dy read, dx written once) and, nearly as much, by VALU issue: 8 x 768 x
+// 4,097 bf16 43 us, 3.5 TB/s, VALU active 87 %.
 template <typename T, int W, bool SILU>
 __global__ __launch_bounds__(kThreads) void causal_conv_grad_kernel(const ConvGradArgs a) {
     const int tw = 1 << a.tw_log2;
@@ -222,6 +223,13 @@ __device__ __forceinline__ float swap16_sum(float a, float b) {
 // the first, and each workgroup here folds those of the later pieces. That
 // launch has a quarter of this one's workgroups per piece, so it cuts the
 // pieces into finer ones.
+//
+// Bound by VALU issue: 390 instructions a wave for 16 tokens, 156 of them with
+// a DPP operand, VALU active 86 %. 8 x 768 x 4,097 bf16,
+// 16 states, in 2 pieces: 350 us here and 53 in the carry launch. The matrix
+// cores could add up dB and dC over the channels, but a product with zeros for
+// the channels past dim or another block's tokens turns an infinity there into
+// NaN, and the lane swaps that it would save are an eighth of the instructions.
 template <typename T, bool GATE, bool SOFTPLUS>
 __global__ __launch_bounds__(kThreads) void causal_grad_kernel(const ScanGradArgs a) {
     __shared__ __attribute__((aligned(16))) float tile[2][2][kRowLanes][kTilePad];
@@ -436,7 +444,8 @@ __global__ __launch_bounds__(kThreads) void causal_grad_kernel(const ScanGradArg
 // The adjoint that a piece's tokens leave at its start from zero at its end,
 // and their sum of delta: lamE <- exp(delta_t A) (lamE + gy_t C_t) from the
 // piece's last token to its first. The wide form of the forward scan (four
-// states a lane, 64 channels a workgroup), without a read-out.
+// states a lane, 64 channels a workgroup), without a read-out. Bound by VALU
+// issue: half of 8 x 768 x 4,097 bf16 53 us.
 template <typename T, bool GATE, bool SOFTPLUS>
 __global__ __launch_bounds__(kThreads) void adjoint_carry_kernel(const ScanGradArgs a) {
     constexpr int kPad = kRowLanes + 4;
@@ -557,6 +566,7 @@ struct BcReduceArgs {
 // dB and dC: the workgroups' chunks added in order; a thread takes four
 // tokens of one state. The workgroups past tok_wgs of batch row 0 add dA, dD
 // and dt_bias over the batch rows and their pieces, one thread per output.
+// Bound by memory: 8 x 768 x 4,097, 203 MB of chunks in 46 us, 4.5 TB/s.
 __global__ __launch_bounds__(kThreads) void bc_reduce_kernel(const BcReduceArgs a) {
     const int tid = threadIdx.x;
     const int64_t b = blockIdx.y;

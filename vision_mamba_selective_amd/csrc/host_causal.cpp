@@ -77,7 +77,7 @@ int check_overlaps(const Span* in, int ni, const Span* out, int no) {
 //   adjoint (16 channels)                  max(2900, 2100 w)
 //   carry launches (64 channels)           max(2450, 1950 w)
 // and what the second launch and the folding of p finer pieces add. Measured,
-// bf16: 8 x 768 x 4,097 tokens narrow 210 us uncut, 189 us in 2 pieces of 8;
+// bf16: 8 x 768 x 4,097 tokens narrow 214 us uncut, 205 us in 2 pieces of 8;
 // 1 x 768 x 4,097 132 us narrow, 48 us wide in 19 pieces; 1 x 1,536 x 16,385
 // 570 us narrow, 210 us wide in 21 pieces; 64 x 1,536 x 197 110 us narrow, 101
 // us wide and uncut. Gradient: 8 x 768 x 4,097 553 us uncut, 469 us in 2 pieces
@@ -146,7 +146,8 @@ ScanCut causal_grad_cut(int64_t batch, int64_t dim, int64_t L) {
 }
 
 // A wave covers kConvGradStep tokens at a time; it takes up to 8 such steps of
-// a row where that leaves 16 waves for each of the 1,024 SIMDs.
+// a row where that leaves 16 waves for each of the 1,024 SIMDs (8 x 768 x 4,097
+// bf16, 9 steps a row: 3 of them 44 us, 1 58, 8 48).
 int64_t conv_grad_segment(int64_t batch, int64_t dim, int64_t L) {
     int64_t steps = batch * dim * ceil_div(L, kConvGradStep) / (16 * 1024);
     steps = steps < 1 ? 1 : (steps > 8 ? 8 : steps);
