@@ -58,8 +58,9 @@ GRAD_SLOTS_PER_UPDATE = 2 + 16
 MFMA_BF16_PEAK_TFLOPS = 2500.0
 
 PROFILE_TRAFFIC = os.path.join(ROOT, "profiles", "traffic.json")
-KERNEL_SRC = os.path.join(ROOT, "vision_mamba_selective_amd", "csrc", "vimscan.hip")
-PROJ_SRC = os.path.join(ROOT, "vision_mamba_selective_amd", "csrc", "proj.hip")
+CSRC = os.path.join(ROOT, "vision_mamba_selective_amd", "csrc")
+KERNEL_SRC = (os.path.join(CSRC, "vs_device.h"), os.path.join(CSRC, "vimscan.hip"))
+PROJ_SRC = (os.path.join(CSRC, "proj.hip"),)
 
 
 def parse():
@@ -109,9 +110,12 @@ def parse():
     return p.parse_args()
 
 
-def kernel_hash(path=KERNEL_SRC):
-    with open(path, "rb") as f:
-        return hashlib.sha256(f.read()).hexdigest()[:16]
+def kernel_hash(paths=KERNEL_SRC):
+    h = hashlib.sha256()
+    for path in paths:
+        with open(path, "rb") as f:
+            h.update(f.read())
+    return h.hexdigest()[:16]
 
 
 def main():
