@@ -174,6 +174,8 @@ def s6_conv_step(x, w, bias, window, slot_in=None, slot_out=None, silu=True, out
     width = w.shape[-1]
     slots = window.shape[0]
     _input("x", x, (batch, dim), dt, dev)
+    if batch > 1 and x.stride(0) == 0:      # one row for all: the ABI's stride 0 means dense rows
+        x = x.contiguous()
     _dense("w", w, (dim, width), _F32, dev)
     _dense("bias", bias, (dim,), _F32, dev)
     _dense("window", window, (slots, dim, width - 1), dt, dev)
