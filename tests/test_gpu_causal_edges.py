@@ -29,3 +29,19 @@ def test_step_of_one_row_for_all():
     y = vms.s6_scan_step(all_(u), all_(d), None, all_(B), all_(C), A, None, None, one)
     assert torch.equal(y, vms.s6_scan_step(u.repeat(6, 1), d.repeat(6, 1), None, B.repeat(6, 1), C.repeat(6, 1), A, None, None, two))
     assert torch.equal(one, two)
+
+
+def test_reorder_refuses_layers_that_share_memory_and_empty_states():
+    import vision_mamba_selective_amd as vms
+    say("case reorder refusals")
+    one = torch.zeros(1, 4, 8, device="cuda")
+    parent = torch.zeros(2, 2, dtype=torch.int32, device="cuda")
+    with pytest.raises(ValueError):
+        vms.beam_reorder(one.expand(3, 4, 8), parent)             # layer stride 0
+    with pytest.raises(ValueError):
+        vms.beam_reorder(one.view(-1).as_strided((2, 4, 4), (8, 4, 1)), parent)
+    for shape in ((0, 4, 8), (1, 4, 0)):
+        with pytest.raises(ValueError):
+            vms.beam_reorder(torch.zeros(shape, device="cuda"), parent)
+    with pytest.raises(ValueError):
+        vms.beam_reorder(torch.zeros(1, 0, 8, device="cuda"), torch.zeros(0, 2, dtype=torch.int32, device="cuda"))

@@ -75,8 +75,10 @@ def beam_reorder(state, parent, out=None):
     batch, beams = parent.shape
     _dense("parent", parent, (batch, beams), torch.int32, state.device)
     layers, rows = state.shape[:2]
-    if not state[0].is_contiguous() if layers else True:
-        raise ValueError("each layer of state must be contiguous")
+    if state.numel() == 0:
+        raise ValueError("state is empty: %s" % (tuple(state.shape),))
+    if not state[0].is_contiguous() or (layers > 1 and state.stride(0) < state[0].numel()):
+        raise ValueError("each layer of state must be contiguous and apart from the others")
     es = state.element_size()
     row_bytes = state[0].numel() // rows * es
     layer_bytes = state.stride(0) * es if layers > 1 else 0
