@@ -94,8 +94,8 @@ def select(logits, scores, done, eos):
                     n = sum(v == inf for v in vals)
                     logp = [-math.log(n) if v == inf else -inf for v in vals]
                 else:
-                    lse = m + math.log(sum(math.exp(v - m) for v in vals))
-                    logp = [v - lse for v in vals]
+                    lse = math.log(sum(math.exp(v - m) for v in vals))
+                    logp = [(v - m) - lse for v in vals]
             for t in range(vocab):
                 total = sc + logp[t]
                 if math.isnan(total):

@@ -45,3 +45,25 @@ def test_reorder_refuses_layers_that_share_memory_and_empty_states():
             vms.beam_reorder(torch.zeros(shape, device="cuda"), parent)
     with pytest.raises(ValueError):
         vms.beam_reorder(torch.zeros(1, 0, 8, device="cuda"), torch.zeros(0, 2, dtype=torch.int32, device="cuda"))
+
+
+def test_select_far_from_zero():
+    """A constant added to a row's logits changes no probability. The logits
+    are multiples of 2^-6 below 16, so that the shifted ones are exact too and
+    the results equal bit for bit; n equal logits, the lowest value among them,
+    have probability 1 / n each: 2^-24 of log(n) and of the sum stay."""
+    import math
+
+    import vision_mamba_selective_amd as vms
+    say("case select far from zero")
+    g = torch.Generator().manual_seed(9)
+    x = (torch.randint(-1000, 1000, (2, 3, 9001), generator=g) / 64.0).cuda()
+    scores = -torch.rand(2, 3, generator=g).cuda()
+    near = vms.beam_select(x, scores)
+    for shift in (4096.0, -65536.0):
+        for a, b in zip(near, vms.beam_select(x + shift, scores)):
+            assert torch.equal(a, b), shift
+    for value in (torch.finfo(torch.float32).min, -1e30, 1e30, 0.0):
+        s, p, t = vms.beam_select(torch.full((1, 2, 9001), value, device="cuda"), torch.tensor([[0.0, -1.0]], device="cuda"))
+        assert t.tolist() == [[0, 1]] and p.tolist() == [[0, 0]], value
+        assert (s.double() + math.log(9001)).abs().max().item() < 8 * 2.0 ** -24 * math.log(9001), (value, s)

@@ -338,7 +338,6 @@ __global__ __launch_bounds__(kMergeThreads) void beam_merge_kernel(const SelectA
         if (top != all) sum = top == -INFINITY || all == INFINITY ? 0.f : sum * __builtin_amdgcn_exp2f((top - all) * kLog2e);
         top = all;
         sum = wave_sum(sum);
-        const float lse = top == INFINITY ? 0.f : top + logf(sum);
         // lane r: the beam's candidate r
         uint64_t pick = 0;
         if (n <= 64) {
@@ -366,7 +365,10 @@ __global__ __launch_bounds__(kMergeThreads) void beam_merge_kernel(const SelectA
         }
         if (lane < K) {
             const float x = key_value(pick);
-            float v = x == -INFINITY ? -INFINITY : (top == INFINITY ? (x == INFINITY ? -logf(sum) : -INFINITY) : x - lse);
+            // (x - top) - log(sum): top + log(sum) would round away what log(sum)
+            // holds where the logits are far from zero
+            const float below = x == top ? 0.f : x - top;  // -inf, too, where only top is +inf
+            float v = x == -INFINITY ? -INFINITY : below - logf(sum);
             v = score + v + 0.f;
             if (v != v) v = -INFINITY;
             cand[k * K + lane] = pick ? make_key(v, static_cast<uint32_t>(k * K + lane)) : 0;
