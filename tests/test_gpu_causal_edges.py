@@ -67,3 +67,20 @@ def test_select_far_from_zero():
         s, p, t = vms.beam_select(torch.full((1, 2, 9001), value, device="cuda"), torch.tensor([[0.0, -1.0]], device="cuda"))
         assert t.tolist() == [[0, 1]] and p.tolist() == [[0, 0]], value
         assert (s.double() + math.log(9001)).abs().max().item() < 8 * 2.0 ** -24 * math.log(9001), (value, s)
+
+
+def test_second_derivatives_are_refused():
+    import vision_mamba_selective_amd as vms
+    say("case second derivatives")
+    g = torch.Generator().manual_seed(3)
+    rnd = lambda *s: torch.randn(*s, generator=g).cuda()   # noqa: E731
+    x = rnd(1, 8, 20).requires_grad_()
+    y, _ = vms.s6_causal_conv_autograd(x, rnd(8, 4))
+    d, = torch.autograd.grad(y.square().sum(), x, create_graph=True)
+    with pytest.raises(RuntimeError):
+        d.sum().backward()
+    u = rnd(1, 8, 20).requires_grad_()
+    y, _ = vms.s6_causal_scan_autograd(u, rnd(1, 8, 20), None, rnd(1, 4, 20), rnd(1, 4, 20), -torch.ones(8, 4, device="cuda"))
+    d, = torch.autograd.grad(y.square().sum(), u, create_graph=True)
+    with pytest.raises(RuntimeError):
+        d.sum().backward()

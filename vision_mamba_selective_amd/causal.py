@@ -13,6 +13,7 @@ from __future__ import annotations
 import ctypes
 
 import torch
+from torch.autograd.function import once_differentiable
 
 from . import _native as nat
 from .scan import _DTYPES, _ptr
@@ -317,7 +318,8 @@ def _rows(g, like):
 
 
 class CausalConvFunction(torch.autograd.Function):
-    """s6_causal_conv for autograd; both outputs are differentiable."""
+    """s6_causal_conv for autograd; both outputs are differentiable, once: a
+    gradient of the gradient is refused."""
 
     @staticmethod
     def forward(ctx, x, w, bias, window, lengths, silu):
@@ -328,6 +330,7 @@ class CausalConvFunction(torch.autograd.Function):
         return y, wo
 
     @staticmethod
+    @once_differentiable
     def backward(ctx, dy, dwo):
         x, w, bias, window, lengths = ctx.saved_tensors
         dy = x.new_zeros(x.shape) if dy is None else _rows(dy, x)
@@ -343,7 +346,8 @@ def s6_causal_conv_autograd(x, w, bias=None, window=None, lengths=None, silu=Tru
 
 class CausalScanFunction(torch.autograd.Function):
     """s6_causal_scan for autograd: the forward keeps the saved buffer for the
-    backward; y and h are differentiable. The gradients of B and C come back
+    backward; y and h are differentiable, once: a gradient of the gradient is
+    refused. The gradients of B and C come back
     in their dtype (the library sums them in fp32)."""
 
     @staticmethod
@@ -356,6 +360,7 @@ class CausalScanFunction(torch.autograd.Function):
         return y, h
 
     @staticmethod
+    @once_differentiable
     def backward(ctx, dy, dh):
         u, delta, z, B, C, A, Dskip, dt_bias, h0, lengths, saved = ctx.saved_tensors
         dy = u.new_zeros(u.shape) if dy is None else _rows(dy, u)
