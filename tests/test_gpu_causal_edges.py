@@ -84,3 +84,55 @@ def test_second_derivatives_are_refused():
     d, = torch.autograd.grad(y.square().sum(), u, create_graph=True)
     with pytest.raises(RuntimeError):
         d.sum().backward()
+
+
+@pytest.mark.parametrize("shape", [(2, 37, 301), (1, 20, 2100)], ids=["rows", "pieces"])
+@pytest.mark.parametrize("value", [float("inf"), float("nan")], ids=["inf", "nan"])
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16], ids=["f32", "bf16"])
+def test_non_finite_inputs_reach_only_what_they_are_part_of(dtype, value, shape):
+    """One bad entry of u or x changes its own channel from its token on, one
+    of dy its own channel up to its token; of the sums over channels and tokens
+    only those that hold it. Everything else keeps its bits."""
+    import vision_mamba_selective_amd as vms
+    batch, dim, L = shape
+    say("case non-finite %s %s %s" % (shape, value, dtype))
+    g = torch.Generator().manual_seed(L)
+    rnd = lambda *s, d=dtype: torch.randn(*s, generator=g).to(d).cuda()   # noqa: E731
+    u, x, dy, delta, z = (rnd(batch, dim, L) for _ in range(5))
+    B, C = rnd(batch, 16, L), rnd(batch, 16, L)
+    A = -(torch.rand(dim, 16, generator=g) + 0.1).cuda() * 4
+    bias, w = (rnd(dim, d=torch.float32) - 2), rnd(dim, 4, d=torch.float32)
+
+    def both(u, x, dy):
+        y, h, saved = vms.s6_causal_scan_saved(u, delta, z, B, C, A, None, bias)
+        return (dict(y=y, h=h, c=vms.s6_causal_conv(x, w)[0], dx=vms.s6_causal_conv_grad(x, w, None, dy)["dx"]),
+                vms.s6_causal_scan_grad(u, delta, z, B, C, A, None, bias, saved, dy))
+
+    def spoilt(v):
+        v = v.clone()
+        v[0, 5, at] = value
+        return v
+
+    at, others = 100, torch.arange(dim) != 5
+    out, grad = both(u, x, dy)
+    out2, grad2 = both(spoilt(u), spoilt(x), dy)
+    out3, grad3 = both(u, x, spoilt(dy))
+    for k in ("y", "c"):
+        assert torch.equal(out[k][0, 5, :at], out2[k][0, 5, :at]), k
+        assert not torch.isfinite(out2[k][0, 5, at]), k
+    assert torch.equal(grad["dB"][0, :, at + 1:], grad2["dB"][0, :, at + 1:])
+    assert torch.equal(grad["dC"][0, :, :at], grad2["dC"][0, :, :at])
+    assert torch.equal(grad["dB"][0, :, at + 1:], grad3["dB"][0, :, at + 1:])
+    assert torch.equal(out["dx"][0, 5, at + 1:], out3["dx"][0, 5, at + 1:])
+    for k in ("du", "ddelta"):
+        assert torch.equal(grad[k][0, 5, at + 1:], grad3[k][0, 5, at + 1:]), k
+        assert not torch.isfinite(grad3[k][0, 5, at]), k
+    for o, gr in ((out2, grad2), (out3, grad3)):
+        for k in ("y", "h", "c", "dx"):
+            assert torch.equal(out[k][0, others], o[k][0, others]) and torch.equal(out[k][1:], o[k][1:]), k
+        for k in ("du", "ddelta", "dz"):
+            assert torch.equal(grad[k][0, others], gr[k][0, others]) and torch.equal(grad[k][1:], gr[k][1:]), k
+        for k in ("dA", "ddt_bias"):
+            assert torch.equal(grad[k][others], gr[k][others]), k
+        for k in ("dB", "dC"):
+            assert torch.equal(grad[k][1:], gr[k][1:]), k
