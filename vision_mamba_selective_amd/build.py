@@ -1,10 +1,12 @@
-"""Build libvimscan.so (HIP, gfx950) in-tree with hipcc."""
+"""Build libvimscan.so (HIP, gfx950) in-tree with hipcc, and _binding.so, the
+torch side of some of its entry points, with the host compiler."""
 from __future__ import annotations
 
 import os
 import re
 import subprocess
 import sys
+import sysconfig
 import tempfile
 from concurrent.futures import ThreadPoolExecutor
 
@@ -16,6 +18,8 @@ SRCS = [SRC] + [os.path.join(PKG, "csrc", f) for f in
                  "host_causal.cpp")]
 LIB = os.path.join(PKG, "libvimscan.so")
 INCLUDE = os.path.join(ROOT, "include")
+BINDING_SRC = os.path.join(PKG, "csrc", "binding.cpp")
+BINDING = os.path.join(PKG, "_binding.so")
 
 HIPCC_FLAGS = [
     "-O3", "-std=c++17", "-fPIC", "--offload-arch=gfx950",
@@ -78,5 +82,27 @@ def build(out: str = LIB, extra=()) -> str:
     return out
 
 
+def build_binding(out: str = BINDING) -> str:
+    """Compile _binding.so against the installed torch."""
+    import torch
+
+    home = os.path.dirname(torch.__file__)
+    rocm = os.environ.get("ROCM_PATH", "/opt/rocm")
+    tmp = out + ".tmp%d" % os.getpid()
+    cmd = [os.environ.get("CXX", "g++"), "-O2", "-std=c++17", "-fPIC", "-shared", "-Wall", "-Wno-unused-function",
+           "-D__HIP_PLATFORM_AMD__=1", "-DUSE_ROCM", "-D_GLIBCXX_USE_CXX11_ABI=%d" % torch._C._GLIBCXX_USE_CXX11_ABI,
+           "-I", INCLUDE, "-isystem", os.path.join(home, "include"),
+           "-isystem", os.path.join(home, "include", "torch", "csrc", "api", "include"),
+           "-isystem", os.path.join(rocm, "include"), "-isystem", sysconfig.get_paths()["include"],
+           BINDING_SRC, "-L", os.path.join(home, "lib"), "-ltorch_python", "-ltorch_cpu", "-lc10", "-lc10_hip", "-o", tmp]
+    r = subprocess.run(cmd, capture_output=True, text=True)
+    if r.returncode != 0:
+        sys.stderr.write(r.stdout + r.stderr)
+        raise RuntimeError("the host compiler failed on %s" % BINDING_SRC)
+    os.replace(tmp, out)
+    return out
+
+
 if __name__ == "__main__":
     print(build())
+    print(build_binding())
