@@ -2,8 +2,9 @@
 form of it that a language model needs, with beam search over its states.
 
 The scan itself lives in libvimscan.so (HIP kernels behind a C ABI,
-include/vimscan.h). This package holds the in-tree build step, the ctypes
-binding with the same entry-point names, and the seeded workload generator.
+include/vimscan.h). This package holds the in-tree build step, the binding
+with the same entry-point names (ctypes; a compiled one for the causal mixer
+and beam search), and the seeded workload generator.
 The binding is imported lazily so that the generator can be used without the
 library.
 """
