@@ -136,3 +136,29 @@ def test_non_finite_inputs_reach_only_what_they_are_part_of(dtype, value, shape)
             assert torch.equal(grad[k][others], gr[k][others]), k
         for k in ("dB", "dC"):
             assert torch.equal(grad[k][1:], gr[k][1:]), k
+
+
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16], ids=["f32", "bf16"])
+@pytest.mark.parametrize("beams", [1, 4, 8, 16, 20, 32])
+def test_select_around_the_sizes_of_a_part(beams, dtype):
+    """Vocabularies on both sides of one, two, four and eight thousand entries
+    and of what one wave joins: the scores against a float64 log-softmax (the
+    bound of test_gpu_beam.py) and, exactly, the logits of the chosen tokens in
+    order; equal logits by the lowest token."""
+    import vision_mamba_selective_amd as vms
+    g = torch.Generator().manual_seed(beams)
+    for vocab in (2047, 2048, 2049, 4096, 4097, 8192, 8193, 16385, 32769, 65537):
+        say("case select part %d %d %s" % (beams, vocab, dtype))
+        x = (torch.randn(1, beams, vocab, generator=g) * 3).to(dtype)
+        x[0, 0, ::7] = x[0, 0, 0]                             # many equal ones, some masked
+        x[0, 0, 5::11] = float("-inf")
+        x[0, -1, vocab - 1] = 40.0
+        scores = torch.zeros(1, beams)
+        scores[0, 1:] = -1e4                                   # the first beam's alone, then the last one's
+        for first in (0, beams - 1):
+            sc = scores.roll(first, 1)
+            s, p, t = (v.cpu() for v in vms.beam_select(x.cuda(), sc.cuda()))
+            order = torch.sort(x[0, first].double(), descending=True, stable=True).indices[:beams]
+            assert p.tolist() == [[first] * beams] and torch.equal(t[0].long(), order), (vocab, first)
+            want = torch.log_softmax(x[0, first].double(), 0)[order]
+            assert ((s[0].double() - want).abs() <= 32 * 2.0 ** -24 * (21 + want.abs())).all(), (vocab, first)
