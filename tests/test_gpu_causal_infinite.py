@@ -1,0 +1,151 @@
+"""Infinite inputs of the causal scan, its gradient and its single-token form,
+at state sizes on both sides of a full 16, in every form of the kernels: each
+output is infinite or NaN exactly where the definition makes it so, evaluated
+in float64 in IEEE arithmetic, and as close as elsewhere where it is finite.
+
+The inputs keep every exp(delta A) of a single token above 2^-40; B, C, D and h0
+are positive, so that an infinity meets others of its own sign and most results
+are infinities, not NaN. The bound on finite values is the one of
+test_gpu_causal.py (400 x 2^-24 of the size, and 2^-8 for bf16)."""
+import pytest
+import torch
+
+import causal_ref as ref
+from gpu_util import say
+from test_gpu_causal import BF16_TOL, DT, F32_TOL
+
+pytestmark = pytest.mark.gpu
+INF = float("inf")
+# narrow, then wide
+SHAPES = [(2, 37, 60), (512, 100, 33)]
+STATES = [1, 5, 8, 12, 16]
+CH = 5                       # the channel that holds the infinity, in batch row 0
+
+
+def same(got, want, what):
+    g = got.detach().to("cpu", torch.float64)
+    assert g.shape == want.shape, (what, g.shape, want.shape)
+    for kind in (torch.isnan, torch.isposinf, torch.isneginf):
+        bad = kind(g) != kind(want)
+        if bad.any():
+            i = tuple(bad.nonzero()[0].tolist())
+            raise AssertionError("%s: %d of %d not alike in %s; first at %s: got %r ref %r" % (
+                what, int(bad.sum()), bad.numel(), kind.__name__, i, float(g[i]), float(want[i])))
+    fin = torch.isfinite(want)
+    if not fin.any():
+        return
+    g, w = g[fin], want[fin]
+    tol = F32_TOL * (float(w.square().mean().sqrt()) + w.abs())
+    if got.dtype == torch.bfloat16:
+        tol = tol + BF16_TOL * w.abs()
+    assert ((g - w).abs() <= tol).all(), (what, float((g - w).abs().max()))
+
+
+def inputs(shape, N, dtype):
+    batch, dim, L = shape
+    g = torch.Generator().manual_seed(L + N)
+    rnd = lambda *s: torch.randn(*s, generator=g)      # noqa: E731
+    dt = DT[dtype]
+    t = dict(u=rnd(batch, dim, L), delta=rnd(batch, dim, L).clamp(-3, 3) * 0.5 + 1, z=rnd(batch, dim, L), dy=rnd(batch, dim, L),
+             B=torch.rand(batch, N, L, generator=g) + 0.5, C=torch.rand(batch, N, L, generator=g) + 0.5)
+    t = {k: v.to(dt).cuda() for k, v in t.items()}
+    t["A"] = (-(torch.rand(dim, N, generator=g) * 7.5 + 0.5)).cuda()
+    t["D"] = (torch.rand(dim, generator=g) + 0.5).cuda()
+    t["h0"] = (torch.rand(batch, dim, N, generator=g) + 0.5).cuda()
+    t["dh"] = (torch.rand(batch, dim, N, generator=g) + 0.5).cuda()
+    return t
+
+
+def definition(t, chans):
+    """y, h, du, ddelta, dz and dh0 of batch row 0 and some channels, token by token in float64."""
+    d = {k: ref.f64(v) for k, v in t.items()}
+    u, delta, z, dy = (d[k][0, chans] for k in ("u", "delta", "z", "dy"))
+    B, C, A, D = d["B"][0], d["C"][0], d["A"][chans], d["D"][chans]
+    L = u.shape[1]
+    step = torch.logaddexp(delta, torch.zeros_like(delta))
+    gate = torch.sigmoid(z)
+    hs, h, ys = [d["h0"][0, chans]], d["h0"][0, chans], []
+    for i in range(L):
+        h = torch.exp(step[:, i, None] * A) * h + (step[:, i] * u[:, i])[:, None] * B[:, i]
+        hs.append(h)
+        ys.append((h * C[:, i]).sum(1) + D * u[:, i])
+    ungated = torch.stack(ys, 1)
+    y = ungated * (z * gate)
+    dz = dy * ungated * (gate * (1 + z * (1 - gate)))
+    gy = dy * (z * gate)
+    lam, du, dd = d["dh"][0, chans], torch.zeros_like(u), torch.zeros_like(u)
+    for i in reversed(range(L)):
+        lam = lam + gy[:, i, None] * C[:, i]
+        through = (lam * B[:, i]).sum(1)
+        back = torch.exp(step[:, i, None] * A) * lam
+        du[:, i] = step[:, i] * through + gy[:, i] * D
+        dd[:, i] = (u[:, i] * through + (back * hs[i] * A).sum(1)) * torch.sigmoid(delta[:, i])
+        lam = back
+    return dict(y=y, h=h, du=du, ddelta=dd, dz=dz, dh0=lam)
+
+
+def spoil(t, name, at):
+    if name in ("h0", "dh"):
+        t[name][0, CH] = INF
+    else:
+        t[name][0, CH, at] = INF
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("N", STATES)
+@pytest.mark.parametrize("shape", SHAPES, ids=lambda s: "b%d-d%d-L%d" % s)
+@pytest.mark.parametrize("name", ["u", "delta", "h0"])
+def test_scan(name, shape, N, dtype):
+    import vision_mamba_selective_amd as vms
+    t = inputs(shape, N, dtype)
+    spoil(t, name, shape[2] // 3)
+    say("case infinite %s scan %s %d %s" % (name, shape, N, dtype))
+    chans = [0, CH, shape[1] - 1]
+    want = definition(t, chans)
+    args = (t["u"], t["delta"], t["z"], t["B"], t["C"], t["A"], t["D"])
+    y, h = vms.s6_causal_scan(*args, h0=t["h0"])
+    assert torch.isinf(want["y"][1]).any() and torch.isfinite(want["y"][0]).all()
+    same(y[0, chans], want["y"], "y")
+    same(h[0, chans], want["h"], "h")
+    y2, h2, _ = vms.s6_causal_scan_saved(*args, h0=t["h0"])
+    same(y2[0, chans], want["y"], "y of the saving form")
+    same(h2[0, chans], want["h"], "h of the saving form")
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("N", STATES)
+@pytest.mark.parametrize("shape", SHAPES, ids=lambda s: "b%d-d%d-L%d" % s)
+@pytest.mark.parametrize("name", ["dy", "dh"])
+def test_gradient(name, shape, N, dtype):
+    import vision_mamba_selective_amd as vms
+    t = inputs(shape, N, dtype)
+    t["u"] = t["u"].abs()
+    spoil(t, name, shape[2] * 2 // 3)
+    say("case infinite %s gradient %s %d %s" % (name, shape, N, dtype))
+    chans = [0, CH, shape[1] - 1]
+    want = definition(t, chans)
+    args = (t["u"], t["delta"], t["z"], t["B"], t["C"], t["A"], t["D"], None)
+    _, _, saved = vms.s6_causal_scan_saved(*args, h0=t["h0"])
+    g = vms.s6_causal_scan_grad(*args, saved, t["dy"], dh=t["dh"], h0=t["h0"])
+    assert torch.isinf(want["du"][1]).any() and torch.isfinite(want["du"][0]).all()
+    for k in ("du", "ddelta", "dz", "dh0"):
+        same(g[k][0, chans], want[k], k)
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("N", STATES)
+@pytest.mark.parametrize("batch", [2, 3000], ids=["one row a thread", "four rows a thread"])
+@pytest.mark.parametrize("name", ["u", "delta", "h0"])
+def test_step(name, batch, N, dtype):
+    import vision_mamba_selective_amd as vms
+    t = inputs((batch, 37, 1), N, dtype)
+    spoil(t, name, 0)
+    say("case infinite %s step %d %d %s" % (name, batch, N, dtype))
+    chans = [0, CH, 36]
+    want = definition(t, chans)
+    col = lambda k: t[k][:, :, 0]      # noqa: E731
+    h = t["h0"].clone()
+    y = vms.s6_scan_step(*(col(k).contiguous() for k in ("u", "delta", "z", "B", "C")), t["A"], t["D"], None, h)
+    assert torch.isinf(want["y"][1]).all()
+    same(y[0, chans], want["y"][:, 0], "y")
+    same(h[0, chans], want["h"], "h")

@@ -239,6 +239,11 @@ __global__ __launch_bounds__(kThreads) void causal_scan_kernel(const ScanFwdArgs
                 h = fmaf(e, h, row_bcast<i>(du) * Bv[i]);
                 c[i] = h * Cv[i];
             });
+            if (a.dstate < kRowLanes && any_non_finite(du)) {      // uniform
+#pragma unroll
+                for (int i = 0; i < 16; ++i) c[i] = n_ok ? c[i] : 0.f;
+                h = n_ok ? h : 0.f;
+            }
             const float sum = fmaf(Dk, cu, row_transpose_sum(c, lane));
             float v = sum;
             if (GATE) v *= silu_f(from_raw<T>(cz_[half]));
@@ -359,6 +364,8 @@ __global__ __launch_bounds__(kThreads) void causal_scan4_kernel(const ScanFwdArg
                 if (4 * q + r < a.dstate) h[r] = a.h0[row * a.dstate + 4 * q + r];
         }
         fold_pieces<4>(a, b, d, piece, len, 4 * q, A2, h);
+#pragma unroll
+        for (int r = 0; r < 4; ++r) h[r] = 4 * q + r < a.dstate ? h[r] : 0.f;      // an infinite sum times A = 0
     }
     float sdl = 0.f;
     for (int it = 0; it < ntile; ++it) {
@@ -399,7 +406,8 @@ __global__ __launch_bounds__(kThreads) void causal_scan4_kernel(const ScanFwdArg
                 }
             }
             float p[16];
-            Unroll<16>::run([&](auto ic) VS_INLINE {
+            // CLEAN: states past dstate are set back to zero at every token
+            auto tokens = [&](auto clean) VS_INLINE { Unroll<16>::run([&](auto ic) VS_INLINE {
                 constexpr int i = decltype(ic)::value;
                 // the exponentials do not wait for the states: left free, all
                 // 64 of a block are formed at its start and held in
@@ -413,11 +421,18 @@ __global__ __launch_bounds__(kThreads) void causal_scan4_kernel(const ScanFwdArg
                 h[1] = fmaf(__builtin_amdgcn_exp2f(dt * A2[1]), h[1], dx * Bv.y);
                 h[2] = fmaf(__builtin_amdgcn_exp2f(dt * A2[2]), h[2], dx * Bv.z);
                 h[3] = fmaf(__builtin_amdgcn_exp2f(dt * A2[3]), h[3], dx * Bv.w);
+                if (decltype(clean)::value) {
+#pragma unroll
+                    for (int r = 0; r < 4; ++r) h[r] = 4 * q + r < a.dstate ? h[r] : 0.f;
+                }
                 if (!CARRY) {
                     const float4 Cv = *reinterpret_cast<const float4*>(row_bc + kRowLanes + 4 * q);
                     p[i] = fmaf(h[3], Cv.w, fmaf(h[2], Cv.z, fmaf(h[1], Cv.y, h[0] * Cv.x)));
                 }
-            });
+            }); };
+            // the carry launch has no read-out: what its unused states hold goes nowhere
+            if (!CARRY && a.dstate < kRowLanes && any_non_finite(du[0], du[1], du[2], du[3])) tokens(std::true_type{});
+            else tokens(std::false_type{});
             if (!CARRY) {
                 float v[4];
 #pragma unroll
@@ -556,7 +571,8 @@ __global__ __launch_bounds__(kThreads) void scan_step_kernel(const ScanStepArgs 
         float sum = 0.f;
 #pragma unroll
         for (int r = 0; r < 4; ++r) {
-            h[k][r] = fmaf(__builtin_amdgcn_exp2f(dlt * A2[r]), h[k][r], du * Bv[k][r]);
+            const float v = fmaf(__builtin_amdgcn_exp2f(dlt * A2[r]), h[k][r], du * Bv[k][r]);
+            h[k][r] = (VEC ? lane_ok : 4 * q + r < a.dstate) ? v : 0.f;     // an infinite du is NaN times zero
             sum = fmaf(h[k][r], Cv[k][r], sum);
         }
         sum += dpp<0xb1>(sum);                       // quad_perm [1,0,3,2]

@@ -224,13 +224,18 @@ __device__ __forceinline__ float swap16_sum(float a, float b) {
 // launch has a quarter of this one's workgroups per piece, so it cuts the
 // pieces into finer ones.
 //
+// FULL: 16 states. Otherwise what the lanes past dstate give to W and V is set
+// to zero (infinities times their zeros are NaN), in a variant of its own: a
+// branch for the blocks that need it takes 139 registers against 127, three
+// waves a SIMD instead of four.
+//
 // Bound by VALU issue: 390 instructions a wave for 16 tokens, 156 of them with
 // a DPP operand, VALU active 86 %. 8 x 768 x 4,097 bf16,
 // 16 states, in 2 pieces: 350 us here and 53 in the carry launch. The matrix
 // cores could add up dB and dC over the channels, but a product with zeros for
 // the channels past dim or another block's tokens turns an infinity there into
 // NaN, and the lane swaps that it would save are an eighth of the instructions.
-template <typename T, bool GATE, bool SOFTPLUS>
+template <typename T, bool GATE, bool SOFTPLUS, bool FULL>
 __global__ __launch_bounds__(kThreads) void causal_grad_kernel(const ScanGradArgs a) {
     __shared__ __attribute__((aligned(16))) float tile[2][2][kRowLanes][kTilePad];
     __shared__ float4 red[2][kWaves][2][64];
@@ -297,6 +302,7 @@ __global__ __launch_bounds__(kThreads) void causal_grad_kernel(const ScanGradArg
             lamE = fmaf(__builtin_amdgcn_exp2f((on ? sd[k] : 0.f) * A2), lamE, on && n_ok ? loc[k] : 0.f);
         }
     }
+    lamE = n_ok ? lamE : 0.f;                        // an infinite sum times A = 0
     // dA adds up all of a row's tokens in one lane: in fp64, a block's sum at a time
     double dA = 0.;
     float dD = 0.f, db = 0.f;
@@ -378,8 +384,8 @@ __global__ __launch_bounds__(kThreads) void causal_grad_kernel(const ScanGradArg
             lamE = lam * es[i];
             const float q = lamE * (i > 0 ? hs[i > 0 ? i - 1 : 0] : h_in);
             dA_blk = row_bcast_fmac<i, i == 15>(dA_blk, dlt, q);
-            wv[i] = lam * Bv[i];
-            vv[i] = q * An;
+            wv[i] = FULL || n_ok ? lam * Bv[i] : 0.f;
+            vv[i] = FULL || n_ok ? q * An : 0.f;
             pb[i & 7] = row_bcast<i>(du_m) * lam;
             pc[i & 7] = row_bcast<i>(gs_m) * hs[i];
             // eight steps' products stand before their swaps: a swap that
@@ -389,6 +395,7 @@ __global__ __launch_bounds__(kThreads) void causal_grad_kernel(const ScanGradArg
                 for (int k = 0; k < 8; ++k) sbc[i + k] = swap32_sum(pb[k], pc[k]);
             }
         });
+        if (!FULL) lamE = n_ok ? lamE : 0.f;
         dA += static_cast<double>(dA_blk);
         const float Rw = row_transpose_sum(wv, lane);
         const float Rv = row_transpose_sum(vv, lane);
@@ -653,6 +660,17 @@ int launch_conv_grad(const vs::ConvCall& c) {
     return launched();
 }
 
+template <typename T, bool FULL>
+void launch_grad(const ScanGradArgs& a, dim3 grid, const vs::CausalCall& c) {
+    const dim3 blk(kThreads);
+    const hipStream_t st = static_cast<hipStream_t>(c.stream);
+    const bool sp = c.flags & VS_FLAG_SOFTPLUS;
+    if (c.z && sp) hipLaunchKernelGGL((causal_grad_kernel<T, true, true, FULL>), grid, blk, 0, st, a);
+    else if (c.z) hipLaunchKernelGGL((causal_grad_kernel<T, true, false, FULL>), grid, blk, 0, st, a);
+    else if (sp) hipLaunchKernelGGL((causal_grad_kernel<T, false, true, FULL>), grid, blk, 0, st, a);
+    else hipLaunchKernelGGL((causal_grad_kernel<T, false, false, FULL>), grid, blk, 0, st, a);
+}
+
 template <typename T>
 int launch_scan_grad(const vs::CausalCall& c) {
     size_t so[2], wo[4];
@@ -688,10 +706,8 @@ int launch_scan_grad(const vs::CausalCall& c) {
         else hipLaunchKernelGGL((adjoint_carry_kernel<T, false, false>), cgrid, blk, 0, st, a);
         if (int rc = launched()) return rc;
     }
-    if (c.z && sp) hipLaunchKernelGGL((causal_grad_kernel<T, true, true>), grid, blk, 0, st, a);
-    else if (c.z) hipLaunchKernelGGL((causal_grad_kernel<T, true, false>), grid, blk, 0, st, a);
-    else if (sp) hipLaunchKernelGGL((causal_grad_kernel<T, false, true>), grid, blk, 0, st, a);
-    else hipLaunchKernelGGL((causal_grad_kernel<T, false, false>), grid, blk, 0, st, a);
+    if (c.dstate == kRowLanes) launch_grad<T, true>(a, grid, c);
+    else launch_grad<T, false>(a, grid, c);
     if (int rc = launched()) return rc;
     BcReduceArgs r{};
     r.part = a.bc_part; r.stat = a.stat; r.lengths = c.lengths; r.dB = c.dB; r.dC = c.dC; r.dA = c.dA; r.dD = c.dD;

@@ -46,6 +46,16 @@ __device__ __forceinline__ void lds_barrier() {
     __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "workgroup", "local");
 }
 
+// States past dstate have A = B = C = 0 and stay zero, so that they add nothing
+// to a sum over the states, as long as all factors are finite: zero times an
+// infinity is NaN. So where dstate < 16 a block of tokens whose delta u is not
+// finite somewhere in the wave sets those states, and what they give to the
+// sums, to zero. A delta that is not finite makes delta u so.
+template <typename... F>
+__device__ __forceinline__ bool any_non_finite(F... v) {
+    return __ballot((... || !(__builtin_fabsf(v) < INFINITY))) != 0;
+}
+
 // A few rows of a tensor behind a buffer descriptor: 32-bit byte offsets from
 // the first row; reads outside return zero, writes outside are dropped. The
 // rows span under 2^31 bytes (4 rows of at most 2^27 entries).
