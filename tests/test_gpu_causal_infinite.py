@@ -3,7 +3,8 @@ at state sizes on both sides of a full 16, in every form of the kernels: each
 output is infinite or NaN exactly where the definition makes it so, evaluated
 in float64 in IEEE arithmetic, and as close as elsewhere where it is finite.
 
-The inputs keep every exp(delta A) of a single token above 2^-40; B, C, D and h0
+The inputs keep every exp(delta A) of a single token above 2^-40, and the
+products of a whole piece far below the smallest fp32 number; B, C, D and h0
 are positive, so that an infinity meets others of its own sign and most results
 are infinities, not NaN. The bound on finite values is the one of
 test_gpu_causal.py (400 x 2^-24 of the size, and 2^-8 for bf16)."""
@@ -16,8 +17,8 @@ from test_gpu_causal import BF16_TOL, DT, F32_TOL
 
 pytestmark = pytest.mark.gpu
 INF = float("inf")
-# narrow, then wide
-SHAPES = [(2, 37, 60), (512, 100, 33)]
+# whole rows, rows in pieces; each narrow, then wide
+SHAPES = [(2, 37, 60), (512, 100, 33), (2, 37, 301), (12, 192, 3000)]
 STATES = [1, 5, 8, 12, 16]
 CH = 5                       # the channel that holds the infinity, in batch row 0
 

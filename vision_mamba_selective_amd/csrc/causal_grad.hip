@@ -299,7 +299,7 @@ __global__ __launch_bounds__(kThreads) void causal_grad_kernel(const ScanGradArg
 #pragma unroll
         for (int k = 0; k < kFold; ++k) {
             const bool on = p1 - k >= later;
-            lamE = fmaf(__builtin_amdgcn_exp2f((on ? sd[k] : 0.f) * A2), lamE, on && n_ok ? loc[k] : 0.f);
+            lamE = fmaf(piece_factor(on ? sd[k] : 0.f, A2, lamE), lamE, on && n_ok ? loc[k] : 0.f);
         }
     }
     lamE = n_ok ? lamE : 0.f;                        // an infinite sum times A = 0

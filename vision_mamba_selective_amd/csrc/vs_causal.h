@@ -233,6 +233,17 @@ struct BcStage {
     }
 };
 
+// exp(A sd), the factor of a whole piece's tokens, for a state (or adjoint) h
+// that it multiplies. Each token's factor alone leaves a zero and an infinity
+// as they are, but all together may underflow to zero or overflow, and zero
+// times infinity is NaN: such an h passes through unchanged as long as every
+// delta is finite, so that a cut row gives what an uncut one does.
+__device__ __forceinline__ float piece_factor(float sd, float A2, float h) {
+    constexpr int kZeroOrInf = 0x264, kFinite = 0x1f8;      // classes of v_cmp_class
+    const float e = __builtin_amdgcn_exp2f(sd * A2);
+    return __builtin_amdgcn_classf(h, kZeroOrInf) && __builtin_amdgcn_classf(sd, kFinite) ? 1.f : e;
+}
+
 // The state that the pieces before `piece` leave behind, folded into h: eight
 // of the finer pieces' aggregates are in flight at a time; past the last, P = 1
 // and h_loc = 0. N states a lane from n0 on, A2 their A log2(e).
@@ -258,7 +269,7 @@ __device__ __forceinline__ void fold_pieces(const ScanFwdArgs& a, int64_t b, int
 #pragma unroll
             for (int r = 0; r < N; ++r) {
                 const float l = on && n0 + r < a.dstate ? loc[k][r] : 0.f;
-                h[r] = fmaf(__builtin_amdgcn_exp2f((on ? sd[k] : 0.f) * A2[r]), h[r], l);
+                h[r] = fmaf(piece_factor(on ? sd[k] : 0.f, A2[r], h[r]), h[r], l);
             }
         }
     }
