@@ -150,3 +150,45 @@ def test_step(name, batch, N, dtype):
     assert torch.isinf(want["y"][1]).all()
     same(y[0, chans], want["y"][:, 0], "y")
     same(h[0, chans], want["h"], "h")
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("N", [5, 16])
+@pytest.mark.parametrize("dim", [37, 16], ids=["channels to spare", "whole groups"])
+@pytest.mark.parametrize("lengths", [None, [50, 33]], ids=["full", "ragged"])
+@pytest.mark.parametrize("name", ["u", "dy", "dh", "h0"])
+def test_gradient_sums(name, lengths, dim, N, dtype):
+    """dB and dC with an infinity in the last channel: of its tokens' sums
+    over the channels only those that hold it are infinite, and padding stays
+    zero, whatever the group of 16 channels and the block of 16 tokens that
+    hold the last ones are filled up with."""
+    import vision_mamba_selective_amd as vms
+    L, ch = 61, dim - 1
+    t = inputs((2, dim, L), N, dtype)
+    t["u"], t["dy"], t["z"] = t["u"].abs() + 0.1, t["dy"].abs() + 0.1, t["z"].abs() + 0.1
+    if name in ("h0", "dh"):
+        t[name][0, ch] = INF
+    else:
+        t[name][0, ch, 20] = INF
+    say("case infinite sums %s %s %d %d %s" % (name, lengths, dim, N, dtype))
+    len_t = None if lengths is None else torch.tensor(lengths, dtype=torch.int32).cuda()
+    args = (t["u"], t["delta"], t["z"], t["B"], t["C"], t["A"], t["D"], None)
+    _, _, saved = vms.s6_causal_scan_saved(*args, h0=t["h0"], lengths=len_t)
+    g = vms.s6_causal_scan_grad(*args, saved, t["dy"], dh=t["dh"], h0=t["h0"], lengths=len_t)
+    d = {k: ref.f64(v) for k, v in t.items()}
+    dB, dC = torch.zeros(2, N, L, dtype=ref.F64), torch.zeros(2, N, L, dtype=ref.F64)
+    step = torch.logaddexp(d["delta"], torch.zeros_like(d["delta"]))
+    gy = d["dy"] * d["z"] * torch.sigmoid(d["z"])
+    for b, n in enumerate(ref.row_lengths(lengths, 2, L)):
+        hs = [d["h0"][b]]
+        for i in range(n):
+            hs.append(torch.exp(step[b, :, i, None] * d["A"]) * hs[-1] + (step[b, :, i] * d["u"][b, :, i])[:, None] * d["B"][b, :, i])
+        lam = d["dh"][b]
+        for i in reversed(range(n)):
+            dC[b, :, i] = (gy[b, :, i, None] * hs[i + 1]).sum(0)
+            lam = lam + gy[b, :, i, None] * d["C"][b, :, i]
+            dB[b, :, i] = (lam * (step[b, :, i] * d["u"][b, :, i])[:, None]).sum(0)
+            lam = torch.exp(step[b, :, i, None] * d["A"]) * lam
+    assert torch.isinf(torch.cat([dB.flatten(), dC.flatten()])).any()
+    same(g["dB"], dB, "dB")
+    same(g["dC"], dC, "dC")

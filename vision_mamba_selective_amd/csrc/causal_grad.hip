@@ -275,14 +275,18 @@ __global__ __launch_bounds__(kThreads) void causal_grad_kernel(const ScanGradArg
     float* chunk = a.bc_part + (static_cast<size_t>(b) * gridDim.x + cg) * static_cast<size_t>(a.nblk) * 512;
     // this piece's tokens [s0, s1), of which [s0, e) are real
     const int s0 = piece * a.piece_len, s1 = min(s0 + a.piece_len, L), e = min(s1, len);
-    const int t_lim = active ? s1 : 0;               // tokens whose outputs this lane may write
+    const int t_real = active ? len : 0;             // tokens that this lane takes part in
 
     BcStage<T> stage(a, b, tid, len);
     const int blk0 = s0 / 16;
     const int nblk = e > s0 ? (e + 15) / 16 : blk0;  // blocks [blk0, nblk)
     const int tile0 = s0 / kTileTok;
     const int ntile = e > s0 ? (e + kTileTok - 1) / kTileTok : tile0;
-    float lamE = a.dh_out && n_ok ? a.dh_out[row * a.dstate + n] : 0.f;
+    // Lanes of channels past dim count for nothing in the sums over channels:
+    // they hold zeros from here on (their memory is channel dim - 1's, and a
+    // zero factor in front of an infinity of that would be NaN)
+    const bool holds = active && n_ok;
+    float lamE = a.dh_out && holds ? a.dh_out[row * a.dstate + n] : 0.f;
     // the adjoint that enters at the piece's end: those of the later pieces
     // that hold tokens, the last of them first, eight in flight at a time
     const int later = (piece + 1) * a.sub;           // the first finer piece after this one
@@ -299,10 +303,10 @@ __global__ __launch_bounds__(kThreads) void causal_grad_kernel(const ScanGradArg
 #pragma unroll
         for (int k = 0; k < kFold; ++k) {
             const bool on = p1 - k >= later;
-            lamE = fmaf(piece_factor(on ? sd[k] : 0.f, A2, lamE), lamE, on && n_ok ? loc[k] : 0.f);
+            lamE = fmaf(piece_factor(on ? sd[k] : 0.f, A2, lamE), lamE, on && holds ? loc[k] : 0.f);
         }
     }
-    lamE = n_ok ? lamE : 0.f;                        // an infinite sum times A = 0
+    lamE = holds ? lamE : 0.f;                       // an infinite sum times A or lamE = 0
     // dA adds up all of a row's tokens in one lane: in fp64, a block's sum at a time
     double dA = 0.;
     float dD = 0.f, db = 0.f;
@@ -311,7 +315,7 @@ __global__ __launch_bounds__(kThreads) void causal_grad_kernel(const ScanGradArg
     // comes in as a scalar
     constexpr int kEs = sizeof(T);
     const uint32_t ou = u.at(wr, n), od = dl.at(wr, n), og = dy.at(wr, n), oz = z.at(wr, n), os = s.at(wr, n);
-    const uint32_t oh = n_ok ? ck.at(wr, n) : kDropped, oo = du.at(wr, n);
+    const uint32_t oh = holds ? ck.at(wr, n) : kDropped, oo = active ? du.at(wr, n) : kDropped;
     auto tok_load = [&](int blk, Tok& k) VS_INLINE {
         const int t0 = blk * 16 * kEs;
         k.u = u.load(ou, t0);
@@ -338,8 +342,8 @@ __global__ __launch_bounds__(kThreads) void causal_grad_kernel(const ScanGradArg
         const Tok cur = nxt;
         tok_load(blk > blk0 ? blk - 1 : blk0, nxt);
         const int t = blk * 16 + n;
-        const bool ok = t < len;
-        const uint32_t out = t < t_lim ? oo : kDropped;
+        const bool ok = t < t_real;
+        const uint32_t out = t < s1 ? oo : kDropped;
         const int out0 = blk * 16 * kEs;
         const float x = from_raw<T>(cur.d) + bias;
         const float dlt = ok ? (SOFTPLUS ? softplus_f(x) : x) : 0.f;
@@ -371,11 +375,9 @@ __global__ __launch_bounds__(kThreads) void causal_grad_kernel(const ScanGradArg
             h = fmaf(es[i], h, row_bcast<i>(du_) * Bv[i]);
             hs[i] = h;
         });
-        // lanes of channels past dim hold another channel's values: they
-        // count for nothing in the sums over channels. Second copies of the
-        // broadcast sources, opaque to the compiler, give every broadcast one
-        // use, which folds it into that use as a DPP operand
-        float du_m = active ? du_ : 0.f, gs_m = active ? gs : 0.f;
+        // second copies of the broadcast sources, opaque to the compiler, give
+        // every broadcast one use, which folds it into that use as a DPP operand
+        float du_m = du_, gs_m = gs;
         asm volatile("" : "+v"(du_m), "+v"(gs_m));
         float dA_blk = 0.f, pb[8], pc[8];
         Unroll<16>::run([&](auto ic) VS_INLINE {
@@ -441,7 +443,7 @@ __global__ __launch_bounds__(kThreads) void causal_grad_kernel(const ScanGradArg
         stat[a.dstate + 1] = db;
     }
     // the gradients of the padding
-    for (int t = nblk * 16 + n; t < t_lim; t += 16) {
+    for (int t = nblk * 16 + n; active && t < s1; t += 16) {
         du.store(du.at(wr, t), 0.f);
         dd.store(dd.at(wr, t), 0.f);
         if (GATE) dz.store(dz.at(wr, t), 0.f);
@@ -609,7 +611,9 @@ __global__ __launch_bounds__(kThreads) void bc_reduce_kernel(const BcReduceArgs 
         }
     }
     float* out = (lane >> 5 ? a.dC : a.dB) + (b * a.dstate + n) * static_cast<int64_t>(a.L) + t;
-    // tokens of the block past the length hold zero sums
+    // tokens of the block past the length: zero times an adjoint or a state
+#pragma unroll
+    for (int k = 0; k < 4; ++k) v[k] = t + k < len ? v[k] : 0.f;
     if (t + 4 <= a.L) {
         store_four(out, v);
     } else {
