@@ -158,7 +158,7 @@ def test_step(name, batch, N, dtype):
 @pytest.mark.parametrize("lengths", [None, [50, 33]], ids=["full", "ragged"])
 @pytest.mark.parametrize("name", ["u", "dy", "dh", "h0"])
 def test_gradient_sums(name, lengths, dim, N, dtype):
-    """dB and dC with an infinity in the last channel: of its tokens' sums
+    """dB, dC and dA with an infinity in the last channel: of its tokens' sums
     over the channels only those that hold it are infinite, and padding stays
     zero, whatever the group of 16 channels and the block of 16 tokens that
     hold the last ones are filled up with."""
@@ -176,7 +176,7 @@ def test_gradient_sums(name, lengths, dim, N, dtype):
     _, _, saved = vms.s6_causal_scan_saved(*args, h0=t["h0"], lengths=len_t)
     g = vms.s6_causal_scan_grad(*args, saved, t["dy"], dh=t["dh"], h0=t["h0"], lengths=len_t)
     d = {k: ref.f64(v) for k, v in t.items()}
-    dB, dC = torch.zeros(2, N, L, dtype=ref.F64), torch.zeros(2, N, L, dtype=ref.F64)
+    dB, dC, dA = torch.zeros(2, N, L, dtype=ref.F64), torch.zeros(2, N, L, dtype=ref.F64), torch.zeros(dim, N, dtype=ref.F64)
     step = torch.logaddexp(d["delta"], torch.zeros_like(d["delta"]))
     gy = d["dy"] * d["z"] * torch.sigmoid(d["z"])
     for b, n in enumerate(ref.row_lengths(lengths, 2, L)):
@@ -189,6 +189,8 @@ def test_gradient_sums(name, lengths, dim, N, dtype):
             lam = lam + gy[b, :, i, None] * d["C"][b, :, i]
             dB[b, :, i] = (lam * (step[b, :, i] * d["u"][b, :, i])[:, None]).sum(0)
             lam = torch.exp(step[b, :, i, None] * d["A"]) * lam
-    assert torch.isinf(torch.cat([dB.flatten(), dC.flatten()])).any()
+            dA += lam * hs[i] * step[b, :, i, None]
+    assert torch.isinf(torch.cat([dB.flatten(), dC.flatten()])).any() and torch.isinf(dA[ch]).all()
     same(g["dB"], dB, "dB")
     same(g["dC"], dC, "dC")
+    same(g["dA"], dA, "dA")

@@ -327,6 +327,7 @@ __global__ __launch_bounds__(kThreads) void causal_grad_kernel(const ScanGradArg
         }
         k.h = ck.load(oh, blk * a.dstate * 4);
     };
+    uint64_t again = 0;
     Tok nxt{};
     if (ntile > tile0) {
         stage.load(ntile - 1);
@@ -398,7 +399,6 @@ __global__ __launch_bounds__(kThreads) void causal_grad_kernel(const ScanGradArg
             }
         });
         if (!FULL) lamE = n_ok ? lamE : 0.f;
-        dA += static_cast<double>(dA_blk);
         const float Rw = row_transpose_sum(wv, lane);
         const float Rv = row_transpose_sum(vv, lane);
         const float ddl = fmaf(cu, Rw, Rv);
@@ -413,6 +413,14 @@ __global__ __launch_bounds__(kThreads) void causal_grad_kernel(const ScanGradArg
         for (int k = 0; k < 2; ++k)
             red[blk & 1][wave][k][lane] = make_float4(swap16_sum(sbc[4 * k], sbc[4 * k + 8]), swap16_sum(sbc[4 * k + 1], sbc[4 * k + 9]),
                                                       swap16_sum(sbc[4 * k + 2], sbc[4 * k + 10]), swap16_sum(sbc[4 * k + 3], sbc[4 * k + 11]));
+        // the padding of a row's last block has delta = 0, but zero times an
+        // infinite adjoint or state is NaN: those lanes' sum of that block is
+        // formed again after the loop, where registers are free
+        if (blk * 16 + 16 > len) {                           // uniform
+            again = __ballot(!(__builtin_fabsf(dA_blk) < INFINITY));
+            dA_blk = __builtin_fabsf(dA_blk) < INFINITY ? dA_blk : 0.f;
+        }
+        dA += static_cast<double>(dA_blk);
         if (stages) stage.store(tile[(it - 1) & 1]);
         lds_barrier();
         // a thread adds two of the waves' sums: the chunk is [i / 4][lane][i % 4]
@@ -426,6 +434,29 @@ __global__ __launch_bounds__(kThreads) void causal_grad_kernel(const ScanGradArg
             }
             *reinterpret_cast<float2*>(chunk + static_cast<size_t>(blk) * 512 + (k * 64 + lane) * 4 + part * 2) = v;
         }
+    }
+    if (again != 0) {                                // uniform
+        const int t0 = (nblk - 1) * 16;
+        const float x = from_raw<T>(dl.load(od, t0 * kEs)) + bias, zz = GATE ? from_raw<T>(z.load(oz, t0 * kEs)) : 0.f;
+        const bool ok = t0 + n < t_real;
+        const float dlt = ok ? (SOFTPLUS ? softplus_f(x) : x) : 0.f;
+        const float du_ = ok ? dlt * from_raw<T>(u.load(ou, t0 * kEs)) : 0.f;
+        float gs = from_raw<T>(dy.load(og, t0 * kEs));
+        if (GATE) gs *= zz * sigmoid_f(zz);
+        const int64_t nc = n_ok ? n : 0;
+        const T* Bn = static_cast<const T*>(a.B) + b * a.sB.b + nc * a.sB.d + t0;
+        const T* Cn = static_cast<const T*>(a.C) + b * a.sC.b + nc * a.sC.d + t0;
+        float lam = a.dh_out && holds ? a.dh_out[row * a.dstate + n] : 0.f, sum = 0.f;
+        for (int i = len - 1 - t0; i >= 0; --i) {
+            // the state before token i, from the block's first one
+            float h = __uint_as_float(ck.load(oh, (nblk - 1) * a.dstate * 4));
+            for (int j = 0; j < i; ++j)
+                h = fmaf(__builtin_amdgcn_exp2f(__shfl(dlt, j, 16) * A2), h, __shfl(du_, j, 16) * ld(Bn, j));
+            const float dt = __shfl(dlt, i, 16);
+            lam = fmaf(__shfl(gs, i, 16), ld(Cn, i), lam) * __builtin_amdgcn_exp2f(dt * A2);
+            sum = fmaf(dt, lam * h, sum);
+        }
+        dA += (again >> lane) & 1 ? static_cast<double>(sum) : 0.;
     }
     float* stat = a.stat + (static_cast<size_t>(b * a.pieces + piece) * a.dim + d) * (a.dstate + 2);
     if (active && n_ok) {
