@@ -194,3 +194,37 @@ def test_gradient_sums(name, lengths, dim, N, dtype):
     same(g["dB"], dB, "dB")
     same(g["dC"], dC, "dC")
     same(g["dA"], dA, "dA")
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("W", [2, 4, 8])
+@pytest.mark.parametrize("L,lengths", [(60, None), (60, [29, 13]), (300, [299, 290]), (1100, [1100, 1001])],
+                         ids=["full", "ragged", "long", "segments"])
+@pytest.mark.parametrize("back", [1, 2, 9])
+def test_convolution_sums(back, L, lengths, W, dtype):
+    """dw of the linear convolution with an infinity `back` tokens before a
+    row's end: only the taps that meet it at a token of the row are infinite."""
+    import vision_mamba_selective_amd as vms
+    g = torch.Generator().manual_seed(L + W)
+    dim, ch = 11, 3
+    x, dy = (torch.randn(2, dim, L, generator=g).to(DT[dtype]).cuda() for _ in range(2))
+    w = (torch.rand(dim, W, generator=g) + 0.5).cuda()
+    n = L if lengths is None else lengths[0]
+    x[0, ch, n - back] = INF
+    say("case infinite convolution sums %d %s %d %s" % (back, lengths, W, dtype))
+    len_t = None if lengths is None else torch.tensor(lengths, dtype=torch.int32).cuda()
+    got = vms.s6_causal_conv_grad(x, w, None, dy, lengths=len_t, silu=False)
+    y, _ = vms.s6_causal_conv(x, w, lengths=len_t, silu=False)
+    d, dyd, wd = ref.f64(x), ref.f64(dy), ref.f64(w)
+    dw, dx, yd = torch.zeros(dim, W, dtype=ref.F64), torch.zeros_like(d), torch.zeros_like(d)
+    for b, m in enumerate(ref.row_lengths(lengths, 2, L)):
+        line = torch.cat([torch.zeros(dim, W - 1, dtype=ref.F64), d[b, :, :m]], dim=1)
+        for j in range(W):
+            dw[:, j] += (dyd[b, :, :m] * line[:, j:j + m]).sum(1)
+            yd[b, :, :m] += wd[:, j, None] * line[:, j:j + m]
+            k = W - 1 - j
+            dx[b, :, :m - k] += wd[:, j, None] * dyd[b, :, k:m]
+    assert int(torch.isinf(dw).sum()) == min(back, W)
+    same(got["dw"], dw, "dw")
+    same(got["dx"], dx, "dx")
+    same(y, yd, "y")

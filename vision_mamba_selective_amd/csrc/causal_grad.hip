@@ -101,13 +101,19 @@ __global__ __launch_bounds__(kThreads) void causal_conv_grad_kernel(const ConvGr
 #pragma unroll
                 for (int i = 0; i < 8; ++i) dpre[i] = t0 + i < len ? dpre[i] : 0.f;
             }
-            if (lane < last) {
+            // padding stays out of dw (its dpre is zero, but the entries
+            // before it may be infinite)
+            auto sums = [&](int n) VS_INLINE {
 #pragma unroll
                 for (int i = 0; i < 8; ++i) {
                     db += dpre[i];
 #pragma unroll
-                    for (int j = 0; j < W; ++j) dw[j] = fmaf(dpre[i], f[i + j], dw[j]);
+                    for (int j = 0; j < W; ++j) dw[j] = i < n ? fmaf(dpre[i], f[i + j], dw[j]) : dw[j];
                 }
+            };
+            if (lane < last) {
+                if (t0 + 8 <= len) sums(8);
+                else sums(len - t0);
             }
         }
 #pragma unroll
