@@ -76,11 +76,30 @@ void axes(const char* name, const at::Tensor& t, int64_t n) {
     if (t.dim() != n) raise(PyExc_ValueError, "%s must have %d axes, got shape %s", name, static_cast<int>(n), shape(t.sizes()).c_str());
 }
 
+// The caller's tensors that a call writes in place: the pools, and whatever was
+// given for an output, a buffer or a state to reorder. After the call each gets
+// a new version, so that a backward pass that saved its former values is
+// refused. Inference tensors have no version, and nothing can save them.
+class Written {
+    const at::Tensor* t[4];
+    int n = 0;
+
+public:
+    void add(Maybe v) {
+        if (v) t[n++] = v;
+    }
+    void changed() const {
+        for (int i = 0; i < n; ++i)
+            if (!t[i]->is_inference()) t[i]->unsafeGetTensorImpl()->bump_version();
+    }
+};
+
 // dtype and device of a call, from its first argument
 struct Call {
     at::ScalarType dt;
     at::Device dev;
     int dtype;                       // the ABI's
+    mutable Written written;
 
     Call(const char* name, const at::Tensor& t, int64_t ndim) : dt(t.scalar_type()), dev(t.device()) {
         if (dt != at::kFloat && dt != at::kBFloat16) raise(PyExc_TypeError, "unsupported dtype %S", dtype_name(dt));
@@ -124,6 +143,7 @@ struct Call {
         Maybe t = maybe(name, given);
         if (!t) return fresh(dims, type);
         dense(name, t, dims, type);
+        written.add(t);
         return *t;
     }
 };
@@ -144,16 +164,17 @@ struct Strides {
     }
 };
 
-// a workspace or saved buffer of at least `need` bytes: the given one or a new one
+// a workspace or saved buffer of at least `need` bytes: the given one (which the call writes, or only reads) or a new one
 struct Buffer {
     at::Tensor t;
     void* p = nullptr;
     size_t bytes;
-    Buffer(const char* name, size_t need, const Call& c, PyObject* given) : bytes(need) {
+    Buffer(const char* name, size_t need, const Call& c, PyObject* given, bool writes = true) : bytes(need) {
         if (Maybe g = maybe(name, given)) {
             bytes = static_cast<size_t>(g->numel()) * g->element_size();
             if (bytes < need || !g->is_contiguous() || g->device() != c.dev)
                 raise(PyExc_ValueError, "%s needs %zu contiguous bytes on %s", name, need, c.dev.str().c_str());
+            if (writes) c.written.add(g);
             t = *g;
         } else if (need > 0) {
             t = c.fresh({static_cast<int64_t>(need)}, at::kByte);
@@ -164,12 +185,12 @@ struct Buffer {
 
 // the call itself, without the interpreter's lock; a status becomes an exception
 template <typename F>
-void run(const char* name, F&& f) {
+void run(const char* name, const Written& written, F&& f) {
     int code;
     Py_BEGIN_ALLOW_THREADS
     code = f();
     Py_END_ALLOW_THREADS
-    if (code == 0) return;
+    if (code == 0) return written.changed();
     PyObject* r = PyObject_CallFunction(check_status, "si", name, code);
     Py_XDECREF(r);
     if (!PyErr_Occurred()) PyErr_Format(PyExc_RuntimeError, "%s failed (%d)", name, code);
@@ -219,7 +240,7 @@ PyObject* conv(PyObject* const* a) {
     const at::Tensor wo = c.out("window_out", a[7], {batch, dim, width - 1}, c.dt);
     const Strides st({&x});
     const int flags = truth(a[5]) ? VS_CONV_SILU : 0;
-    run("s6_causal_conv", [&] {
+    run("s6_causal_conv", c.written, [&] {
         return abi.s6_causal_conv(batch, dim, width, L, c.dtype, flags, xp, st.p, wp, bp, win, len, y.data_ptr(), wo.data_ptr(), c.stream());
     });
     return tuple({y, wo});
@@ -245,7 +266,7 @@ PyObject* conv_grad(PyObject* const* a) {
     if (win) dwin = c.fresh({batch, dim, width - 1}, c.dt);
     const Strides st({&x, &dy});
     const int flags = truth(a[7]) ? VS_CONV_SILU : 0;
-    run("s6_causal_conv_grad", [&] {
+    run("s6_causal_conv_grad", c.written, [&] {
         return abi.s6_causal_conv_grad(batch, dim, width, L, c.dtype, flags, xp, dyp, st.p, wp, bp, win, len, dwo, dx.data_ptr(),
                                        f32(dw), f32(db), at_or_null(dwin), ws.p, ws.bytes, c.stream());
     });
@@ -266,12 +287,13 @@ PyObject* conv_step(PyObject* const* a) {
     const float* wp = c.dense<float>("w", &w, {dim, width});
     const float* bp = c.dense<float>("bias", maybe("bias", a[2]), {dim});
     void* pool = c.dense("window", &window, {slots, dim, width - 1}, c.dt);
+    c.written.add(&window);
     const int32_t* si = c.dense<int32_t>("slot_in", maybe("slot_in", a[4]), {batch});
     const int32_t* so = c.dense<int32_t>("slot_out", maybe("slot_out", a[5]), {batch});
     const at::Tensor y = c.out("out", a[7], {batch, dim}, c.dt);
     const int64_t stride = batch > 1 ? x.stride(0) : 0;
     const int flags = truth(a[6]) ? VS_CONV_SILU : 0;
-    run("s6_conv_step", [&] {
+    run("s6_conv_step", c.written, [&] {
         return abi.s6_conv_step(batch, dim, width, c.dtype, flags, x.data_ptr(), stride, wp, bp, pool, slots, si, so, y.data_ptr(), c.stream());
     });
     return wrap(y);
@@ -317,14 +339,14 @@ PyObject* scan_call(PyObject* const* a, bool saves) {
     const int flags = truth(a[10]) ? VS_FLAG_SOFTPLUS : 0;
     if (!saves) {
         const Buffer ws("workspace", s.bytes(VS_S6_SCAN), c, a[13]);
-        run("s6_causal_scan", [&] {
+        run("s6_causal_scan", c.written, [&] {
             return abi.s6_causal_scan(s.batch, s.dim, s.N, s.L, c.dtype, flags, s.u, s.delta, s.z, s.B, s.C, st.p, s.A, s.Dskip, s.dt_bias,
                                       h0, s.lengths, y.data_ptr(), f32(h), ws.p, ws.bytes, c.stream());
         });
         return tuple({y, h});
     }
     const Buffer saved("saved", s.bytes(VS_S6_SAVED), c, a[14]), ws("workspace", s.bytes(VS_S6_SCAN), c, a[13]);
-    run("s6_causal_scan_saved", [&] {
+    run("s6_causal_scan_saved", c.written, [&] {
         return abi.s6_causal_scan_saved(s.batch, s.dim, s.N, s.L, c.dtype, flags, s.u, s.delta, s.z, s.B, s.C, st.p, s.A, s.Dskip,
                                         s.dt_bias, h0, s.lengths, y.data_ptr(), f32(h), saved.p, saved.bytes, ws.p, ws.bytes, c.stream());
     });
@@ -342,7 +364,7 @@ PyObject* scan_grad(PyObject* const* a) {
     const float* dh = c.dense<float>("dh", maybe("dh", a[10]), {s.batch, s.dim, s.N});
     const float* h0 = c.dense<float>("h0", maybe("h0", a[11]), {s.batch, s.dim, s.N});
     need("saved", a[8]);
-    const Buffer saved("saved", s.bytes(VS_S6_SAVED), c, a[8]), ws("workspace", s.bytes(VS_S6_GRAD), c, a[14]);
+    const Buffer saved("saved", s.bytes(VS_S6_SAVED), c, a[8], false), ws("workspace", s.bytes(VS_S6_GRAD), c, a[14]);
     const auto act = [&] { return c.fresh({s.batch, s.dim, s.L}, c.dt); };
     const auto fp = [&](Dims d) { return c.fresh(d, at::kFloat); };
     const at::Tensor du = act(), dd = act();
@@ -352,7 +374,7 @@ PyObject* scan_grad(PyObject* const* a) {
     const at::Tensor dB = fp({s.batch, s.N, s.L}), dC = fp({s.batch, s.N, s.L}), dA = fp({s.dim, s.N}), dD = fp({s.dim}), db = fp({s.dim});
     const Strides st({&s.tu, &s.td, s.tz, &s.tB, &s.tC, &tdy});
     const int flags = truth(a[13]) ? VS_FLAG_SOFTPLUS : 0;
-    run("s6_causal_scan_grad", [&] {
+    run("s6_causal_scan_grad", c.written, [&] {
         return abi.s6_causal_scan_grad(s.batch, s.dim, s.N, s.L, c.dtype, flags, s.u, s.delta, s.z, s.B, s.C, dy, st.p, s.A, s.Dskip,
                                        s.dt_bias, s.lengths, saved.p, saved.bytes, dh, du.data_ptr(), dd.data_ptr(), at_or_null(dz),
                                        f32(dB), f32(dC), f32(dA), f32(dD), f32(db), f32(dh0), ws.p, ws.bytes, c.stream());
@@ -375,6 +397,7 @@ PyObject* scan_step(PyObject* const* a) {
     const float* Dp = c.dense<float>("Dskip", maybe("Dskip", a[6]), {dim});
     const float* bias = c.dense<float>("dt_bias", maybe("dt_bias", a[7]), {dim});
     float* hp = c.dense<float>("h", &h, {slots, dim, N});
+    c.written.add(&h);
     const int32_t* si = c.dense<int32_t>("slot_in", maybe("slot_in", a[9]), {batch});
     const int32_t* so = c.dense<int32_t>("slot_out", maybe("slot_out", a[10]), {batch});
     const at::Tensor y = c.out("out", a[12], {batch, dim}, c.dt);
@@ -386,7 +409,7 @@ PyObject* scan_step(PyObject* const* a) {
         st[k++] = t ? t->stride(0) : 0;
     }
     const int flags = truth(a[11]) ? VS_FLAG_SOFTPLUS : 0;
-    run("s6_scan_step", [&] {
+    run("s6_scan_step", c.written, [&] {
         return abi.s6_scan_step(batch, dim, N, c.dtype, flags, up, dp, zp, Bp, Cp, stp, Ap, Dp, bias, hp, slots, si, so, y.data_ptr(), c.stream());
     });
     return wrap(y);
@@ -414,7 +437,7 @@ PyObject* select(PyObject* const* a) {
     const at::Tensor t = c.out("out[2]", a[7], {batch, beams}, at::kInt);
     const Strides st({&logits});
     const Buffer ws("workspace", abi.beam_workspace_bytes(batch, beams, vocab), c, a[4]);
-    run("beam_select", [&] {
+    run("beam_select", c.written, [&] {
         return abi.beam_select(batch, beams, vocab, c.dtype, lp, st.p, sp, static_cast<const uint8_t*>(done), eos, f32(s),
                                static_cast<int32_t*>(p.data_ptr()), static_cast<int32_t*>(t.data_ptr()), ws.p, ws.bytes, c.stream());
     });
@@ -444,9 +467,11 @@ PyObject* reorder(PyObject* const* a) {
     if (out.scalar_type() != state.scalar_type() || out.sizes() != state.sizes() || out.strides() != state.strides() ||
         out.device() != state.device())
         raise(PyExc_ValueError, "out must have state's dtype, shape, strides and device");
+    Written written;
+    written.add(&out);
     const int64_t es = static_cast<int64_t>(state.element_size());
     const int64_t row_bytes = layer / rows * es, layer_bytes = layers > 1 ? state.stride(0) * es : 0;
-    run("beam_reorder", [&] {
+    run("beam_reorder", written, [&] {
         return abi.beam_reorder(layers, parent.size(0), parent.size(1), row_bytes, layer_bytes, state.data_ptr(),
                                 static_cast<const int32_t*>(parent.data_ptr()), out.data_ptr(),
                                 c10::hip::getCurrentHIPStream(state.device().index()).stream());
