@@ -115,3 +115,26 @@ def test_inference_tensors_are_written():
     vms.s6_conv_step(row, w, None, plain)
     vms.s6_scan_step(row, row, None, rnd(B, N), rnd(B, N), A, None, None, h)
     assert torch.equal(pool, plain) and plain._version >= 2
+
+
+@pytest.mark.parametrize("name", ["window", "h", "state", "out"])
+def test_written_tensors_that_require_a_gradient_are_refused(name):
+    """The write is not part of the graph: a gradient through it would be wrong. Without gradients it goes through."""
+    import vision_mamba_selective_amd as vms
+    say("case written tensors with gradients %s" % name)
+    w, row, A = rnd(DIM, W), rnd(B, DIM), -rnd(DIM, N).abs()
+    t = {"window": rnd(B, DIM, W - 1), "h": rnd(B, DIM, N), "state": rnd(2, B * K, 5), "out": rnd(B, DIM, L)}[name].requires_grad_()
+    parent, x = i32([[0, 0, 1], [3, 5, 5]]), rnd(B, DIM, L)
+    bt, ct = rnd(B, N), rnd(B, N)
+    call = {"window": lambda v: vms.s6_conv_step(row, w, None, v),
+            "h": lambda v: vms.s6_scan_step(row, row, None, bt, ct, A, None, None, v),
+            "state": lambda v: vms.beam_reorder(v, parent),
+            "out": lambda v: vms.s6_causal_conv(x, w, out=v)}[name]
+    for v in (t, t * 1):                                       # a leaf, and a tensor of the graph
+        was = v.detach().clone()
+        with pytest.raises(ValueError, match="%s .*requires a gradient" % name):
+            call(v)
+        assert torch.equal(v, was)
+        with torch.no_grad():
+            call(v)
+        call(v.detach())

@@ -1,5 +1,6 @@
 """Torch-facing binding of beam search (include/vimscan.h, "Beam search over
-the states above")."""
+the states above"). Nothing here is differentiable; what a call writes in place
+(the state, given outputs and buffers) is treated as in causal.py."""
 from __future__ import annotations
 
 from . import _calls

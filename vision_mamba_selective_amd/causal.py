@@ -7,6 +7,12 @@ channel strides are free, so the halves of a projection's output or a span of
 a longer tensor go in as they are. Outputs are contiguous. lengths is an int32
 tensor [batch] on the device, or None when every row has L tokens: what stands
 at and past a row's length is never used, outputs there are zero.
+
+Only s6_causal_conv_autograd and s6_causal_scan_autograd are differentiable:
+what every other function returns is outside any graph, also where an input
+requires a gradient. A tensor that a call writes in place (a pool, a given
+output or buffer) gets a new version, as after torch's in-place operations, and
+is refused if it requires a gradient while gradients are recorded.
 """
 from __future__ import annotations
 

@@ -12,6 +12,7 @@
 #include <Python.h>
 
 #include <ATen/core/Tensor.h>
+#include <ATen/core/grad_mode.h>
 #include <ATen/ops/empty.h>
 #include <c10/hip/HIPStream.h>
 #include <torch/csrc/DynamicTypes.h>
@@ -77,16 +78,21 @@ void axes(const char* name, const at::Tensor& t, int64_t n) {
 }
 
 // The caller's tensors that a call writes in place: the pools, and whatever was
-// given for an output, a buffer or a state to reorder. After the call each gets
-// a new version, so that a backward pass that saved its former values is
-// refused. Inference tensors have no version, and nothing can save them.
+// given for an output, a buffer or a state to reorder. The write is no part of
+// a graph, so none of them may require a gradient while gradients are recorded;
+// and after the call each gets a new version, so that a backward pass that
+// saved its former values is refused. Inference tensors have no version, and
+// nothing can save them.
 class Written {
     const at::Tensor* t[4];
     int n = 0;
 
 public:
-    void add(Maybe v) {
-        if (v) t[n++] = v;
+    void add(const char* name, Maybe v) {
+        if (!v) return;
+        if (v->requires_grad() && at::GradMode::is_enabled())
+            raise(PyExc_ValueError, "%s is written in place, but requires a gradient: detach it, or call under torch.no_grad()", name);
+        t[n++] = v;
     }
     void changed() const {
         for (int i = 0; i < n; ++i)
@@ -143,7 +149,7 @@ struct Call {
         Maybe t = maybe(name, given);
         if (!t) return fresh(dims, type);
         dense(name, t, dims, type);
-        written.add(t);
+        written.add(name, t);
         return *t;
     }
 };
@@ -174,7 +180,7 @@ struct Buffer {
             bytes = static_cast<size_t>(g->numel()) * g->element_size();
             if (bytes < need || !g->is_contiguous() || g->device() != c.dev)
                 raise(PyExc_ValueError, "%s needs %zu contiguous bytes on %s", name, need, c.dev.str().c_str());
-            if (writes) c.written.add(g);
+            if (writes) c.written.add(name, g);
             t = *g;
         } else if (need > 0) {
             t = c.fresh({static_cast<int64_t>(need)}, at::kByte);
@@ -287,7 +293,7 @@ PyObject* conv_step(PyObject* const* a) {
     const float* wp = c.dense<float>("w", &w, {dim, width});
     const float* bp = c.dense<float>("bias", maybe("bias", a[2]), {dim});
     void* pool = c.dense("window", &window, {slots, dim, width - 1}, c.dt);
-    c.written.add(&window);
+    c.written.add("window", &window);
     const int32_t* si = c.dense<int32_t>("slot_in", maybe("slot_in", a[4]), {batch});
     const int32_t* so = c.dense<int32_t>("slot_out", maybe("slot_out", a[5]), {batch});
     const at::Tensor y = c.out("out", a[7], {batch, dim}, c.dt);
@@ -397,7 +403,7 @@ PyObject* scan_step(PyObject* const* a) {
     const float* Dp = c.dense<float>("Dskip", maybe("Dskip", a[6]), {dim});
     const float* bias = c.dense<float>("dt_bias", maybe("dt_bias", a[7]), {dim});
     float* hp = c.dense<float>("h", &h, {slots, dim, N});
-    c.written.add(&h);
+    c.written.add("h", &h);
     const int32_t* si = c.dense<int32_t>("slot_in", maybe("slot_in", a[9]), {batch});
     const int32_t* so = c.dense<int32_t>("slot_out", maybe("slot_out", a[10]), {batch});
     const at::Tensor y = c.out("out", a[12], {batch, dim}, c.dt);
@@ -468,7 +474,7 @@ PyObject* reorder(PyObject* const* a) {
         out.device() != state.device())
         raise(PyExc_ValueError, "out must have state's dtype, shape, strides and device");
     Written written;
-    written.add(&out);
+    written.add(given ? "out" : "state", &out);
     const int64_t es = static_cast<int64_t>(state.element_size());
     const int64_t row_bytes = layer / rows * es, layer_bytes = layers > 1 ? state.stride(0) * es : 0;
     run("beam_reorder", written, [&] {
