@@ -394,6 +394,9 @@ int s6_scan_1d(int64_t batch, int64_t dim, int64_t dstate, int64_t seqlen, int d
  *     incoming state on.
  *   - 1 <= L < 2^27, batch at most 65535, dim below 2^20, dstate 1..16,
  *     width 2..8.
+ *   - A launch has fewer than 2^32 threads along an axis: a convolution whose
+ *     batch row holds about 2^35 entries or more (its gradient: 2^38) returns
+ *     VS_ERR_UNSUPPORTED.
  *   - No output may overlap an input or another output (VS_ERR_ALIAS).
  */
 #define VS_MAX_CONV_WIDTH 8
@@ -545,7 +548,8 @@ int s6_scan_step(int64_t batch, int64_t dim, int64_t dstate, int dtype, int flag
  * ranks as -inf. Within a beam candidates are ordered by their logits and
  * equal ones by the lowest token; across beams by their scores and equal ones
  * by the lowest beam. Sums are fp32.
- * beams 1..VS_MAX_BEAMS, vocab < 2^30, batch at most 65535.
+ * beams 1..VS_MAX_BEAMS, vocab < 2^30, batch at most 65535, and over all rows
+ * fewer than 2^24 parts of 8,192 logits.
  * workspace: beam_workspace_bytes(batch, beams, vocab) bytes.
  */
 #define VS_MAX_BEAMS 32
@@ -563,6 +567,8 @@ int beam_select(int64_t batch, int64_t beams, int64_t vocab, int dtype, const vo
  *               sequence's rows counts as the row itself
  *   out         may be state itself: rows that keep their own parent are then
  *               not touched; any other overlap is refused
+ * A row is below 2^36 bytes and 2^32 accesses, of 16, 4, 2 or 1 bytes as its
+ * length and the addresses allow.
  */
 int beam_reorder(int64_t layers, int64_t batch, int64_t beams, int64_t row_bytes,
                  int64_t layer_bytes, const void* state, const int32_t* parent, void* out,

@@ -456,7 +456,7 @@ template <typename V>
 int launch_reorder(ReorderArgs a, int64_t layers, int64_t batch, hipStream_t st) {
     a.cols = a.row_bytes / static_cast<int64_t>(sizeof(V));
     const int64_t wgs = (a.cols + kThreads - 1) / kThreads;
-    if (wgs >= (int64_t(1) << 31)) return fail(VS_ERR_UNSUPPORTED, "rows too long for one launch");
+    if (wgs > vs::kMaxGroups) return fail(VS_ERR_UNSUPPORTED, "rows too long for one launch");
     const dim3 grid(static_cast<unsigned>(wgs), static_cast<unsigned>(batch), static_cast<unsigned>(layers));
     if (a.beams <= 4) hipLaunchKernelGGL((beam_reorder_kernel<V, 4>), grid, dim3(kThreads), 0, st, a);
     else if (a.beams <= 8) hipLaunchKernelGGL((beam_reorder_kernel<V, 8>), grid, dim3(kThreads), 0, st, a);
@@ -484,7 +484,7 @@ int beam_select(int64_t batch, int64_t beams, int64_t vocab, int dtype, const vo
     a.beams = static_cast<int>(beams);
     a.parts = static_cast<int>((vocab + kPart - 1) / kPart);
     const int64_t wgs = batch * beams * a.parts;
-    if (wgs >= (int64_t(1) << 31)) return fail(VS_ERR_UNSUPPORTED, "batch * beams * vocab too large for one launch");
+    if (wgs > vs::kMaxGroups) return fail(VS_ERR_UNSUPPORTED, "batch * beams * vocab too large for one launch");
     a.keys = static_cast<uint64_t*>(workspace);
     a.sums = reinterpret_cast<float2*>(a.keys + wgs * beams);
     const hipStream_t s = static_cast<hipStream_t>(stream);

@@ -624,7 +624,7 @@ int launch_conv(const vs::ConvCall& c) {
     const int64_t per = vs::kConvVec << a.tw_log2;
     a.segs = static_cast<int>((c.L + per - 1) / per);
     const int64_t rows = kThreads >> a.tw_log2, groups = (c.dim + rows - 1) / rows * a.segs;
-    if (groups >= (int64_t(1) << 31)) return fail(VS_ERR_UNSUPPORTED, "too many tokens and channels for one launch");
+    if (groups > vs::kMaxGroups) return fail(VS_ERR_UNSUPPORTED, "too many tokens and channels for one launch");
     const dim3 grid(static_cast<unsigned>(groups), static_cast<unsigned>(c.batch));
     return with_width(c.width, [&](auto w) {
         constexpr int W = decltype(w)::value;

@@ -679,8 +679,7 @@ int launch_conv_grad(const vs::ConvCall& c) {
     while (a.tw_log2 < 6 && ((1 << a.tw_log2) - 1) * vs::kConvVec < c.L) ++a.tw_log2;
     const int64_t per = kThreads >> a.tw_log2;
     const int64_t wgs = (c.dim * a.segs + per - 1) / per;
-    // rows cut into segments are counted in 32 bits
-    if (wgs >= (int64_t(1) << 31) || (a.segs > 1 && c.dim * a.segs >= (int64_t(1) << 31) - kWaves)) return fail(VS_ERR_UNSUPPORTED, "too many tokens and channels for one launch");
+    if (wgs > vs::kMaxGroups) return fail(VS_ERR_UNSUPPORTED, "too many tokens and channels for one launch");
     const dim3 grid(static_cast<unsigned>(wgs), static_cast<unsigned>(c.batch));
     const hipStream_t st = static_cast<hipStream_t>(c.stream);
     switch (c.width) {

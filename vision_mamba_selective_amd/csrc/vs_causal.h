@@ -58,7 +58,7 @@ __device__ __forceinline__ bool any_non_finite(F... v) {
 
 // A few rows of a tensor behind a buffer descriptor: 32-bit byte offsets from
 // the first row; reads outside return zero, writes outside are dropped. The
-// rows span under 2^31 bytes (4 rows of at most 2^27 entries).
+// rows span at most 2^31 bytes (4 rows of at most 2^27 entries).
 constexpr uint32_t kDropped = 0xfffffff0u;          // an offset past every descriptor
 template <typename T>
 using Raw = std::conditional_t<sizeof(T) == 2, uint16_t, uint32_t>;

@@ -124,7 +124,9 @@ int validate_out_proj(int64_t batch, int64_t dim_in, int64_t dim_out, int64_t se
 
 // ---- the causal mixer and beam search (host_causal.cpp)
 constexpr int64_t kCausalMaxL = int64_t(1) << 27;    // tokens and channel strides: 4 rows of a wave
-                                                     // stay below 2^32 bytes
+                                                     // span at most 2^31 bytes
+// workgroups of 256 threads along an axis: a launch has fewer than 2^32 threads there
+constexpr int64_t kMaxGroups = (int64_t(1) << 24) - 1;
 constexpr int64_t kCausalMaxDim = int64_t(1) << 20;
 constexpr int kCausalCh = 16;                        // channels per workgroup of the narrow scan kernels
 constexpr int kCausalWideCh = 64;                    // and of the wide ones
