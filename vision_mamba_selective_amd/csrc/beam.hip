@@ -16,7 +16,7 @@ using vs::fail;
 
 constexpr int kThreads = 256;
 constexpr int kWaves = kThreads / 64;
-constexpr int kPart = 8192;                 // entries of one workgroup's part of a row
+constexpr int kPart = static_cast<int>(vs::kBeamPart);   // entries of one workgroup's part of a row
 constexpr int kPer = kPart / kThreads;      // and of one thread: chunks of 8 consecutive ones
 constexpr int kChunks = kPer / 8;
 
@@ -482,7 +482,7 @@ int beam_select(int64_t batch, int64_t beams, int64_t vocab, int dtype, const vo
     a.logits = logits; a.scores = scores; a.done = done; a.out_scores = out_scores; a.out_parent = out_parent;
     a.out_token = out_token; a.sb = st[0]; a.sk = st[1]; a.batch = batch; a.vocab = vocab; a.eos = eos;
     a.beams = static_cast<int>(beams);
-    a.parts = static_cast<int>((vocab + kPart - 1) / kPart);
+    a.parts = static_cast<int>(vs::beam_parts(vocab));
     const int64_t wgs = batch * beams * a.parts;
     if (wgs > vs::kMaxGroups) return fail(VS_ERR_UNSUPPORTED, "batch * beams * vocab too large for one launch");
     a.keys = static_cast<uint64_t*>(workspace);

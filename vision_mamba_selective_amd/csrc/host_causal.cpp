@@ -362,8 +362,6 @@ int prepare_scan_step(StepCall& c) {
 }
 
 // ---- beam search
-int64_t beam_part(int64_t, int64_t, int64_t) { return 8192; }
-
 namespace {
 
 bool beam_sizes_ok(int64_t batch, int64_t beams, int64_t vocab) {
@@ -434,8 +432,7 @@ size_t s6_workspace_bytes(int op, int64_t batch, int64_t dim, int64_t dstate, in
 size_t beam_workspace_bytes(int64_t batch, int64_t beams, int64_t vocab) {
     if (!vs::beam_sizes_ok(batch, beams, vocab)) return 0;
     // per part of a row: `beams` candidates of 8 bytes, then its maximum and its sum
-    const int64_t parts = (vocab + vs::beam_part(batch, beams, vocab) - 1) / vs::beam_part(batch, beams, vocab);
-    return static_cast<size_t>(batch * beams * parts) * static_cast<size_t>(beams + 1) * 8;
+    return static_cast<size_t>(batch * beams * vs::beam_parts(vocab)) * static_cast<size_t>(beams + 1) * 8;
 }
 
 }  // extern "C"

@@ -217,7 +217,9 @@ int validate_beam_select(int64_t batch, int64_t beams, int64_t vocab, int dtype,
                          const void* ws, size_t ws_bytes, int64_t st[2]);
 int validate_beam_reorder(int64_t layers, int64_t batch, int64_t beams, int64_t row_bytes,
                           int64_t& layer_bytes, const void* state, const int32_t* parent, const void* out);
-// beam_select: vocabulary entries of one workgroup's part of a row, and the parts of a row
-int64_t beam_part(int64_t batch, int64_t beams, int64_t vocab);
+// beam_select: vocabulary entries of one workgroup's part of a row; the kernels
+// and the size of their workspace rest on the same parts
+constexpr int64_t kBeamPart = 8192;
+inline int64_t beam_parts(int64_t vocab) { return (vocab + kBeamPart - 1) / kBeamPart; }
 
 }  // namespace vs
