@@ -488,10 +488,12 @@ PyObject* reorder(PyObject* const* a) {
 }
 
 // ------------------------------------------------------------------ module
-// addresses of the library's functions by name, and what turns a status into an exception
+// addresses of the library's functions by name, and what turns a status into an
+// exception; where one is missing, those bound before stay
 PyObject* bind(PyObject*, PyObject* args) {
     PyObject *table, *check;
     if (!PyArg_ParseTuple(args, "O!O", &PyDict_Type, &table, &check)) return nullptr;
+    Abi found;
 #define VS_FIND(f)                                                                          \
     {                                                                                       \
         PyObject* v = PyDict_GetItemString(table, #f);                                      \
@@ -500,10 +502,11 @@ PyObject* bind(PyObject*, PyObject* args) {
             if (!PyErr_Occurred()) PyErr_SetString(PyExc_ValueError, "no address of " #f);  \
             return nullptr;                                                                 \
         }                                                                                   \
-        abi.f = reinterpret_cast<decltype(abi.f)>(p);                                       \
+        found.f = reinterpret_cast<decltype(found.f)>(p);                                   \
     }
     VS_BOUND(VS_FIND)
 #undef VS_FIND
+    abi = found;
     Py_INCREF(check);
     Py_XSETREF(check_status, check);
     Py_RETURN_NONE;
