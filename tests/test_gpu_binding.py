@@ -29,3 +29,21 @@ def test_a_failed_bind_changes_nothing():
     finally:
         _calls._binding.bind(real, nat.check)
     assert all(torch.equal(a, b) for a, b in zip(got, want))
+
+
+@pytest.mark.skipif(torch.cuda.device_count() < 2, reason="needs two devices")
+def test_calls_run_on_the_tensors_device():
+    """Tensors of one device while another is the current one: the same bits."""
+    import vision_mamba_selective_amd as vms
+    say("case other device")
+    g = torch.Generator().manual_seed(3)
+    u, B, A = torch.randn(2, 20, 700, generator=g), torch.randn(2, 8, 700, generator=g), -torch.rand(20, 8, generator=g)
+    x, s = torch.randn(2, 3, 9000, generator=g), torch.randn(2, 3, generator=g)
+
+    def both(d):
+        y, h = vms.s6_causal_scan(*(v.to(d) for v in (u, u, u, B, B, A)))
+        return [v.cpu() for v in (y, h, *vms.beam_select(x.to(d), s.to(d)))]
+    with torch.cuda.device(0):
+        want = both("cuda:0")
+        got = both("cuda:1")
+    assert all(torch.equal(a, b) for a, b in zip(got, want))

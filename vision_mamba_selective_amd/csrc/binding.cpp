@@ -14,6 +14,8 @@
 #include <ATen/core/Tensor.h>
 #include <ATen/core/grad_mode.h>
 #include <ATen/ops/empty.h>
+#include <c10/core/DeviceGuard.h>
+#include <c10/hip/HIPFunctions.h>
 #include <c10/hip/HIPStream.h>
 #include <torch/csrc/DynamicTypes.h>
 #include <torch/csrc/Exceptions.h>
@@ -189,9 +191,11 @@ struct Buffer {
     }
 };
 
-// the call itself, without the interpreter's lock; a status becomes an exception
+// the call itself, on the tensors' device and without the interpreter's lock; a status becomes an exception
 template <typename F>
-void run(const char* name, const Written& written, F&& f) {
+void run(const char* name, const at::Device& dev, const Written& written, F&& f) {
+    c10::OptionalDeviceGuard guard;
+    if (c10::hip::current_device() != dev.index()) guard.reset_device(dev);
     int code;
     Py_BEGIN_ALLOW_THREADS
     code = f();
@@ -246,7 +250,7 @@ PyObject* conv(PyObject* const* a) {
     const at::Tensor wo = c.out("window_out", a[7], {batch, dim, width - 1}, c.dt);
     const Strides st({&x});
     const int flags = truth(a[5]) ? VS_CONV_SILU : 0;
-    run("s6_causal_conv", c.written, [&] {
+    run("s6_causal_conv", c.dev, c.written, [&] {
         return abi.s6_causal_conv(batch, dim, width, L, c.dtype, flags, xp, st.p, wp, bp, win, len, y.data_ptr(), wo.data_ptr(), c.stream());
     });
     return tuple({y, wo});
@@ -272,7 +276,7 @@ PyObject* conv_grad(PyObject* const* a) {
     if (win) dwin = c.fresh({batch, dim, width - 1}, c.dt);
     const Strides st({&x, &dy});
     const int flags = truth(a[7]) ? VS_CONV_SILU : 0;
-    run("s6_causal_conv_grad", c.written, [&] {
+    run("s6_causal_conv_grad", c.dev, c.written, [&] {
         return abi.s6_causal_conv_grad(batch, dim, width, L, c.dtype, flags, xp, dyp, st.p, wp, bp, win, len, dwo, dx.data_ptr(),
                                        f32(dw), f32(db), at_or_null(dwin), ws.p, ws.bytes, c.stream());
     });
@@ -299,7 +303,7 @@ PyObject* conv_step(PyObject* const* a) {
     const at::Tensor y = c.out("out", a[7], {batch, dim}, c.dt);
     const int64_t stride = batch > 1 ? x.stride(0) : 0;
     const int flags = truth(a[6]) ? VS_CONV_SILU : 0;
-    run("s6_conv_step", c.written, [&] {
+    run("s6_conv_step", c.dev, c.written, [&] {
         return abi.s6_conv_step(batch, dim, width, c.dtype, flags, x.data_ptr(), stride, wp, bp, pool, slots, si, so, y.data_ptr(), c.stream());
     });
     return wrap(y);
@@ -345,14 +349,14 @@ PyObject* scan_call(PyObject* const* a, bool saves) {
     const int flags = truth(a[10]) ? VS_FLAG_SOFTPLUS : 0;
     if (!saves) {
         const Buffer ws("workspace", s.bytes(VS_S6_SCAN), c, a[13]);
-        run("s6_causal_scan", c.written, [&] {
+        run("s6_causal_scan", c.dev, c.written, [&] {
             return abi.s6_causal_scan(s.batch, s.dim, s.N, s.L, c.dtype, flags, s.u, s.delta, s.z, s.B, s.C, st.p, s.A, s.Dskip, s.dt_bias,
                                       h0, s.lengths, y.data_ptr(), f32(h), ws.p, ws.bytes, c.stream());
         });
         return tuple({y, h});
     }
     const Buffer saved("saved", s.bytes(VS_S6_SAVED), c, a[14]), ws("workspace", s.bytes(VS_S6_SCAN), c, a[13]);
-    run("s6_causal_scan_saved", c.written, [&] {
+    run("s6_causal_scan_saved", c.dev, c.written, [&] {
         return abi.s6_causal_scan_saved(s.batch, s.dim, s.N, s.L, c.dtype, flags, s.u, s.delta, s.z, s.B, s.C, st.p, s.A, s.Dskip,
                                         s.dt_bias, h0, s.lengths, y.data_ptr(), f32(h), saved.p, saved.bytes, ws.p, ws.bytes, c.stream());
     });
@@ -380,7 +384,7 @@ PyObject* scan_grad(PyObject* const* a) {
     const at::Tensor dB = fp({s.batch, s.N, s.L}), dC = fp({s.batch, s.N, s.L}), dA = fp({s.dim, s.N}), dD = fp({s.dim}), db = fp({s.dim});
     const Strides st({&s.tu, &s.td, s.tz, &s.tB, &s.tC, &tdy});
     const int flags = truth(a[13]) ? VS_FLAG_SOFTPLUS : 0;
-    run("s6_causal_scan_grad", c.written, [&] {
+    run("s6_causal_scan_grad", c.dev, c.written, [&] {
         return abi.s6_causal_scan_grad(s.batch, s.dim, s.N, s.L, c.dtype, flags, s.u, s.delta, s.z, s.B, s.C, dy, st.p, s.A, s.Dskip,
                                        s.dt_bias, s.lengths, saved.p, saved.bytes, dh, du.data_ptr(), dd.data_ptr(), at_or_null(dz),
                                        f32(dB), f32(dC), f32(dA), f32(dD), f32(db), f32(dh0), ws.p, ws.bytes, c.stream());
@@ -415,7 +419,7 @@ PyObject* scan_step(PyObject* const* a) {
         st[k++] = t ? t->stride(0) : 0;
     }
     const int flags = truth(a[11]) ? VS_FLAG_SOFTPLUS : 0;
-    run("s6_scan_step", c.written, [&] {
+    run("s6_scan_step", c.dev, c.written, [&] {
         return abi.s6_scan_step(batch, dim, N, c.dtype, flags, up, dp, zp, Bp, Cp, stp, Ap, Dp, bias, hp, slots, si, so, y.data_ptr(), c.stream());
     });
     return wrap(y);
@@ -443,7 +447,7 @@ PyObject* select(PyObject* const* a) {
     const at::Tensor t = c.out("out[2]", a[7], {batch, beams}, at::kInt);
     const Strides st({&logits});
     const Buffer ws("workspace", abi.beam_workspace_bytes(batch, beams, vocab), c, a[4]);
-    run("beam_select", c.written, [&] {
+    run("beam_select", c.dev, c.written, [&] {
         return abi.beam_select(batch, beams, vocab, c.dtype, lp, st.p, sp, static_cast<const uint8_t*>(done), eos, f32(s),
                                static_cast<int32_t*>(p.data_ptr()), static_cast<int32_t*>(t.data_ptr()), ws.p, ws.bytes, c.stream());
     });
@@ -477,7 +481,7 @@ PyObject* reorder(PyObject* const* a) {
     written.add(given ? "out" : "state", &out);
     const int64_t es = static_cast<int64_t>(state.element_size());
     const int64_t row_bytes = layer / rows * es, layer_bytes = layers > 1 ? state.stride(0) * es : 0;
-    run("beam_reorder", written, [&] {
+    run("beam_reorder", state.device(), written, [&] {
         return abi.beam_reorder(layers, parent.size(0), parent.size(1), row_bytes, layer_bytes, state.data_ptr(),
                                 static_cast<const int32_t*>(parent.data_ptr()), out.data_ptr(),
                                 c10::hip::getCurrentHIPStream(state.device().index()).stream());
