@@ -1,7 +1,7 @@
 """A small causal language model of S6 mixers, trained and decoded with the
 library's causal entry points.
 
-    python examples/causal_lm.py [--steps N]
+    python examples/causal_lm.py [--steps N] [--beams K] [--move]
 
 It learns arithmetic progressions modulo the vocabulary (the first two tokens
 give the step), then continues prompts of different lengths by beam search:
@@ -10,7 +10,9 @@ give the step), then continues prompts of different lengths by beam search:
   prompts    s6_causal_conv and s6_causal_scan on a ragged batch, keeping states
   decoding   s6_conv_step and s6_scan_step on pools of two sets of states:
              a step reads one set, at the parents that beam_select chose, and
-             writes the other, so no state is moved between tokens
+             writes the other, so no state is moved between tokens; or, with
+             --move, on one set, half the memory, which beam_reorder brings
+             into the beams' order after each token
 
 Random weights and synthetic sequences; the linear maps, norms and the loss are
 torch's own.
@@ -124,17 +126,21 @@ def step(p, token, pools, slot_in, slot_out):
 
 
 @torch.no_grad()
-def beam_search(p, tokens, lengths, beams, count, eos=None):
-    """Continue each prompt by `count` tokens. Returns (sequences [rows, beams, count], scores [rows, beams])."""
+def beam_search(p, tokens, lengths, beams, count, eos=None, move=False):
+    """Continue each prompt by `count` tokens. Returns (sequences [rows, beams, count], scores [rows, beams]).
+
+    move: keep one set of states and move them to the beams that go on, instead
+    of two sets that are read and written in turn. Both give the same."""
     rows, dev = tokens.shape[0], tokens.device
     n = rows * beams
     logits, states = prompt(p, tokens, lengths)
-    # two sets of n slots; every beam of a prompt starts from the state at its first slot
-    pools = []
-    for window, h in states:
-        w, s = window.new_zeros(2 * n, *window.shape[1:]), h.new_zeros(2 * n, *h.shape[1:])
-        w[:n:beams], s[:n:beams] = window, h
-        pools.append((w, s))
+    # one or two sets of n slots, all layers in one tensor; every beam of a prompt
+    # starts from the state at its first slot
+    total = n if move else 2 * n
+    windows, hs = (v[0].new_zeros(LAYERS, total, *v[0].shape[1:]) for v in zip(*states))
+    for i, (window, h) in enumerate(states):
+        windows[i, :n:beams], hs[i, :n:beams] = window, h
+    pools = list(zip(windows, hs))
     slots = torch.arange(n, dtype=torch.int32, device=dev)
     scores = torch.full((rows, beams), -math.inf, device=dev)
     scores[:, 0] = 0
@@ -149,9 +155,14 @@ def beam_search(p, tokens, lengths, beams, count, eos=None):
             done = done.flatten()[flat.long()].view(rows, beams) | (token == eos)
         if k + 1 == count:
             break
+        source = flat // beams * beams if k == 0 else flat          # at first all beams share their prompt's state
+        if move:
+            for state in (windows, hs):
+                vms.beam_reorder(state, source.view(rows, beams))
+            logits = step(p, token.flatten(), pools, slots, slots).view(rows, beams, VOCAB)
+            continue
         # read the set that the last token wrote, at the parents; write the other
         read, write = (0, n) if k % 2 == 0 else (n, 0)
-        source = flat // beams * beams if k == 0 else flat          # at first all beams share their prompt's state
         logits = step(p, token.flatten(), pools, source + read, slots + write).view(rows, beams, VOCAB)
     return picked, scores
 
@@ -160,6 +171,7 @@ def main():
     ap = argparse.ArgumentParser(description=__doc__, formatter_class=argparse.RawDescriptionHelpFormatter)
     ap.add_argument("--steps", type=int, default=300, help="training steps")
     ap.add_argument("--beams", type=int, default=4)
+    ap.add_argument("--move", action="store_true", help="one set of states, moved to the beams that go on")
     a = ap.parse_args()
     p = init()
     losses = train(p, a.steps)
@@ -167,7 +179,7 @@ def main():
     g = torch.Generator().manual_seed(7)
     t = progressions(3, 20, g)
     lengths = torch.tensor([4, 9, 12], dtype=torch.int32, device=t.device)
-    out, scores = beam_search(p, t[:, :12], lengths, a.beams, 8)
+    out, scores = beam_search(p, t[:, :12], lengths, a.beams, 8, move=a.move)
     for i in range(3):
         n = int(lengths[i])
         print("prompt %s" % t[i, :n].tolist())
