@@ -197,6 +197,39 @@ def test_gradient_sums(name, lengths, dim, N, dtype):
 
 
 @pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("dim", [1, 37, 16])
+@pytest.mark.parametrize("name", ["B", "C"])
+def test_gradient_sums_of_infinite_rows(name, dim, dtype):
+    """dB and dC where one entry of B or C is infinite: the lanes of a group of
+    16 channels past the last one add nothing there either. All other factors
+    are positive, so that the sums are infinities."""
+    import vision_mamba_selective_amd as vms
+    N, L, at = 7, 45, 19
+    t = inputs((1, dim, L), N, dtype)
+    t["u"], t["dy"] = t["u"].abs() + 0.1, t["dy"].abs() + 0.1
+    t[name][0, 2, at] = INF
+    say("case infinite row %s %d %s" % (name, dim, dtype))
+    args = (t["u"], t["delta"], None, t["B"], t["C"], t["A"], t["D"], None)
+    _, _, saved = vms.s6_causal_scan_saved(*args, h0=t["h0"])
+    g = vms.s6_causal_scan_grad(*args, saved, t["dy"], dh=t["dh"], h0=t["h0"])
+    d = {k: ref.f64(v)[0] if v.dim() == 3 else ref.f64(v) for k, v in t.items()}
+    step = torch.logaddexp(d["delta"], torch.zeros_like(d["delta"]))
+    hs, dB, dC = [d["h0"]], torch.zeros(N, L, dtype=ref.F64), torch.zeros(N, L, dtype=ref.F64)
+    for i in range(L):
+        hs.append(torch.exp(step[:, i, None] * d["A"]) * hs[-1] + (step[:, i] * d["u"][:, i])[:, None] * d["B"][:, i])
+    lam = d["dh"]
+    for i in reversed(range(L)):
+        dC[:, i] = (d["dy"][:, i, None] * hs[i + 1]).sum(0)
+        lam = lam + d["dy"][:, i, None] * d["C"][:, i]
+        dB[:, i] = (lam * (step[:, i] * d["u"][:, i])[:, None]).sum(0)
+        lam = torch.exp(step[:, i, None] * d["A"]) * lam
+    hit = dC if name == "B" else dB
+    assert torch.isinf(hit[2]).any() and torch.isfinite(hit[:2]).all()
+    same(g["dB"][0], dB, "dB")
+    same(g["dC"][0], dC, "dC")
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
 @pytest.mark.parametrize("W", [2, 4, 8])
 @pytest.mark.parametrize("L,lengths", [(60, None), (60, [29, 13]), (300, [299, 290]), (1100, [1100, 1001])],
                          ids=["full", "ragged", "long", "segments"])

@@ -243,9 +243,11 @@ __device__ __forceinline__ float swap16_sum(float a, float b) {
 // NaN, and the lane swaps that it would save are an eighth of the instructions.
 template <typename T, bool GATE, bool SOFTPLUS, bool FULL>
 __global__ __launch_bounds__(kThreads) void causal_grad_kernel(const ScanGradArgs a) {
-    __shared__ __attribute__((aligned(16))) float tile[2][2][kRowLanes][kTilePad];
+    // row kRowLanes stays zero: the B and C of lanes whose channel is past dim
+    __shared__ __attribute__((aligned(16))) float tile[2][2][kRowLanes + 1][kTilePad];
     __shared__ float4 red[2][kWaves][2][64];
     const int tid = threadIdx.x;
+    if (tid < 4 * kTilePad) tile[tid / (2 * kTilePad)][tid / kTilePad & 1][kRowLanes][tid % kTilePad] = 0.f;
     const int lane = tid & 63;
     const int wave = tid >> 6;
     const int n = lane & 15;
@@ -289,9 +291,10 @@ __global__ __launch_bounds__(kThreads) void causal_grad_kernel(const ScanGradArg
     const int tile0 = s0 / kTileTok;
     const int ntile = e > s0 ? (e + kTileTok - 1) / kTileTok : tile0;
     // Lanes of channels past dim count for nothing in the sums over channels:
-    // they hold zeros from here on (their memory is channel dim - 1's, and a
-    // zero factor in front of an infinity of that would be NaN)
+    // they hold zeros from here on, B and C among them (their memory is channel
+    // dim - 1's, and a zero factor in front of an infinity would be NaN)
     const bool holds = active && n_ok;
+    const int bc_row = active ? n : kRowLanes;
     float lamE = a.dh_out && holds ? a.dh_out[row * a.dstate + n] : 0.f;
     // the adjoint that enters at the piece's end: those of the later pieces
     // that hold tokens, the last of them first, eight in flight at a time
@@ -365,8 +368,8 @@ __global__ __launch_bounds__(kThreads) void causal_grad_kernel(const ScanGradArg
             dz.store(out, ok ? v : 0.f, out0);
         }
         gs = ok ? gs : 0.f;
-        const float4* Bt = reinterpret_cast<const float4*>(&tile[it & 1][0][n][half * 16]);
-        const float4* Ct = reinterpret_cast<const float4*>(&tile[it & 1][1][n][half * 16]);
+        const float4* Bt = reinterpret_cast<const float4*>(&tile[it & 1][0][bc_row][half * 16]);
+        const float4* Ct = reinterpret_cast<const float4*>(&tile[it & 1][1][bc_row][half * 16]);
         float Bv[16], Cv[16], hs[16], es[16], wv[16], vv[16], sbc[16];
 #pragma unroll
         for (int q = 0; q < 4; ++q) {

@@ -226,7 +226,8 @@ struct BcStage {
 #pragma unroll
         for (int i = 0; i < 4; ++i) raw[i] = ld_raw(src[i], tc);
     }
-    __device__ __forceinline__ void store(float (&dst)[2][kRowLanes][kTilePad]) {
+    template <int ROWS>
+    __device__ __forceinline__ void store(float (&dst)[2][ROWS][kTilePad]) {
 #pragma unroll
         for (int i = 0; i < 4; ++i)
             dst[i >> 1][(r0 + 8 * i) & 15][col] = ok[i] && in ? from_raw<T>(raw[i]) : 0.f;
