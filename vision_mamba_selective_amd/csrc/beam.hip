@@ -124,10 +124,14 @@ __device__ __forceinline__ void load_eight(const uint16_t* p, float (&f)[8]) {
 // an entry at or above it). Where the list cannot hold what that leaves, the
 // threshold becomes the beams-th largest maximum of a lane: fewer than `beams`
 // lanes of 32 entries are above that.
-// Bound by VALU issue: 64 x 8 beams x 49,999 bf16 25 us, 663 instructions a
-// wave, VALU active 82 %; its 51 MB would take 10 us. The smallest GROUPS is
-// taken: for those 8 beams 31 us with 16 and 63 with 32, whose longer lists
-// leave fewer workgroups a compute unit. With 64 entries a thread 29 us.
+// 64 x 8 beams x 49,999 bf16 24 us. The logits' 47 MB would take 9 us, the 663
+// VALU instructions a wave about 10 at their issue costs (the counter, in steps
+// of four cycles, has the VALU active 81 %). The rest has not been taken apart:
+// its steps follow one another (the prefix sum, the second read of the
+// candidates, their ranking, and the last one by one wave). The smallest GROUPS is taken: for
+// those 8 beams 31 us with 16 and 63 with 32, whose longer lists leave fewer
+// workgroups a compute unit; as many logits take, with the merge, 55 us at 32 x
+// 16 beams and 168 at 16 x 32. With 64 entries a thread 29 us.
 template <typename T, int GROUPS>
 __global__ __launch_bounds__(kThreads) void beam_part_kernel(const SelectArgs a) {
     constexpr int kMost = kPer * (GROUPS - 1);

@@ -34,8 +34,10 @@ struct ConvArgs {
 // y = silu(bias + sum_j w[j] line[t + j]): a lane takes eight consecutive
 // tokens of a row (one or two 16-byte loads, and a second load of the W - 1
 // entries before them, which the caches hold); short rows share a workgroup.
-// Bound by memory: each entry of x comes from HBM once. 8 x 768 x 4,097 bf16
-// 28 us, 3.6 TB/s read and written (a plain copy reaches 5.1).
+// Each entry of x comes from HBM once. 8 x 768 x 4,097 bf16 28 us, 3.7 TB/s read
+// and written (a plain copy reaches 5.1), VALU active 61 %. Padding goes
+// through the straddling lane's entry-by-entry path: rows of 2,049 to 4,097
+// tokens take 32 us for 92 MB.
 template <typename T, int W, bool SILU>
 __global__ __launch_bounds__(kThreads) void causal_conv_kernel(const ConvArgs a) {
     const int tid = threadIdx.x;
@@ -130,11 +132,13 @@ __global__ __launch_bounds__(kThreads) void conv_step_kernel(const ConvStepArgs 
 // enters as delta = 0 and zero u, B: it leaves the state as it is whatever
 // the padded memory holds. Where that evens out the load of the compute units
 // the sequence is cut into a few pieces, as described for the wide form below.
-// Bound by VALU issue: 122 instructions a wave for 16 tokens, half of them
-// with a DPP operand and 17 exponentials, which take two to four times a plain
-// one's slot. 8 x 768 x 4,097 bf16, 16 states: 205 us with the
-// carry launch (52 of it), VALU active 74 % of the time; the 100 MB it has to
-// move would take 40 us.
+// VALU issue takes most of the time: 165 instructions a wave for 16 tokens, 62
+// of them with a DPP operand and 20 transcendental, which cost two to four
+// times a plain one's slot: 626 cycles, 100 us of the 169 that the saving form
+// takes for 8 x 768 x 4,097 bf16, 16 states, in 2 pieces (carry launch 49), VALU
+// active 76 %; without saving both together 190. With rows of 2,049 to 4,097
+// tokens, a quarter less work, the launch takes 147 us: an XCD holds one batch
+// row there, and the longest row's is the last to end.
 template <typename T, bool GATE, bool SOFTPLUS, bool SAVE>
 __global__ __launch_bounds__(kThreads) void causal_scan_kernel(const ScanFwdArgs a) {
     __shared__ __attribute__((aligned(16))) float tile[2][2][kRowLanes][kTilePad];
@@ -279,11 +283,11 @@ __global__ __launch_bounds__(kThreads) void causal_scan_kernel(const ScanFwdArgs
 // last from zero, with no read-out, and stores h_loc and the sum of delta;
 // the second folds those of the earlier pieces into its own starting state
 // and scans its tokens in full. Bound by VALU issue like the narrow form: 1 x
-// 1,536 x 16,385 bf16 in 21 pieces 137 us and 97 us for the carry, VALU active
-// 76 and 73 % (uncut, the narrow form takes 570). Two other layouts were
-// slower there: one channel a lane with 16 states in registers (375 us: two
-// waves a SIMD), and the broadcasts as moves in front of plain
-// multiplications (6 % more than as DPP operands).
+// 1,536 x 16,385 bf16 in 21 pieces 140 us and 97 us for the carry, VALU active
+// 76 and 72 %, 212 us together where they follow at once (uncut, the narrow
+// form takes 570). Two other layouts were slower there: one channel a lane with
+// 16 states in registers (375 us: two waves a SIMD), and the broadcasts as moves
+// in front of plain multiplications (6 % more than as DPP operands).
 template <typename T, bool GATE, bool SOFTPLUS, bool SAVE, bool CARRY>
 __global__ __launch_bounds__(kThreads) void causal_scan4_kernel(const ScanFwdArgs a) {
     __shared__ __attribute__((aligned(16))) float tile[2][kTileTok][kWidePad];
@@ -406,7 +410,7 @@ __global__ __launch_bounds__(kThreads) void causal_scan4_kernel(const ScanFwdArg
                 }
             }
             float p[16];
-            // CLEAN: states past dstate are set back to zero at every token
+            // clean: states past dstate are set back to zero at every token
             auto tokens = [&](auto clean) VS_INLINE { Unroll<16>::run([&](auto ic) VS_INLINE {
                 constexpr int i = decltype(ic)::value;
                 // the exponentials do not wait for the states: left free, all

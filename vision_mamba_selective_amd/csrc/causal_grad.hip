@@ -44,7 +44,7 @@ struct ConvGradArgs {
 // to 248 tokens share a wave (tw lanes each). Each lane sums dw and dbias of
 // its tokens; the segment's sums go to its partial row. Bound by memory (x
 // and dy read, dx written once) and, nearly as much, by VALU issue: 8 x 768 x
-// 4,097 bf16 43 us, 3.5 TB/s, VALU active 87 %.
+// 4,097 bf16 43 us, 3.7 TB/s, VALU active 86 %.
 template <typename T, int W, bool SILU>
 __global__ __launch_bounds__(kThreads) void causal_conv_grad_kernel(const ConvGradArgs a) {
     const int tw = 1 << a.tw_log2;
@@ -235,9 +235,9 @@ __device__ __forceinline__ float swap16_sum(float a, float b) {
 // branch for the blocks that need it takes 139 registers against 127, three
 // waves a SIMD instead of four.
 //
-// Bound by VALU issue: 390 instructions a wave for 16 tokens, 156 of them with
+// Bound by VALU issue: 391 instructions a wave for 16 tokens, 156 of them with
 // a DPP operand, VALU active 86 %. 8 x 768 x 4,097 bf16,
-// 16 states, in 2 pieces: 350 us here and 53 in the carry launch. The matrix
+// 16 states, in 2 pieces: 348 us here and 52 in the carry launch. The matrix
 // cores could add up dB and dC over the channels, but a product with zeros for
 // the channels past dim or another block's tokens turns an infinity there into
 // NaN, and the lane swaps that it would save are an eighth of the instructions.
@@ -494,7 +494,7 @@ __global__ __launch_bounds__(kThreads) void causal_grad_kernel(const ScanGradArg
 // and their sum of delta: lamE <- exp(delta_t A) (lamE + gy_t C_t) from the
 // piece's last token to its first. The wide form of the forward scan (four
 // states a lane, 64 channels a workgroup), without a read-out. Bound by VALU
-// issue: half of 8 x 768 x 4,097 bf16 53 us.
+// issue: half of 8 x 768 x 4,097 bf16 52 us.
 template <typename T, bool GATE, bool SOFTPLUS>
 __global__ __launch_bounds__(kThreads) void adjoint_carry_kernel(const ScanGradArgs a) {
     constexpr int kPad = kRowLanes + 4;

@@ -76,12 +76,14 @@ int check_overlaps(const Span* in, int ni, const Span* out, int no) {
 //   wide scan (64 channels)                max(3300, 2600 w)
 //   adjoint (16 channels)                  max(2900, 2100 w)
 //   carry launches (64 channels)           max(2450, 1950 w)
-// and what the second launch and the folding of p finer pieces add. Measured,
-// bf16: 8 x 768 x 4,097 tokens narrow 214 us uncut, 205 us in 2 pieces of 8;
-// 1 x 768 x 4,097 132 us narrow, 48 us wide in 19 pieces; 1 x 1,536 x 16,385
-// 570 us narrow, 210 us wide in 21 pieces; 64 x 1,536 x 197 110 us narrow, 101
-// us wide and uncut. Gradient: 8 x 768 x 4,097 553 us uncut, 469 us in 2 pieces
-// of 8; 1 x 768 x 4,097 335 us uncut, 87 us in 16 pieces.
+// and what the second launch and the folding of p finer pieces add. When they
+// were fitted, bf16, both launches together: 8 x 768 x 4,097 tokens narrow 214 us
+// uncut, 205 us in 2 pieces of 8; 1 x 768 x 4,097 132 us narrow and uncut; 1 x
+// 1,536 x 16,385 570 us narrow, 210 us wide in 21 pieces; 64 x 1,536 x 197 110 us
+// narrow, 101 us wide and uncut. Gradient: 8 x 768 x 4,097 553 us uncut, 469 us
+// in 2 pieces of 8; 1 x 768 x 4,097 335 us uncut, 87 us in 16 pieces. What is
+// chosen now takes, in that order, 190 us, 46 (narrow, 10 pieces of 2), 212, 98;
+// gradient 442 and 88 us.
 namespace {
 
 int64_t most(int64_t a, int64_t b) { return a > b ? a : b; }
