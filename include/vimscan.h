@@ -574,6 +574,79 @@ int beam_reorder(int64_t layers, int64_t batch, int64_t beams, int64_t row_bytes
                  int64_t layer_bytes, const void* state, const int32_t* parent, void* out,
                  void* stream);
 
+/*
+ * ---- The gated linear recurrence
+ *
+ * A mixer with one state a channel whose decay and input are gated by the
+ * token, beside the scan above: with k = rate softplus(lam),
+ *   s_t = k sigmoid(r_t), a_t = exp(-s_t)
+ *   h_t = a_t h_{t-1} + sqrt(1 - a_t^2) sigmoid(i_t) x_t
+ *   y_t = h_t silu(z_t)                           (y_t = h_t when z is NULL)
+ * Layout, strides, lengths, limits and overlaps are those of the causal mixer;
+ * batch x dim is below 2^24 rows. Arithmetic and states are fp32. 1 - a^2 is
+ * computed from s_t, so that slow decays lose nothing. rate is finite and >= 0
+ * (8 is usual). A decay is held at 2^-126 or more, so that an infinite state
+ * stays infinite however the sequence is cut.
+ */
+
+/* Bytes of the buffers of the entry points below; 0 for sizes they refuse.
+ * VS_GATED_SAVED: the saved states of gated_scan_saved;
+ * VS_GATED_GRAD: workspace of gated_scan_grad. */
+enum { VS_GATED_SAVED = 0, VS_GATED_GRAD = 1 };
+size_t gated_workspace_bytes(int op, int64_t batch, int64_t dim, int64_t seqlen);
+
+/*
+ * The recurrence over prompts.
+ *   strides     x, r, i, z
+ *   x, r, i, z  [batch][dim][L]; z may be NULL
+ *   lam         [dim] fp32
+ *   h0          [batch][dim] fp32, the state before token 0; NULL for zeros
+ *   y           [batch][dim][L]
+ *   h_out       [batch][dim] fp32 or NULL: the state after the row's last token
+ */
+int gated_scan(int64_t batch, int64_t dim, int64_t seqlen, int dtype, const void* x, const void* r,
+               const void* i, const void* z, const int64_t* strides, const float* lam, float rate,
+               const float* h0, const int32_t* lengths, void* y, float* h_out, void* stream);
+
+/* gated_scan for training: the same y and h_out, and into `saved`
+ * (gated_workspace_bytes(VS_GATED_SAVED, ...) bytes, layout private to the
+ * library) the states that gated_scan_grad starts from. */
+int gated_scan_saved(int64_t batch, int64_t dim, int64_t seqlen, int dtype, const void* x,
+                     const void* r, const void* i, const void* z, const int64_t* strides,
+                     const float* lam, float rate, const float* h0, const int32_t* lengths, void* y,
+                     float* h_out, void* saved, size_t saved_bytes, void* stream);
+
+/*
+ * Gradient of gated_scan from the saved buffer of a gated_scan_saved call on
+ * the same inputs (not checked).
+ *   strides     x, r, i, z, dy
+ *   dh_out      [batch][dim] fp32 or NULL: dL/d h_out
+ *   dx, dr, di, dz [batch][dim][L], dtype (dz NULL when z is)
+ *   dlam        [dim] fp32, summed over rows and tokens
+ *   dh0         [batch][dim] fp32 or NULL
+ *   workspace   gated_workspace_bytes(VS_GATED_GRAD, ...)
+ * Every output is overwritten and repeats bit for bit (no atomics). Where a
+ * gate has closed so far that s_t is below 1e-36, dr_t and that token's part
+ * of dlam are zero (they tend to zero with the root of s_t).
+ */
+int gated_scan_grad(int64_t batch, int64_t dim, int64_t seqlen, int dtype, const void* x,
+                    const void* r, const void* i, const void* z, const void* dy,
+                    const int64_t* strides, const float* lam, float rate, const int32_t* lengths,
+                    const void* saved, size_t saved_bytes, const float* dh_out, void* dx, void* dr,
+                    void* di, void* dz, float* dlam, float* dh0, void* workspace,
+                    size_t workspace_bytes, void* stream);
+
+/*
+ * One token of gated_scan for each row, on a pool of states.
+ *   x, r, i, z  [batch][dim]; strides: their row strides (NULL: contiguous)
+ *   h           [slots][dim] fp32; slot_in, slot_out as for s6_conv_step
+ *   y           [batch][dim]
+ */
+int gated_scan_step(int64_t batch, int64_t dim, int dtype, const void* x, const void* r,
+                    const void* i, const void* z, const int64_t* strides, const float* lam,
+                    float rate, float* h, int64_t slots, const int32_t* slot_in,
+                    const int32_t* slot_out, void* y, void* stream);
+
 /* Static name of a status code ("VS_OK", ...). Never NULL. */
 const char* vs_strerror(int status);
 

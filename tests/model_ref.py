@@ -1,0 +1,27 @@
+"""The gated linear recurrence, the norm and the vocabulary loss written out
+plainly in float64 torch on the CPU, from the definitions in include/vimscan.h.
+Gradients come from autograd over these steps. Test infrastructure; shares no
+code with the library."""
+import torch
+
+from causal_ref import F64, f64, gradients, row_lengths  # noqa: F401
+
+
+def gated(x, r, i, lam, z, h0, lengths, rate=8.0):
+    batch, dim, L = x.shape
+    k = rate * torch.logaddexp(lam, torch.zeros_like(lam))
+    ys, hs = [], []
+    for b, n in enumerate(row_lengths(lengths, batch, L)):
+        h = torch.zeros(dim, dtype=F64) if h0 is None else h0[b]
+        s = k[:, None] * torch.sigmoid(r[b, :, :n])
+        a, v = torch.exp(-s), torch.sqrt(-torch.expm1(-2 * s)) * torch.sigmoid(i[b, :, :n]) * x[b, :, :n]
+        cols = []
+        for t in range(n):
+            h = a[:, t] * h + v[:, t]
+            cols.append(h)
+        y = torch.stack(cols, dim=1) if cols else torch.zeros(dim, 0, dtype=F64)
+        if z is not None:
+            y = y * z[b, :, :n] * torch.sigmoid(z[b, :, :n])
+        ys.append(torch.cat([y, torch.zeros(dim, L - n, dtype=F64)], dim=1))
+        hs.append(h)
+    return torch.stack(ys), torch.stack(hs)

@@ -19,7 +19,9 @@ _CAUSAL = ["s6_workspace_bytes", "s6_causal_conv", "s6_causal_conv_grad", "s6_co
            "CausalConvFunction", "s6_causal_conv_autograd", "CausalScanFunction",
            "s6_causal_scan_autograd"]
 _BEAM = ["beam_select", "beam_reorder", "beam_workspace_bytes"]
-__all__ += _CAUSAL + _BEAM
+_GATED = ["gated_workspace_bytes", "gated_scan", "gated_scan_saved", "gated_scan_grad", "gated_scan_step",
+          "GatedScanFunction", "gated_scan_autograd"]
+__all__ += _CAUSAL + _BEAM + _GATED
 
 
 def __getattr__(name):
@@ -27,6 +29,8 @@ def __getattr__(name):
         from . import causal as module
     elif name in _BEAM:
         from . import beam as module
+    elif name in _GATED:
+        from . import gated as module
     elif name in __all__:
         from . import scan as module
     else:

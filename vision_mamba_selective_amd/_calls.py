@@ -1,4 +1,4 @@
-"""The causal mixer's and beam search's calls (csrc/binding.cpp): each checks
+"""The calls of the language model's operators (csrc/binding.cpp): each checks
 its arguments, allocates its outputs and calls the library, in one step of the
 host. The library's functions are those that _native loaded."""
 from __future__ import annotations
@@ -37,3 +37,7 @@ s6_causal_scan_grad = _binding.s6_causal_scan_grad
 s6_scan_step = _binding.s6_scan_step
 beam_select = _binding.beam_select
 beam_reorder = _binding.beam_reorder
+gated_scan = _binding.gated_scan
+gated_scan_saved = _binding.gated_scan_saved
+gated_scan_grad = _binding.gated_scan_grad
+gated_scan_step = _binding.gated_scan_step

@@ -20,12 +20,14 @@ VS_NOALLOC_MAX_ELEMS = 1 << 25
 VS_S6_SCAN, VS_S6_SAVED, VS_S6_GRAD, VS_S6_CONV_GRAD = 0, 1, 2, 3
 VS_MAX_CONV_WIDTH = 8
 VS_MAX_BEAMS = 32
+VS_GATED_SAVED, VS_GATED_GRAD = 0, 1
 
 # names and argument types of every entry point declared in include/vimscan.h
 _I64 = ctypes.c_int64
 _I = ctypes.c_int
 _P = ctypes.c_void_p
 _SZ = ctypes.c_size_t
+_F = ctypes.c_float
 SIGNATURES = {
     "vs_workspace_bytes": (_SZ, [_I, _I64, _I64, _I64, _I]),
     "vim_scan_bidir": (_I, [_I64, _I64, _I64, _I64, _I, _P, _P, _P, _P, _P, _P, _P, _P, _I,
@@ -63,6 +65,11 @@ SIGNATURES = {
     "beam_workspace_bytes": (_SZ, [_I64, _I64, _I64]),
     "beam_select": (_I, [_I64, _I64, _I64, _I] + [_P] * 4 + [_I64] + [_P] * 4 + [_SZ, _P]),
     "beam_reorder": (_I, [_I64, _I64, _I64, _I64, _I64, _P, _P, _P, _P]),
+    "gated_workspace_bytes": (_SZ, [_I, _I64, _I64, _I64]),
+    "gated_scan": (_I, [_I64, _I64, _I64, _I] + [_P] * 6 + [_F] + [_P] * 5),
+    "gated_scan_saved": (_I, [_I64, _I64, _I64, _I] + [_P] * 6 + [_F] + [_P] * 5 + [_SZ, _P]),
+    "gated_scan_grad": (_I, [_I64, _I64, _I64, _I] + [_P] * 7 + [_F, _P, _P, _SZ] + [_P] * 8 + [_SZ, _P]),
+    "gated_scan_step": (_I, [_I64, _I64, _I] + [_P] * 6 + [_F, _P, _I64] + [_P] * 4),
     "vs_strerror": (ctypes.c_char_p, [_I]),
     "vs_last_error": (ctypes.c_char_p, []),
     "vs_abi_version": (_I, []),

@@ -14,8 +14,8 @@ PKG = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(PKG)
 SRC = os.path.join(PKG, "csrc", "vimscan.hip")
 SRCS = [SRC] + [os.path.join(PKG, "csrc", f) for f in
-                ("proj.hip", "causal.hip", "causal_grad.hip", "beam.hip", "host.cpp",
-                 "host_causal.cpp")]
+                ("proj.hip", "causal.hip", "causal_grad.hip", "beam.hip", "gated.hip",
+                 "host.cpp", "host_causal.cpp", "host_model.cpp")]
 LIB = os.path.join(PKG, "libvimscan.so")
 INCLUDE = os.path.join(ROOT, "include")
 BINDING_SRC = os.path.join(PKG, "csrc", "binding.cpp")

@@ -1,5 +1,6 @@
 // binding.cpp -- the torch side of the causal mixer's and beam search's entry
-// points (causal.py and beam.py hold their names, defaults and documentation):
+// points and of those beside them (causal.py, beam.py and gated.py hold their
+// names, defaults and documentation):
 // checks of the arguments, allocation of the outputs and the call of the C
 // ABI. A single-token call's kernels take 2 to 6 us; checked argument by
 // argument in Python such a call cost the host 9 us.
@@ -32,7 +33,8 @@ namespace {
 #define VS_BOUND(X)                                                                                   \
     X(s6_workspace_bytes) X(s6_causal_conv) X(s6_causal_conv_grad) X(s6_conv_step) X(s6_causal_scan)  \
     X(s6_causal_scan_saved) X(s6_causal_scan_grad) X(s6_scan_step) X(beam_workspace_bytes)            \
-    X(beam_select) X(beam_reorder)
+    X(beam_select) X(beam_reorder)                                                                    \
+    X(gated_workspace_bytes) X(gated_scan) X(gated_scan_saved) X(gated_scan_grad) X(gated_scan_step)
 
 struct Abi {
 #define VS_MEMBER(f) decltype(&::f) f;
@@ -73,6 +75,15 @@ bool truth(PyObject* o) {
     const int r = PyObject_IsTrue(o);
     if (r < 0) throw python_error();
     return r != 0;
+}
+
+float number(const char* name, PyObject* o) {
+    const double v = PyFloat_AsDouble(o);
+    if (v == -1.0 && PyErr_Occurred()) {
+        PyErr_Clear();
+        raise(PyExc_TypeError, "%s must be a number, not %s", name, Py_TYPE(o)->tp_name);
+    }
+    return static_cast<float>(v);
 }
 
 void axes(const char* name, const at::Tensor& t, int64_t n) {
@@ -425,6 +436,107 @@ PyObject* scan_step(PyObject* const* a) {
     return wrap(y);
 }
 
+// ------------------------------------------------- gated linear recurrence
+// what the forms over prompts share: x, r, i, lam, z, lengths and rate
+struct GatedIn {
+    const at::Tensor &tx, &tr, &ti;
+    Maybe tz;
+    Call c;
+    int64_t batch, dim, L;
+    const void *x, *r, *i, *z;
+    const float* lam;
+    const int32_t* lengths;
+    float rate;
+
+    GatedIn(PyObject* const* a, PyObject* zed, PyObject* lens, PyObject* rt)
+        : tx(need("x", a[0])), tr(need("r", a[1])), ti(need("i", a[2])), tz(maybe("z", zed)), c("x", tx, 3), batch(tx.size(0)),
+          dim(tx.size(1)), L(tx.size(2)) {
+        x = c.input("x", &tx, {batch, dim, L});
+        r = c.input("r", &tr, {batch, dim, L});
+        i = c.input("i", &ti, {batch, dim, L});
+        z = c.input("z", tz, {batch, dim, L});
+        lam = c.dense<float>("lam", &need("lam", a[3]), {dim});
+        lengths = c.dense<int32_t>("lengths", maybe("lengths", lens), {batch});
+        rate = number("rate", rt);
+    }
+    size_t bytes(int op) const { return abi.gated_workspace_bytes(op, batch, dim, L); }
+};
+
+// x, r, i, lam, z, h0, lengths, rate, out, h_out[, saved]
+PyObject* gated_call(PyObject* const* a, bool saves) {
+    const GatedIn s(a, a[4], a[6], a[7]);
+    const Call& c = s.c;
+    const float* h0 = c.dense<float>("h0", maybe("h0", a[5]), {s.batch, s.dim});
+    const at::Tensor y = c.out("out", a[8], {s.batch, s.dim, s.L}, c.dt), h = c.out("h_out", a[9], {s.batch, s.dim}, at::kFloat);
+    const Strides st({&s.tx, &s.tr, &s.ti, s.tz});
+    if (!saves) {
+        run("gated_scan", c.dev, c.written, [&] {
+            return abi.gated_scan(s.batch, s.dim, s.L, c.dtype, s.x, s.r, s.i, s.z, st.p, s.lam, s.rate, h0, s.lengths, y.data_ptr(), f32(h),
+                                  c.stream());
+        });
+        return tuple({y, h});
+    }
+    const Buffer saved("saved", s.bytes(VS_GATED_SAVED), c, a[10]);
+    run("gated_scan_saved", c.dev, c.written, [&] {
+        return abi.gated_scan_saved(s.batch, s.dim, s.L, c.dtype, s.x, s.r, s.i, s.z, st.p, s.lam, s.rate, h0, s.lengths, y.data_ptr(),
+                                    f32(h), saved.p, saved.bytes, c.stream());
+    });
+    return tuple({y, h, saved.t});
+}
+PyObject* gated(PyObject* const* a) { return gated_call(a, false); }
+PyObject* gated_saved(PyObject* const* a) { return gated_call(a, true); }
+
+// x, r, i, lam, saved, dy, z, dh, h0, lengths, rate, workspace
+PyObject* gated_grad(PyObject* const* a) {
+    const GatedIn s(a, a[6], a[9], a[10]);
+    const Call& c = s.c;
+    const at::Tensor& tdy = need("dy", a[5]);
+    const void* dy = c.input("dy", &tdy, {s.batch, s.dim, s.L});
+    const float* dh = c.dense<float>("dh", maybe("dh", a[7]), {s.batch, s.dim});
+    const float* h0 = c.dense<float>("h0", maybe("h0", a[8]), {s.batch, s.dim});
+    need("saved", a[4]);
+    const Buffer saved("saved", s.bytes(VS_GATED_SAVED), c, a[4], false), ws("workspace", s.bytes(VS_GATED_GRAD), c, a[11]);
+    const auto act = [&] { return c.fresh({s.batch, s.dim, s.L}, c.dt); };
+    const at::Tensor dx = act(), dr = act(), di = act(), dlam = c.fresh({s.dim}, at::kFloat);
+    at::Tensor dz, dh0;
+    if (s.tz) dz = act();
+    if (h0) dh0 = c.fresh({s.batch, s.dim}, at::kFloat);
+    const Strides st({&s.tx, &s.tr, &s.ti, s.tz, &tdy});
+    run("gated_scan_grad", c.dev, c.written, [&] {
+        return abi.gated_scan_grad(s.batch, s.dim, s.L, c.dtype, s.x, s.r, s.i, s.z, dy, st.p, s.lam, s.rate, s.lengths, saved.p, saved.bytes,
+                                   dh, dx.data_ptr(), dr.data_ptr(), di.data_ptr(), at_or_null(dz), f32(dlam), f32(dh0), ws.p, ws.bytes,
+                                   c.stream());
+    });
+    return dict({{"dx", dx}, {"dr", dr}, {"di", di}, {"dz", dz}, {"dlam", dlam}, {"dh0", dh0}});
+}
+
+// x, r, i, lam, h, z, slot_in, slot_out, rate, out
+PyObject* gated_step(PyObject* const* a) {
+    const at::Tensor &x = need("x", a[0]), &r = need("r", a[1]), &i = need("i", a[2]), &lam = need("lam", a[3]), &h = need("h", a[4]);
+    Maybe z = maybe("z", a[5]);
+    const Call c("x", x, 2);
+    axes("h", h, 2);
+    const int64_t batch = x.size(0), dim = x.size(1), slots = h.size(0);
+    const void *xp = c.input("x", &x, {batch, dim}), *rp = c.input("r", &r, {batch, dim}), *ip = c.input("i", &i, {batch, dim});
+    const void* zp = c.input("z", z, {batch, dim});
+    const float* lp = c.dense<float>("lam", &lam, {dim});
+    float* hp = c.dense<float>("h", &h, {slots, dim});
+    c.written.add("h", &h);
+    const int32_t* si = c.dense<int32_t>("slot_in", maybe("slot_in", a[6]), {batch});
+    const int32_t* so = c.dense<int32_t>("slot_out", maybe("slot_out", a[7]), {batch});
+    const float rate = number("rate", a[8]);
+    const at::Tensor y = c.out("out", a[9], {batch, dim}, c.dt);
+    int64_t st[4] = {};                                      // one row has no stride
+    if (batch > 1) {
+        int k = 0;
+        for (Maybe t : {&x, &r, &i, z}) st[k++] = t ? t->stride(0) : 0;
+    }
+    run("gated_scan_step", c.dev, c.written, [&] {
+        return abi.gated_scan_step(batch, dim, c.dtype, xp, rp, ip, zp, st, lp, rate, hp, slots, si, so, y.data_ptr(), c.stream());
+    });
+    return wrap(y);
+}
+
 // ------------------------------------------------------------- beam search
 // logits, scores, done, eos, workspace, out[0], out[1], out[2]
 PyObject* select(PyObject* const* a) {
@@ -534,6 +646,8 @@ PyMethodDef methods[] = {
     method<conv, 8>("s6_causal_conv"), method<conv_grad, 9>("s6_causal_conv_grad"), method<conv_step, 8>("s6_conv_step"),
     method<scan, 14>("s6_causal_scan"), method<scan_saved, 15>("s6_causal_scan_saved"), method<scan_grad, 15>("s6_causal_scan_grad"),
     method<scan_step, 13>("s6_scan_step"), method<select, 8>("beam_select"), method<reorder, 3>("beam_reorder"),
+    method<gated, 10>("gated_scan"), method<gated_saved, 11>("gated_scan_saved"), method<gated_grad, 12>("gated_scan_grad"),
+    method<gated_step, 10>("gated_scan_step"),
     {nullptr, nullptr, 0, nullptr}};
 
 PyModuleDef module_def = {PyModuleDef_HEAD_INIT, "_binding", nullptr, -1, methods, nullptr, nullptr, nullptr, nullptr};

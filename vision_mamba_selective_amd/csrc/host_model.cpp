@@ -1,0 +1,133 @@
+// host_model.cpp -- argument validation, workspace layout and the choice of
+// form of the gated linear recurrence, the norm and the vocabulary loss. Plain
+// C++ with no HIP, like host.cpp.
+#include <cmath>
+#include <cstdint>
+#include <string>
+
+#include "vs_host.h"
+#include "vs_model.h"
+
+namespace vs {
+
+// ------------------------------------------------- gated linear recurrence
+namespace {
+
+const char* gated_problem(int64_t batch, int64_t dim, int64_t L, int& code) {
+    if (const char* p = sizes_problem(batch, dim, 1, L, 1, 1, code)) return p;
+    code = VS_ERR_UNSUPPORTED;
+    if (batch * dim > kMaxGroups) return "2^24 rows (batch x dim) or more are not supported";
+    return nullptr;
+}
+
+const char* rate_problem(float rate) {
+    return std::isfinite(rate) && rate >= 0 ? nullptr : "rate must be finite and >= 0";
+}
+
+}  // namespace
+
+GatedForm gated_form(int64_t batch, int64_t dim, int64_t L) {
+    const int64_t rows = batch * dim;
+    if (L <= 256) return {16, 1};
+    if (rows >= 2048 || L <= 1024) return {64, 1};
+    if (rows >= 512 || L <= 4096) return {64, 4};
+    return {64, 8};
+}
+
+size_t gated_ws_bytes(int op, int64_t batch, int64_t dim, int64_t L) {
+    int code;
+    if (gated_problem(batch, dim, L, code)) return 0;
+    const size_t rows = static_cast<size_t>(batch * dim);
+    if (op == VS_GATED_SAVED) return rows * static_cast<size_t>(ceil_div(L, gated_form(batch, dim, L).block())) * kF;
+    if (op == VS_GATED_GRAD) return rows * kF;           // per row: its part of dlam
+    return 0;
+}
+
+int prepare_gated(GatedCall& c) {
+    clear_error();
+    if (c.dtype != VS_F32 && c.dtype != VS_BF16) return fail(VS_ERR_DTYPE, "unknown dtype");
+    int code;
+    if (const char* p = gated_problem(c.batch, c.dim, c.L, code)) return fail(code, p);
+    if (const char* p = rate_problem(c.rate)) return fail(VS_ERR_UNSUPPORTED, p);
+    if (!c.x || !c.r || !c.i || !c.lam) return fail(VS_ERR_NULL, "x, r, i and lam must not be NULL");
+    if (c.grad) {
+        if (!c.dy || !c.dx || !c.dr || !c.di || !c.dlam) return fail(VS_ERR_NULL, "dy, dx, dr, di and dlam must not be NULL");
+        if (c.z && !c.dz) return fail(VS_ERR_NULL, "dz must not be NULL when z is given");
+        if (!c.z) c.dz = nullptr;
+    } else if (!c.y) {
+        return fail(VS_ERR_NULL, "y must not be NULL");
+    }
+    for (int k = 0; k < (c.grad ? 5 : 4); ++k) {
+        c.st[k] = c.strides ? Strides{c.strides[2 * k], c.strides[2 * k + 1]} : Strides{c.dim * c.L, c.L};
+        if (k == 3 && !c.z) { c.st[k] = Strides{0, 0}; continue; }
+        if (int rc = check_strides(c.st[k], c.batch)) return rc;
+    }
+    c.form = gated_form(c.batch, c.dim, c.L);
+    const size_t es = esize(c.dtype), act = static_cast<size_t>(c.batch * c.dim * c.L) * es;
+    const size_t states = static_cast<size_t>(c.batch * c.dim) * kF, par = static_cast<size_t>(c.dim) * kF;
+    const size_t saved = gated_ws_bytes(VS_GATED_SAVED, c.batch, c.dim, c.L);
+    const size_t ws = c.grad ? gated_ws_bytes(VS_GATED_GRAD, c.batch, c.dim, c.L) : 0;
+    if ((c.save || c.grad) && (!c.saved || c.saved_bytes < saved))
+        return fail(VS_ERR_WORKSPACE, "saved-state buffer missing or smaller than gated_workspace_bytes(VS_GATED_SAVED)");
+    if (ws > 0 && (!c.ws || c.ws_bytes < ws)) return fail(VS_ERR_WORKSPACE, "workspace missing or smaller than gated_workspace_bytes()");
+    auto span = [&](const void* p, int k) { return Span{p, p ? span_bytes(c.batch, c.dim, c.L, c.st[k], es) : 0}; };
+    const Span ins[] = {span(c.x, 0), span(c.r, 1), span(c.i, 2), span(c.z, 3), span(c.grad ? c.dy : nullptr, 4),
+                        {c.lam, par}, {c.h0, states}, {c.lengths, static_cast<size_t>(c.batch) * 4},
+                        {c.grad ? c.dh_out : nullptr, states}, {c.grad ? c.saved : nullptr, saved}};
+    if (int rc = check_aligned(ins, 5, es, "activation pointer misaligned")) return rc;
+    if (int rc = check_aligned(ins + 5, 5, 4, "32-bit pointer misaligned")) return rc;
+    if (!c.grad) {
+        const Span outs[] = {{c.y, act}, {c.h_out, states}, {c.save ? c.saved : nullptr, saved}};
+        if (int rc = check_aligned(outs, 1, es, "activation pointer misaligned")) return rc;
+        if (int rc = check_aligned(outs + 1, 2, 4, "32-bit pointer misaligned")) return rc;
+        return check_overlaps(ins, 10, outs, 3);
+    }
+    const Span outs[] = {{c.dx, act}, {c.dr, act}, {c.di, act}, {c.dz, act}, {c.dlam, par}, {c.dh0, states}, {c.ws, ws}};
+    if (int rc = check_aligned(outs, 4, es, "activation pointer misaligned")) return rc;
+    if (int rc = check_aligned(outs + 4, 3, 4, "32-bit pointer misaligned")) return rc;
+    return check_overlaps(ins, 10, outs, 7);
+}
+
+int prepare_gated_step(GatedStepCall& c) {
+    clear_error();
+    if (c.dtype != VS_F32 && c.dtype != VS_BF16) return fail(VS_ERR_DTYPE, "unknown dtype");
+    int code;
+    if (const char* p = sizes_problem(c.batch, c.dim, 1, 1, 1, 1, code)) return fail(code, p);
+    if (const char* p = rate_problem(c.rate)) return fail(VS_ERR_UNSUPPORTED, p);
+    if (c.slots < 1) return fail(VS_ERR_SHAPE, "the pool must have at least one slot");
+    if (c.slots >= (int64_t(1) << 31)) return fail(VS_ERR_UNSUPPORTED, "pools of 2^31 slots or more are not supported");
+    if (c.batch * ceil_div(c.dim, 4) > kMaxGroups * 256)
+        return fail(VS_ERR_UNSUPPORTED, "a step of 2^34 channels or more is not supported");
+    if (!c.x || !c.r || !c.i || !c.lam || !c.h || !c.y) return fail(VS_ERR_NULL, "x, r, i, lam, h and y must not be NULL");
+    if ((!c.slot_in || !c.slot_out) && c.slots < c.batch)
+        return fail(VS_ERR_SHAPE, "without slot_in or slot_out the pool needs a slot for every row");
+    for (int k = 0; k < 4; ++k) {
+        c.st[k] = c.strides ? c.strides[k] : c.dim;
+        if (c.st[k] < 0) return fail(VS_ERR_SHAPE, "strides must be >= 0");
+        if (c.st[k] >= (int64_t(1) << 28)) return fail(VS_ERR_UNSUPPORTED, "row strides of 2^28 elements or more are not supported");
+    }
+    const size_t es = esize(c.dtype);
+    auto span = [&](const void* p, int k) {
+        return Span{p, p ? (static_cast<size_t>((c.batch - 1) * c.st[k]) + static_cast<size_t>(c.dim)) * es : 0};
+    };
+    const size_t idx = static_cast<size_t>(c.batch) * 4;
+    const Span ins[] = {span(c.x, 0), span(c.r, 1), span(c.i, 2), span(c.z, 3),
+                        {c.lam, static_cast<size_t>(c.dim) * kF}, {c.slot_in, idx}, {c.slot_out, idx}};
+    const Span outs[] = {{c.y, static_cast<size_t>(c.batch * c.dim) * es}, {c.h, static_cast<size_t>(c.slots * c.dim) * kF}};
+    if (int rc = check_aligned(ins, 4, es, "activation pointer misaligned")) return rc;
+    if (int rc = check_aligned(ins + 4, 3, 4, "32-bit pointer misaligned")) return rc;
+    if (int rc = check_aligned(outs, 1, es, "activation pointer misaligned")) return rc;
+    if (int rc = check_aligned(outs + 1, 1, 4, "state pointer misaligned")) return rc;
+    return check_overlaps(ins, 7, outs, 2);
+}
+
+}  // namespace vs
+
+// ---------------------------------------------------------------- C ABI
+extern "C" {
+
+size_t gated_workspace_bytes(int op, int64_t batch, int64_t dim, int64_t seqlen) {
+    return vs::gated_ws_bytes(op, batch, dim, seqlen);
+}
+
+}  // extern "C"

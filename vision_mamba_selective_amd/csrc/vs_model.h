@@ -1,0 +1,65 @@
+// Argument records, workspace layouts and choices of form of the gated linear
+// recurrence, the norm and the vocabulary loss. Filled and checked by
+// host_model.cpp (plain C++, no HIP); read by the kernel files. Internal to
+// libvimscan.so.
+#pragma once
+
+#include "vs_internal.h"
+
+namespace __attribute__((visibility("hidden"))) vs {
+
+// ---- the gated linear recurrence (gated.hip)
+constexpr int kGatedVec = 8;                        // consecutive tokens of one lane
+// A row is taken by `lanes` lanes of a wave (16 or 64) or by `waves` whole
+// waves (1, 4 or 8), each lane eight tokens at a time; a state is saved for
+// every `block` tokens of a row.
+struct GatedForm {
+    int lanes, waves;
+    int block() const { return kGatedVec * lanes; }
+};
+GatedForm gated_form(int64_t batch, int64_t dim, int64_t L);
+size_t gated_ws_bytes(int op, int64_t batch, int64_t dim, int64_t L);
+
+struct GatedCall {
+    int64_t batch, dim, L;
+    int dtype;
+    const void *x, *r, *i, *z, *dy;
+    const int64_t* strides;                          // as the caller gave them (may be NULL)
+    const float* lam;
+    float rate;
+    const float* h0;
+    const int32_t* lengths;
+    void* y;
+    float* h_out;
+    void* saved;
+    size_t saved_bytes;
+    void* stream;
+    // gradient
+    const float* dh_out;
+    void *dx, *dr, *di, *dz;
+    float *dlam, *dh0;
+    void* ws;
+    size_t ws_bytes;
+    bool save = false, grad = false;
+    Strides st[5];                                   // x, r, i, z, dy
+    GatedForm form;
+};
+int prepare_gated(GatedCall& c);
+
+struct GatedStepCall {
+    int64_t batch, dim;
+    int dtype;
+    const void *x, *r, *i, *z;
+    const int64_t* strides;
+    const float* lam;
+    float rate;
+    float* h;
+    int64_t slots;
+    const int32_t *slot_in, *slot_out;
+    void* y;
+    void* stream;
+    int64_t st[4];
+};
+int prepare_gated_step(GatedStepCall& c);
+
+}  // namespace vs
