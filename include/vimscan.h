@@ -647,6 +647,45 @@ int gated_scan_step(int64_t batch, int64_t dim, int dtype, const void* x, const 
                     float rate, float* h, int64_t slots, const int32_t* slot_in,
                     const int32_t* slot_out, void* y, void* stream);
 
+/*
+ * ---- The norm between the mixers
+ *
+ * Root-mean-square norm over the channels of each token, with the addition of
+ * the residual stream before it:
+ *   s = x + residual, rounded to dtype (s = x without a residual)
+ *   y = s / sqrt(mean_d s^2 + eps) w
+ *   strides     x, residual (batch and channel strides as for the causal
+ *               mixer, any token stride 1 tensor; NULL: contiguous)
+ *   x, residual, y, sum [batch][dim][L], dtype; residual and sum are both NULL
+ *               or both given, and sum may be the residual itself (in place)
+ *   w           [dim] fp32 or NULL for ones
+ *   lengths     as for the causal mixer: y and sum are zero at padding
+ * L = 1 with channel stride 1 is one row of channels for each token, and
+ * takes a form of its own. dim is at most 8192, eps finite and >= 0, batch x
+ * ceil(L / 32) below 2^24. Sums are fp32. Outputs may overlap nothing else.
+ */
+int rms_norm(int64_t batch, int64_t dim, int64_t seqlen, int dtype, const void* x,
+             const void* residual, const int64_t* strides, const float* w, float eps,
+             const int32_t* lengths, void* y, void* sum, void* stream);
+
+/* Bytes of rms_norm_grad's workspace; 0 for sizes it refuses. */
+size_t norm_workspace_bytes(int64_t batch, int64_t dim, int64_t seqlen);
+
+/*
+ * Gradient of rms_norm at the sum s.
+ *   strides     s, dy, dsum
+ *   s, dy       [batch][dim][L]; dsum, dL/dsum from elsewhere, or NULL
+ *   ds          [batch][dim][L], the gradient of x and of the residual alike;
+ *               zero at padding
+ *   dw          [dim] fp32 or NULL, summed over tokens in a fixed order: it
+ *               repeats bit for bit
+ *   workspace   norm_workspace_bytes(batch, dim, seqlen), where dw is given
+ */
+int rms_norm_grad(int64_t batch, int64_t dim, int64_t seqlen, int dtype, const void* s,
+                  const void* dy, const void* dsum, const int64_t* strides, const float* w,
+                  float eps, const int32_t* lengths, void* ds, float* dw, void* workspace,
+                  size_t workspace_bytes, void* stream);
+
 /* Static name of a status code ("VS_OK", ...). Never NULL. */
 const char* vs_strerror(int status);
 

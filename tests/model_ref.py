@@ -25,3 +25,17 @@ def gated(x, r, i, lam, z, h0, lengths, rate=8.0):
         ys.append(torch.cat([y, torch.zeros(dim, L - n, dtype=F64)], dim=1))
         hs.append(h)
     return torch.stack(ys), torch.stack(hs)
+
+
+def norm(x, w, residual, lengths, eps, dtype):
+    """(y, s) of [batch, dim, L]; s is rounded to dtype, which a gradient passes unchanged."""
+    s = x if residual is None else x + residual
+    s = s + (s.detach().to(dtype).to(F64) - s.detach())
+    live = torch.zeros(x.shape[0], 1, x.shape[2], dtype=F64)
+    for b, n in enumerate(row_lengths(lengths, x.shape[0], x.shape[2])):
+        live[b, :, :n] = 1
+    s = s * live
+    y = s / torch.sqrt(s.square().mean(1, keepdim=True) + eps)
+    if w is not None:
+        y = y * w[:, None]
+    return y * live, s

@@ -21,7 +21,8 @@ _CAUSAL = ["s6_workspace_bytes", "s6_causal_conv", "s6_causal_conv_grad", "s6_co
 _BEAM = ["beam_select", "beam_reorder", "beam_workspace_bytes"]
 _GATED = ["gated_workspace_bytes", "gated_scan", "gated_scan_saved", "gated_scan_grad", "gated_scan_step",
           "GatedScanFunction", "gated_scan_autograd"]
-__all__ += _CAUSAL + _BEAM + _GATED
+_NORM = ["rms_norm", "rms_norm_grad", "norm_workspace_bytes", "RmsNormFunction", "rms_norm_autograd"]
+__all__ += _CAUSAL + _BEAM + _GATED + _NORM
 
 
 def __getattr__(name):
@@ -31,6 +32,8 @@ def __getattr__(name):
         from . import beam as module
     elif name in _GATED:
         from . import gated as module
+    elif name in _NORM:
+        from . import norm as module
     elif name in __all__:
         from . import scan as module
     else:

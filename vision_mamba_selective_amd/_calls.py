@@ -41,3 +41,5 @@ gated_scan = _binding.gated_scan
 gated_scan_saved = _binding.gated_scan_saved
 gated_scan_grad = _binding.gated_scan_grad
 gated_scan_step = _binding.gated_scan_step
+rms_norm = _binding.rms_norm
+rms_norm_grad = _binding.rms_norm_grad

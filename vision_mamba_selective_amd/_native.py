@@ -70,6 +70,9 @@ SIGNATURES = {
     "gated_scan_saved": (_I, [_I64, _I64, _I64, _I] + [_P] * 6 + [_F] + [_P] * 5 + [_SZ, _P]),
     "gated_scan_grad": (_I, [_I64, _I64, _I64, _I] + [_P] * 7 + [_F, _P, _P, _SZ] + [_P] * 8 + [_SZ, _P]),
     "gated_scan_step": (_I, [_I64, _I64, _I] + [_P] * 6 + [_F, _P, _I64] + [_P] * 4),
+    "norm_workspace_bytes": (_SZ, [_I64, _I64, _I64]),
+    "rms_norm": (_I, [_I64, _I64, _I64, _I] + [_P] * 4 + [_F] + [_P] * 4),
+    "rms_norm_grad": (_I, [_I64, _I64, _I64, _I] + [_P] * 5 + [_F] + [_P] * 4 + [_SZ, _P]),
     "vs_strerror": (ctypes.c_char_p, [_I]),
     "vs_last_error": (ctypes.c_char_p, []),
     "vs_abi_version": (_I, []),

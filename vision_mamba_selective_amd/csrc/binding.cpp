@@ -1,6 +1,6 @@
 // binding.cpp -- the torch side of the causal mixer's and beam search's entry
-// points and of those beside them (causal.py, beam.py and gated.py hold their
-// names, defaults and documentation):
+// points and of those beside them (causal.py, beam.py, gated.py and norm.py hold
+// their names, defaults and documentation):
 // checks of the arguments, allocation of the outputs and the call of the C
 // ABI. A single-token call's kernels take 2 to 6 us; checked argument by
 // argument in Python such a call cost the host 9 us.
@@ -34,7 +34,8 @@ namespace {
     X(s6_workspace_bytes) X(s6_causal_conv) X(s6_causal_conv_grad) X(s6_conv_step) X(s6_causal_scan)  \
     X(s6_causal_scan_saved) X(s6_causal_scan_grad) X(s6_scan_step) X(beam_workspace_bytes)            \
     X(beam_select) X(beam_reorder)                                                                    \
-    X(gated_workspace_bytes) X(gated_scan) X(gated_scan_saved) X(gated_scan_grad) X(gated_scan_step)
+    X(gated_workspace_bytes) X(gated_scan) X(gated_scan_saved) X(gated_scan_grad) X(gated_scan_step)   \
+    X(norm_workspace_bytes) X(rms_norm) X(rms_norm_grad)
 
 struct Abi {
 #define VS_MEMBER(f) decltype(&::f) f;
@@ -537,6 +538,69 @@ PyObject* gated_step(PyObject* const* a) {
     return wrap(y);
 }
 
+// -------------------------------------------------------------------- norm
+// A row form [rows, dim] is the channel-major form's [rows, dim, 1] with
+// channel stride 1.
+struct NormIn {
+    Call c;
+    int64_t batch, dim, L;
+    bool rows;
+    int64_t st[6];
+
+    NormIn(const char* name, const at::Tensor& t) : c(name, t, t.dim() == 2 ? 2 : 3), batch(t.size(0)), dim(t.size(1)), L(t.dim() == 2 ? 1 : t.size(2)), rows(t.dim() == 2) {}
+    const void* input(const char* name, Maybe t, int k) {
+        st[2 * k] = st[2 * k + 1] = 0;
+        if (!t) return nullptr;
+        const void* p = rows ? c.input(name, t, {batch, dim}) : c.input(name, t, {batch, dim, L});
+        st[2 * k] = batch > 1 ? t->stride(0) : 0;
+        st[2 * k + 1] = dim > 1 ? t->stride(1) : 1;
+        return p;
+    }
+    at::Tensor out(const char* name, PyObject* given) const {
+        return rows ? c.out(name, given, {batch, dim}, c.dt) : c.out(name, given, {batch, dim, L}, c.dt);
+    }
+    const float* weight(PyObject* o) const { return c.dense<float>("w", maybe("w", o), {dim}); }
+    const int32_t* lengths(PyObject* o) const { return c.dense<int32_t>("lengths", maybe("lengths", o), {batch}); }
+};
+
+// x, w, residual, eps, lengths, out, sum_out
+PyObject* norm(PyObject* const* a) {
+    const at::Tensor& x = need("x", a[0]);
+    NormIn n("x", x);
+    Maybe res = maybe("residual", a[2]);
+    const void *xp = n.input("x", &x, 0), *rp = n.input("residual", res, 1);
+    const float* w = n.weight(a[1]);
+    const float eps = number("eps", a[3]);
+    const int32_t* len = n.lengths(a[4]);
+    const at::Tensor y = n.out("out", a[5]);
+    at::Tensor sum;
+    if (res) sum = n.out("sum_out", a[6]);
+    else if (a[6] != Py_None) raise(PyExc_ValueError, "sum_out needs a residual");
+    run("rms_norm", n.c.dev, n.c.written, [&] {
+        return abi.rms_norm(n.batch, n.dim, n.L, n.c.dtype, xp, rp, n.st, w, eps, len, y.data_ptr(), at_or_null(sum), n.c.stream());
+    });
+    return tuple({y, sum});
+}
+
+// s, w, dy, dsum, eps, lengths, workspace
+PyObject* norm_grad(PyObject* const* a) {
+    const at::Tensor &s = need("s", a[0]), &dy = need("dy", a[2]);
+    NormIn n("s", s);
+    const void *sp = n.input("s", &s, 0), *yp = n.input("dy", &dy, 1), *dp = n.input("dsum", maybe("dsum", a[3]), 2);
+    const float* w = n.weight(a[1]);
+    const float eps = number("eps", a[4]);
+    const int32_t* len = n.lengths(a[5]);
+    const at::Tensor ds = n.out("ds", Py_None);
+    at::Tensor dw;
+    if (w) dw = n.c.fresh({n.dim}, at::kFloat);
+    const Buffer ws("workspace", w ? abi.norm_workspace_bytes(n.batch, n.dim, n.L) : 0, n.c, a[6]);
+    run("rms_norm_grad", n.c.dev, n.c.written, [&] {
+        return abi.rms_norm_grad(n.batch, n.dim, n.L, n.c.dtype, sp, yp, dp, n.st, w, eps, len, ds.data_ptr(), f32(dw), ws.p, ws.bytes,
+                                 n.c.stream());
+    });
+    return dict({{"dx", ds}, {"dw", dw}});
+}
+
 // ------------------------------------------------------------- beam search
 // logits, scores, done, eos, workspace, out[0], out[1], out[2]
 PyObject* select(PyObject* const* a) {
@@ -647,7 +711,7 @@ PyMethodDef methods[] = {
     method<scan, 14>("s6_causal_scan"), method<scan_saved, 15>("s6_causal_scan_saved"), method<scan_grad, 15>("s6_causal_scan_grad"),
     method<scan_step, 13>("s6_scan_step"), method<select, 8>("beam_select"), method<reorder, 3>("beam_reorder"),
     method<gated, 10>("gated_scan"), method<gated_saved, 11>("gated_scan_saved"), method<gated_grad, 12>("gated_scan_grad"),
-    method<gated_step, 10>("gated_scan_step"),
+    method<gated_step, 10>("gated_scan_step"), method<norm, 7>("rms_norm"), method<norm_grad, 7>("rms_norm_grad"),
     {nullptr, nullptr, 0, nullptr}};
 
 PyModuleDef module_def = {PyModuleDef_HEAD_INIT, "_binding", nullptr, -1, methods, nullptr, nullptr, nullptr, nullptr};

@@ -121,6 +121,76 @@ int prepare_gated_step(GatedStepCall& c) {
     return check_overlaps(ins, 7, outs, 2);
 }
 
+// -------------------------------------------------------------------- norm
+namespace {
+
+const char* norm_problem(int64_t batch, int64_t dim, int64_t L, int& code) {
+    code = VS_ERR_SHAPE;
+    if (batch < 1 || dim < 1 || L < 1) return "batch, dim and the sequence length must be >= 1";
+    code = VS_ERR_UNSUPPORTED;
+    if (dim > kNormMaxDim) return "dim above 8192 is not supported";
+    if (L >= kCausalMaxL) return "sequences of 2^27 tokens or more are not supported";
+    if (batch >= (int64_t(1) << 31) || batch * ceil_div(L, kNormTile) >= kMaxGroups)
+        return "2^24 rows or tiles of 32 tokens or more are not supported";
+    if (!product_below(batch, dim, L, int64_t(1) << 40)) return "outputs of 2^40 elements or more are not supported";
+    return nullptr;
+}
+
+NormForm norm_rows(int64_t dim, int dtype) {
+    const int64_t lanes = dtype == VS_BF16 ? 8 : 4;     // entries of 16 bytes
+    if (dim <= 64 * lanes) return kNormRow1;
+    if (dim <= 256 * lanes) return kNormRow4;
+    return kNormRow16;
+}
+
+// lines of dw's sums: one for each tile, or for each wave or workgroup that takes rows
+int64_t norm_parts(NormForm f, int64_t batch, int64_t L) {
+    if (f == kNormColumn) return batch * ceil_div(L, kNormTile);
+    const int64_t per = f == kNormRow1 ? 4 : 1, groups = ceil_div(batch, per);
+    return (groups < 512 ? groups : 512) * per;
+}
+
+}  // namespace
+
+int prepare_norm(NormCall& c) {
+    clear_error();
+    if (c.dtype != VS_F32 && c.dtype != VS_BF16) return fail(VS_ERR_DTYPE, "unknown dtype");
+    int code;
+    if (const char* p = norm_problem(c.batch, c.dim, c.L, code)) return fail(code, p);
+    if (!(std::isfinite(c.eps) && c.eps >= 0)) return fail(VS_ERR_UNSUPPORTED, "eps must be finite and >= 0");
+    if (!c.x || !c.y) return fail(VS_ERR_NULL, c.grad ? "s and ds must not be NULL" : "x and y must not be NULL");
+    if (c.grad && !c.dy) return fail(VS_ERR_NULL, "dy must not be NULL");
+    if (!c.grad && !c.residual != !c.sum) return fail(VS_ERR_NULL, "residual and sum must be given together");
+    const void* second = c.grad ? c.dy : c.residual;
+    const void* ins[] = {c.x, second, c.grad ? c.dsum : nullptr};
+    bool rows = c.L == 1;
+    for (int k = 0; k < (c.grad ? 3 : 2); ++k) {
+        c.st[k] = c.strides ? Strides{c.strides[2 * k], c.strides[2 * k + 1]} : Strides{c.dim * c.L, c.L};
+        if (!ins[k]) { c.st[k] = Strides{0, 0}; continue; }
+        if (int rc = check_strides(c.st[k], c.batch)) return rc;
+        rows = rows && (c.st[k].d == 1 || c.dim == 1);
+    }
+    c.form = rows ? norm_rows(c.dim, c.dtype) : kNormColumn;
+    c.parts = norm_parts(c.form, c.batch, c.L);
+    const size_t es = esize(c.dtype), act = static_cast<size_t>(c.batch * c.dim * c.L) * es;
+    const size_t par = static_cast<size_t>(c.dim) * kF, ws = c.dw ? static_cast<size_t>(c.parts) * par : 0;
+    if (ws > 0 && (!c.ws || c.ws_bytes < ws)) return fail(VS_ERR_WORKSPACE, "workspace missing or smaller than norm_workspace_bytes()");
+    auto span = [&](int k) { return Span{ins[k], ins[k] ? span_bytes(c.batch, c.dim, c.L, c.st[k], es) : 0}; };
+    // the sum may be the residual itself
+    const bool inplace = !c.grad && c.sum && c.sum == c.residual && c.st[1].d == c.L && (c.st[1].b == c.dim * c.L || c.batch == 1);
+    const Span in[] = {span(0), span(1), span(2), {c.w, par}, {c.lengths, static_cast<size_t>(c.batch) * 4}};
+    const Span out[] = {{c.y, act}, {c.grad ? nullptr : c.sum, act}, {c.dw, par}, {c.dw ? c.ws : nullptr, ws}};
+    if (int rc = check_aligned(in, 3, es, "activation pointer misaligned")) return rc;
+    if (int rc = check_aligned(in + 3, 2, 4, "32-bit pointer misaligned")) return rc;
+    if (int rc = check_aligned(out, 2, es, "activation pointer misaligned")) return rc;
+    if (int rc = check_aligned(out + 2, 2, 4, "32-bit pointer misaligned")) return rc;
+    if (!inplace) return check_overlaps(in, 5, out, 4);
+    // all but the sum against its residual
+    const Span apart[] = {in[0], in[3], in[4]};
+    if (int rc = check_overlaps(apart, 3, out, 4)) return rc;
+    return check_overlaps(in + 1, 1, out, 1);
+}
+
 }  // namespace vs
 
 // ---------------------------------------------------------------- C ABI
@@ -128,6 +198,18 @@ extern "C" {
 
 size_t gated_workspace_bytes(int op, int64_t batch, int64_t dim, int64_t seqlen) {
     return vs::gated_ws_bytes(op, batch, dim, seqlen);
+}
+
+size_t norm_workspace_bytes(int64_t batch, int64_t dim, int64_t seqlen) {
+    int code;
+    if (vs::norm_problem(batch, dim, seqlen, code)) return 0;
+    // whichever form the strides and the type lead to
+    int64_t parts = vs::norm_parts(vs::kNormColumn, batch, seqlen);
+    if (seqlen == 1) {
+        const int64_t rows = vs::norm_parts(vs::kNormRow1, batch, 1);
+        parts = parts > rows ? parts : rows;
+    }
+    return static_cast<size_t>(parts * dim) * vs::kF;
 }
 
 }  // extern "C"

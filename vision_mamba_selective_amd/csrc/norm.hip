@@ -1,0 +1,516 @@
+// norm.hip -- the root-mean-square norm with the residual's addition,
+//     s = x + residual (rounded to the activations' type), q = 1 / sqrt(mean_d s^2 + eps),
+//     y = s q w
+// and its gradient
+//     ds = dsum + q (w dy) - s q^3 mean_d(w dy s),  dw = sum over tokens of dy s q
+// for channel-major prompts [batch][dim][L] and for rows [tokens][dim].
+//
+// Channel-major: a workgroup takes 32 tokens and all channels. A lane holds 16
+// bytes of tokens of one channel, a wave 16 channels (8 in fp32), and a sweep of
+// the workgroup 128 (64); the sweeps' s stay in registers between the sum of
+// squares and the scaling, so that every input is read once. Rows: a wave or a
+// workgroup takes a row, in the same way.
+//
+// dw is summed in a fixed order: per tile of 32 tokens (or per workgroup, which
+// takes every n-th row) into the workspace, then over those.
+#include <hip/hip_runtime.h>
+
+#include <cstdint>
+
+#include "vimscan.h"
+#include "vs_device.h"
+#include "vs_model.h"
+
+namespace {
+
+// 16 bytes of consecutive entries, kept as loaded; rows start at any element
+template <typename T>
+struct Pack {
+    static constexpr int N = 16 / static_cast<int>(sizeof(T));
+    uint32_t v[4];
+    __device__ __forceinline__ void load(const T* p) { __builtin_memcpy(v, p, 16); }
+    // entries of p whose index, from first on, is below n; zeros for the others
+    __device__ __forceinline__ void load(const T* p, int first, int n) {
+        if (first + N <= n) return load(p + first);
+        float f[N];
+#pragma unroll
+        for (int i = 0; i < N; ++i) f[i] = first + i < n ? ld(p, first + i) : 0.f;
+        set(f);
+    }
+    __device__ __forceinline__ float get(int i) const {
+        if constexpr (sizeof(T) == 2) return __uint_as_float(i & 1 ? v[i / 2] & 0xffff0000u : v[i / 2] << 16);
+        else return __uint_as_float(v[i]);
+    }
+    // rounds to nearest even
+    __device__ __forceinline__ void set(const float (&f)[N]) {
+        if constexpr (sizeof(T) == 2) {
+            typedef __bf16 Vec8 __attribute__((ext_vector_type(8)));
+            const Vec8 b = {static_cast<__bf16>(f[0]), static_cast<__bf16>(f[1]), static_cast<__bf16>(f[2]), static_cast<__bf16>(f[3]),
+                            static_cast<__bf16>(f[4]), static_cast<__bf16>(f[5]), static_cast<__bf16>(f[6]), static_cast<__bf16>(f[7])};
+            __builtin_memcpy(v, &b, 16);
+        } else {
+            __builtin_memcpy(v, f, 16);
+        }
+    }
+    __device__ __forceinline__ void store(T* p, int first, int n) const {
+        if (first + N <= n) {
+            __builtin_memcpy(p + first, v, 16);
+        } else {
+#pragma unroll
+            for (int i = 0; i < N; ++i)
+                if (first + i < n) st(p, first + i, get(i));
+        }
+    }
+};
+
+// weights first .. first + N - 1, ones without weights and past the last
+template <int N>
+__device__ __forceinline__ void weights(const float* w, int first, int n, float (&f)[N]) {
+    if (w && first + N <= n) {
+        __builtin_memcpy(f, w + first, sizeof(f));
+    } else {
+#pragma unroll
+        for (int i = 0; i < N; ++i) f[i] = w && first + i < n ? w[first + i] : 1.f;
+    }
+}
+
+struct NormArgs {
+    const void *x, *res, *dy, *dsum;        // gradient: x is s
+    vs::Strides sx, sres, sdy, sdsum;
+    const float* w;
+    float eps, inv_dim;
+    const int32_t* lengths;
+    void *y, *sum;                          // gradient: y is ds
+    float *part, *dw;
+    int64_t rows;                           // the batch
+    int dim, L, tiles;                      // tiles of a batch row
+    int parts;
+};
+
+template <typename T>
+__device__ __forceinline__ const T* at(const void* p, int64_t off) { return static_cast<const T*>(p) + off; }
+
+// ------------------------------------------------------------ channel-major
+constexpr int kTile = vs::kNormTile;         // tokens
+constexpr int kColWaves = 8;
+
+template <typename T>
+struct Column {
+    static constexpr int N = Pack<T>::N, kTl = kTile / N, kCh = 64 / kTl;
+    static constexpr int kSweep = kCh * kColWaves;      // channels of a sweep
+    int lane, wave, t, ch, len;
+    int64_t b;
+    uint32_t tile;
+    __device__ __forceinline__ explicit Column(const NormArgs& a) {
+        // neighbouring tiles share the lines at their border: contiguous ranges of tiles to each XCD
+        uint32_t zero;
+        xcd_block(tile, zero);
+        b = tile / a.tiles;
+        lane = threadIdx.x & 63;
+        wave = threadIdx.x >> 6;
+        t = static_cast<int>(tile - b * a.tiles) * kTile + lane % kTl * N;
+        ch = wave * kCh + lane / kTl;
+        len = a.lengths ? min(max(a.lengths[b], 0), a.L) : a.L;
+    }
+};
+
+// sums over the workgroup's channels of each lane's tokens
+template <typename T>
+__device__ __forceinline__ void column_sum(const Column<T>& c, float (&v)[Pack<T>::N], float (*red)[kTile]) {
+    constexpr int N = Pack<T>::N, kTl = Column<T>::kTl;
+#pragma unroll
+    for (int o = kTl; o < 64; o *= 2)
+#pragma unroll
+        for (int i = 0; i < N; ++i) v[i] += __shfl_xor(v[i], o, 64);
+    if (c.lane < kTl) {
+#pragma unroll
+        for (int i = 0; i < N; ++i) red[c.wave][c.lane * N + i] = v[i];
+    }
+    __syncthreads();
+#pragma unroll
+    for (int i = 0; i < N; ++i) v[i] = 0.f;
+#pragma unroll
+    for (int o = 0; o < kColWaves; ++o)
+#pragma unroll
+        for (int i = 0; i < N; ++i) v[i] += red[o][c.lane % kTl * N + i];
+}
+
+template <typename T, int HOLD, bool ADD>
+__global__ __launch_bounds__(64 * kColWaves) void norm_column_kernel(const NormArgs a) {
+    constexpr int N = Pack<T>::N;
+    __shared__ float red[kColWaves][kTile];
+    const Column<T> c(a);
+    const T* x = at<T>(a.x, c.b * a.sx.b);
+    const T* res = ADD ? at<T>(a.res, c.b * a.sres.b) : nullptr;
+    const int64_t base = c.b * a.dim * static_cast<int64_t>(a.L);
+    T *y = static_cast<T*>(a.y) + base, *sum = ADD ? static_cast<T*>(a.sum) + base : nullptr;
+    Pack<T> held[HOLD];
+    float ss[N];
+#pragma unroll
+    for (int i = 0; i < N; ++i) ss[i] = 0.f;
+    auto take = [&](int ch, Pack<T>& s) VS_INLINE {
+        s.load(x + ch * a.sx.d, c.t, c.len);
+        if constexpr (ADD) {
+            Pack<T> r;
+            r.load(res + ch * a.sres.d, c.t, c.len);
+            float f[N];
+#pragma unroll
+            for (int i = 0; i < N; ++i) f[i] = s.get(i) + r.get(i);
+            s.set(f);
+            s.store(sum + static_cast<int64_t>(ch) * a.L, c.t, a.L);
+        }
+#pragma unroll
+        for (int i = 0; i < N; ++i) ss[i] = fmaf(s.get(i), s.get(i), ss[i]);
+    };
+#pragma unroll
+    for (int k = 0; k < HOLD; ++k) {
+        const int ch = c.ch + k * Column<T>::kSweep;
+        if (ch < a.dim) take(ch, held[k]);
+    }
+    for (int ch = c.ch + HOLD * Column<T>::kSweep; ch < a.dim; ch += Column<T>::kSweep) {
+        Pack<T> s;
+        take(ch, s);
+    }
+    column_sum(c, ss, red);
+    float q[N];
+#pragma unroll
+    for (int i = 0; i < N; ++i) q[i] = __builtin_amdgcn_rsqf(fmaf(ss[i], a.inv_dim, a.eps));
+    auto put = [&](int ch, const Pack<T>& s) VS_INLINE {
+        const float w = a.w ? a.w[ch] : 1.f;
+        float f[N];
+#pragma unroll
+        for (int i = 0; i < N; ++i) f[i] = c.t + i < c.len ? s.get(i) * q[i] * w : 0.f;
+        Pack<T> o;
+        o.set(f);
+        o.store(y + static_cast<int64_t>(ch) * a.L, c.t, a.L);
+    };
+#pragma unroll
+    for (int k = 0; k < HOLD; ++k) {
+        const int ch = c.ch + k * Column<T>::kSweep;
+        if (ch < a.dim) put(ch, held[k]);
+    }
+    // channels past what is held: read again (the lane's own entries of the sum, or x)
+    for (int ch = c.ch + HOLD * Column<T>::kSweep; ch < a.dim; ch += Column<T>::kSweep) {
+        Pack<T> s;
+        if constexpr (ADD) s.load(sum + static_cast<int64_t>(ch) * a.L, c.t, c.len);
+        else s.load(x + ch * a.sx.d, c.t, c.len);
+        put(ch, s);
+    }
+}
+
+template <typename T, int HOLD>
+__global__ __launch_bounds__(64 * kColWaves) void norm_column_grad_kernel(const NormArgs a) {
+    constexpr int N = Pack<T>::N, kTl = Column<T>::kTl;
+    __shared__ float red[2][kColWaves][kTile];
+    const Column<T> c(a);
+    const T *s = at<T>(a.x, c.b * a.sx.b), *dy = at<T>(a.dy, c.b * a.sdy.b);
+    const T* dsum = a.dsum ? at<T>(a.dsum, c.b * a.sdsum.b) : nullptr;
+    T* ds = static_cast<T*>(a.y) + c.b * a.dim * static_cast<int64_t>(a.L);
+    float* part = a.part ? a.part + static_cast<size_t>(c.tile) * a.dim : nullptr;
+    Pack<T> hs[HOLD], hy[HOLD];
+    float ss[N], sd[N];
+#pragma unroll
+    for (int i = 0; i < N; ++i) ss[i] = sd[i] = 0.f;
+    auto take = [&](int ch, Pack<T>& ps, Pack<T>& py) VS_INLINE {
+        ps.load(s + ch * a.sx.d, c.t, c.len);
+        py.load(dy + ch * a.sdy.d, c.t, c.len);
+        const float w = a.w ? a.w[ch] : 1.f;
+#pragma unroll
+        for (int i = 0; i < N; ++i) {
+            ss[i] = fmaf(ps.get(i), ps.get(i), ss[i]);
+            sd[i] = fmaf(w * py.get(i), ps.get(i), sd[i]);
+        }
+    };
+#pragma unroll
+    for (int k = 0; k < HOLD; ++k) {
+        const int ch = c.ch + k * Column<T>::kSweep;
+        if (ch < a.dim) take(ch, hs[k], hy[k]);
+    }
+    for (int ch = c.ch + HOLD * Column<T>::kSweep; ch < a.dim; ch += Column<T>::kSweep) {
+        Pack<T> ps, py;
+        take(ch, ps, py);
+    }
+    column_sum(c, ss, red[0]);
+    column_sum(c, sd, red[1]);
+    float q[N], m[N];
+#pragma unroll
+    for (int i = 0; i < N; ++i) {
+        q[i] = __builtin_amdgcn_rsqf(fmaf(ss[i], a.inv_dim, a.eps));
+        m[i] = q[i] * q[i] * (sd[i] * a.inv_dim);
+    }
+    auto put = [&](int ch, const Pack<T>& ps, const Pack<T>& py) VS_INLINE {
+        const float w = a.w ? a.w[ch] : 1.f;
+        Pack<T> g;
+        if (dsum) g.load(dsum + ch * a.sdsum.d, c.t, c.len);
+        float f[N], dw = 0.f;
+#pragma unroll
+        for (int i = 0; i < N; ++i) {
+            const float sv = ps.get(i), yv = py.get(i);
+            const float d = q[i] * (w * yv - sv * m[i]);
+            const bool on = c.t + i < c.len;
+            f[i] = on ? (dsum ? g.get(i) + d : d) : 0.f;
+            if (on) dw = fmaf(yv * q[i], sv, dw);
+        }
+        Pack<T> o;
+        o.set(f);
+        o.store(ds + static_cast<int64_t>(ch) * a.L, c.t, a.L);
+        if (part) {
+#pragma unroll
+            for (int o2 = 1; o2 < kTl; o2 *= 2) dw += __shfl_xor(dw, o2, 64);
+            if (c.lane % kTl == 0) part[ch] = dw;
+        }
+    };
+#pragma unroll
+    for (int k = 0; k < HOLD; ++k) {
+        const int ch = c.ch + k * Column<T>::kSweep;
+        if (ch < a.dim) put(ch, hs[k], hy[k]);
+    }
+    for (int ch = c.ch + HOLD * Column<T>::kSweep; ch < a.dim; ch += Column<T>::kSweep) {
+        Pack<T> ps, py;
+        ps.load(s + ch * a.sx.d, c.t, c.len);
+        py.load(dy + ch * a.sdy.d, c.t, c.len);
+        put(ch, ps, py);
+    }
+}
+
+// -------------------------------------------------------------------- rows
+// W waves a row; one-wave rows stand four to a workgroup
+template <int W>
+struct RowOf {
+    int lane, wave, tid;
+    __device__ __forceinline__ RowOf() {
+        lane = threadIdx.x & 63;
+        wave = threadIdx.x >> 6;
+        tid = W == 1 ? lane : static_cast<int>(threadIdx.x);
+    }
+    __device__ __forceinline__ float sum(float v, float* red) const {
+#pragma unroll
+        for (int o = 1; o < 64; o *= 2) v += __shfl_xor(v, o, 64);
+        if constexpr (W > 1) {
+            if (lane == 0) red[wave] = v;
+            __syncthreads();
+            v = 0.f;
+#pragma unroll
+            for (int o = 0; o < W; ++o) v += red[o];
+        }
+        return v;
+    }
+};
+
+template <typename T, int W, int HOLD, bool ADD>
+__global__ __launch_bounds__(W == 1 ? 256 : 64 * W) void norm_row_kernel(const NormArgs a) {
+    constexpr int N = Pack<T>::N, kStep = 64 * W * N;
+    __shared__ float red[W];
+    const RowOf<W> r;
+    const int64_t b = W == 1 ? static_cast<int64_t>(blockIdx.x) * 4 + r.wave : blockIdx.x;
+    if (W == 1 && b >= a.rows) return;
+    const int n = a.lengths && a.lengths[b] < 1 ? 0 : a.dim;          // an empty row reads nothing
+    const T* x = at<T>(a.x, b * a.sx.b);
+    const T* res = ADD ? at<T>(a.res, b * a.sres.b) : nullptr;
+    T *y = static_cast<T*>(a.y) + b * a.dim, *sum = ADD ? static_cast<T*>(a.sum) + b * a.dim : nullptr;
+    Pack<T> s[HOLD];
+    float ss = 0.f;
+#pragma unroll
+    for (int k = 0; k < HOLD; ++k) {
+        const int i0 = k * kStep + r.tid * N;
+        if (i0 >= a.dim) continue;
+        s[k].load(x, i0, n);
+        if constexpr (ADD) {
+            Pack<T> o;
+            o.load(res, i0, n);
+            float f[N];
+#pragma unroll
+            for (int i = 0; i < N; ++i) f[i] = s[k].get(i) + o.get(i);
+            s[k].set(f);
+            s[k].store(sum, i0, a.dim);
+        }
+#pragma unroll
+        for (int i = 0; i < N; ++i) ss = fmaf(s[k].get(i), s[k].get(i), ss);
+    }
+    const float q = __builtin_amdgcn_rsqf(fmaf(r.sum(ss, red), a.inv_dim, a.eps));
+#pragma unroll
+    for (int k = 0; k < HOLD; ++k) {
+        const int i0 = k * kStep + r.tid * N;
+        if (i0 >= a.dim) continue;
+        float f[N], w[N];
+        weights(a.w, i0, a.dim, w);
+#pragma unroll
+        for (int i = 0; i < N; ++i) f[i] = n ? s[k].get(i) * q * w[i] : 0.f;
+        s[k].set(f);
+        s[k].store(y, i0, a.dim);
+    }
+}
+
+// every gridDim.x-th row (or four of them), the sums of dw in registers
+template <typename T, int W, int HOLD>
+__global__ __launch_bounds__(W == 1 ? 256 : 64 * W) void norm_row_grad_kernel(const NormArgs a) {
+    constexpr int N = Pack<T>::N, kStep = 64 * W * N;
+    __shared__ float red[2][2][W];
+    const RowOf<W> r;
+    float dw[HOLD][N];
+#pragma unroll
+    for (int k = 0; k < HOLD; ++k)
+#pragma unroll
+        for (int i = 0; i < N; ++i) dw[k][i] = 0.f;
+    const int64_t first = W == 1 ? static_cast<int64_t>(blockIdx.x) * 4 + r.wave : blockIdx.x;
+    const int64_t step = static_cast<int64_t>(gridDim.x) * (W == 1 ? 4 : 1);
+    int odd = 0;
+    for (int64_t b = first; b < a.rows; b += step, odd ^= 1) {
+        const int n = a.lengths && a.lengths[b] < 1 ? 0 : a.dim;
+        const T *s = at<T>(a.x, b * a.sx.b), *dy = at<T>(a.dy, b * a.sdy.b);
+        const T* dsum = a.dsum ? at<T>(a.dsum, b * a.sdsum.b) : nullptr;
+        T* ds = static_cast<T*>(a.y) + b * a.dim;
+        Pack<T> ps[HOLD], py[HOLD], pg;                  // longer rows read dsum where they use it
+        float ss = 0.f, sd = 0.f;
+#pragma unroll
+        for (int k = 0; k < HOLD; ++k) {
+            const int i0 = k * kStep + r.tid * N;
+            ps[k].load(s, i0, n);
+            py[k].load(dy, i0, n);
+            if (HOLD == 1 && dsum) pg.load(dsum, i0, n);
+            float w[N];
+            weights(a.w, i0, a.dim, w);
+#pragma unroll
+            for (int i = 0; i < N; ++i) {
+                ss = fmaf(ps[k].get(i), ps[k].get(i), ss);
+                sd = fmaf(w[i] * py[k].get(i), ps[k].get(i), sd);
+            }
+        }
+        ss = r.sum(ss, red[odd][0]);
+        sd = r.sum(sd, red[odd][1]);
+        const float q = __builtin_amdgcn_rsqf(fmaf(ss, a.inv_dim, a.eps)), m = q * q * (sd * a.inv_dim);
+#pragma unroll
+        for (int k = 0; k < HOLD; ++k) {
+            const int i0 = k * kStep + r.tid * N;
+            if (i0 >= a.dim) continue;
+            if (HOLD > 1 && dsum) pg.load(dsum, i0, n);
+            float f[N], w[N];
+            weights(a.w, i0, a.dim, w);
+#pragma unroll
+            for (int i = 0; i < N; ++i) {
+                const float sv = ps[k].get(i), yv = py[k].get(i);
+                const float d = q * (w[i] * yv - sv * m);
+                f[i] = n ? (dsum ? pg.get(i) + d : d) : 0.f;
+                if (n) dw[k][i] = fmaf(yv * q, sv, dw[k][i]);
+            }
+            Pack<T> o;
+            o.set(f);
+            o.store(ds, i0, a.dim);
+        }
+    }
+    if (!a.part) return;
+    float* part = a.part + static_cast<size_t>(W == 1 ? blockIdx.x * 4 + r.wave : blockIdx.x) * a.dim;
+#pragma unroll
+    for (int k = 0; k < HOLD; ++k)
+#pragma unroll
+        for (int i = 0; i < N; ++i) {
+            const int at_ = k * kStep + r.tid * N + i;
+            if (at_ < a.dim) part[at_] = dw[k][i];
+        }
+}
+
+// dw from the parts: 16 channels a workgroup, 64 lines of parts side by side
+constexpr int kDwCh = 16, kDwLines = 64;
+__global__ __launch_bounds__(kDwCh* kDwLines) void norm_dw_kernel(const NormArgs a) {
+    __shared__ float red[kDwLines][kDwCh + 1];
+    const int ch = blockIdx.x * kDwCh + threadIdx.x % kDwCh, line = threadIdx.x / kDwCh;
+    float s = 0.f;
+    if (ch < a.dim)
+        for (int p = line; p < a.parts; p += kDwLines) s += a.part[static_cast<size_t>(p) * a.dim + ch];
+    red[line][threadIdx.x % kDwCh] = s;
+    __syncthreads();
+    if (threadIdx.x < kDwCh && ch < a.dim) {
+        s = 0.f;
+        for (int o = 0; o < kDwLines; ++o) s += red[o][threadIdx.x];
+        a.dw[ch] = s;
+    }
+}
+
+// ------------------------------------------------------------------ launch
+template <typename T>
+constexpr int kRowHold = static_cast<int>(vs::kNormMaxDim) / (1024 * Pack<T>::N);   // the longest rows, in 16 waves
+
+template <typename T, bool ADD>
+void launch_rows(const NormArgs& a, const vs::NormCall& c, hipStream_t s) {
+    const dim3 four(static_cast<uint32_t>((c.batch + 3) / 4)), one(static_cast<uint32_t>(c.batch));
+    switch (c.form) {
+        case vs::kNormRow1: norm_row_kernel<T, 1, 1, ADD><<<four, 256, 0, s>>>(a); break;
+        case vs::kNormRow4: norm_row_kernel<T, 4, 1, ADD><<<one, 256, 0, s>>>(a); break;
+        default: norm_row_kernel<T, 16, kRowHold<T>, ADD><<<one, 1024, 0, s>>>(a); break;
+    }
+}
+template <typename T, bool ADD>
+void launch_columns(const NormArgs& a, const vs::NormCall& c, hipStream_t s) {
+    const dim3 grid(static_cast<uint32_t>(c.batch * a.tiles));
+    constexpr int kThreads = 64 * kColWaves;
+    if (c.dim <= 6 * Column<T>::kSweep) norm_column_kernel<T, 6, ADD><<<grid, kThreads, 0, s>>>(a);
+    else norm_column_kernel<T, 12, ADD><<<grid, kThreads, 0, s>>>(a);
+}
+template <typename T>
+void launch_grad(const NormArgs& a, const vs::NormCall& c, hipStream_t s) {
+    if (c.form == vs::kNormColumn) {
+        const dim3 grid(static_cast<uint32_t>(c.batch * a.tiles));
+        constexpr int kThreads = 64 * kColWaves;
+        if (c.dim <= 6 * Column<T>::kSweep) norm_column_grad_kernel<T, 6><<<grid, kThreads, 0, s>>>(a);
+        else norm_column_grad_kernel<T, 12><<<grid, kThreads, 0, s>>>(a);
+    } else {
+        const dim3 grid(static_cast<uint32_t>(c.form == vs::kNormRow1 ? a.parts / 4 : a.parts));
+        switch (c.form) {
+            case vs::kNormRow1: norm_row_grad_kernel<T, 1, 1><<<grid, 256, 0, s>>>(a); break;
+            case vs::kNormRow4: norm_row_grad_kernel<T, 4, 1><<<grid, 256, 0, s>>>(a); break;
+            default: norm_row_grad_kernel<T, 16, kRowHold<T>><<<grid, 1024, 0, s>>>(a); break;
+        }
+    }
+    if (a.dw) norm_dw_kernel<<<dim3((a.dim + kDwCh - 1) / kDwCh), kDwCh * kDwLines, 0, s>>>(a);
+}
+
+int run(vs::NormCall& c) {
+    if (int rc = vs::prepare_norm(c)) return rc;
+    NormArgs a{};
+    a.x = c.x; a.res = c.residual; a.dy = c.dy; a.dsum = c.dsum;
+    a.sx = c.st[0]; a.sres = c.st[1]; a.sdy = c.st[1]; a.sdsum = c.st[2];
+    a.w = c.w; a.eps = c.eps; a.inv_dim = 1.f / static_cast<float>(c.dim); a.lengths = c.lengths;
+    a.y = c.y; a.sum = c.sum; a.part = c.dw ? static_cast<float*>(c.ws) : nullptr; a.dw = c.dw;
+    a.rows = c.batch; a.dim = static_cast<int>(c.dim); a.L = static_cast<int>(c.L);
+    a.tiles = static_cast<int>((c.L + kTile - 1) / kTile);
+    a.parts = static_cast<int>(c.parts);
+    const auto s = static_cast<hipStream_t>(c.stream);
+    const bool bf16 = c.dtype == VS_BF16;
+    if (c.grad) {
+        if (bf16) launch_grad<uint16_t>(a, c, s);
+        else launch_grad<float>(a, c, s);
+    } else if (c.form == vs::kNormColumn) {
+        if (bf16) c.residual ? launch_columns<uint16_t, true>(a, c, s) : launch_columns<uint16_t, false>(a, c, s);
+        else c.residual ? launch_columns<float, true>(a, c, s) : launch_columns<float, false>(a, c, s);
+    } else {
+        if (bf16) c.residual ? launch_rows<uint16_t, true>(a, c, s) : launch_rows<uint16_t, false>(a, c, s);
+        else c.residual ? launch_rows<float, true>(a, c, s) : launch_rows<float, false>(a, c, s);
+    }
+    const hipError_t e = hipGetLastError();
+    return e == hipSuccess ? VS_OK : vs::fail(VS_ERR_HIP, std::string("kernel launch: ") + hipGetErrorString(e));
+}
+
+}  // namespace
+
+extern "C" {
+
+int rms_norm(int64_t batch, int64_t dim, int64_t seqlen, int dtype, const void* x, const void* residual,
+             const int64_t* strides, const float* w, float eps, const int32_t* lengths, void* y, void* sum,
+             void* stream) {
+    vs::NormCall c{};
+    c.batch = batch; c.dim = dim; c.L = seqlen; c.dtype = dtype; c.x = x; c.residual = residual; c.strides = strides;
+    c.w = w; c.eps = eps; c.lengths = lengths; c.y = y; c.sum = sum; c.stream = stream;
+    return run(c);
+}
+
+int rms_norm_grad(int64_t batch, int64_t dim, int64_t seqlen, int dtype, const void* s, const void* dy,
+                  const void* dsum, const int64_t* strides, const float* w, float eps, const int32_t* lengths,
+                  void* ds, float* dw, void* workspace, size_t workspace_bytes, void* stream) {
+    vs::NormCall c{};
+    c.batch = batch; c.dim = dim; c.L = seqlen; c.dtype = dtype; c.x = s; c.dy = dy; c.dsum = dsum; c.strides = strides;
+    c.w = w; c.eps = eps; c.lengths = lengths; c.y = ds; c.dw = dw; c.ws = workspace; c.ws_bytes = workspace_bytes;
+    c.stream = stream; c.grad = true;
+    return run(c);
+}
+
+}  // extern "C"

@@ -62,4 +62,31 @@ struct GatedStepCall {
 };
 int prepare_gated_step(GatedStepCall& c);
 
+// ---- the norm (norm.hip)
+constexpr int kNormTile = 32;                        // tokens of a workgroup, channel-major
+constexpr int64_t kNormMaxDim = 8192;
+// channel-major, or rows in 1, 4 or 16 waves: the channels a lane holds bound
+// the row's length
+enum NormForm { kNormColumn, kNormRow1, kNormRow4, kNormRow16 };
+struct NormCall {
+    int64_t batch, dim, L;
+    int dtype;
+    const void *x, *residual;                        // gradient: x is the sum s
+    const void *dy, *dsum;
+    const int64_t* strides;                          // as the caller gave them (may be NULL)
+    const float* w;
+    float eps;
+    const int32_t* lengths;
+    void *y, *sum;                                   // gradient: y is ds
+    float* dw;
+    void* ws;
+    size_t ws_bytes;
+    void* stream;
+    bool grad = false;
+    Strides st[3];                                   // x, residual; gradient: s, dy, dsum
+    NormForm form;
+    int64_t parts;                                   // gradient: lines of sums for dw
+};
+int prepare_norm(NormCall& c);
+
 }  // namespace vs
