@@ -686,6 +686,45 @@ int rms_norm_grad(int64_t batch, int64_t dim, int64_t seqlen, int dtype, const v
                   float eps, const int32_t* lengths, void* ds, float* dw, void* workspace,
                   size_t workspace_bytes, void* stream);
 
+/*
+ * ---- The loss over a vocabulary
+ *
+ * Softmax cross entropy of a linear head, without keeping the logits: with
+ * l_t = W x_t,
+ *   lse_t  = log sum_v exp(l_tv)
+ *   loss_t = lse_t - l_t,target(t)
+ * A target outside 0..vocab-1 leaves its token out: its loss and gradients are
+ * zero, and its row of x is no part of dW, whatever it holds (its lse is
+ * computed all the same). Logits are products of the inputs as they are,
+ * summed in fp32; a token with a logit of +inf or NaN has NaN for lse and loss.
+ *   x           [tokens][dim], dtype; row stride x_stride (0: dim)
+ *   W           [vocab][dim], dtype, at an address of whole 4 bytes (where dim
+ *               is odd, of whole elements)
+ *   target      [tokens] integers of target_bits (32 or 64) bits
+ *   loss, lse   [tokens] fp32
+ *   workspace   vocab_workspace_bytes(VS_VOCAB_LOSS, ...), 16-byte aligned
+ * dim is at most 65536, tokens and vocab below 2^24, tokens x vocab below 2^36.
+ */
+enum { VS_VOCAB_LOSS = 0, VS_VOCAB_GRAD = 1 };
+size_t vocab_workspace_bytes(int op, int64_t tokens, int64_t dim, int64_t vocab, int dtype);
+int vocab_loss(int64_t tokens, int64_t dim, int64_t vocab, int dtype, const void* x,
+               int64_t x_stride, const void* W, const void* target, int target_bits, float* loss,
+               float* lse, void* workspace, size_t workspace_bytes, void* stream);
+
+/*
+ * Gradient of sum_t dloss_t loss_t, with the lse of a vocab_loss call on the
+ * same inputs (not checked). The vocabulary is taken in pieces: of each the
+ * logits again, P = (exp(l - lse) - [v = target]) dloss, rounded to dtype for
+ * the two products that follow, and sums in fp32.
+ *   dloss       [tokens] fp32; not used where the target leaves the token out
+ *   dx          [tokens][dim], dW [vocab][dim], dtype; both repeat bit for bit
+ *   workspace   vocab_workspace_bytes(VS_VOCAB_GRAD, ...)
+ */
+int vocab_loss_grad(int64_t tokens, int64_t dim, int64_t vocab, int dtype, const void* x,
+                    int64_t x_stride, const void* W, const void* target, int target_bits,
+                    const float* lse, const float* dloss, void* dx, void* dW, void* workspace,
+                    size_t workspace_bytes, void* stream);
+
 /* Static name of a status code ("VS_OK", ...). Never NULL. */
 const char* vs_strerror(int status);
 

@@ -39,3 +39,13 @@ def norm(x, w, residual, lengths, eps, dtype):
     if w is not None:
         y = y * w[:, None]
     return y * live, s
+
+
+def vocab(x, W, target):
+    """(loss, lse) of [tokens, dim] activations, wherever they are; float64 in, float64 out."""
+    l = x @ W.T
+    top = l.max(dim=1, keepdim=True).values
+    lse = (top + torch.log(torch.exp(l - top).sum(dim=1, keepdim=True)))[:, 0]
+    kept = (target >= 0) & (target < W.shape[0])
+    at = torch.where(kept, target, torch.zeros_like(target)).long()
+    return torch.where(kept, lse - l.gather(1, at[:, None])[:, 0], torch.zeros_like(lse)), lse

@@ -22,7 +22,8 @@ _BEAM = ["beam_select", "beam_reorder", "beam_workspace_bytes"]
 _GATED = ["gated_workspace_bytes", "gated_scan", "gated_scan_saved", "gated_scan_grad", "gated_scan_step",
           "GatedScanFunction", "gated_scan_autograd"]
 _NORM = ["rms_norm", "rms_norm_grad", "norm_workspace_bytes", "RmsNormFunction", "rms_norm_autograd"]
-__all__ += _CAUSAL + _BEAM + _GATED + _NORM
+_LOSS = ["vocab_loss", "vocab_loss_grad", "vocab_workspace_bytes", "VocabLossFunction", "vocab_loss_autograd"]
+__all__ += _CAUSAL + _BEAM + _GATED + _NORM + _LOSS
 
 
 def __getattr__(name):
@@ -34,6 +35,8 @@ def __getattr__(name):
         from . import gated as module
     elif name in _NORM:
         from . import norm as module
+    elif name in _LOSS:
+        from . import loss as module
     elif name in __all__:
         from . import scan as module
     else:

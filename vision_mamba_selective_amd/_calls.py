@@ -43,3 +43,5 @@ gated_scan_grad = _binding.gated_scan_grad
 gated_scan_step = _binding.gated_scan_step
 rms_norm = _binding.rms_norm
 rms_norm_grad = _binding.rms_norm_grad
+vocab_loss = _binding.vocab_loss
+vocab_loss_grad = _binding.vocab_loss_grad

@@ -21,6 +21,7 @@ VS_S6_SCAN, VS_S6_SAVED, VS_S6_GRAD, VS_S6_CONV_GRAD = 0, 1, 2, 3
 VS_MAX_CONV_WIDTH = 8
 VS_MAX_BEAMS = 32
 VS_GATED_SAVED, VS_GATED_GRAD = 0, 1
+VS_VOCAB_LOSS, VS_VOCAB_GRAD = 0, 1
 
 # names and argument types of every entry point declared in include/vimscan.h
 _I64 = ctypes.c_int64
@@ -73,6 +74,9 @@ SIGNATURES = {
     "norm_workspace_bytes": (_SZ, [_I64, _I64, _I64]),
     "rms_norm": (_I, [_I64, _I64, _I64, _I] + [_P] * 4 + [_F] + [_P] * 4),
     "rms_norm_grad": (_I, [_I64, _I64, _I64, _I] + [_P] * 5 + [_F] + [_P] * 4 + [_SZ, _P]),
+    "vocab_workspace_bytes": (_SZ, [_I, _I64, _I64, _I64, _I]),
+    "vocab_loss": (_I, [_I64, _I64, _I64, _I, _P, _I64, _P, _P, _I, _P, _P, _P, _SZ, _P]),
+    "vocab_loss_grad": (_I, [_I64, _I64, _I64, _I, _P, _I64, _P, _P, _I, _P, _P, _P, _P, _P, _SZ, _P]),
     "vs_strerror": (ctypes.c_char_p, [_I]),
     "vs_last_error": (ctypes.c_char_p, []),
     "vs_abi_version": (_I, []),

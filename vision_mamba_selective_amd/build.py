@@ -15,7 +15,7 @@ ROOT = os.path.dirname(PKG)
 SRC = os.path.join(PKG, "csrc", "vimscan.hip")
 SRCS = [SRC] + [os.path.join(PKG, "csrc", f) for f in
                 ("proj.hip", "causal.hip", "causal_grad.hip", "beam.hip", "gated.hip",
-                 "norm.hip", "host.cpp", "host_causal.cpp", "host_model.cpp")]
+                 "norm.hip", "vocab.hip", "host.cpp", "host_causal.cpp", "host_model.cpp")]
 LIB = os.path.join(PKG, "libvimscan.so")
 INCLUDE = os.path.join(ROOT, "include")
 BINDING_SRC = os.path.join(PKG, "csrc", "binding.cpp")

@@ -1,6 +1,6 @@
 // binding.cpp -- the torch side of the causal mixer's and beam search's entry
-// points and of those beside them (causal.py, beam.py, gated.py and norm.py hold
-// their names, defaults and documentation):
+// points and of those beside them (causal.py, beam.py, gated.py, norm.py and loss.py
+// hold their names, defaults and documentation):
 // checks of the arguments, allocation of the outputs and the call of the C
 // ABI. A single-token call's kernels take 2 to 6 us; checked argument by
 // argument in Python such a call cost the host 9 us.
@@ -35,7 +35,8 @@ namespace {
     X(s6_causal_scan_saved) X(s6_causal_scan_grad) X(s6_scan_step) X(beam_workspace_bytes)            \
     X(beam_select) X(beam_reorder)                                                                    \
     X(gated_workspace_bytes) X(gated_scan) X(gated_scan_saved) X(gated_scan_grad) X(gated_scan_step)   \
-    X(norm_workspace_bytes) X(rms_norm) X(rms_norm_grad)
+    X(norm_workspace_bytes) X(rms_norm) X(rms_norm_grad)                                              \
+    X(vocab_workspace_bytes) X(vocab_loss) X(vocab_loss_grad)
 
 struct Abi {
 #define VS_MEMBER(f) decltype(&::f) f;
@@ -601,6 +602,65 @@ PyObject* norm_grad(PyObject* const* a) {
     return dict({{"dx", ds}, {"dw", dw}});
 }
 
+// --------------------------------------------------------- vocabulary loss
+// x, W, target
+struct VocabIn {
+    const at::Tensor &tx, &tW, &tt;
+    Call c;
+    int64_t tokens, dim, vocab, stride;
+    const void *x, *W, *target;
+    int bits;
+
+    explicit VocabIn(PyObject* const* a) : tx(need("x", a[0])), tW(need("W", a[1])), tt(need("target", a[2])), c("x", tx, 2), tokens(tx.size(0)), dim(tx.size(1)) {
+        axes("W", tW, 2);
+        vocab = tW.size(0);
+        x = c.input("x", &tx, {tokens, dim});
+        stride = tokens > 1 ? tx.stride(0) : dim;
+        W = c.dense("W", &tW, {vocab, dim}, c.dt);
+        bits = tt.scalar_type() == at::kInt ? 32 : 64;
+        target = c.dense("target", &tt, {tokens}, bits == 32 ? at::kInt : at::kLong);
+    }
+    size_t bytes(int op) const { return abi.vocab_workspace_bytes(op, tokens, dim, vocab, c.dtype); }
+};
+
+// x, W, target, workspace
+PyObject* vocab_forward(PyObject* const* a) {
+    VocabIn v(a);
+    const Call& c = v.c;
+    at::Tensor x = v.tx;
+    if (v.tokens > 1 && v.stride < v.dim) {                  // one row for all, or overlapping rows
+        x = v.tx.contiguous();
+        v.stride = v.dim;
+    }
+    const Buffer ws("workspace", v.bytes(VS_VOCAB_LOSS), c, a[3]);
+    const at::Tensor loss = c.fresh({v.tokens}, at::kFloat), lse = c.fresh({v.tokens}, at::kFloat);
+    run("vocab_loss", c.dev, c.written, [&] {
+        return abi.vocab_loss(v.tokens, v.dim, v.vocab, c.dtype, x.data_ptr(), v.stride, v.W, v.target, v.bits, f32(loss), f32(lse), ws.p,
+                              ws.bytes, c.stream());
+    });
+    return tuple({loss, lse});
+}
+
+// x, W, target, lse, dloss, workspace
+PyObject* vocab_grad(PyObject* const* a) {
+    VocabIn v(a);
+    const Call& c = v.c;
+    at::Tensor x = v.tx;
+    if (v.tokens > 1 && v.stride < v.dim) {
+        x = v.tx.contiguous();
+        v.stride = v.dim;
+    }
+    const float* lse = c.dense<float>("lse", &need("lse", a[3]), {v.tokens});
+    const float* dloss = c.dense<float>("dloss", &need("dloss", a[4]), {v.tokens});
+    const Buffer ws("workspace", v.bytes(VS_VOCAB_GRAD), c, a[5]);
+    const at::Tensor dx = c.fresh({v.tokens, v.dim}, c.dt), dW = c.fresh({v.vocab, v.dim}, c.dt);
+    run("vocab_loss_grad", c.dev, c.written, [&] {
+        return abi.vocab_loss_grad(v.tokens, v.dim, v.vocab, c.dtype, x.data_ptr(), v.stride, v.W, v.target, v.bits, lse, dloss,
+                                   dx.data_ptr(), dW.data_ptr(), ws.p, ws.bytes, c.stream());
+    });
+    return dict({{"dx", dx}, {"dW", dW}});
+}
+
 // ------------------------------------------------------------- beam search
 // logits, scores, done, eos, workspace, out[0], out[1], out[2]
 PyObject* select(PyObject* const* a) {
@@ -712,6 +772,7 @@ PyMethodDef methods[] = {
     method<scan_step, 13>("s6_scan_step"), method<select, 8>("beam_select"), method<reorder, 3>("beam_reorder"),
     method<gated, 10>("gated_scan"), method<gated_saved, 11>("gated_scan_saved"), method<gated_grad, 12>("gated_scan_grad"),
     method<gated_step, 10>("gated_scan_step"), method<norm, 7>("rms_norm"), method<norm_grad, 7>("rms_norm_grad"),
+    method<vocab_forward, 4>("vocab_loss"), method<vocab_grad, 6>("vocab_loss_grad"),
     {nullptr, nullptr, 0, nullptr}};
 
 PyModuleDef module_def = {PyModuleDef_HEAD_INIT, "_binding", nullptr, -1, methods, nullptr, nullptr, nullptr, nullptr};

@@ -191,6 +191,107 @@ int prepare_norm(NormCall& c) {
     return check_overlaps(in + 1, 1, out, 1);
 }
 
+// --------------------------------------------------------- vocabulary loss
+namespace {
+
+const char* vocab_problem(int64_t tokens, int64_t dim, int64_t vocab, int& code) {
+    code = VS_ERR_SHAPE;
+    if (tokens < 1 || dim < 1 || vocab < 1) return "tokens, dim and vocab must be >= 1";
+    code = VS_ERR_UNSUPPORTED;
+    if (dim > 65536) return "dim above 65536 is not supported";
+    if (tokens >= (int64_t(1) << 24) || vocab >= (int64_t(1) << 24)) return "2^24 tokens or vocabulary entries or more are not supported";
+    if (ceil_div(tokens, 128) * ceil_div(vocab, 128) >= (int64_t(1) << 22)) return "2^36 logits or more are not supported";
+    return nullptr;
+}
+
+// The larger tile reads half as much per product, the smaller fills the chip
+// with fewer entries; a product with too few tiles for either cuts its k.
+VocabTiles vocab_tiles(int64_t m, int64_t n, int64_t k, int dtype, bool cut) {
+    const int64_t stages = ceil_div(k * static_cast<int64_t>(esize(dtype)), kVocabStage);
+    const int64_t wide = ceil_div(m, 256) * ceil_div(n, 256), narrow = ceil_div(m, 128) * ceil_div(n, 128);
+    VocabTiles t{wide >= 192, 1};
+    if (cut && !t.wide && narrow < 512) {
+        int64_t s = 512 / narrow;
+        const int64_t most = stages / 8 > 0 ? stages / 8 : 1;
+        s = s > most ? most : s;
+        t.splits = static_cast<int>(s > 64 ? 64 : s);
+    }
+    return t;
+}
+
+}  // namespace
+
+VocabPlan vocab_plan(bool grad, int64_t tokens, int64_t dim, int64_t vocab, int dtype) {
+    VocabPlan p{};
+    const size_t es = esize(dtype);
+    p.dp = ceil_div(dim, 8) * 8;
+    p.pack_w = dim * static_cast<int64_t>(es) % 4 != 0;         // a row starts between words
+    size_t off = 0;
+    auto take = [&](size_t n) { const size_t at = off; off += al256(n); return at; };
+    p.x = take(static_cast<size_t>(tokens * p.dp) * es);
+    p.w = take(p.pack_w ? static_cast<size_t>(vocab * p.dp) * es : 0);
+    if (!grad) {
+        p.logits = vocab_tiles(vocab, tokens, dim, dtype, false);
+        p.tiles = static_cast<int>(ceil_div(vocab, p.logits.wide ? 256 : 128));
+        p.part = take(static_cast<size_t>(p.tiles) * static_cast<size_t>(tokens) * 2 * kF);
+        p.logit = take(static_cast<size_t>(tokens) * kF);
+    } else {
+        // P of a piece takes up to 512 MB
+        int64_t piece = (int64_t(1) << 29) / (tokens * static_cast<int64_t>(es)) / 256 * 256;
+        piece = piece < 256 ? 256 : piece;
+        p.pieces = ceil_div(vocab, piece);
+        p.piece = ceil_div(ceil_div(vocab, p.pieces), 256) * 256;
+        p.pieces = ceil_div(vocab, p.piece);
+        const int64_t n = p.piece < vocab ? p.piece : vocab;
+        p.logits = vocab_tiles(n, tokens, dim, dtype, false);
+        p.dx = vocab_tiles(dim, tokens, n, dtype, true);
+        p.dw = vocab_tiles(dim, n, tokens, dtype, true);
+        p.P = take(static_cast<size_t>(tokens * (ceil_div(n, 8) * 8)) * es);
+        const size_t dx = p.dx.splits > 1 ? static_cast<size_t>(p.dx.splits * tokens * dim) * kF : 0;
+        const size_t dw = p.dw.splits > 1 ? static_cast<size_t>(p.dw.splits * n * dim) * kF : 0;
+        p.part = take(dx > dw ? dx : dw);
+        p.sum = take(p.pieces > 1 ? static_cast<size_t>(tokens * dim) * kF : 0);
+    }
+    p.bytes = off;
+    return p;
+}
+
+int prepare_vocab(VocabCall& c) {
+    clear_error();
+    if (c.dtype != VS_F32 && c.dtype != VS_BF16) return fail(VS_ERR_DTYPE, "unknown dtype");
+    int code;
+    if (const char* p = vocab_problem(c.tokens, c.dim, c.vocab, code)) return fail(code, p);
+    if (c.target_bits != 32 && c.target_bits != 64) return fail(VS_ERR_UNSUPPORTED, "targets have 32 or 64 bits");
+    c.target64 = c.target_bits == 64;
+    if (!c.x || !c.W || !c.target) return fail(VS_ERR_NULL, "x, W and target must not be NULL");
+    if (c.grad ? !c.lse_in || !c.dloss || !c.dx || !c.dW : !c.loss || !c.lse)
+        return fail(VS_ERR_NULL, c.grad ? "lse, dloss, dx and dW must not be NULL" : "loss and lse must not be NULL");
+    if (c.ldx == 0) c.ldx = c.dim;
+    if (c.ldx < c.dim && c.tokens > 1) return fail(VS_ERR_SHAPE, "x_stride is smaller than dim");
+    if (c.ldx >= (int64_t(1) << 28)) return fail(VS_ERR_UNSUPPORTED, "row strides of 2^28 elements or more are not supported");
+    c.plan = vocab_plan(c.grad, c.tokens, c.dim, c.vocab, c.dtype);
+    const size_t es = esize(c.dtype);
+    if (!c.ws || c.ws_bytes < c.plan.bytes) return fail(VS_ERR_WORKSPACE, "workspace missing or smaller than vocab_workspace_bytes()");
+    c.plan.pack_x = !aligned(c.x, 4) || c.ldx * static_cast<int64_t>(es) % 4 != 0 || c.ldx > 65536;
+    const size_t xs = (static_cast<size_t>((c.tokens - 1) * c.ldx) + static_cast<size_t>(c.dim)) * es, ws = static_cast<size_t>(c.vocab * c.dim) * es;
+    const size_t row = static_cast<size_t>(c.tokens) * kF;
+    const Span ins[] = {{c.x, xs}, {c.W, ws}, {c.target, static_cast<size_t>(c.tokens) * (c.target64 ? 8 : 4)},
+                        {c.grad ? c.lse_in : nullptr, row}, {c.grad ? c.dloss : nullptr, row}};
+    if (int rc = check_aligned(ins, 1, es, "x misaligned")) return rc;
+    if (int rc = check_aligned(ins + 1, 1, c.plan.pack_w ? es : 4, "W misaligned (4 bytes, 2 where dim is odd)")) return rc;
+    if (int rc = check_aligned(ins + 2, 1, c.target64 ? 8 : 4, "target misaligned")) return rc;
+    if (int rc = check_aligned(ins + 3, 2, 4, "32-bit pointer misaligned")) return rc;
+    if (!aligned(c.ws, 16)) return fail(VS_ERR_ALIGN, "workspace misaligned (16 bytes)");
+    if (!c.grad) {
+        const Span outs[] = {{c.loss, row}, {c.lse, row}, {c.ws, c.plan.bytes}};
+        if (int rc = check_aligned(outs, 2, 4, "32-bit pointer misaligned")) return rc;
+        return check_overlaps(ins, 5, outs, 3);
+    }
+    const Span outs[] = {{c.dx, static_cast<size_t>(c.tokens * c.dim) * es}, {c.dW, ws}, {c.ws, c.plan.bytes}};
+    if (int rc = check_aligned(outs, 2, es, "gradient misaligned")) return rc;
+    return check_overlaps(ins, 5, outs, 3);
+}
+
 }  // namespace vs
 
 // ---------------------------------------------------------------- C ABI
@@ -210,6 +311,14 @@ size_t norm_workspace_bytes(int64_t batch, int64_t dim, int64_t seqlen) {
         parts = parts > rows ? parts : rows;
     }
     return static_cast<size_t>(parts * dim) * vs::kF;
+}
+
+size_t vocab_workspace_bytes(int op, int64_t tokens, int64_t dim, int64_t vocab, int dtype) {
+    int code;
+    if ((op != VS_VOCAB_LOSS && op != VS_VOCAB_GRAD) || (dtype != VS_F32 && dtype != VS_BF16) ||
+        vs::vocab_problem(tokens, dim, vocab, code))
+        return 0;
+    return vs::vocab_plan(op == VS_VOCAB_GRAD, tokens, dim, vocab, dtype).bytes;
 }
 
 }  // extern "C"

@@ -1,0 +1,595 @@
+// vocab.hip -- softmax cross entropy of a linear head over a large vocabulary,
+// without keeping the logits, and its gradient: with l = x W^T,
+//     lse_t = log sum_v exp(l_tv),  loss_t = lse_t - l_t,target(t)
+//     P_tv = (exp(l_tv - lse_t) - [v = target(t)]) dloss_t
+//     dx = P W,  dW = P^T x.
+//
+// Three matrix products share one kernel body (matrix cores, 32 x 32 tiles,
+// fp32 accumulation). It computes out[n][m] = sum_k A(m, k) B(n, k), so that a
+// lane's accumulators are 16 rows m of one column n:
+//   logits  m a vocabulary entry, n a token: a token's maximum and its sum of
+//           exponentials are taken inside the lane, and its row of P is
+//           written in runs of four entries
+//   dx      m a channel, n a token, k the vocabulary
+//   dW      m a channel, n a vocabulary entry, k the tokens
+// An operand lies in memory with its k side by side (x and W for the logits, P
+// for dx) or with its rows side by side (W for dx, x and P for dW). Both are
+// copied to LDS as they lie, 128 bytes of k a stage, straight from the buffer
+// without a register; the second kind is turned on the way from LDS to the
+// registers (ds_read_b64_tr_b16, or single words in fp32), so nothing is
+// transposed in memory.
+//
+// The forward pass leaves a maximum and a sum for each token and tile of the
+// vocabulary, 8 bytes for 256 logits. The gradient takes the vocabulary in
+// pieces: logits again, P of the piece into the workspace, then both products
+// that read it.
+#include <hip/hip_runtime.h>
+
+#include <cstdint>
+
+#include "vimscan.h"
+#include "vs_device.h"
+#include "vs_model.h"
+
+namespace {
+
+typedef __attribute__((ext_vector_type(8))) __bf16 bf16x8;
+typedef __attribute__((ext_vector_type(4))) float f32x4;
+typedef __attribute__((ext_vector_type(16))) float f32x16;
+typedef __attribute__((ext_vector_type(4))) short v4s;
+typedef __attribute__((ext_vector_type(8))) short v8s;
+typedef __attribute__((address_space(3))) void lds_void;
+
+constexpr int kStage = vs::kVocabStage;          // bytes of k a stage
+
+enum Epilogue { kLse, kProb, kSum };
+
+struct GemmArgs {
+    const void *A, *B;
+    int64_t lda, ldb;               // elements
+    int M, N, K;
+    int tiles_m, tiles_n;
+    int k_split;                    // k of one split (a multiple of a stage's), blockIdx.y of them
+    // logits
+    const void* target;
+    int target64;
+    int v0, vocab;                  // the vocabulary entry of m = 0; entries in all
+    float *part_max, *part_sum, *target_logit;      // kLse: [tiles_m][N], [N]
+    const float *lse, *dloss;       // kProb
+    void* P;                        // [N][ldp]
+    int ldp;
+    // kSum: sum[n][m] = (add ? sum : 0) + product, or out in the operands' type
+    void* out;
+    int64_t ldo;
+    float* sum;                     // [N][M], or one for each split
+    int add;
+};
+
+template <typename T>
+struct Types;
+template <>
+struct Types<uint16_t> {
+    typedef bf16x8 Frag;
+    static __device__ __forceinline__ void mma(const Frag& a, const Frag& b, f32x16& c) {
+        c = __builtin_amdgcn_mfma_f32_32x32x16_bf16(a, b, c, 0, 0, 0);
+    }
+};
+template <>
+struct Types<float> {
+    typedef f32x4 Frag;
+    // lane half h holds k = 4 h .. 4 h + 3 of the step's eight: each instruction takes one of both halves
+    static __device__ __forceinline__ void mma(const Frag& a, const Frag& b, f32x16& c) {
+#pragma unroll
+        for (int j = 0; j < 4; ++j) c = __builtin_amdgcn_mfma_f32_32x32x2f32(a[j], b[j], c, 0, 0, 0);
+    }
+};
+
+// One operand's tile: R rows of a stage. The 16-byte chunks of a line of LDS
+// are permuted so that the fragment reads fall on distinct banks; a chunk's
+// place is chosen by the address that its lane reads from.
+template <typename T, bool OUTER, int R, int WAVES>
+struct Operand {
+    static constexpr int kEs = sizeof(T), kBk = kStage / kEs, kBytes = R * kStage;
+    static constexpr int kLine = OUTER ? R * kEs : kStage;          // bytes of a line of LDS
+    static constexpr int kLanes = kLine / 16;                       // lanes to a line
+    static constexpr int kLines = 64 / kLanes;                      // lines of one instruction
+    static constexpr int kIters = kBytes / 1024 / WAVES;
+    static_assert(kLanes <= 64 && kIters >= 1 && kBytes % (1024 * WAVES) == 0, "whole instructions");
+    static_assert(WAVES % 4 == 0, "a lane's chunk is the same in every instruction");
+
+    const char* base;
+    int64_t ld;              // bytes
+    int64_t bytes;           // from base to the operand's end
+    uint32_t off;            // this lane's first chunk
+    int wave;
+    // fragment reads
+    uint32_t at[OUTER ? 4 : 4];
+
+    static __device__ __forceinline__ int turn(int line) {
+        if constexpr (!OUTER) return (line >> 1) & 7;
+        else if constexpr (kEs == 2) return 4 * (line & 3);
+        else return 8 * ((line >> 2) & 1);
+    }
+    // The range check goes by words: one that an odd row's end shares with what
+    // follows counts as part of the operand (only packed rows and P's are odd:
+    // they are padded).
+    static __device__ __forceinline__ int64_t whole(int64_t bytes) { return (bytes + 3) & ~int64_t(3); }
+    // rows from `first` on of an operand with `rows` of them and K in all
+    __device__ __forceinline__ void open(const void* p, int64_t ld_, int first, int rows, int K, int lane, int wave_) {
+        ld = ld_ * kEs;
+        wave = wave_;
+        const int line = wave * kLines + lane / kLanes, chunk = lane % kLanes ^ turn(line);
+        if constexpr (OUTER) {
+            base = static_cast<const char*>(p) + static_cast<int64_t>(first) * kEs;
+            bytes = (K - 1) * ld + whole(static_cast<int64_t>(rows - first) * kEs);
+        } else {
+            base = static_cast<const char*>(p) + first * ld;
+            bytes = (rows - first - 1) * ld + whole(static_cast<int64_t>(K) * kEs);
+        }
+        off = static_cast<uint32_t>(line * ld) + chunk * 16;
+    }
+    // the stage from k on; reads past the operand's end return zeros
+    __device__ __forceinline__ void load(char* lds, int k) const {
+        const int64_t skip = OUTER ? k * ld : static_cast<int64_t>(k) * kEs;
+        const int64_t left = bytes - skip;
+        const auto rsrc = __builtin_amdgcn_make_buffer_rsrc(const_cast<char*>(base + skip), 0,
+                                                            static_cast<int>(left < 0x7fffffff ? (left > 0 ? left : 0) : 0x7fffffff), 0x00020000);
+#pragma unroll
+        for (int i = 0; i < kIters; ++i)
+            __builtin_amdgcn_raw_ptr_buffer_load_lds(rsrc, (lds_void*)(lds + (i * WAVES + wave) * 1024), 16, static_cast<int>(off),
+                                                     static_cast<int>(i * WAVES * kLines * ld), 0, 0);
+    }
+    // zeros for k >= n of a stage in LDS
+    __device__ __forceinline__ void cut(char* lds, int n, int tid) const {
+        if constexpr (OUTER) {
+            for (int i = n * kLine + tid * 16; i < kBytes; i += WAVES * 64 * 16) *reinterpret_cast<f32x4*>(lds + i) = f32x4{0.f, 0.f, 0.f, 0.f};
+        } else {
+            for (int i = tid; i < R * kBk; i += WAVES * 64) {
+                const int row = i / kBk, k = i % kBk;
+                if (k >= n) *reinterpret_cast<T*>(lds + row * kStage + ((k * kEs / 16) ^ turn(row)) * 16 + k * kEs % 16) = 0;
+            }
+        }
+    }
+    // prepares the fragments of 32 rows each from row w0 of the tile on
+    __device__ __forceinline__ void aim(int w0, int lane) {
+        const int r = lane & 31, h = lane >> 5, i = lane & 15;
+#pragma unroll
+        for (int s = 0; s < 4; ++s) {
+            if constexpr (!OUTER) at[s] = (w0 + r) * kStage + ((2 * s + h) ^ turn(r)) * 16;      // of step s
+            else if constexpr (kEs == 2)                                                        // of fragment s
+                at[s] = (8 * h + i / 4) * kLine + (((w0 / 8 + s * 4) ^ turn(i / 4)) + (r / 16) * 2 + (i % 4) / 2) * 16 + (i & 1) * 8;
+            else at[s] = 4 * h * kLine + (((w0 + s * 32 + r) / 4) ^ (8 * h)) * 16 + (r & 3) * 4;
+        }
+    }
+    __device__ __forceinline__ typename Types<T>::Frag read(const char* lds, int f, int s) const {
+        typename Types<T>::Frag v;
+        if constexpr (!OUTER) {
+            v = *reinterpret_cast<const typename Types<T>::Frag*>(lds + at[s] + f * 32 * kStage);
+        } else if constexpr (kEs == 2) {
+            typedef __attribute__((address_space(3))) v4s* Ptr;
+            const v4s lo = __builtin_amdgcn_ds_read_tr16_b64_v4i16((Ptr)(lds + at[f] + 16 * s * kLine));
+            const v4s hi = __builtin_amdgcn_ds_read_tr16_b64_v4i16((Ptr)(lds + at[f] + (16 * s + 4) * kLine));
+            v = __builtin_bit_cast(bf16x8, __builtin_shufflevector(lo, hi, 0, 1, 2, 3, 4, 5, 6, 7));
+        } else {
+#pragma unroll
+            for (int j = 0; j < 4; ++j) v[j] = *reinterpret_cast<const float*>(lds + at[f] + (8 * s + j) * kLine);
+        }
+        return v;
+    }
+};
+
+__device__ __forceinline__ int64_t target_of(const GemmArgs& a, int t) {
+    return a.target64 ? static_cast<const int64_t*>(a.target)[t] : static_cast<const int32_t*>(a.target)[t];
+}
+
+// four consecutive entries of a row of n
+__device__ __forceinline__ void put_four(float* p, int at, int n, const float (&f)[4]) {
+    if (at + 4 <= n) __builtin_memcpy(p + at, f, 16);
+    else
+        for (int i = 0; i < 4; ++i)
+            if (at + i < n) p[at + i] = f[i];
+}
+__device__ __forceinline__ void put_four(uint16_t* p, int at, int n, const float (&f)[4]) {
+    uint16_t b[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) st(b, i, f[i]);
+    if (at + 4 <= n) __builtin_memcpy(p + at, b, 8);
+    else
+        for (int i = 0; i < 4; ++i)
+            if (at + i < n) p[at + i] = b[i];
+}
+
+template <typename T, int BM, int BN, int WM, int WN, bool AO, bool BO, Epilogue EPI>
+__global__ __launch_bounds__(64 * WM * WN) void vocab_gemm_kernel(const GemmArgs a) {
+    constexpr int kWaves = WM * WN, MF = BM / WM / 32, NF = BN / WN / 32;
+    static_assert(MF <= 4 && NF <= 4, "fragments of a wave");
+    typedef Operand<T, AO, BM, kWaves> OpA;
+    typedef Operand<T, BO, BN, kWaves> OpB;
+    // two stages; arrays of their own, so that a stage's reads do not wait for the next one's loads
+    __shared__ __attribute__((aligned(1024))) char sA0[OpA::kBytes];
+    __shared__ __attribute__((aligned(1024))) char sA1[OpA::kBytes];
+    __shared__ __attribute__((aligned(1024))) char sB0[OpB::kBytes];
+    __shared__ __attribute__((aligned(1024))) char sB1[OpB::kBytes];
+
+    const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+    const int wm = wave / WN, wn = wave % WN;
+    // each XCD a contiguous range of tiles; eight columns of tiles at a time, so
+    // that the tiles that run together share rows of both operands in its L2
+    int tm, tn;
+    {
+        const uint32_t G = gridDim.x, x = blockIdx.x % kXcds, k = blockIdx.x / kXcds, q = G / kXcds, r = G % kXcds;
+        const int v = static_cast<int>(x * q + (x < r ? x : r) + k);
+        const int band = v / (8 * a.tiles_m), n0 = band * 8, width = min(8, a.tiles_n - n0);
+        const int in = v - band * 8 * a.tiles_m;
+        tm = in / width;
+        tn = n0 + in % width;
+    }
+    const int m0 = tm * BM, n0 = tn * BN;
+    const int k_lo = blockIdx.y * a.k_split, k_hi = min(a.K, k_lo + a.k_split);
+
+    OpA A;
+    OpB B;
+    A.open(a.A, a.lda, m0, a.M, a.K, lane, wave);
+    B.open(a.B, a.ldb, n0, a.N, a.K, lane, wave);
+    A.aim(wm * (BM / WM), lane);
+    B.aim(wn * (BN / WN), lane);
+    f32x16 acc[MF][NF];
+#pragma unroll
+    for (int i = 0; i < MF; ++i)
+#pragma unroll
+        for (int j = 0; j < NF; ++j)
+#pragma unroll
+            for (int r = 0; r < 16; ++r) acc[i][j][r] = 0.f;
+
+    auto stage = [&](char* pa, char* pb, int k) VS_INLINE {
+        if (k + OpA::kBk > k_hi) {
+            A.cut(pa, k_hi - k, tid);
+            B.cut(pb, k_hi - k, tid);
+            __syncthreads();
+        }
+#pragma unroll
+        for (int s = 0; s < 4; ++s) {
+            typename Types<T>::Frag fa[MF], fb[NF];
+#pragma unroll
+            for (int i = 0; i < MF; ++i) fa[i] = A.read(pa, i, s);
+#pragma unroll
+            for (int j = 0; j < NF; ++j) fb[j] = B.read(pb, j, s);
+#pragma unroll
+            for (int i = 0; i < MF; ++i)
+#pragma unroll
+                for (int j = 0; j < NF; ++j) Types<T>::mma(fa[i], fb[j], acc[i][j]);
+        }
+        __syncthreads();
+    };
+    A.load(sA0, k_lo);
+    B.load(sB0, k_lo);
+    __syncthreads();
+    int k = k_lo;
+    for (; k + OpA::kBk < k_hi; k += 2 * OpA::kBk) {
+        A.load(sA1, k + OpA::kBk);
+        B.load(sB1, k + OpA::kBk);
+        stage(sA0, sB0, k);
+        if (k + 2 * OpA::kBk < k_hi) {
+            A.load(sA0, k + 2 * OpA::kBk);
+            B.load(sB0, k + 2 * OpA::kBk);
+        }
+        stage(sA1, sB1, k + OpA::kBk);
+    }
+    if (k < k_hi) stage(sA0, sB0, k);
+
+    // acc[i][j][r] of a lane: row m0 + wm BM / WM + 32 i + 8 (r / 4) + 4 (lane / 32) + r % 4, column n0 + wn BN / WN + 32 j + lane % 32
+    const int mw = m0 + wm * (BM / WM) + 4 * (lane >> 5), nw = n0 + wn * (BN / WN) + (lane & 31);
+    if constexpr (EPI == kLse) {
+        float* red = reinterpret_cast<float*>(sA0);                 // [2][WM][BN]
+        if (m0 + BM > a.M) {
+#pragma unroll
+            for (int i = 0; i < MF; ++i)
+#pragma unroll
+                for (int r = 0; r < 16; ++r) {
+                    const bool out = mw + 32 * i + 8 * (r / 4) + r % 4 >= a.M;
+#pragma unroll
+                    for (int j = 0; j < NF; ++j) acc[i][j][r] = out ? -INFINITY : acc[i][j][r];
+                }
+        }
+#pragma unroll
+        for (int j = 0; j < NF; ++j) {
+            const int n = nw + 32 * j;
+            float mx = -INFINITY;
+#pragma unroll
+            for (int i = 0; i < MF; ++i)
+#pragma unroll
+                for (int r = 0; r < 16; ++r) mx = fmaxf(mx, acc[i][j][r]);
+            mx = fmaxf(mx, __shfl_xor(mx, 32, 64));
+            const float from = (mx == -INFINITY ? 0.f : mx) * kLog2e;
+            float sum = 0.f;
+#pragma unroll
+            for (int i = 0; i < MF; ++i)
+#pragma unroll
+                for (int r = 0; r < 16; ++r) sum += __builtin_amdgcn_exp2f(fmaf(acc[i][j][r], kLog2e, -from));
+            sum += __shfl_xor(sum, 32, 64);
+            if (lane < 32) {
+                red[wm * BN + n - n0] = mx;
+                red[(WM + wm) * BN + n - n0] = sum;
+            }
+            // the target's logit, where this wave holds it
+            const int64_t t = n < a.N ? target_of(a, n) - a.v0 - mw : -1;
+            const bool here = t >= 0 && t < BM / WM && (t & 4) == 0 && t + mw < a.M;
+            if (__ballot(here)) {
+#pragma unroll
+                for (int i = 0; i < MF; ++i)
+#pragma unroll
+                    for (int r = 0; r < 16; ++r)
+                        if (here && t == 32 * i + 8 * (r / 4) + r % 4) a.target_logit[n] = acc[i][j][r];
+            }
+        }
+        __syncthreads();
+        for (int c = tid; c < BN; c += 64 * kWaves) {
+            if (n0 + c >= a.N) break;
+            float mx = red[c], sum = 0.f;
+#pragma unroll
+            for (int o = 1; o < WM; ++o) mx = fmaxf(mx, red[o * BN + c]);
+            const float safe = mx == -INFINITY ? 0.f : mx;
+#pragma unroll
+            for (int o = 0; o < WM; ++o) sum += red[(WM + o) * BN + c] * __builtin_amdgcn_exp2f((red[o * BN + c] - safe) * kLog2e);
+            a.part_max[static_cast<int64_t>(tm) * a.N + n0 + c] = mx;
+            a.part_sum[static_cast<int64_t>(tm) * a.N + n0 + c] = sum;
+        }
+    } else if constexpr (EPI == kProb) {
+#pragma unroll
+        for (int j = 0; j < NF; ++j) {
+            const int n = nw + 32 * j;
+            if (n >= a.N) continue;
+            const int64_t t = target_of(a, n);
+            const bool on = t >= 0 && t < a.vocab;
+            const float lse = a.lse[n] * kLog2e, g = on ? a.dloss[n] : 0.f;
+            T* row = static_cast<T*>(a.P) + static_cast<int64_t>(n) * a.ldp;
+#pragma unroll
+            for (int i = 0; i < MF; ++i)
+#pragma unroll
+                for (int q = 0; q < 4; ++q) {
+                    const int m = mw + 32 * i + 8 * q;
+                    float f[4];
+#pragma unroll
+                    for (int r = 0; r < 4; ++r) {
+                        float p = __builtin_amdgcn_exp2f(fmaf(acc[i][j][4 * q + r], kLog2e, -lse));
+                        if (a.v0 + m + r == t) p -= 1.f;
+                        f[r] = on && m + r < a.M ? p * g : 0.f;
+                    }
+                    if (m < a.M) put_four(row, m, a.M, f);
+                }
+        }
+    } else {
+        const bool split = gridDim.y > 1;
+#pragma unroll
+        for (int j = 0; j < NF; ++j) {
+            const int n = nw + 32 * j;
+            if (n >= a.N) continue;
+            float* sum = a.sum ? a.sum + (static_cast<int64_t>(blockIdx.y) * a.N + n) * a.M : nullptr;
+#pragma unroll
+            for (int i = 0; i < MF; ++i)
+#pragma unroll
+                for (int q = 0; q < 4; ++q) {
+                    const int m = mw + 32 * i + 8 * q;
+                    if (m >= a.M) continue;
+                    float f[4];
+#pragma unroll
+                    for (int r = 0; r < 4; ++r) f[r] = acc[i][j][4 * q + r] + (a.add && !split && m + r < a.M ? sum[m + r] : 0.f);
+                    if (a.out && !split) put_four(static_cast<T*>(a.out) + static_cast<int64_t>(n) * a.ldo, m, a.M, f);
+                    else put_four(sum, m, a.M, f);
+                }
+        }
+    }
+}
+
+// ------------------------------------------------------------- around them
+// rows of `dim` entries into rows of `dp`, zeros behind them; with targets, rows
+// that they leave out become zeros
+struct PackArgs {
+    const void* in;
+    int64_t ld;
+    void* out;
+    int64_t rows;
+    int dim, dp;
+    const void* target;
+    int target64, vocab;
+};
+template <typename T>
+__global__ __launch_bounds__(256) void vocab_pack_kernel(const PackArgs a) {
+    const int per = a.dp / 8;                       // runs of eight
+    const int64_t id = static_cast<int64_t>(blockIdx.x) * 256 + threadIdx.x;
+    if (id >= a.rows * per) return;
+    const int64_t row = id / per;
+    const int c = static_cast<int>(id - row * per) * 8;
+    bool on = true;
+    if (a.target) {
+        const int64_t t = a.target64 ? static_cast<const int64_t*>(a.target)[row] : static_cast<const int32_t*>(a.target)[row];
+        on = t >= 0 && t < a.vocab;
+    }
+    const T* in = static_cast<const T*>(a.in) + row * a.ld;
+    T v[8];
+    if (on && c + 8 <= a.dim) {
+        __builtin_memcpy(v, in + c, sizeof(v));
+    } else {
+#pragma unroll
+        for (int i = 0; i < 8; ++i) v[i] = on && c + i < a.dim ? in[c + i] : T(0);
+    }
+    __builtin_memcpy(static_cast<T*>(a.out) + row * a.dp + c, v, sizeof(v));
+}
+
+// a token's tiles into its lse and loss: 32 tokens a workgroup, 8 lines of tiles
+struct LseArgs {
+    const float *part_max, *part_sum, *target_logit;
+    const void* target;
+    int target64, vocab, tiles;
+    int tokens;
+    float *loss, *lse;
+};
+__global__ __launch_bounds__(256) void vocab_lse_kernel(const LseArgs a) {
+    __shared__ float red[2][8][32];
+    const int c = threadIdx.x & 31, line = threadIdx.x >> 5, t = blockIdx.x * 32 + c;
+    float mx = -INFINITY, sum = 0.f;
+    if (t < a.tokens)
+        for (int v = line; v < a.tiles; v += 8) {
+            const float m = a.part_max[static_cast<int64_t>(v) * a.tokens + t], s = a.part_sum[static_cast<int64_t>(v) * a.tokens + t];
+            const float top = fmaxf(mx, m), safe = top == -INFINITY ? 0.f : top;
+            sum = sum * __builtin_amdgcn_exp2f((mx - safe) * kLog2e) + s * __builtin_amdgcn_exp2f((m - safe) * kLog2e);
+            mx = top;
+        }
+    red[0][line][c] = mx;
+    red[1][line][c] = sum;
+    __syncthreads();
+    if (line || t >= a.tokens) return;
+    for (int o = 1; o < 8; ++o) mx = fmaxf(mx, red[0][o][c]);
+    const float safe = mx == -INFINITY ? 0.f : mx;
+    sum = 0.f;
+    for (int o = 0; o < 8; ++o) sum += red[1][o][c] * __builtin_amdgcn_exp2f((red[0][o][c] - safe) * kLog2e);
+    const float lse = safe + logf(sum);
+    a.lse[t] = lse;
+    const int64_t g = a.target64 ? static_cast<const int64_t*>(a.target)[t] : static_cast<const int32_t*>(a.target)[t];
+    a.loss[t] = g >= 0 && g < a.vocab ? lse - a.target_logit[t] : 0.f;
+}
+
+// the splits of a product, in order
+struct JoinArgs {
+    const float* part;
+    int splits;
+    int64_t count;                  // entries of one split
+    int M;
+    float* sum;                     // added to and written where there is no out
+    int add;
+    void* out;
+    int64_t ldo;
+};
+template <typename T>
+__global__ __launch_bounds__(256) void vocab_join_kernel(const JoinArgs a) {
+    const int64_t i = static_cast<int64_t>(blockIdx.x) * 256 + threadIdx.x;
+    if (i >= a.count) return;
+    float s = a.add ? a.sum[i] : 0.f;
+    for (int z = 0; z < a.splits; ++z) s += a.part[z * a.count + i];
+    if (a.out) st(static_cast<T*>(a.out) + i / a.M * a.ldo, i % a.M, s);
+    else a.sum[i] = s;
+}
+
+// ------------------------------------------------------------------ launch
+int ceil_div(int64_t a, int64_t b) { return static_cast<int>((a + b - 1) / b); }
+
+template <typename T, bool AO, bool BO, Epilogue EPI>
+void gemm(GemmArgs a, bool wide, int splits, hipStream_t s) {
+    const int tile = wide ? 256 : 128;
+    a.tiles_m = ceil_div(a.M, tile);
+    a.tiles_n = ceil_div(a.N, tile);
+    constexpr int kBk = kStage / static_cast<int>(sizeof(T));
+    a.k_split = ceil_div(ceil_div(a.K, kBk), splits) * kBk;
+    const dim3 grid(static_cast<uint32_t>(a.tiles_m) * static_cast<uint32_t>(a.tiles_n), ceil_div(a.K, a.k_split));
+    if (wide) vocab_gemm_kernel<T, 256, 256, 2, 4, AO, BO, EPI><<<grid, 512, 0, s>>>(a);
+    else vocab_gemm_kernel<T, 128, 128, 2, 2, AO, BO, EPI><<<grid, 256, 0, s>>>(a);
+}
+
+// a product into `out` (or added to `sum`), through the splits' parts where there are several
+template <typename T, bool BO>
+void product(GemmArgs a, const vs::VocabTiles& t, float* part, hipStream_t s) {
+    constexpr int kBk = kStage / static_cast<int>(sizeof(T));
+    const int splits = ceil_div(a.K, ceil_div(ceil_div(a.K, kBk), t.splits) * kBk);     // none of them empty
+    if (splits == 1) return gemm<T, true, BO, kSum>(a, t.wide, 1, s);
+    GemmArgs g = a;
+    g.sum = part;
+    gemm<T, true, BO, kSum>(g, t.wide, splits, s);
+    JoinArgs j{};
+    j.part = part; j.splits = splits; j.count = static_cast<int64_t>(a.N) * a.M; j.M = a.M; j.sum = a.sum; j.add = a.add;
+    j.out = a.out; j.ldo = a.ldo;
+    vocab_join_kernel<T><<<ceil_div(j.count, 256), 256, 0, s>>>(j);
+}
+
+template <typename T>
+void pack(const void* in, int64_t ld, void* out, int64_t rows, const vs::VocabCall& c, const void* target, hipStream_t s) {
+    PackArgs a{};
+    a.in = in; a.ld = ld; a.out = out; a.rows = rows; a.dim = static_cast<int>(c.dim); a.dp = static_cast<int>(c.plan.dp);
+    a.target = target; a.target64 = c.target64; a.vocab = static_cast<int>(c.vocab);
+    vocab_pack_kernel<T><<<ceil_div(rows * (a.dp / 8), 256), 256, 0, s>>>(a);
+}
+
+template <typename T>
+int launch(const vs::VocabCall& c) {
+    const auto s = static_cast<hipStream_t>(c.stream);
+    const vs::VocabPlan& p = c.plan;
+    char* ws = static_cast<char*>(c.ws);
+    const T *x = static_cast<const T*>(c.x), *W = static_cast<const T*>(c.W);
+    int64_t ldx = c.ldx, ldw = c.dim;
+    if (c.grad || p.pack_x) {
+        pack<T>(x, ldx, ws + p.x, c.tokens, c, c.grad ? c.target : nullptr, s);
+        x = reinterpret_cast<const T*>(ws + p.x);
+        ldx = p.dp;
+    }
+    if (p.pack_w) {
+        pack<T>(W, ldw, ws + p.w, c.vocab, c, nullptr, s);
+        W = reinterpret_cast<const T*>(ws + p.w);
+        ldw = p.dp;
+    }
+    GemmArgs l{};
+    l.A = W; l.lda = ldw; l.B = x; l.ldb = ldx; l.N = static_cast<int>(c.tokens); l.K = static_cast<int>(c.dim);
+    l.target = c.target; l.target64 = c.target64; l.vocab = static_cast<int>(c.vocab);
+    if (!c.grad) {
+        l.M = static_cast<int>(c.vocab);
+        l.part_max = reinterpret_cast<float*>(ws + p.part);
+        l.part_sum = l.part_max + static_cast<int64_t>(p.tiles) * c.tokens;
+        l.target_logit = reinterpret_cast<float*>(ws + p.logit);
+        gemm<T, false, false, kLse>(l, p.logits.wide, 1, s);
+        LseArgs e{};
+        e.part_max = l.part_max; e.part_sum = l.part_sum; e.target_logit = l.target_logit; e.target = c.target; e.target64 = c.target64;
+        e.vocab = l.vocab; e.tiles = p.tiles; e.tokens = l.N; e.loss = c.loss; e.lse = c.lse;
+        vocab_lse_kernel<<<ceil_div(c.tokens, 32), 256, 0, s>>>(e);
+    } else {
+        float *part = reinterpret_cast<float*>(ws + p.part), *sum = reinterpret_cast<float*>(ws + p.sum);
+        for (int64_t v0 = 0; v0 < c.vocab; v0 += p.piece) {
+            const int n = static_cast<int>(c.vocab - v0 < p.piece ? c.vocab - v0 : p.piece);
+            const bool last = v0 + n == c.vocab;
+            l.A = W + v0 * ldw; l.M = n; l.v0 = static_cast<int>(v0);
+            l.lse = c.lse_in; l.dloss = c.dloss; l.P = ws + p.P;
+            l.ldp = ceil_div(n, 8) * 8;                 // rows of whole 16 bytes
+            gemm<T, false, false, kProb>(l, p.logits.wide, 1, s);
+            GemmArgs g{};
+            g.A = W + v0 * ldw; g.lda = ldw; g.B = l.P; g.ldb = l.ldp;
+            g.M = static_cast<int>(c.dim); g.N = static_cast<int>(c.tokens); g.K = n;
+            g.add = v0 > 0; g.sum = p.pieces > 1 ? sum : nullptr;
+            g.out = last ? c.dx : nullptr; g.ldo = c.dim;
+            product<T, false>(g, p.dx, part, s);
+            g = GemmArgs{};
+            g.A = x; g.lda = ldx; g.B = l.P; g.ldb = l.ldp;
+            g.M = static_cast<int>(c.dim); g.N = n; g.K = static_cast<int>(c.tokens);
+            g.out = static_cast<T*>(c.dW) + v0 * c.dim; g.ldo = c.dim;
+            product<T, true>(g, p.dw, part, s);
+        }
+    }
+    const hipError_t e = hipGetLastError();
+    return e == hipSuccess ? VS_OK : vs::fail(VS_ERR_HIP, std::string("kernel launch: ") + hipGetErrorString(e));
+}
+
+int run(vs::VocabCall& c) {
+    if (int rc = vs::prepare_vocab(c)) return rc;
+    return c.dtype == VS_BF16 ? launch<uint16_t>(c) : launch<float>(c);
+}
+
+}  // namespace
+
+extern "C" {
+
+int vocab_loss(int64_t tokens, int64_t dim, int64_t vocab, int dtype, const void* x, int64_t x_stride,
+               const void* W, const void* target, int target_bits, float* loss, float* lse,
+               void* workspace, size_t workspace_bytes, void* stream) {
+    vs::VocabCall c{};
+    c.tokens = tokens; c.dim = dim; c.vocab = vocab; c.dtype = dtype; c.x = x; c.ldx = x_stride; c.W = W; c.target = target;
+    c.target_bits = target_bits; c.loss = loss; c.lse = lse; c.ws = workspace; c.ws_bytes = workspace_bytes; c.stream = stream;
+    return run(c);
+}
+
+int vocab_loss_grad(int64_t tokens, int64_t dim, int64_t vocab, int dtype, const void* x, int64_t x_stride,
+                    const void* W, const void* target, int target_bits, const float* lse, const float* dloss,
+                    void* dx, void* dW, void* workspace, size_t workspace_bytes, void* stream) {
+    vs::VocabCall c{};
+    c.tokens = tokens; c.dim = dim; c.vocab = vocab; c.dtype = dtype; c.x = x; c.ldx = x_stride; c.W = W; c.target = target;
+    c.target_bits = target_bits; c.lse_in = lse; c.dloss = dloss; c.dx = dx; c.dW = dW; c.ws = workspace;
+    c.ws_bytes = workspace_bytes; c.stream = stream; c.grad = true;
+    return run(c);
+}
+
+}  // extern "C"

@@ -89,4 +89,39 @@ struct NormCall {
 };
 int prepare_norm(NormCall& c);
 
+// ---- the vocabulary loss (vocab.hip)
+constexpr int kVocabStage = 128;                     // bytes of k that a product takes at a time
+// tiles of 256 x 256 (or 128 x 128), the product's k cut into `splits`
+struct VocabTiles { bool wide; int splits; };
+struct VocabPlan {
+    int64_t dp;                                      // row length of packed operands
+    bool pack_x, pack_w;
+    VocabTiles logits, dx, dw;
+    int tiles;                                       // of the vocabulary, forward
+    int64_t piece;                                   // vocabulary entries of a piece of the gradient
+    int64_t pieces;
+    size_t x, w, part, logit, P, sum, bytes;         // offsets in the workspace, and its size
+};
+struct VocabCall {
+    int64_t tokens, dim, vocab;
+    int dtype;
+    const void* x;
+    int64_t ldx;
+    const void* W;
+    const void* target;
+    int target_bits;
+    float *loss, *lse;
+    void* ws;
+    size_t ws_bytes;
+    void* stream;
+    // gradient
+    bool grad = false;
+    const float *lse_in, *dloss;
+    void *dx, *dW;
+    int target64;
+    VocabPlan plan;
+};
+VocabPlan vocab_plan(bool grad, int64_t tokens, int64_t dim, int64_t vocab, int dtype);
+int prepare_vocab(VocabCall& c);
+
 }  // namespace vs
