@@ -267,7 +267,7 @@ int prepare_vocab(VocabCall& c) {
     if (c.grad ? !c.lse_in || !c.dloss || !c.dx || !c.dW : !c.loss || !c.lse)
         return fail(VS_ERR_NULL, c.grad ? "lse, dloss, dx and dW must not be NULL" : "loss and lse must not be NULL");
     if (c.ldx == 0) c.ldx = c.dim;
-    if (c.ldx < c.dim && c.tokens > 1) return fail(VS_ERR_SHAPE, "x_stride is smaller than dim");
+    if (c.ldx < c.dim) return fail(VS_ERR_SHAPE, "x_stride is smaller than dim");
     if (c.ldx >= (int64_t(1) << 28)) return fail(VS_ERR_UNSUPPORTED, "row strides of 2^28 elements or more are not supported");
     c.plan = vocab_plan(c.grad, c.tokens, c.dim, c.vocab, c.dtype);
     const size_t es = esize(c.dtype);
