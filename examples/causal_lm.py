@@ -1,21 +1,23 @@
-"""A small causal language model of S6 mixers, trained and decoded with the
-library's causal entry points.
+"""A small causal language model of S6 mixers (or of gated recurrences), trained
+and decoded with the library's entry points for language models.
 
-    python examples/causal_lm.py [--steps N] [--beams K] [--move]
+    python examples/causal_lm.py [--steps N] [--beams K] [--move] [--mixer s6|gated]
 
 It learns arithmetic progressions modulo the vocabulary (the first two tokens
 give the step), then continues prompts of different lengths by beam search:
 
-  training   s6_causal_conv_autograd and s6_causal_scan_autograd
-  prompts    s6_causal_conv and s6_causal_scan on a ragged batch, keeping states
-  decoding   s6_conv_step and s6_scan_step on pools of two sets of states:
+  training   s6_causal_conv_autograd, s6_causal_scan_autograd (or
+             gated_scan_autograd), rms_norm_autograd with each residual, and
+             vocab_loss_autograd, which keeps no logits
+  prompts    s6_causal_conv and s6_causal_scan (gated_scan) on a ragged batch,
+             keeping states
+  decoding   s6_conv_step and s6_scan_step (gated_scan_step) on pools of two sets of states:
              a step reads one set, at the parents that beam_select chose, and
              writes the other, so no state is moved between tokens; or, with
              --move, on one set, half the memory, which beam_reorder brings
              into the beams' order after each token
 
-Random weights and synthetic sequences; the linear maps, norms and the loss are
-torch's own.
+Random weights and synthetic sequences; the linear maps are torch's own.
 """
 import argparse
 import math
@@ -23,7 +25,6 @@ import os
 import sys
 
 import torch
-import torch.nn.functional as F
 
 sys.path.insert(0, os.path.dirname(os.path.dirname(os.path.abspath(__file__))))
 import vision_mamba_selective_amd as vms  # noqa: E402
@@ -31,8 +32,9 @@ import vision_mamba_selective_amd as vms  # noqa: E402
 VOCAB, MODEL, INNER, STATE, WIDTH, LAYERS = 32, 64, 128, 16, 4, 2
 
 
-def init(seed=0, device="cuda"):
-    """The model's weights: a dict of leaf tensors."""
+def init(seed=0, device="cuda", mixer="s6"):
+    """The model's weights: a dict of leaf tensors. mixer: "s6", or "gated" for
+    the gated recurrence, whose two gates are projections of its input."""
     g = torch.Generator().manual_seed(seed)
     rnd = lambda *s, scale: (torch.randn(*s, generator=g) * scale).to(device).requires_grad_()   # noqa: E731
     p = dict(embed=rnd(VOCAB, MODEL, scale=0.5), head=rnd(VOCAB, MODEL, scale=MODEL ** -0.5))
@@ -40,18 +42,21 @@ def init(seed=0, device="cuda"):
         dt = torch.exp(torch.rand(INNER, generator=g) * math.log(100.0) + math.log(1e-3))
         p["in%d" % i] = rnd(2 * INNER, MODEL, scale=MODEL ** -0.5)
         p["out%d" % i] = rnd(MODEL, INNER, scale=INNER ** -0.5)
-        p["x%d" % i] = rnd(2 * STATE + 1, INNER, scale=INNER ** -0.5)
-        p["dt%d" % i] = rnd(INNER, scale=0.1)
+        p["norm%d" % i] = torch.ones(MODEL, device=device, requires_grad=True)
+        if mixer == "gated":
+            p["gates%d" % i] = rnd(2 * INNER, INNER, scale=INNER ** -0.5)
+            top = 0.9 + 0.099 * torch.rand(INNER, generator=g)      # decays at a full gate
+            p["lam%d" % i] = torch.log(torch.expm1(-torch.log(top) / 8)).to(device).requires_grad_()
+        else:
+            p["x%d" % i] = rnd(2 * STATE + 1, INNER, scale=INNER ** -0.5)
+            p["dt%d" % i] = rnd(INNER, scale=0.1)
+            p["bias%d" % i] = torch.log(torch.expm1(dt)).to(device).requires_grad_()
+            p["A%d" % i] = (-(torch.arange(STATE) + 1.0)).repeat(INNER, 1).to(device).requires_grad_()
+            p["D%d" % i] = torch.ones(INNER, device=device, requires_grad=True)
         p["w%d" % i] = rnd(INNER, WIDTH, scale=WIDTH ** -0.5)
         p["b%d" % i] = rnd(INNER, scale=0.0)
-        p["bias%d" % i] = torch.log(torch.expm1(dt)).to(device).requires_grad_()
-        p["A%d" % i] = (-(torch.arange(STATE) + 1.0)).repeat(INNER, 1).to(device).requires_grad_()
-        p["D%d" % i] = torch.ones(INNER, device=device, requires_grad=True)
+    p["norm%d" % LAYERS] = torch.ones(MODEL, device=device, requires_grad=True)
     return p
-
-
-def norm(x):
-    return x * torch.rsqrt(x.square().mean(1, keepdim=True) + 1e-6)
 
 
 def projections(p, i, u):
@@ -60,17 +65,31 @@ def projections(p, i, u):
     return p["dt%d" % i][:, None] * r[:, 2 * STATE:], r[:, :STATE], r[:, STATE:2 * STATE]
 
 
+def gates(p, i, u):
+    """Both gates of the recurrence from its input u [rows, INNER, L]."""
+    return (p["gates%d" % i] @ u).split(INNER, dim=1)
+
+
+def hidden(p, tokens):
+    """What the head reads of whole sequences, [rows, MODEL, L], differentiable."""
+    branch, x = p["embed"][tokens].transpose(1, 2).contiguous(), None      # channel-major: [rows, MODEL, L]
+    for i in range(LAYERS):
+        y, x = vms.rms_norm_autograd(branch, p["norm%d" % i], residual=x)
+        xz = p["in%d" % i] @ y
+        u, _ = vms.s6_causal_conv_autograd(xz[:, :INNER], p["w%d" % i], p["b%d" % i])
+        if "lam%d" % i in p:
+            y, _ = vms.gated_scan_autograd(u, *gates(p, i, u), p["lam%d" % i], z=xz[:, INNER:])
+        else:
+            delta, B, C = projections(p, i, u)
+            y, _ = vms.s6_causal_scan_autograd(u, delta.contiguous(), xz[:, INNER:], B.contiguous(), C.contiguous(), p["A%d" % i],
+                                               p["D%d" % i], p["bias%d" % i])
+        branch = p["out%d" % i] @ y
+    return vms.rms_norm_autograd(branch, p["norm%d" % LAYERS], residual=x)[0]
+
+
 def forward(p, tokens):
     """Logits [rows, L, VOCAB] of whole sequences, differentiable."""
-    x = p["embed"][tokens].transpose(1, 2)                          # channel-major: [rows, MODEL, L]
-    for i in range(LAYERS):
-        xz = p["in%d" % i] @ norm(x)
-        u, _ = vms.s6_causal_conv_autograd(xz[:, :INNER], p["w%d" % i], p["b%d" % i])
-        delta, B, C = projections(p, i, u)
-        y, _ = vms.s6_causal_scan_autograd(u, delta.contiguous(), xz[:, INNER:], B.contiguous(), C.contiguous(), p["A%d" % i],
-                                           p["D%d" % i], p["bias%d" % i])
-        x = x + p["out%d" % i] @ y
-    return norm(x).transpose(1, 2) @ p["head"].T
+    return hidden(p, tokens).transpose(1, 2) @ p["head"].T
 
 
 def progressions(rows, length, g, device="cuda"):
@@ -86,7 +105,8 @@ def train(p, steps, seed=1, rows=64, length=24, lr=3e-3):
     losses = []
     for _ in range(steps):
         t = progressions(rows, length + 1, g)
-        loss = F.cross_entropy(forward(p, t[:, :-1]).reshape(-1, VOCAB), t[:, 1:].reshape(-1))
+        h = hidden(p, t[:, :-1]).transpose(1, 2).reshape(-1, MODEL)
+        loss = vms.vocab_loss_autograd(h, p["head"], t[:, 1:].reshape(-1)).mean()
         opt.zero_grad()
         loss.backward()
         opt.step()
@@ -97,32 +117,43 @@ def train(p, steps, seed=1, rows=64, length=24, lr=3e-3):
 @torch.no_grad()
 def prompt(p, tokens, lengths):
     """The last token's logits [rows, VOCAB] of a ragged batch, and each layer's (window, h)."""
-    x = p["embed"][tokens].transpose(1, 2)
+    branch, x = p["embed"][tokens].transpose(1, 2).contiguous(), None
     states = []
     for i in range(LAYERS):
-        xz = p["in%d" % i] @ norm(x)
+        y, x = vms.rms_norm(branch, p["norm%d" % i], residual=x, lengths=lengths)
+        xz = p["in%d" % i] @ y
         u, window = vms.s6_causal_conv(xz[:, :INNER], p["w%d" % i], p["b%d" % i], lengths=lengths)
-        delta, B, C = projections(p, i, u)
-        y, h = vms.s6_causal_scan(u, delta.contiguous(), xz[:, INNER:], B, C, p["A%d" % i], p["D%d" % i], p["bias%d" % i],
-                                  lengths=lengths)
+        if "lam%d" % i in p:
+            y, h = vms.gated_scan(u, *gates(p, i, u), p["lam%d" % i], z=xz[:, INNER:], lengths=lengths)
+        else:
+            delta, B, C = projections(p, i, u)
+            y, h = vms.s6_causal_scan(u, delta.contiguous(), xz[:, INNER:], B, C, p["A%d" % i], p["D%d" % i], p["bias%d" % i],
+                                      lengths=lengths)
         states.append((window, h))
-        x = x + p["out%d" % i] @ y
-    last = x.gather(2, (lengths.long() - 1)[:, None, None].expand(-1, MODEL, 1))
-    return (norm(last).squeeze(2) @ p["head"].T), states
+        branch = p["out%d" % i] @ y
+    at = (lengths.long() - 1)[:, None, None].expand(-1, MODEL, 1)
+    last, _ = vms.rms_norm(branch.gather(2, at).squeeze(2), p["norm%d" % LAYERS], residual=x.gather(2, at).squeeze(2))
+    return last @ p["head"].T, states
 
 
 @torch.no_grad()
 def step(p, token, pools, slot_in, slot_out):
     """One token of every row: logits [rows, VOCAB]; pools hold each layer's (window, h)."""
-    x = p["embed"][token.long()]
+    branch, x = p["embed"][token.long()], None
     for i, (window, h) in enumerate(pools):
-        xz = norm(x) @ p["in%d" % i].T
+        y, x = vms.rms_norm(branch, p["norm%d" % i], residual=x)
+        xz = y @ p["in%d" % i].T
         u = vms.s6_conv_step(xz[:, :INNER], p["w%d" % i], p["b%d" % i], window, slot_in=slot_in, slot_out=slot_out)
-        r = u @ p["x%d" % i].T
-        y = vms.s6_scan_step(u, r[:, 2 * STATE:] * p["dt%d" % i], xz[:, INNER:], r[:, :STATE], r[:, STATE:2 * STATE],
-                             p["A%d" % i], p["D%d" % i], p["bias%d" % i], h, slot_in=slot_in, slot_out=slot_out)
-        x = x + y @ p["out%d" % i].T
-    return norm(x) @ p["head"].T
+        if "lam%d" % i in p:
+            r, gate = (u @ p["gates%d" % i].T).split(INNER, dim=1)
+            y = vms.gated_scan_step(u, r, gate, p["lam%d" % i], h, z=xz[:, INNER:], slot_in=slot_in, slot_out=slot_out)
+        else:
+            r = u @ p["x%d" % i].T
+            y = vms.s6_scan_step(u, r[:, 2 * STATE:] * p["dt%d" % i], xz[:, INNER:], r[:, :STATE], r[:, STATE:2 * STATE],
+                                 p["A%d" % i], p["D%d" % i], p["bias%d" % i], h, slot_in=slot_in, slot_out=slot_out)
+        branch = y @ p["out%d" % i].T
+    y, _ = vms.rms_norm(branch, p["norm%d" % LAYERS], residual=x)
+    return y @ p["head"].T
 
 
 @torch.no_grad()
@@ -172,8 +203,9 @@ def main():
     ap.add_argument("--steps", type=int, default=300, help="training steps")
     ap.add_argument("--beams", type=int, default=4)
     ap.add_argument("--move", action="store_true", help="one set of states, moved to the beams that go on")
+    ap.add_argument("--mixer", choices=("s6", "gated"), default="s6")
     a = ap.parse_args()
-    p = init()
+    p = init(mixer=a.mixer)
     losses = train(p, a.steps)
     print("loss %.3f at the start, %.3f at the end of %d steps" % (losses[0], losses[-1], a.steps))
     g = torch.Generator().manual_seed(7)
