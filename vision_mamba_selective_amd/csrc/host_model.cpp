@@ -147,7 +147,7 @@ NormForm norm_rows(int64_t dim, int dtype) {
 int64_t norm_parts(NormForm f, int64_t batch, int64_t L) {
     if (f == kNormColumn) return batch * ceil_div(L, kNormTile);
     const int64_t per = f == kNormRow1 ? 4 : 1, groups = ceil_div(batch, per);
-    return (groups < 512 ? groups : 512) * per;
+    return (groups < kNormGroups ? groups : kNormGroups) * per;
 }
 
 }  // namespace

@@ -474,26 +474,45 @@ __global__ __launch_bounds__(W == 1 ? 256 : 64 * W) void norm_row_grad_kernel(co
         for (int i = 0; i < N; ++i) dw[k][i] = 0.f;
     const int64_t first = W == 1 ? static_cast<int64_t>(blockIdx.x) * 4 + r.wave : blockIdx.x;
     const int64_t step = static_cast<int64_t>(gridDim.x) * (W == 1 ? 4 : 1);
-    int odd = 0;
-    for (int64_t b = first; b < a.rows; b += step, odd ^= 1) {
-        const int n = a.lengths && a.lengths[b] < 1 ? 0 : a.dim;
+    // the next row is read while this one is worked on
+    Pack<T> ps[HOLD], py[HOLD], pg[HOLD];
+    int n = 0;
+    auto read = [&](int64_t b) VS_INLINE {
+        n = a.lengths && a.lengths[b] < 1 ? 0 : a.dim;                // an empty row reads nothing
         const T *s = at<T>(a.x, b * a.sx.b), *dy = at<T>(a.dy, b * a.sdy.b);
         const T* dsum = a.dsum ? at<T>(a.dsum, b * a.sdsum.b) : nullptr;
-        T* ds = static_cast<T*>(a.y) + b * a.dim;
-        Pack<T> ps[HOLD], py[HOLD], pg;                  // longer rows read dsum where they use it
-        float ss = 0.f, sd = 0.f;
 #pragma unroll
         for (int k = 0; k < HOLD; ++k) {
             const int i0 = k * kStep + r.tid * N;
             ps[k].load(s, i0, n);
             py[k].load(dy, i0, n);
-            if (HOLD == 1 && dsum) pg.load(dsum, i0, n);
+            if (dsum) pg[k].load(dsum, i0, n);
+        }
+    };
+    if (first < a.rows) read(first);
+    int odd = 0;
+    for (int64_t b = first; b < a.rows; b += step, odd ^= 1) {
+        T* ds = static_cast<T*>(a.y) + b * a.dim;
+        const bool real = n != 0;
+        Pack<T> hs[HOLD], hy[HOLD], hg[HOLD];
+        float ss = 0.f, sd = 0.f;
+#pragma unroll
+        for (int k = 0; k < HOLD; ++k) {
+            hs[k] = ps[k];
+            hy[k] = py[k];
+            hg[k] = pg[k];
+            hs[k].settle();
+            hy[k].settle();
+        }
+        if (b + step < a.rows) read(b + step);
+#pragma unroll
+        for (int k = 0; k < HOLD; ++k) {
             float w[N];
-            weights(a.w, i0, a.dim, w);
+            weights(a.w, k * kStep + r.tid * N, a.dim, w);
 #pragma unroll
             for (int i = 0; i < N; ++i) {
-                ss = fmaf(ps[k].get(i), ps[k].get(i), ss);
-                sd = fmaf(w[i] * py[k].get(i), ps[k].get(i), sd);
+                ss = fmaf(hs[k].get(i), hs[k].get(i), ss);
+                sd = fmaf(w[i] * hy[k].get(i), hs[k].get(i), sd);
             }
         }
         ss = r.sum(ss, red[odd][0]);
@@ -503,15 +522,14 @@ __global__ __launch_bounds__(W == 1 ? 256 : 64 * W) void norm_row_grad_kernel(co
         for (int k = 0; k < HOLD; ++k) {
             const int i0 = k * kStep + r.tid * N;
             if (i0 >= a.dim) continue;
-            if (HOLD > 1 && dsum) pg.load(dsum, i0, n);
             float f[N], w[N];
             weights(a.w, i0, a.dim, w);
 #pragma unroll
             for (int i = 0; i < N; ++i) {
-                const float sv = ps[k].get(i), yv = py[k].get(i);
+                const float sv = hs[k].get(i), yv = hy[k].get(i);
                 const float d = q * (w[i] * yv - sv * m);
-                f[i] = n ? (dsum ? pg.get(i) + d : d) : 0.f;
-                if (n) dw[k][i] = fmaf(yv * q, sv, dw[k][i]);
+                f[i] = real ? (a.dsum ? hg[k].get(i) + d : d) : 0.f;
+                if (real) dw[k][i] = fmaf(yv * q, sv, dw[k][i]);
             }
             Pack<T> o;
             o.set(f);
@@ -536,6 +554,7 @@ __global__ __launch_bounds__(kDwCh* kDwLines) void norm_dw_kernel(const NormArgs
     const int ch = blockIdx.x * kDwCh + threadIdx.x % kDwCh, line = threadIdx.x / kDwCh;
     float s = 0.f;
     if (ch < a.dim)
+#pragma unroll 8
         for (int p = line; p < a.parts; p += kDwLines) s += a.part[static_cast<size_t>(p) * a.dim + ch];
     red[line][threadIdx.x % kDwCh] = s;
     __syncthreads();

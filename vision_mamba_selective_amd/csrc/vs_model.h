@@ -65,6 +65,7 @@ int prepare_gated_step(GatedStepCall& c);
 // ---- the norm (norm.hip)
 constexpr int kNormTile = 32;                        // tokens of a workgroup, channel-major
 constexpr int64_t kNormMaxDim = 8192;
+constexpr int64_t kNormGroups = 1024;                // workgroups that take the rows of a gradient in turn
 // channel-major, or rows in 1, 4 or 16 waves: the channels a lane holds bound
 // the row's length
 enum NormForm { kNormColumn, kNormRow1, kNormRow4, kNormRow16 };
