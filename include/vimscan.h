@@ -626,7 +626,7 @@ int gated_scan_saved(int64_t batch, int64_t dim, int64_t seqlen, int dtype, cons
  *   dh0         [batch][dim] fp32 or NULL
  *   workspace   gated_workspace_bytes(VS_GATED_GRAD, ...)
  * Every output is overwritten and repeats bit for bit (no atomics). Where a
- * gate has closed so far that s_t is below 1e-36, dr_t and that token's part
+ * gate has closed so far that s_t is below 5e-37, dr_t and that token's part
  * of dlam are zero (they tend to zero with the root of s_t).
  */
 int gated_scan_grad(int64_t batch, int64_t dim, int64_t seqlen, int dtype, const void* x,

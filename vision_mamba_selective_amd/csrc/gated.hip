@@ -48,29 +48,36 @@ __device__ __forceinline__ float sigmoid_f(float v) {
     return __builtin_amdgcn_rcpf(1.f + __builtin_amdgcn_exp2f(-v * kLog2e));
 }
 constexpr float kTiny = 0x1p-126f;
+constexpr float kSlow = 0.25f * kLog2e;
 
-// s, a = exp(-s) and q = 1 - a^2 from u = 1 - a, q = u (2 - u). Below s = 1/4
-// u = s p(s), with p the interpolation of (1 - exp(-s)) / s at Chebyshev points
-// of [0, 1/4] (degree 4, off by 5e-9): 1 - exp(-s) would cancel, and a = 1 - u is
-// rounded to nearest, where the hardware's exp2 leans to one side: over the
-// thousands of tokens that such decays remember that adds up (off by 1e-5 of
-// the state at decays of 0.999). a is held at 2^-126 or more: a zero would turn
-// an infinite state into NaN.
+// With w = s log2(e): a = 2^-w, u = 1 - a and q = 1 - a^2 = u (2 - u). Below
+// s = 1/4 u = w p(w), with p the interpolation of (1 - 2^-w) / w at Chebyshev
+// points (degree 4, off by 1.2e-8): 1 - 2^-w would cancel, and a = 1 - u is rounded
+// to nearest, where the hardware's exp2 leans to one side: over the thousands of
+// tokens that such decays remember that adds up (off by 1e-5 of the state at
+// decays of 0.999). a is held at 2^-126 or more: a zero would turn an infinite
+// state into NaN. A row whose gate can't reach 1/4 (SLOW) needs no other case: a
+// sixth of a token's instructions (8 x 768 x 4,097 bf16: XX us with it, XX without).
 struct Decay {
-    float s, a, q;
-    __device__ __forceinline__ void set(float k, float sr) {
-        s = k * sr;
-        const float e = __builtin_amdgcn_exp2f(at_least(-s * kLog2e, -126.f));
-        float p = fmaf(s, 0.007514301f, -0.041491f);
-        p = fmaf(s, p, 0.16665113f);
-        p = fmaf(s, p, -0.49999952f);
-        p = fmaf(s, p, 1.f);
-        const bool slow = s < 0.25f;
-        const float u = slow ? s * p : 1.f - e;
-        a = slow ? 1.f - u : e;
+    float w, a, q;
+    template <bool SLOW>
+    __device__ __forceinline__ void set(float k2, float sr) {
+        w = k2 * sr;
+        float p = fmaf(w, 0.0012023085f, -0.00957758f);
+        p = fmaf(w, p, 0.055498935f);
+        p = fmaf(w, p, -0.24022627f);
+        p = fmaf(w, p, 0.6931472f);
+        float u = w * p;
+        a = 1.f - u;
+        if constexpr (!SLOW) {
+            const float e = __builtin_amdgcn_exp2f(at_least(-w, -126.f));
+            const bool slow = w < kSlow;
+            u = slow ? u : 1.f - e;
+            a = slow ? a : e;
+        }
         q = u * (2.f - u);
     }
-    __device__ __forceinline__ void none() { s = 0.f; a = 1.f; q = 0.f; }
+    __device__ __forceinline__ void none() { w = 0.f; a = 1.f; q = 0.f; }
 };
 
 // ------------------------------------------------------------- lane scans
@@ -144,21 +151,33 @@ __device__ __forceinline__ void later_and_all(float P, float M, int lane, float&
 }
 
 // ------------------------------------------------------------------ tokens
-// eight tokens from t on of a row with len real ones, zeros past them
-template <typename T>
-__device__ __forceinline__ void load_tokens(Eight<T>& e, const T* p, int t, int len) {
-    if (t + kVec <= len) e.load(p + t);
-    else e.load_some(p, t, len);
-}
-template <typename T>
-__device__ __forceinline__ void store_tokens(T* p, int t, int L, const float (&f)[kVec]) {
-    if (t + kVec <= L) {
-        store_eight(p + t, f);
-    } else {
-#pragma unroll
-        for (int j = 0; j < kVec; ++j)
-            if (t + j < L) st(p, t + j, f[j]);
+// V tokens of a lane from t on (eight, or one in a row's short last block);
+// PART: of a row with len real ones, zeros past them
+template <typename T, int V>
+struct Tokens {
+    Eight<T> e;
+    template <bool PART>
+    __device__ __forceinline__ void load(const T* p, int t, int len) {
+        if (!PART || t + V <= len) e.load(p + t);
+        else e.load_some(p, t, len);
     }
+    __device__ __forceinline__ float get(int j) const { return e.get(j); }
+};
+template <typename T>
+struct Tokens<T, 1> {
+    uint32_t raw;
+    template <bool PART>
+    __device__ __forceinline__ void load(const T* p, int t, int len) { raw = t < len ? ld_raw(p, t) : 0u; }
+    __device__ __forceinline__ float get(int) const { return from_raw<T>(raw); }
+};
+template <bool PART, typename T, int V>
+__device__ __forceinline__ void store_tokens(T* p, int t, int L, const float (&f)[V]) {
+    if constexpr (V == 8) {
+        if (!PART || t + V <= L) return store_eight(p + t, f);
+    }
+#pragma unroll
+    for (int j = 0; j < V; ++j)
+        if (t + j < L) st(p, t + j, f[j]);
 }
 
 // What a lane knows of its row. Rows past the last are walked with no tokens
@@ -175,10 +194,24 @@ struct RowLane {
         b = row / a.dim;
         d = row - b * a.dim;
         lane = tid & (G - 1);
-        wave = NW > 1 ? tid >> 6 : 0;
+        wave = NW > 1 ? __builtin_amdgcn_readfirstlane(tid >> 6) : 0;
         L = real ? a.L : 0;
         len = L;
         if (a.lengths) len = min(max(a.lengths[b], 0), L);
+        if constexpr (G == 64) len = __builtin_amdgcn_readfirstlane(len);
+    }
+    // the wave's first token of chunk c, and this lane's
+    __device__ __forceinline__ int block_start(int c) const { return (c * NW + wave) * kVec * G; }
+    __device__ __forceinline__ int start(int c) const { return block_start(c) + lane * kVec; }
+    // whether any token of the wave's block is real, and whether all are (the
+    // same for the wave, which may be the only one of its row to go that way)
+    __device__ __forceinline__ bool live(int c) const {
+        if constexpr (G == 64) return block_start(c) < len;
+        else return __ballot(start(c) < len) != 0;
+    }
+    __device__ __forceinline__ bool full(int c) const {
+        if constexpr (G == 64) return block_start(c) + kVec * G <= len;
+        else return __ballot(start(c) + kVec > len) == 0;
     }
     __device__ __forceinline__ const T* in(const void* p, const vs::Strides& s) const {
         return static_cast<const T*>(p) + static_cast<int64_t>(b) * s.b + static_cast<int64_t>(d) * s.d;
@@ -191,6 +224,35 @@ struct Exchange {
     float P[2][NW], H[2][NW];
 };
 
+// What the waves of a row hand each other: the composition of each one's block.
+// A wave is at most one barrier ahead, so two buffers do.
+template <int NW, bool LATER>
+__device__ __forceinline__ float pass_on(Exchange<NW>& ex, int buf, int wave, int lane, float P, float H, float& carry) {
+    float mine = carry;
+    if constexpr (NW > 1) {
+        if (lane == 0) { ex.P[buf][wave] = P; ex.H[buf][wave] = H; }
+        __syncthreads();
+#pragma unroll
+        for (int k = 0; k < NW; ++k) {
+            const int o = LATER ? NW - 1 - k : k;
+            if (o == wave) mine = carry;
+            carry = fmaf(ex.P[buf][o], carry, ex.H[buf][o]);
+        }
+    } else {
+        carry = fmaf(P, carry, H);
+    }
+    return mine;
+}
+
+typedef std::integral_constant<int, kVec> Wide;
+typedef std::integral_constant<int, 1> Narrow;
+// A row's last block of at most 64 tokens is taken one token a lane: with eight a
+// row of 4,097 would spend a ninth of its time on one token.
+template <int G, int NW>
+__device__ __forceinline__ bool narrow_end(int L) {
+    return G == 64 && NW == 1 && L > kVec * G && (L - 1) % (kVec * G) < 64;
+}
+
 // ----------------------------------------------------------------- forward
 template <typename T, int G, int NW, bool GATED>
 __global__ __launch_bounds__(NW > 4 ? 64 * NW : 256) void gated_scan_kernel(const GatedArgs a) {
@@ -199,63 +261,92 @@ __global__ __launch_bounds__(NW > 4 ? 64 * NW : 256) void gated_scan_kernel(cons
     const RowLane<T, G, NW> w(a);
     const T *x = w.in(a.x, a.sx), *r = w.in(a.r, a.sr), *ig = w.in(a.i, a.si), *z = GATED ? w.in(a.z, a.sz) : nullptr;
     T* y = w.out(a.y, a.L);
-    const float k = a.rate * softplus_f(a.lam[w.d]);
+    const float k2 = a.rate * softplus_f(a.lam[w.d]) * kLog2e;
+    const bool slow = __ballot(!(k2 < kSlow)) == 0;
     float h = a.h0 ? a.h0[w.row] : 0.f;
 
-    Eight<T> ex_, er, ei, ez;
-    int t = w.wave * kBlock + w.lane * kVec;
-    auto load = [&](int at) VS_INLINE {
-        load_tokens(ex_, x, at, w.len);
-        load_tokens(er, r, at, w.len);
-        load_tokens(ei, ig, at, w.len);
-        if constexpr (GATED) load_tokens(ez, z, at, w.len);
-    };
-    load(t);
-    const int chunks = (a.L + kChunk - 1) / kChunk;
-    for (int c = 0; c < chunks; ++c, t += kChunk) {
-        float al[kVec], v[kVec], g[kVec];
+    // one block: composition of its tokens, of the lanes, of the waves, then the tokens again
+    auto block = [&](auto vec, auto is_slow, auto is_part, auto& tx, auto& tr, auto& ti, auto& tz, int t, int c, auto&& next) VS_INLINE {
+        constexpr int V = decltype(vec)::value;
+        constexpr bool SLOW = decltype(is_slow)::value, PART = decltype(is_part)::value;
+        float al[V], v[V], g[V];
         float P = 1.f, H = 0.f;
 #pragma unroll
-        for (int j = 0; j < kVec; ++j) {
+        for (int j = 0; j < V; ++j) {
             Decay e;
-            e.set(k, sigmoid_f(er.get(j)));
-            float in = __builtin_amdgcn_sqrtf(e.q) * sigmoid_f(ei.get(j)) * ex_.get(j);
-            if (t + j >= w.len) { e.a = 1.f; in = 0.f; }
+            e.template set<SLOW>(k2, sigmoid_f(tr.get(j)));
+            float in = __builtin_amdgcn_sqrtf(e.q) * (sigmoid_f(ti.get(j)) * tx.get(j));
+            if (PART && t + j >= w.len) { e.a = 1.f; in = 0.f; }
             al[j] = e.a;
             v[j] = in;
-            if constexpr (GATED) g[j] = silu_f(ez.get(j));
+            if constexpr (GATED) g[j] = silu_f(tz.get(j));
             H = fmaf(e.a, H, in);
             P *= e.a;
         }
         P = at_least(P, kTiny);
-        load(t + kChunk);
+        next();
         scan_up<G>(P, H);
         float Pb, Hb, Pa, Ha;
         before_and_all<G>(P, H, Pb, Hb, Pa, Ha);
-        float start = h;                                  // the state before this wave's block
-        if constexpr (NW > 1) {
-            const int buf = c & 1;
-            if (w.lane == 0) { ex.P[buf][w.wave] = Pa; ex.H[buf][w.wave] = Ha; }
-            __syncthreads();
-#pragma unroll
-            for (int o = 0; o < NW; ++o) {
-                if (o == w.wave) start = h;
-                h = fmaf(ex.P[buf][o], h, ex.H[buf][o]);
-            }
-        } else {
-            h = fmaf(Pa, h, Ha);
-        }
-        if (a.saved && w.lane == 0 && t < w.L) a.saved[static_cast<size_t>(w.row) * a.nblk + t / kBlock] = start;
+        const float start = pass_on<NW, false>(ex, c & 1, w.wave, w.lane, Pa, Ha, h);
+        if (a.saved && w.lane == 0 && w.L > 0) a.saved[static_cast<size_t>(w.row) * a.nblk + c * NW + w.wave] = start;
         float s = fmaf(Pb, start, Hb);
-        float f[kVec];
+        float f[V];
 #pragma unroll
-        for (int j = 0; j < kVec; ++j) {
+        for (int j = 0; j < V; ++j) {
             s = fmaf(al[j], s, v[j]);
             f[j] = s;
             if constexpr (GATED) f[j] *= g[j];
-            if (t + j >= w.len) f[j] = 0.f;
+            if (PART && t + j >= w.len) f[j] = 0.f;
         }
-        store_tokens(y, t, w.L, f);
+        store_tokens<PART>(y, t, w.L, f);
+    };
+
+    Tokens<T, kVec> tx, tr, ti, tz;
+    auto load = [&](int c) VS_INLINE {
+        if (!w.live(c)) return;
+        const int t = w.start(c);
+        if (w.full(c)) {
+            tx.template load<false>(x, t, w.len);
+            tr.template load<false>(r, t, w.len);
+            ti.template load<false>(ig, t, w.len);
+            if constexpr (GATED) tz.template load<false>(z, t, w.len);
+        } else {
+            tx.template load<true>(x, t, w.len);
+            tr.template load<true>(r, t, w.len);
+            ti.template load<true>(ig, t, w.len);
+            if constexpr (GATED) tz.template load<true>(z, t, w.len);
+        }
+    };
+    const int chunks = (a.L + kChunk - 1) / kChunk, wide = chunks - (narrow_end<G, NW>(a.L) ? 1 : 0);
+    load(0);
+    for (int c = 0; c < wide; ++c) {
+        const int t = w.start(c);
+        auto next = [&]() VS_INLINE {
+            if (c + 1 < wide) load(c + 1);
+        };
+        if (!w.live(c)) {                                  // padding
+            pass_on<NW, false>(ex, c & 1, w.wave, w.lane, 1.f, 0.f, h);
+            const float f[kVec] = {};
+            store_tokens<true>(y, t, w.L, f);
+        } else if (!w.full(c)) {
+            block(Wide{}, std::false_type{}, std::true_type{}, tx, tr, ti, tz, t, c, next);
+        } else if (slow) {
+            block(Wide{}, std::true_type{}, std::false_type{}, tx, tr, ti, tz, t, c, next);
+        } else {
+            block(Wide{}, std::false_type{}, std::false_type{}, tx, tr, ti, tz, t, c, next);
+        }
+    }
+    if constexpr (G == 64 && NW == 1) {
+        if (wide < chunks) {
+            const int t = wide * kBlock + w.lane;
+            Tokens<T, 1> nx, nr, ni, nz;
+            nx.template load<true>(x, t, w.len);
+            nr.template load<true>(r, t, w.len);
+            ni.template load<true>(ig, t, w.len);
+            if constexpr (GATED) nz.template load<true>(z, t, w.len);
+            block(Narrow{}, std::false_type{}, std::true_type{}, nx, nr, ni, nz, t, wide, [] {});
+        }
     }
     if (a.h_out && w.lane == 0 && w.wave == 0 && w.L > 0) a.h_out[w.row] = h;
 }
@@ -274,31 +365,34 @@ __global__ __launch_bounds__(NW > 4 ? 64 * NW : 256) void gated_grad_kernel(cons
     const T* dy = w.in(a.dy, a.sdy);
     T *dx = w.out(a.dx, a.L), *dr = w.out(a.dr, a.L), *di = w.out(a.di, a.L), *dz = GATED ? w.out(a.dz, a.L) : nullptr;
     const float* saved = a.saved + static_cast<size_t>(w.row) * a.nblk;
-    const float lam = a.lam[w.d], k = a.rate * softplus_f(lam);
+    const float k2 = a.rate * softplus_f(a.lam[w.d]) * kLog2e;
+    const bool slow = __ballot(!(k2 < kSlow)) == 0;
     float mu = a.dh_out ? a.dh_out[w.row] : 0.f;
     float sum = 0.f;
 
-    const int chunks = (a.L + kChunk - 1) / kChunk;
-    for (int c = chunks - 1; c >= 0; --c) {
-        const int t = c * kChunk + w.wave * kBlock + w.lane * kVec;
-        Eight<T> ex_, er, ei, ez, ey;
-        load_tokens(ex_, x, t, w.len);
-        load_tokens(er, r, t, w.len);
-        load_tokens(ei, ig, t, w.len);
-        load_tokens(ey, dy, t, w.len);
-        if constexpr (GATED) load_tokens(ez, z, t, w.len);
-        const float start = t < w.len ? saved[t / kBlock] : 0.f;
-        Decay e[kVec];
-        float sr[kVec], si[kVec], rq[kVec], v[kVec];
+    auto block = [&](auto vec, auto is_slow, auto is_part, int t, int c) VS_INLINE {
+        constexpr int V = decltype(vec)::value;
+        constexpr bool SLOW = decltype(is_slow)::value, PART = decltype(is_part)::value;
+        Tokens<T, V> tx, tr, ti, tz, ty;
+        tx.template load<PART>(x, t, w.len);
+        tr.template load<PART>(r, t, w.len);
+        ti.template load<PART>(ig, t, w.len);
+        ty.template load<PART>(dy, t, w.len);
+        if constexpr (GATED) tz.template load<PART>(z, t, w.len);
+        const float start = w.L > 0 ? saved[c * NW + w.wave] : 0.f;
+        Decay e[V];
+        float sr[V], si[V], rq[V], in[V], v[V];            // rq = 1 / m, in = sigmoid(i) x, v = m in
         float P = 1.f, H = 0.f;
 #pragma unroll
-        for (int j = 0; j < kVec; ++j) {
-            sr[j] = sigmoid_f(er.get(j));
-            si[j] = sigmoid_f(ei.get(j));
-            e[j].set(k, sr[j]);
-            if (t + j >= w.len) e[j].none();
+        for (int j = 0; j < V; ++j) {
+            sr[j] = sigmoid_f(tr.get(j));
+            si[j] = sigmoid_f(ti.get(j));
+            e[j].template set<SLOW>(k2, sr[j]);
+            if (PART && t + j >= w.len) e[j].none();
             rq[j] = e[j].q < 1e-36f ? 0.f : __builtin_amdgcn_rsqf(e[j].q);
-            v[j] = t + j < w.len ? e[j].q * rq[j] * si[j] * ex_.get(j) : 0.f;
+            in[j] = si[j] * tx.get(j);
+            v[j] = e[j].q * rq[j] * in[j];
+            if (PART && t + j >= w.len) v[j] = 0.f;
             H = fmaf(e[j].a, H, v[j]);
             P *= e[j].a;
         }
@@ -306,54 +400,64 @@ __global__ __launch_bounds__(NW > 4 ? 64 * NW : 256) void gated_grad_kernel(cons
         float Pi = P, Pb, Hb, Pa, Ha;
         scan_up<G>(Pi, H);
         before_and_all<G>(Pi, H, Pb, Hb, Pa, Ha);
-        float hb[kVec], gy[kVec], M = 0.f;
-        float h = fmaf(Pb, start, Hb), fz[kVec];
+        float hb[V], gy[V], M = 0.f;
+        float h = fmaf(Pb, start, Hb), fz[V];
 #pragma unroll
-        for (int j = 0; j < kVec; ++j) {
+        for (int j = 0; j < V; ++j) {
             hb[j] = h;
             h = fmaf(e[j].a, h, v[j]);
-            gy[j] = ey.get(j);
+            gy[j] = ty.get(j);
             if constexpr (GATED) {
-                const float zv = ez.get(j), sz = sigmoid_f(zv);
-                fz[j] = t + j < w.len ? gy[j] * h * sz * fmaf(zv, 1.f - sz, 1.f) : 0.f;
-                gy[j] *= zv * sz;
+                const float zv = tz.get(j), sz = sigmoid_f(zv), dsz = gy[j] * sz;
+                fz[j] = dsz * h * fmaf(zv, 1.f - sz, 1.f);
+                if (PART && t + j >= w.len) fz[j] = 0.f;
+                gy[j] = dsz * zv;
             }
         }
-        if constexpr (GATED) store_tokens(dz, t, w.L, fz);
+        if constexpr (GATED) store_tokens<PART>(dz, t, w.L, fz);
 #pragma unroll
-        for (int j = kVec - 1; j >= 0; --j) M = e[j].a * (gy[j] + M);
+        for (int j = V - 1; j >= 0; --j) M = e[j].a * (gy[j] + M);
         float Pl, Ml;
         later_and_all<G>(P, M, w.lane, Pl, Ml, Pa, Ha);
-        float from = mu;                                  // mu after this wave's block
-        if constexpr (NW > 1) {
-            const int buf = c & 1;
-            if (w.lane == 0) { ex.P[buf][w.wave] = Pa; ex.H[buf][w.wave] = Ha; }
-            __syncthreads();
+        const float from = pass_on<NW, true>(ex, c & 1, w.wave, w.lane, Pa, Ha, mu);
+        float m = fmaf(Pl, from, Ml), fx[V], fr[V], fi[V];
 #pragma unroll
-            for (int o = NW - 1; o >= 0; --o) {
-                if (o == w.wave) from = mu;
-                mu = fmaf(ex.P[buf][o], mu, ex.H[buf][o]);
-            }
-        } else {
-            mu = fmaf(Pa, mu, Ha);
-        }
-        float m = fmaf(Pl, from, Ml), fx[kVec], fr[kVec], fi[kVec];
-#pragma unroll
-        for (int j = kVec - 1; j >= 0; --j) {
+        for (int j = V - 1; j >= 0; --j) {
+            const bool on = !PART || t + j < w.len;
             const float lt = gy[j] + m;
-            const bool on = t + j < w.len;
-            fx[j] = on ? lt * e[j].q * rq[j] * si[j] : 0.f;
-            fi[j] = on ? lt * v[j] * (1.f - si[j]) : 0.f;
-            // s dL/ds: through m, a^2 s / m sigmoid(i) x, and through a, -s a h_before
-            const float through = e[j].a * e[j].a * (e[j].s * rq[j]) * si[j] * ex_.get(j);
-            const float gs = on && !(e[j].s < 1e-36f) ? lt * (through - e[j].s * e[j].a * hb[j]) : 0.f;
-            fr[j] = gs * (1.f - sr[j]);
-            sum += gs;
             m = e[j].a * lt;
+            fx[j] = on ? lt * (e[j].q * rq[j]) * si[j] : 0.f;
+            fi[j] = on ? lt * v[j] * (1.f - si[j]) : 0.f;
+            // s dL/ds (over ln 2): through m, a^2 s / m in, and through a, -s a h_before
+            const float gs = on && rq[j] != 0.f ? e[j].w * m * fmaf(e[j].a * rq[j], in[j], -hb[j]) : 0.f;
+            fr[j] = gs * fmaf(-sr[j], kLn2, kLn2);
+            sum += gs;
         }
-        store_tokens(dx, t, w.L, fx);
-        store_tokens(dr, t, w.L, fr);
-        store_tokens(di, t, w.L, fi);
+        store_tokens<PART>(dx, t, w.L, fx);
+        store_tokens<PART>(dr, t, w.L, fr);
+        store_tokens<PART>(di, t, w.L, fi);
+    };
+
+    const int chunks = (a.L + kChunk - 1) / kChunk, wide = chunks - (narrow_end<G, NW>(a.L) ? 1 : 0);
+    if constexpr (G == 64 && NW == 1) {
+        if (wide < chunks) block(Narrow{}, std::false_type{}, std::true_type{}, wide * kBlock + w.lane, wide);
+    }
+    for (int c = wide - 1; c >= 0; --c) {
+        const int t = w.start(c);
+        if (!w.live(c)) {                                  // padding
+            pass_on<NW, true>(ex, c & 1, w.wave, w.lane, 1.f, 0.f, mu);
+            const float f[kVec] = {};
+            store_tokens<true>(dx, t, w.L, f);
+            store_tokens<true>(dr, t, w.L, f);
+            store_tokens<true>(di, t, w.L, f);
+            if constexpr (GATED) store_tokens<true>(dz, t, w.L, f);
+        } else if (!w.full(c)) {
+            block(Wide{}, std::false_type{}, std::true_type{}, t, c);
+        } else if (slow) {
+            block(Wide{}, std::true_type{}, std::false_type{}, t, c);
+        } else {
+            block(Wide{}, std::false_type{}, std::false_type{}, t, c);
+        }
     }
     if (a.dh0 && w.lane == 0 && w.wave == 0 && w.L > 0) a.dh0[w.row] = mu;
     // the row's part of dlam: lanes, then waves, in a fixed order
@@ -367,7 +471,7 @@ __global__ __launch_bounds__(NW > 4 ? 64 * NW : 256) void gated_grad_kernel(cons
 #pragma unroll
         for (int o = 0; o < NW; ++o) sum += ex.P[0][o];
     }
-    if (w.lane == 0 && w.wave == 0 && w.L > 0) a.part[w.row] = sum;
+    if (w.lane == 0 && w.wave == 0 && w.L > 0) a.part[w.row] = sum * kLn2;
 }
 
 // dlam: the rows of each channel, in 64 bits (their terms have either sign)
@@ -435,7 +539,7 @@ __global__ __launch_bounds__(256) void gated_step_kernel(const GatedStepArgs a) 
 #pragma unroll
     for (int j = 0; j < 4; ++j) {
         Decay e;
-        e.set(a.rate * softplus_f(lam.get(j)), sigmoid_f(r.get(j)));
+        e.set<false>(a.rate * softplus_f(lam.get(j)) * kLog2e, sigmoid_f(r.get(j)));
         s[j] = fmaf(e.a, h.get(j), __builtin_amdgcn_sqrtf(e.q) * sigmoid_f(ig.get(j)) * x.get(j));
         f[j] = s[j];
         if constexpr (GATED) f[j] *= silu_f(z.get(j));
