@@ -370,33 +370,32 @@ __global__ __launch_bounds__(NW > 4 ? 64 * NW : 256) void gated_grad_kernel(cons
     float mu = a.dh_out ? a.dh_out[w.row] : 0.f;
     float sum = 0.f;
 
-    auto block = [&](auto vec, auto is_slow, auto is_part, int t, int c) VS_INLINE {
+    auto block = [&](auto vec, auto is_slow, auto is_part, auto& tx, auto& tr, auto& ti, auto& tz, auto& ty, float& first, int t, int c,
+                     auto&& next) VS_INLINE {
         constexpr int V = decltype(vec)::value;
         constexpr bool SLOW = decltype(is_slow)::value, PART = decltype(is_part)::value;
-        Tokens<T, V> tx, tr, ti, tz, ty;
-        tx.template load<PART>(x, t, w.len);
-        tr.template load<PART>(r, t, w.len);
-        ti.template load<PART>(ig, t, w.len);
-        ty.template load<PART>(dy, t, w.len);
-        if constexpr (GATED) tz.template load<PART>(z, t, w.len);
-        const float start = w.L > 0 ? saved[c * NW + w.wave] : 0.f;
-        Decay e[V];
-        float sr[V], si[V], rq[V], in[V], v[V];            // rq = 1 / m, in = sigmoid(i) x, v = m in
+        const float start = first;
+        float al[V], sr[V], si[V], rq[V], m[V], in[V];     // m = sqrt(q), rq = 1 / m, in = sigmoid(i) x (0 at padding)
         float P = 1.f, H = 0.f;
 #pragma unroll
         for (int j = 0; j < V; ++j) {
             sr[j] = sigmoid_f(tr.get(j));
             si[j] = sigmoid_f(ti.get(j));
-            e[j].template set<SLOW>(k2, sr[j]);
-            if (PART && t + j >= w.len) e[j].none();
-            rq[j] = e[j].q < 1e-36f ? 0.f : __builtin_amdgcn_rsqf(e[j].q);
+            Decay e;
+            e.template set<SLOW>(k2, sr[j]);
             in[j] = si[j] * tx.get(j);
-            v[j] = e[j].q * rq[j] * in[j];
-            if (PART && t + j >= w.len) v[j] = 0.f;
-            H = fmaf(e[j].a, H, v[j]);
-            P *= e[j].a;
+            if (PART && t + j >= w.len) {
+                e.none();
+                in[j] = 0.f;
+            }
+            al[j] = e.a;
+            rq[j] = e.q < 1e-36f ? 0.f : __builtin_amdgcn_rsqf(e.q);
+            m[j] = e.q * rq[j];
+            H = fmaf(al[j], H, m[j] * in[j]);
+            P *= al[j];
         }
         P = at_least(P, kTiny);
+        next(std::false_type{});
         float Pi = P, Pb, Hb, Pa, Ha;
         scan_up<G>(Pi, H);
         before_and_all<G>(Pi, H, Pb, Hb, Pa, Ha);
@@ -405,7 +404,7 @@ __global__ __launch_bounds__(NW > 4 ? 64 * NW : 256) void gated_grad_kernel(cons
 #pragma unroll
         for (int j = 0; j < V; ++j) {
             hb[j] = h;
-            h = fmaf(e[j].a, h, v[j]);
+            h = fmaf(al[j], h, m[j] * in[j]);
             gy[j] = ty.get(j);
             if constexpr (GATED) {
                 const float zv = tz.get(j), sz = sigmoid_f(zv), dsz = gy[j] * sz;
@@ -414,22 +413,23 @@ __global__ __launch_bounds__(NW > 4 ? 64 * NW : 256) void gated_grad_kernel(cons
                 gy[j] = dsz * zv;
             }
         }
+        next(std::true_type{});
         if constexpr (GATED) store_tokens<PART>(dz, t, w.L, fz);
 #pragma unroll
-        for (int j = V - 1; j >= 0; --j) M = e[j].a * (gy[j] + M);
+        for (int j = V - 1; j >= 0; --j) M = al[j] * (gy[j] + M);
         float Pl, Ml;
         later_and_all<G>(P, M, w.lane, Pl, Ml, Pa, Ha);
         const float from = pass_on<NW, true>(ex, c & 1, w.wave, w.lane, Pa, Ha, mu);
-        float m = fmaf(Pl, from, Ml), fx[V], fr[V], fi[V];
+        float back = fmaf(Pl, from, Ml), fx[V], fr[V], fi[V];
 #pragma unroll
         for (int j = V - 1; j >= 0; --j) {
             const bool on = !PART || t + j < w.len;
-            const float lt = gy[j] + m;
-            m = e[j].a * lt;
-            fx[j] = on ? lt * (e[j].q * rq[j]) * si[j] : 0.f;
-            fi[j] = on ? lt * v[j] * (1.f - si[j]) : 0.f;
+            const float lt = gy[j] + back, lm = lt * m[j];
+            back = al[j] * lt;
+            fx[j] = on ? lm * si[j] : 0.f;
+            fi[j] = on ? lm * in[j] * (1.f - si[j]) : 0.f;
             // s dL/ds (over ln 2): through m, a^2 s / m in, and through a, -s a h_before
-            const float gs = on && rq[j] != 0.f ? e[j].w * m * fmaf(e[j].a * rq[j], in[j], -hb[j]) : 0.f;
+            const float gs = on && rq[j] != 0.f ? k2 * sr[j] * back * fmaf(al[j] * rq[j], in[j], -hb[j]) : 0.f;
             fr[j] = gs * fmaf(-sr[j], kLn2, kLn2);
             sum += gs;
         }
@@ -440,10 +440,44 @@ __global__ __launch_bounds__(NW > 4 ? 64 * NW : 256) void gated_grad_kernel(cons
 
     const int chunks = (a.L + kChunk - 1) / kChunk, wide = chunks - (narrow_end<G, NW>(a.L) ? 1 : 0);
     if constexpr (G == 64 && NW == 1) {
-        if (wide < chunks) block(Narrow{}, std::false_type{}, std::true_type{}, wide * kBlock + w.lane, wide);
+        if (wide < chunks) {
+            const int t = wide * kBlock + w.lane;
+            Tokens<T, 1> nx, nr, ni, nz, ny;
+            nx.template load<true>(x, t, w.len);
+            nr.template load<true>(r, t, w.len);
+            ni.template load<true>(ig, t, w.len);
+            ny.template load<true>(dy, t, w.len);
+            if constexpr (GATED) nz.template load<true>(z, t, w.len);
+            float first = w.L > 0 ? saved[wide] : 0.f;
+            block(Narrow{}, std::false_type{}, std::true_type{}, nx, nr, ni, nz, ny, first, t, wide, [](auto) {});
+        }
     }
+    Tokens<T, kVec> tx, tr, ti, tz, ty;
+    float first = 0.f;
+    // a block's inputs in two parts: those that the recurrence reads, and those that the gate does
+    auto load_part = [&](int c, auto part, auto gate) VS_INLINE {
+        constexpr bool PART = decltype(part)::value;
+        const int t = w.start(c);
+        if constexpr (!decltype(gate)::value) {
+            tx.template load<PART>(x, t, w.len);
+            tr.template load<PART>(r, t, w.len);
+            ti.template load<PART>(ig, t, w.len);
+            first = w.L > 0 ? saved[c * NW + w.wave] : 0.f;
+        } else {
+            ty.template load<PART>(dy, t, w.len);
+            if constexpr (GATED) tz.template load<PART>(z, t, w.len);
+        }
+    };
+    auto load = [&](int c, auto gate) VS_INLINE {
+        if (c < 0 || !w.live(c)) return;
+        if (w.full(c)) load_part(c, std::false_type{}, gate);
+        else load_part(c, std::true_type{}, gate);
+    };
+    load(wide - 1, std::false_type{});
+    load(wide - 1, std::true_type{});
     for (int c = wide - 1; c >= 0; --c) {
         const int t = w.start(c);
+        auto next = [&](auto gate) VS_INLINE { load(c - 1, gate); };
         if (!w.live(c)) {                                  // padding
             pass_on<NW, true>(ex, c & 1, w.wave, w.lane, 1.f, 0.f, mu);
             const float f[kVec] = {};
@@ -451,12 +485,14 @@ __global__ __launch_bounds__(NW > 4 ? 64 * NW : 256) void gated_grad_kernel(cons
             store_tokens<true>(dr, t, w.L, f);
             store_tokens<true>(di, t, w.L, f);
             if constexpr (GATED) store_tokens<true>(dz, t, w.L, f);
+            next(std::false_type{});
+            next(std::true_type{});
         } else if (!w.full(c)) {
-            block(Wide{}, std::false_type{}, std::true_type{}, t, c);
+            block(Wide{}, std::false_type{}, std::true_type{}, tx, tr, ti, tz, ty, first, t, c, next);
         } else if (slow) {
-            block(Wide{}, std::true_type{}, std::false_type{}, t, c);
+            block(Wide{}, std::true_type{}, std::false_type{}, tx, tr, ti, tz, ty, first, t, c, next);
         } else {
-            block(Wide{}, std::false_type{}, std::false_type{}, t, c);
+            block(Wide{}, std::false_type{}, std::false_type{}, tx, tr, ti, tz, ty, first, t, c, next);
         }
     }
     if (a.dh0 && w.lane == 0 && w.wave == 0 && w.L > 0) a.dh0[w.row] = mu;
