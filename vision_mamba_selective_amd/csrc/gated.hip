@@ -151,6 +151,12 @@ __device__ __forceinline__ void later_and_all(float P, float M, int lane, float&
 }
 
 // ------------------------------------------------------------------ tokens
+// token t of a row: a scalar base and 32 bits of offset (t is below 2^28)
+template <typename P>
+__device__ __forceinline__ P* at_token(P* row, int t) {
+    typedef std::conditional_t<std::is_const_v<P>, const char, char> Byte;
+    return reinterpret_cast<P*>(reinterpret_cast<Byte*>(row) + static_cast<uint32_t>(t) * static_cast<uint32_t>(sizeof(P)));
+}
 // V tokens of a lane from t on (eight, or one in a row's short last block);
 // PART: of a row with len real ones, zeros past them
 template <typename T, int V>
@@ -158,7 +164,7 @@ struct Tokens {
     Eight<T> e;
     template <bool PART>
     __device__ __forceinline__ void load(const T* p, int t, int len) {
-        if (!PART || t + V <= len) e.load(p + t);
+        if (!PART || t + V <= len) e.load(at_token(p, t));
         else e.load_some(p, t, len);
     }
     __device__ __forceinline__ float get(int j) const { return e.get(j); }
@@ -173,7 +179,7 @@ struct Tokens<T, 1> {
 template <bool PART, typename T, int V>
 __device__ __forceinline__ void store_tokens(T* p, int t, int L, const float (&f)[V]) {
     if constexpr (V == 8) {
-        if (!PART || t + V <= L) return store_eight(p + t, f);
+        if (!PART || t + V <= L) return store_eight(at_token(p, t), f);
     }
 #pragma unroll
     for (int j = 0; j < V; ++j)
@@ -191,6 +197,7 @@ struct RowLane {
         const uint32_t id = NW > 1 ? blockIdx.x : (blockIdx.x * blockDim.x + tid) / G;
         const bool real = id < a.rows;
         row = real ? id : a.rows - 1;
+        if constexpr (G == 64) row = __builtin_amdgcn_readfirstlane(row);   // its pointers are scalars
         b = row / a.dim;
         d = row - b * a.dim;
         lane = tid & (G - 1);
@@ -246,17 +253,17 @@ __device__ __forceinline__ float pass_on(Exchange<NW>& ex, int buf, int wave, in
 
 typedef std::integral_constant<int, kVec> Wide;
 typedef std::integral_constant<int, 1> Narrow;
-// A row's last block of at most 64 tokens is taken one token a lane: with eight a
-// row of 4,097 would spend a ninth of its time on one token.
+// A row's last chunk of at most 64 tokens is taken one token a lane, by the first
+// wave: with eight a row of 4,097 would spend a ninth of its time on one token.
 template <int G, int NW>
 __device__ __forceinline__ bool narrow_end(int L) {
-    return G == 64 && NW == 1 && L > kVec * G && (L - 1) % (kVec * G) < 64;
+    return G == 64 && L > kVec * G * NW && (L - 1) % (kVec * G * NW) < 64;
 }
 
 // ----------------------------------------------------------------- forward
 template <typename T, int G, int NW, bool GATED>
 __global__ __launch_bounds__(NW > 4 ? 64 * NW : 256) void gated_scan_kernel(const GatedArgs a) {
-    constexpr int kBlock = kVec * G, kChunk = kBlock * NW;
+    constexpr int kChunk = kVec * G * NW;
     __shared__ Exchange<NW> ex;
     const RowLane<T, G, NW> w(a);
     const T *x = w.in(a.x, a.sx), *r = w.in(a.r, a.sr), *ig = w.in(a.i, a.si), *z = GATED ? w.in(a.z, a.sz) : nullptr;
@@ -337,9 +344,11 @@ __global__ __launch_bounds__(NW > 4 ? 64 * NW : 256) void gated_scan_kernel(cons
             block(Wide{}, std::false_type{}, std::false_type{}, tx, tr, ti, tz, t, c, next);
         }
     }
-    if constexpr (G == 64 && NW == 1) {
-        if (wide < chunks) {
-            const int t = wide * kBlock + w.lane;
+    if constexpr (G == 64) {
+        if (wide < chunks && w.wave > 0) {
+            pass_on<NW, false>(ex, wide & 1, w.wave, w.lane, 1.f, 0.f, h);
+        } else if (wide < chunks) {
+            const int t = wide * kChunk + w.lane;
             Tokens<T, 1> nx, nr, ni, nz;
             nx.template load<true>(x, t, w.len);
             nr.template load<true>(r, t, w.len);
@@ -358,7 +367,7 @@ __device__ __forceinline__ float lam_slope(float lam) { return lam < -20.f ? 1.f
 
 template <typename T, int G, int NW, bool GATED>
 __global__ __launch_bounds__(NW > 4 ? 64 * NW : 256) void gated_grad_kernel(const GatedArgs a) {
-    constexpr int kBlock = kVec * G, kChunk = kBlock * NW;
+    constexpr int kChunk = kVec * G * NW;
     __shared__ Exchange<NW> ex;
     const RowLane<T, G, NW> w(a);
     const T *x = w.in(a.x, a.sx), *r = w.in(a.r, a.sr), *ig = w.in(a.i, a.si), *z = GATED ? w.in(a.z, a.sz) : nullptr;
@@ -439,16 +448,18 @@ __global__ __launch_bounds__(NW > 4 ? 64 * NW : 256) void gated_grad_kernel(cons
     };
 
     const int chunks = (a.L + kChunk - 1) / kChunk, wide = chunks - (narrow_end<G, NW>(a.L) ? 1 : 0);
-    if constexpr (G == 64 && NW == 1) {
-        if (wide < chunks) {
-            const int t = wide * kBlock + w.lane;
+    if constexpr (G == 64) {
+        if (wide < chunks && w.wave > 0) {
+            pass_on<NW, true>(ex, wide & 1, w.wave, w.lane, 1.f, 0.f, mu);
+        } else if (wide < chunks) {
+            const int t = wide * kChunk + w.lane;
             Tokens<T, 1> nx, nr, ni, nz, ny;
             nx.template load<true>(x, t, w.len);
             nr.template load<true>(r, t, w.len);
             ni.template load<true>(ig, t, w.len);
             ny.template load<true>(dy, t, w.len);
             if constexpr (GATED) nz.template load<true>(z, t, w.len);
-            float first = w.L > 0 ? saved[wide] : 0.f;
+            float first = w.L > 0 ? saved[wide * NW] : 0.f;
             block(Narrow{}, std::false_type{}, std::true_type{}, nx, nr, ni, nz, ny, first, t, wide, [](auto) {});
         }
     }
@@ -515,7 +526,14 @@ __global__ __launch_bounds__(256) void gated_lam_kernel(const GatedArgs a) {
     const uint32_t d = blockIdx.x * 256 + threadIdx.x;
     if (d >= a.dim) return;
     double s = 0;
-    for (uint32_t row = d; row < a.rows; row += a.dim) s += a.part[row];
+    // eight rows in flight
+    for (uint32_t row = d; row < a.rows; row += 8 * a.dim) {
+        float v[8];
+#pragma unroll
+        for (uint32_t j = 0; j < 8; ++j) v[j] = row + j * a.dim < a.rows ? a.part[row + j * a.dim] : 0.f;
+#pragma unroll
+        for (uint32_t j = 0; j < 8; ++j) s += v[j];
+    }
     a.dlam[d] = static_cast<float>(s * lam_slope(a.lam[d]));
 }
 
