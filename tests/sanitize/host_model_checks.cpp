@@ -122,15 +122,15 @@ int main() {
                 if (d > 65536 || t * v >= (int64_t(1) << 36)) continue;
                 for (int dtype : {VS_F32, VS_BF16}) {
                     const vs::VocabPlan f = vs::vocab_plan(false, t, d, v, dtype), g = vs::vocab_plan(true, t, d, v, dtype);
-                    expect(int64_t(f.tiles) * (f.logits.wide ? 256 : 128) >= v, "tiles cover the vocabulary");
+                    expect(int64_t(f.tiles) * (f.wide ? 256 : 128) >= v, "tiles cover the vocabulary");
                     expect(g.piece * g.pieces >= v && g.piece * (g.pieces - 1) < v && g.piece % 256 == 0, "pieces cover it, none is empty");
                     expect(f.dp >= d && f.dp % 8 == 0, "packed rows are whole");
-                    expect(g.dx.splits >= 1 && g.dw.splits >= 1 && g.dx.splits <= 64 && g.dw.splits <= 64, "splits");
+                    expect(g.dx_splits >= 1 && g.dw_splits >= 1 && g.dx_splits <= 64 && g.dw_splits <= 64, "splits");
                     expect(f.part + size_t(f.tiles) * size_t(t) * 8 <= f.logit && f.logit + size_t(t) * 4 <= f.bytes, "forward workspace");
                     const size_t n = size_t(g.piece < v ? g.piece : v);
-                    expect(g.P + size_t(t) * ((n + 7) / 8 * 8) * (dtype == VS_BF16 ? 2 : 4) <= g.part, "P's place");
-                    if (g.dx.splits > 1) expect(g.part + size_t(g.dx.splits) * size_t(t * d) * 4 <= g.sum, "dx's parts");
-                    if (g.dw.splits > 1) expect(g.part + size_t(g.dw.splits) * n * size_t(d) * 4 <= g.sum, "dW's parts");
+                    expect(g.P + size_t(t) * ((n + 7) / 8 * 8) * (dtype == VS_BF16 ? 2 : 4) <= g.part_dx, "P's place");
+                    if (g.dx_splits > 1) expect(g.part_dx + size_t(g.dx_splits) * size_t(t * d) * 4 <= g.part_dw, "dx's parts");
+                    if (g.dw_splits > 1) expect(g.part_dw + size_t(g.dw_splits) * n * size_t(d) * 4 <= g.sum, "dW's parts");
                     if (g.pieces > 1) expect(g.sum + size_t(t * d) * 4 <= g.bytes, "the sum of dx");
                 }
                 const vs::GatedForm form = vs::gated_form(t, d, v);

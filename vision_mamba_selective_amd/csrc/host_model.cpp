@@ -204,19 +204,29 @@ const char* vocab_problem(int64_t tokens, int64_t dim, int64_t vocab, int& code)
     return nullptr;
 }
 
-// The larger tile reads half as much per product, the smaller fills the chip
-// with fewer entries; a product with too few tiles for either cuts its k.
-VocabTiles vocab_tiles(int64_t m, int64_t n, int64_t k, int dtype, bool cut) {
-    const int64_t stages = ceil_div(k * static_cast<int64_t>(esize(dtype)), kVocabStage);
-    const int64_t wide = ceil_div(m, 256) * ceil_div(n, 256), narrow = ceil_div(m, 128) * ceil_div(n, 128);
-    VocabTiles t{wide >= 192, 1};
-    if (cut && !t.wide && narrow < 512) {
-        int64_t s = 512 / narrow;
-        const int64_t most = stages / 8 > 0 ? stages / 8 : 1;
-        s = s > most ? most : s;
-        t.splits = static_cast<int>(s > 64 ? 64 : s);
-    }
-    return t;
+int64_t tiles_of(int64_t m, int64_t n, int64_t tile) { return ceil_div(m, tile) * ceil_div(n, tile); }
+
+// Whether the logits take the larger tile: by rounds of tiles over the chip, one
+// larger tile or two smaller ones on a compute unit at a time. A round of smaller
+// ones takes 0.65 of a larger one's time in bf16, whose operands are read twice
+// as often, and half in fp32, which the matrix cores bound.
+bool vocab_wide(int64_t m, int64_t n, int dtype) {
+    const int64_t wide = ceil_div(tiles_of(m, n, 256), kNumCUs), narrow = ceil_div(tiles_of(m, n, 128), 2 * kNumCUs);
+    return 20 * wide <= (dtype == VS_BF16 ? 13 : 10) * narrow;
+}
+
+int64_t stages_of(int64_t k, int dtype) { return ceil_div(k * static_cast<int64_t>(esize(dtype)), kVocabStage); }
+
+// both products of a piece run together: no workgroup takes more than its share
+// of all stages, or eight, and a product is cut into at most 64
+struct Splits { int64_t work; int dx, dw; };
+Splits vocab_splits(int64_t dim, int64_t tokens, int64_t n, int64_t tile, int dtype) {
+    const int64_t tx = tiles_of(dim, tokens, tile), tw = tiles_of(dim, n, tile), kx = stages_of(n, dtype), kw = stages_of(tokens, dtype);
+    const int64_t work = tx * kx + tw * kw, slots = tile == 256 ? kNumCUs : 2 * kNumCUs;
+    int64_t share = ceil_div(work, slots);
+    share = share < 8 ? 8 : share;
+    auto cut = [&](int64_t k) { const int64_t s = ceil_div(k, share); return static_cast<int>(s > 64 ? 64 : s); };
+    return {work, cut(kx), cut(kw)};
 }
 
 }  // namespace
@@ -231,8 +241,8 @@ VocabPlan vocab_plan(bool grad, int64_t tokens, int64_t dim, int64_t vocab, int 
     p.x = take(static_cast<size_t>(tokens * p.dp) * es);
     p.w = take(p.pack_w ? static_cast<size_t>(vocab * p.dp) * es : 0);
     if (!grad) {
-        p.logits = vocab_tiles(vocab, tokens, dim, dtype, false);
-        p.tiles = static_cast<int>(ceil_div(vocab, p.logits.wide ? 256 : 128));
+        p.wide = vocab_wide(vocab, tokens, dtype);
+        p.tiles = static_cast<int>(ceil_div(vocab, p.wide ? 256 : 128));
         p.part = take(static_cast<size_t>(p.tiles) * static_cast<size_t>(tokens) * 2 * kF);
         p.logit = take(static_cast<size_t>(tokens) * kF);
     } else {
@@ -243,13 +253,15 @@ VocabPlan vocab_plan(bool grad, int64_t tokens, int64_t dim, int64_t vocab, int 
         p.piece = ceil_div(ceil_div(vocab, p.pieces), 256) * 256;
         p.pieces = ceil_div(vocab, p.piece);
         const int64_t n = p.piece < vocab ? p.piece : vocab;
-        p.logits = vocab_tiles(n, tokens, dim, dtype, false);
-        p.dx = vocab_tiles(dim, tokens, n, dtype, true);
-        p.dw = vocab_tiles(dim, n, tokens, dtype, true);
+        p.prob_wide = vocab_wide(n, tokens, dtype);
+        // a quarter of the larger tile's work costs the smaller one 1.3 (fp32: 1.05) quarters
+        const Splits wide = vocab_splits(dim, tokens, n, 256, dtype), narrow = vocab_splits(dim, tokens, n, 128, dtype);
+        p.wide = 80 * wide.work <= (dtype == VS_BF16 ? 26 : 21) * narrow.work;
+        p.dx_splits = p.wide ? wide.dx : narrow.dx;
+        p.dw_splits = p.wide ? wide.dw : narrow.dw;
         p.P = take(static_cast<size_t>(tokens * (ceil_div(n, 8) * 8)) * es);
-        const size_t dx = p.dx.splits > 1 ? static_cast<size_t>(p.dx.splits * tokens * dim) * kF : 0;
-        const size_t dw = p.dw.splits > 1 ? static_cast<size_t>(p.dw.splits * n * dim) * kF : 0;
-        p.part = take(dx > dw ? dx : dw);
+        p.part_dx = take(p.dx_splits > 1 ? static_cast<size_t>(p.dx_splits * tokens * dim) * kF : 0);
+        p.part_dw = take(p.dw_splits > 1 ? static_cast<size_t>(p.dw_splits * n * dim) * kF : 0);
         p.sum = take(p.pieces > 1 ? static_cast<size_t>(tokens * dim) * kF : 0);
     }
     p.bytes = off;

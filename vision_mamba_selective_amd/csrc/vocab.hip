@@ -49,7 +49,7 @@ struct GemmArgs {
     int64_t lda, ldb;               // elements
     int M, N, K;
     int tiles_m, tiles_n;
-    int k_split;                    // k of one split (a multiple of a stage's), blockIdx.y of them
+    int k_split;                    // k of one split (a multiple of a stage's)
     // logits
     const void* target;
     int target64;
@@ -199,33 +199,75 @@ __device__ __forceinline__ void put_four(uint16_t* p, int at, int n, const float
             if (at + i < n) p[at + i] = b[i];
 }
 
+// A workgroup's LDS: two stages of both operands, in arrays of their own, so
+// that a stage's reads do not wait for the next one's loads.
+struct Lds {
+    char *a0, *a1, *b0, *b1;
+};
+
+// what a wave has written to its part of LDS is there for its other lanes
+__device__ __forceinline__ void wave_sync() {
+    __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront", "local");
+    __builtin_amdgcn_wave_barrier();
+    __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "wavefront", "local");
+}
+
+// Rows of out (n, 32 of them) by columns (m, MW of them) of one wave, from the
+// accumulators' order to whole rows: through the wave's own part of LDS, 16 bytes
+// of a row a lane. Chunks are permuted by the row, so that neither side meets on
+// a bank. f(i, r) is the value of accumulator r of fragment i.
+template <typename T, int BM, int WM, typename F>
+__device__ __forceinline__ void write_rows(const Lds& s, int wave, int lane, T* out, int64_t ld, int rows, int cols, F&& f) {
+    constexpr int kEs = sizeof(T), MW = BM / WM, kRow = MW * kEs, kRegion = 32 * kRow, kPer = BM * kStage / kRegion;
+    constexpr int kChunks = kRow / 16, kN = 16 / kEs;
+    const int k = wave / kPer;
+    char* lds = (k == 0 ? s.a0 : k == 1 ? s.a1 : k == 2 ? s.b0 : s.b1) + wave % kPer * kRegion;
+    const int n = lane & 31, h = lane >> 5;
+#pragma unroll
+    for (int i = 0; i < MW / 32; ++i)
+#pragma unroll
+        for (int q = 0; q < 4; ++q) {
+            const int m = (32 * i + 8 * q + 4 * h) * kEs;
+            T v[4];
+#pragma unroll
+            for (int r = 0; r < 4; ++r) st(v, r, f(i, 4 * q + r));
+            __builtin_memcpy(lds + n * kRow + ((m / 16) ^ (n & (kChunks - 1) & 15)) * 16 + m % 16, v, sizeof(v));
+        }
+    wave_sync();
+#pragma unroll
+    for (int k2 = 0; k2 < 32 * kChunks / 64; ++k2) {
+        const int row = (k2 * 64 + lane) / kChunks, c = lane % kChunks;
+        T v[kN];
+        __builtin_memcpy(v, lds + row * kRow + (c ^ (row & (kChunks - 1) & 15)) * 16, 16);
+        if (row >= rows) continue;
+        T* to = out + row * ld + c * kN;
+        if (c * kN + kN <= cols) __builtin_memcpy(to, v, 16);
+        else
+#pragma unroll
+            for (int j = 0; j < kN; ++j)
+                if (c * kN + j < cols) to[j] = v[j];
+    }
+    wave_sync();
+}
+
+// One tile of a product, of the split `z` of its k.
 template <typename T, int BM, int BN, int WM, int WN, bool AO, bool BO, Epilogue EPI>
-__global__ __launch_bounds__(64 * WM * WN) void vocab_gemm_kernel(const GemmArgs a) {
+__device__ __forceinline__ void gemm_tile(const GemmArgs& a, int tile, int z, const Lds& lds) {
     constexpr int kWaves = WM * WN, MF = BM / WM / 32, NF = BN / WN / 32;
     static_assert(MF <= 4 && NF <= 4, "fragments of a wave");
     typedef Operand<T, AO, BM, kWaves> OpA;
     typedef Operand<T, BO, BN, kWaves> OpB;
-    // two stages; arrays of their own, so that a stage's reads do not wait for the next one's loads
-    __shared__ __attribute__((aligned(1024))) char sA0[OpA::kBytes];
-    __shared__ __attribute__((aligned(1024))) char sA1[OpA::kBytes];
-    __shared__ __attribute__((aligned(1024))) char sB0[OpB::kBytes];
-    __shared__ __attribute__((aligned(1024))) char sB1[OpB::kBytes];
-
     const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
     const int wm = wave / WN, wn = wave % WN;
-    // each XCD a contiguous range of tiles; eight columns of tiles at a time, so
-    // that the tiles that run together share rows of both operands in its L2
+    // eight columns of tiles at a time, so that the tiles that run together share rows of both operands in an L2
     int tm, tn;
     {
-        const uint32_t G = gridDim.x, x = blockIdx.x % kXcds, k = blockIdx.x / kXcds, q = G / kXcds, r = G % kXcds;
-        const int v = static_cast<int>(x * q + (x < r ? x : r) + k);
-        const int band = v / (8 * a.tiles_m), n0 = band * 8, width = min(8, a.tiles_n - n0);
-        const int in = v - band * 8 * a.tiles_m;
+        const int band = tile / (8 * a.tiles_m), width = min(8, a.tiles_n - band * 8), in = tile - band * 8 * a.tiles_m;
         tm = in / width;
-        tn = n0 + in % width;
+        tn = band * 8 + in % width;
     }
     const int m0 = tm * BM, n0 = tn * BN;
-    const int k_lo = blockIdx.y * a.k_split, k_hi = min(a.K, k_lo + a.k_split);
+    const int k_lo = z * a.k_split, k_hi = min(a.K, k_lo + a.k_split);
 
     OpA A;
     OpB B;
@@ -247,40 +289,45 @@ __global__ __launch_bounds__(64 * WM * WN) void vocab_gemm_kernel(const GemmArgs
             B.cut(pb, k_hi - k, tid);
             __syncthreads();
         }
+        // a step's fragments are read while the matrix cores work on the last one's
+        typename Types<T>::Frag fa[2][MF], fb[2][NF];
+        auto read = [&](int s) VS_INLINE {
+#pragma unroll
+            for (int j = 0; j < NF; ++j) fb[s & 1][j] = B.read(pb, j, s);
+#pragma unroll
+            for (int i = 0; i < MF; ++i) fa[s & 1][i] = A.read(pa, i, s);
+        };
+        read(0);
 #pragma unroll
         for (int s = 0; s < 4; ++s) {
-            typename Types<T>::Frag fa[MF], fb[NF];
-#pragma unroll
-            for (int i = 0; i < MF; ++i) fa[i] = A.read(pa, i, s);
-#pragma unroll
-            for (int j = 0; j < NF; ++j) fb[j] = B.read(pb, j, s);
+            if (s < 3) read(s + 1);
 #pragma unroll
             for (int i = 0; i < MF; ++i)
 #pragma unroll
-                for (int j = 0; j < NF; ++j) Types<T>::mma(fa[i], fb[j], acc[i][j]);
+                for (int j = 0; j < NF; ++j) Types<T>::mma(fa[s & 1][i], fb[s & 1][j], acc[i][j]);
         }
         __syncthreads();
     };
-    A.load(sA0, k_lo);
-    B.load(sB0, k_lo);
+    A.load(lds.a0, k_lo);
+    B.load(lds.b0, k_lo);
     __syncthreads();
     int k = k_lo;
     for (; k + OpA::kBk < k_hi; k += 2 * OpA::kBk) {
-        A.load(sA1, k + OpA::kBk);
-        B.load(sB1, k + OpA::kBk);
-        stage(sA0, sB0, k);
+        A.load(lds.a1, k + OpA::kBk);
+        B.load(lds.b1, k + OpA::kBk);
+        stage(lds.a0, lds.b0, k);
         if (k + 2 * OpA::kBk < k_hi) {
-            A.load(sA0, k + 2 * OpA::kBk);
-            B.load(sB0, k + 2 * OpA::kBk);
+            A.load(lds.a0, k + 2 * OpA::kBk);
+            B.load(lds.b0, k + 2 * OpA::kBk);
         }
-        stage(sA1, sB1, k + OpA::kBk);
+        stage(lds.a1, lds.b1, k + OpA::kBk);
     }
-    if (k < k_hi) stage(sA0, sB0, k);
+    if (k < k_hi) stage(lds.a0, lds.b0, k);
 
     // acc[i][j][r] of a lane: row m0 + wm BM / WM + 32 i + 8 (r / 4) + 4 (lane / 32) + r % 4, column n0 + wn BN / WN + 32 j + lane % 32
     const int mw = m0 + wm * (BM / WM) + 4 * (lane >> 5), nw = n0 + wn * (BN / WN) + (lane & 31);
     if constexpr (EPI == kLse) {
-        float* red = reinterpret_cast<float*>(sA0);                 // [2][WM][BN]
+        float* red = reinterpret_cast<float*>(lds.a0);               // [2][WM][BN]
         if (m0 + BM > a.M) {
 #pragma unroll
             for (int i = 0; i < MF; ++i)
@@ -337,34 +384,36 @@ __global__ __launch_bounds__(64 * WM * WN) void vocab_gemm_kernel(const GemmArgs
     } else if constexpr (EPI == kProb) {
 #pragma unroll
         for (int j = 0; j < NF; ++j) {
-            const int n = nw + 32 * j;
-            if (n >= a.N) continue;
-            const int64_t t = target_of(a, n);
+            const int n = nw + 32 * j, nc = min(n, a.N - 1);
+            const int64_t t = target_of(a, nc);
             const bool on = t >= 0 && t < a.vocab;
-            const float lse = a.lse[n] * kLog2e, g = on ? a.dloss[n] : 0.f;
-            T* row = static_cast<T*>(a.P) + static_cast<int64_t>(n) * a.ldp;
-#pragma unroll
-            for (int i = 0; i < MF; ++i)
-#pragma unroll
-                for (int q = 0; q < 4; ++q) {
-                    const int m = mw + 32 * i + 8 * q;
-                    float f[4];
-#pragma unroll
-                    for (int r = 0; r < 4; ++r) {
-                        float p = __builtin_amdgcn_exp2f(fmaf(acc[i][j][4 * q + r], kLog2e, -lse));
-                        if (a.v0 + m + r == t) p -= 1.f;
-                        f[r] = on && m + r < a.M ? p * g : 0.f;
-                    }
-                    if (m < a.M) put_four(row, m, a.M, f);
-                }
+            const float lse = a.lse[nc] * kLog2e, g = on ? a.dloss[nc] : 0.f;
+            // the target's place among this lane's rows
+            const int64_t hot = t - a.v0 - mw;
+            const int first = n0 + wn * (BN / WN) + 32 * j, mf = m0 + wm * (BM / WM);
+            write_rows<T, BM, WM>(lds, wave, lane, static_cast<T*>(a.P) + static_cast<int64_t>(first) * a.ldp + mf, a.ldp, a.N - first, a.ldp - mf,
+                                  [&](int i, int r) VS_INLINE {
+                                      const int m = 32 * i + 8 * (r / 4) + r % 4;
+                                      float p = __builtin_amdgcn_exp2f(fmaf(acc[i][j][r], kLog2e, -lse));
+                                      if (hot == m) p -= 1.f;
+                                      return on && mw + m < a.M ? p * g : 0.f;
+                                  });
         }
     } else {
-        const bool split = gridDim.y > 1;
+        const bool split = a.k_split < a.K;
 #pragma unroll
         for (int j = 0; j < NF; ++j) {
-            const int n = nw + 32 * j;
+            const int n = nw + 32 * j, first = n0 + wn * (BN / WN) + 32 * j, mf = m0 + wm * (BM / WM);
+            float* sum = a.sum ? a.sum + (static_cast<int64_t>(split ? z : 0) * a.N + min(n, a.N - 1)) * a.M : nullptr;
+            if (a.out && !split) {
+                write_rows<T, BM, WM>(lds, wave, lane, static_cast<T*>(a.out) + static_cast<int64_t>(first) * a.ldo + mf, a.ldo, a.N - first,
+                                      a.M - mf, [&](int i, int r) VS_INLINE {
+                                          const int m = mw + 32 * i + 8 * (r / 4) + r % 4;
+                                          return acc[i][j][r] + (a.add && m < a.M ? sum[m] : 0.f);
+                                      });
+                continue;
+            }
             if (n >= a.N) continue;
-            float* sum = a.sum ? a.sum + (static_cast<int64_t>(blockIdx.y) * a.N + n) * a.M : nullptr;
 #pragma unroll
             for (int i = 0; i < MF; ++i)
 #pragma unroll
@@ -374,10 +423,47 @@ __global__ __launch_bounds__(64 * WM * WN) void vocab_gemm_kernel(const GemmArgs
                     float f[4];
 #pragma unroll
                     for (int r = 0; r < 4; ++r) f[r] = acc[i][j][4 * q + r] + (a.add && !split && m + r < a.M ? sum[m + r] : 0.f);
-                    if (a.out && !split) put_four(static_cast<T*>(a.out) + static_cast<int64_t>(n) * a.ldo, m, a.M, f);
-                    else put_four(sum, m, a.M, f);
+                    put_four(sum, m, a.M, f);
                 }
         }
+    }
+}
+
+// Workgroups are dealt to the XCDs in turn: each gets one contiguous range of the
+// tiles 0..n-1 (of those of `more` behind them).
+struct Range { int first, count; };
+__device__ __forceinline__ Range xcd_range(int n, int x) {
+    const int q = n / static_cast<int>(kXcds), r = n % static_cast<int>(kXcds);
+    return {x * q + min(x, r), q + (x < r ? 1 : 0)};
+}
+
+#define VS_GEMM_LDS(T, AO, BO)                                                                          \
+    __shared__ __attribute__((aligned(1024))) char sA0[Operand<T, AO, BM, WM * WN>::kBytes];            \
+    __shared__ __attribute__((aligned(1024))) char sA1[Operand<T, AO, BM, WM * WN>::kBytes];            \
+    __shared__ __attribute__((aligned(1024))) char sB0[Operand<T, BO, BN, WM * WN>::kBytes];            \
+    __shared__ __attribute__((aligned(1024))) char sB1[Operand<T, BO, BN, WM * WN>::kBytes];            \
+    const Lds lds{sA0, sA1, sB0, sB1};
+
+template <typename T, int BM, int BN, int WM, int WN, Epilogue EPI>
+__global__ __launch_bounds__(64 * WM * WN) void vocab_logits_kernel(const GemmArgs a) {
+    VS_GEMM_LDS(T, false, false)
+    const int x = blockIdx.x % kXcds, k = blockIdx.x / kXcds;
+    gemm_tile<T, BM, BN, WM, WN, false, false, EPI>(a, xcd_range(gridDim.x, x).first + k, 0, lds);
+}
+
+// dx and dW of a piece in one launch: the tiles of dx, whose k is the longer one
+// with large pieces, first, and those of dW in the room that they leave.
+template <typename T, int BM, int BN, int WM, int WN>
+__global__ __launch_bounds__(64 * WM * WN) void vocab_grads_kernel(const GemmArgs dx, const GemmArgs dw, int n_dx) {
+    VS_GEMM_LDS(T, true, true)
+    const int x = blockIdx.x % kXcds, k = blockIdx.x / kXcds;
+    const Range all = xcd_range(gridDim.x, x), one = xcd_range(n_dx, x);
+    if (k < one.count) {
+        const int v = one.first + k, tiles = dx.tiles_m * dx.tiles_n;
+        gemm_tile<T, BM, BN, WM, WN, true, false, kSum>(dx, v % tiles, v / tiles, lds);
+    } else {
+        const int v = all.first - one.first + k - one.count, tiles = dw.tiles_m * dw.tiles_n;
+        gemm_tile<T, BM, BN, WM, WN, true, true, kSum>(dw, v % tiles, v / tiles, lds);
     }
 }
 
@@ -416,7 +502,7 @@ __global__ __launch_bounds__(256) void vocab_pack_kernel(const PackArgs a) {
     __builtin_memcpy(static_cast<T*>(a.out) + row * a.dp + c, v, sizeof(v));
 }
 
-// a token's tiles into its lse and loss: 32 tokens a workgroup, 8 lines of tiles
+// a token's tiles into its lse and loss: 16 tokens a workgroup, 16 lines of tiles
 struct LseArgs {
     const float *part_max, *part_sum, *target_logit;
     const void* target;
@@ -425,24 +511,37 @@ struct LseArgs {
     float *loss, *lse;
 };
 __global__ __launch_bounds__(256) void vocab_lse_kernel(const LseArgs a) {
-    __shared__ float red[2][8][32];
-    const int c = threadIdx.x & 31, line = threadIdx.x >> 5, t = blockIdx.x * 32 + c;
+    __shared__ float red[2][16][17];
+    const int c = threadIdx.x & 15, line = threadIdx.x >> 4, t = blockIdx.x * 16 + c;
     float mx = -INFINITY, sum = 0.f;
     if (t < a.tokens)
-        for (int v = line; v < a.tiles; v += 8) {
-            const float m = a.part_max[static_cast<int64_t>(v) * a.tokens + t], s = a.part_sum[static_cast<int64_t>(v) * a.tokens + t];
-            const float top = fmaxf(mx, m), safe = top == -INFINITY ? 0.f : top;
-            sum = sum * __builtin_amdgcn_exp2f((mx - safe) * kLog2e) + s * __builtin_amdgcn_exp2f((m - safe) * kLog2e);
+        for (int v = line; v < a.tiles; v += 16 * 8) {         // eight tiles in flight
+            float m[8], s[8];
+#pragma unroll
+            for (int j = 0; j < 8; ++j) {
+                const int64_t at = static_cast<int64_t>(min(v + 16 * j, a.tiles - 1)) * a.tokens + t;
+                m[j] = v + 16 * j < a.tiles ? a.part_max[at] : -INFINITY;
+                s[j] = v + 16 * j < a.tiles ? a.part_sum[at] : 0.f;
+            }
+            float top = mx;
+#pragma unroll
+            for (int j = 0; j < 8; ++j) top = fmaxf(top, m[j]);
+            const float safe = top == -INFINITY ? 0.f : top;
+            sum *= __builtin_amdgcn_exp2f((mx - safe) * kLog2e);
+#pragma unroll
+            for (int j = 0; j < 8; ++j) sum += s[j] * __builtin_amdgcn_exp2f((m[j] - safe) * kLog2e);
             mx = top;
         }
     red[0][line][c] = mx;
     red[1][line][c] = sum;
     __syncthreads();
     if (line || t >= a.tokens) return;
-    for (int o = 1; o < 8; ++o) mx = fmaxf(mx, red[0][o][c]);
+#pragma unroll
+    for (int o = 1; o < 16; ++o) mx = fmaxf(mx, red[0][o][c]);
     const float safe = mx == -INFINITY ? 0.f : mx;
     sum = 0.f;
-    for (int o = 0; o < 8; ++o) sum += red[1][o][c] * __builtin_amdgcn_exp2f((red[0][o][c] - safe) * kLog2e);
+#pragma unroll
+    for (int o = 0; o < 16; ++o) sum += red[1][o][c] * __builtin_amdgcn_exp2f((red[0][o][c] - safe) * kLog2e);
     const float lse = safe + logf(sum);
     a.lse[t] = lse;
     const int64_t g = a.target64 ? static_cast<const int64_t*>(a.target)[t] : static_cast<const int32_t*>(a.target)[t];
@@ -473,31 +572,47 @@ __global__ __launch_bounds__(256) void vocab_join_kernel(const JoinArgs a) {
 // ------------------------------------------------------------------ launch
 int ceil_div(int64_t a, int64_t b) { return static_cast<int>((a + b - 1) / b); }
 
-template <typename T, bool AO, bool BO, Epilogue EPI>
-void gemm(GemmArgs a, bool wide, int splits, hipStream_t s) {
+template <typename T>
+void cut(GemmArgs& a, bool wide, int splits) {
     const int tile = wide ? 256 : 128;
     a.tiles_m = ceil_div(a.M, tile);
     a.tiles_n = ceil_div(a.N, tile);
     constexpr int kBk = kStage / static_cast<int>(sizeof(T));
-    a.k_split = ceil_div(ceil_div(a.K, kBk), splits) * kBk;
-    const dim3 grid(static_cast<uint32_t>(a.tiles_m) * static_cast<uint32_t>(a.tiles_n), ceil_div(a.K, a.k_split));
-    if (wide) vocab_gemm_kernel<T, 256, 256, 2, 4, AO, BO, EPI><<<grid, 512, 0, s>>>(a);
-    else vocab_gemm_kernel<T, 128, 128, 2, 2, AO, BO, EPI><<<grid, 256, 0, s>>>(a);
+    a.k_split = ceil_div(ceil_div(a.K, kBk), splits) * kBk;      // no split is empty
 }
 
-// a product into `out` (or added to `sum`), through the splits' parts where there are several
-template <typename T, bool BO>
-void product(GemmArgs a, const vs::VocabTiles& t, float* part, hipStream_t s) {
-    constexpr int kBk = kStage / static_cast<int>(sizeof(T));
-    const int splits = ceil_div(a.K, ceil_div(ceil_div(a.K, kBk), t.splits) * kBk);     // none of them empty
-    if (splits == 1) return gemm<T, true, BO, kSum>(a, t.wide, 1, s);
-    GemmArgs g = a;
-    g.sum = part;
-    gemm<T, true, BO, kSum>(g, t.wide, splits, s);
+template <typename T, Epilogue EPI>
+void logits(GemmArgs a, bool wide, hipStream_t s) {
+    cut<T>(a, wide, 1);
+    const uint32_t grid = static_cast<uint32_t>(a.tiles_m) * static_cast<uint32_t>(a.tiles_n);
+    if (wide) vocab_logits_kernel<T, 256, 256, 2, 4, EPI><<<grid, 512, 0, s>>>(a);
+    else vocab_logits_kernel<T, 128, 128, 2, 2, EPI><<<grid, 256, 0, s>>>(a);
+}
+
+// a product's splits into its `out`, or its `sum`
+template <typename T>
+void join(const GemmArgs& a, const float* part, int splits, hipStream_t s) {
     JoinArgs j{};
     j.part = part; j.splits = splits; j.count = static_cast<int64_t>(a.N) * a.M; j.M = a.M; j.sum = a.sum; j.add = a.add;
     j.out = a.out; j.ldo = a.ldo;
     vocab_join_kernel<T><<<ceil_div(j.count, 256), 256, 0, s>>>(j);
+}
+
+// both products of a piece; those that cut their k leave their parts in part_dx and part_dw
+template <typename T>
+void products(GemmArgs dx, GemmArgs dw, const vs::VocabPlan& p, float* part_dx, float* part_dw, hipStream_t s) {
+    cut<T>(dx, p.wide, p.dx_splits);
+    cut<T>(dw, p.wide, p.dw_splits);
+    const int nx = ceil_div(dx.K, dx.k_split), nw = ceil_div(dw.K, dw.k_split);
+    GemmArgs gx = dx, gw = dw;
+    if (nx > 1) gx.sum = part_dx;
+    if (nw > 1) gw.sum = part_dw;
+    const int n_dx = dx.tiles_m * dx.tiles_n * nx, n_dw = dw.tiles_m * dw.tiles_n * nw;
+    const uint32_t grid = static_cast<uint32_t>(n_dx + n_dw);
+    if (p.wide) vocab_grads_kernel<T, 256, 256, 2, 4><<<grid, 512, 0, s>>>(gx, gw, n_dx);
+    else vocab_grads_kernel<T, 128, 128, 2, 2><<<grid, 256, 0, s>>>(gx, gw, n_dx);
+    if (nx > 1) join<T>(dx, part_dx, nx, s);
+    if (nw > 1) join<T>(dw, part_dw, nw, s);
 }
 
 template <typename T>
@@ -533,31 +648,29 @@ int launch(const vs::VocabCall& c) {
         l.part_max = reinterpret_cast<float*>(ws + p.part);
         l.part_sum = l.part_max + static_cast<int64_t>(p.tiles) * c.tokens;
         l.target_logit = reinterpret_cast<float*>(ws + p.logit);
-        gemm<T, false, false, kLse>(l, p.logits.wide, 1, s);
+        logits<T, kLse>(l, p.wide, s);
         LseArgs e{};
         e.part_max = l.part_max; e.part_sum = l.part_sum; e.target_logit = l.target_logit; e.target = c.target; e.target64 = c.target64;
         e.vocab = l.vocab; e.tiles = p.tiles; e.tokens = l.N; e.loss = c.loss; e.lse = c.lse;
-        vocab_lse_kernel<<<ceil_div(c.tokens, 32), 256, 0, s>>>(e);
+        vocab_lse_kernel<<<ceil_div(c.tokens, 16), 256, 0, s>>>(e);
     } else {
-        float *part = reinterpret_cast<float*>(ws + p.part), *sum = reinterpret_cast<float*>(ws + p.sum);
+        float* sum = reinterpret_cast<float*>(ws + p.sum);
         for (int64_t v0 = 0; v0 < c.vocab; v0 += p.piece) {
             const int n = static_cast<int>(c.vocab - v0 < p.piece ? c.vocab - v0 : p.piece);
             const bool last = v0 + n == c.vocab;
             l.A = W + v0 * ldw; l.M = n; l.v0 = static_cast<int>(v0);
             l.lse = c.lse_in; l.dloss = c.dloss; l.P = ws + p.P;
             l.ldp = ceil_div(n, 8) * 8;                 // rows of whole 16 bytes
-            gemm<T, false, false, kProb>(l, p.logits.wide, 1, s);
-            GemmArgs g{};
-            g.A = W + v0 * ldw; g.lda = ldw; g.B = l.P; g.ldb = l.ldp;
-            g.M = static_cast<int>(c.dim); g.N = static_cast<int>(c.tokens); g.K = n;
-            g.add = v0 > 0; g.sum = p.pieces > 1 ? sum : nullptr;
-            g.out = last ? c.dx : nullptr; g.ldo = c.dim;
-            product<T, false>(g, p.dx, part, s);
-            g = GemmArgs{};
-            g.A = x; g.lda = ldx; g.B = l.P; g.ldb = l.ldp;
-            g.M = static_cast<int>(c.dim); g.N = n; g.K = static_cast<int>(c.tokens);
-            g.out = static_cast<T*>(c.dW) + v0 * c.dim; g.ldo = c.dim;
-            product<T, true>(g, p.dw, part, s);
+            logits<T, kProb>(l, p.prob_wide, s);
+            GemmArgs dx{}, dw{};
+            dx.A = W + v0 * ldw; dx.lda = ldw; dx.B = l.P; dx.ldb = l.ldp;
+            dx.M = static_cast<int>(c.dim); dx.N = static_cast<int>(c.tokens); dx.K = n;
+            dx.add = v0 > 0; dx.sum = p.pieces > 1 ? sum : nullptr;
+            dx.out = last ? c.dx : nullptr; dx.ldo = c.dim;
+            dw.A = x; dw.lda = ldx; dw.B = l.P; dw.ldb = l.ldp;
+            dw.M = static_cast<int>(c.dim); dw.N = n; dw.K = static_cast<int>(c.tokens);
+            dw.out = static_cast<T*>(c.dW) + v0 * c.dim; dw.ldo = c.dim;
+            products<T>(dx, dw, p, reinterpret_cast<float*>(ws + p.part_dx), reinterpret_cast<float*>(ws + p.part_dw), s);
         }
     }
     const hipError_t e = hipGetLastError();

@@ -92,16 +92,18 @@ int prepare_norm(NormCall& c);
 
 // ---- the vocabulary loss (vocab.hip)
 constexpr int kVocabStage = 128;                     // bytes of k that a product takes at a time
-// tiles of 256 x 256 (or 128 x 128), the product's k cut into `splits`
-struct VocabTiles { bool wide; int splits; };
+// Tiles are 256 x 256 (wide) or 128 x 128; a product with few of them cuts its k
+// into splits.
 struct VocabPlan {
     int64_t dp;                                      // row length of packed operands
     bool pack_x, pack_w;
-    VocabTiles logits, dx, dw;
+    bool wide;                                       // forward: the logits; gradient: both products
     int tiles;                                       // of the vocabulary, forward
+    bool prob_wide;                                  // gradient: the logits
+    int dx_splits, dw_splits;
     int64_t piece;                                   // vocabulary entries of a piece of the gradient
     int64_t pieces;
-    size_t x, w, part, logit, P, sum, bytes;         // offsets in the workspace, and its size
+    size_t x, w, part, logit, P, part_dx, part_dw, sum, bytes;    // offsets in the workspace, and its size
 };
 struct VocabCall {
     int64_t tokens, dim, vocab;
