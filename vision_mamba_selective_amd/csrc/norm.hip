@@ -313,18 +313,23 @@ __device__ __forceinline__ void norm_column_grad(const NormArgs& a, const Column
         }
     };
     {
-        Pack<T> hy[HOLD];
+        // two sweeps ahead: asked for all at once, the loads of a unit's two
+        // workgroups come in one burst (bf16 8 x 768 x 4,097 training step: 131 us,
+        // three ahead 126.5, two 126.1)
+        Pack<T> hy[2];
 #pragma unroll
-        for (int k = 0; k < HOLD; ++k) {
+        for (int k = 0; k < 2; ++k) {
             const int ch = c.ch + k * (Column<T, W>::kSweep);
             if (ch < a.dim) read(ch, hs[k], hy[k]);
         }
 #pragma unroll
         for (int k = 0; k < HOLD; ++k) {
-            const int ch = c.ch + k * (Column<T, W>::kSweep);
-            if (ch < a.dim) take(ch, hs[k], hy[k]);
+            const int ch = c.ch + k * (Column<T, W>::kSweep), next = ch + 2 * (Column<T, W>::kSweep);
+            Pack<T>& py = hy[k % 2];
+            if (ch < a.dim) take(ch, hs[k], py);
             hs[k].settle();
-            held[k][threadIdx.x] = uint4{hy[k].v[0], hy[k].v[1], hy[k].v[2], hy[k].v[3]};
+            held[k][threadIdx.x] = uint4{py.v[0], py.v[1], py.v[2], py.v[3]};
+            if (k + 2 < HOLD && next < a.dim) read(next, hs[k + 2], py);
         }
     }
     for (int ch = c.ch + HOLD * (Column<T, W>::kSweep); ch < a.dim; ch += (Column<T, W>::kSweep)) {
@@ -588,9 +593,13 @@ void launch_column(const NormArgs& a, uint32_t tiles, hipStream_t s) {
 template <typename T, bool ADD>
 void launch_columns(const NormArgs& a, const vs::NormCall& c, hipStream_t s) {
     const uint32_t tiles = static_cast<uint32_t>(c.batch * a.tiles);
-    // with at most two workgroups for a compute unit, twice the waves halve what
-    // each of them waits for (fp32 8 x 384 x 1,025: 12.6 -> 10.9 us)
-    if (tiles <= 512) launch_column<T, ADD, 16, 1, 3, 6>(a, tiles, s);
+    // Sixteen waves, each with half the sweeps: with at most two workgroups for a
+    // compute unit they halve what each wave waits for (fp32 8 x 384 x 1,025:
+    // 12.6 -> 10.9 us), and past six sweeps of eight waves these would leave a unit
+    // one workgroup (fp32 8 x 768 x 4,097 44.8 -> 39.7 us, bf16 4 x 1,536 x 4,097
+    // with a residual 60.6 -> 58.7). Else eight (bf16 8 x 768 x 4,097 with a
+    // residual: 56.7 us, with sixteen 60.1, with four 59.5).
+    if (tiles <= 512 || a.dim > 6 * Column<T, 8>::kSweep) launch_column<T, ADD, 16, 1, 3, 6>(a, tiles, s);
     else launch_column<T, ADD, 8, 2, 6, 12>(a, tiles, s);
 }
 template <typename T, int W, int HOLD, int... MORE>
