@@ -62,6 +62,9 @@ CASES = [
     (1, 3, 1025, [1024], False, False),
     (2, 20, 2100, [2100, 1100], True, True),
     (2, 300, 2049, [2049, 1], True, False),
+    (3, 700, 300, [300, 129, 0], True, True),
+    (2, 1024, 384, None, True, False),
+    (2, 1030, 1025, [1025, 513], True, False),
     (1, 3, 4097, None, True, False),
     (1, 2, 9000, [8193], True, True),
 ]
