@@ -92,10 +92,11 @@ def test_loss_and_gradient(case, dtype):
     check(*make(sum(case[:3]), dtype, *case, bits=32 if case[0] % 2 else 64))
 
 
-@pytest.mark.parametrize("dtype,tokens,dim,vocab", [("bf16", 5003, 136, 58001), ("f32", 2501, 68, 55003)])
+@pytest.mark.parametrize("dtype,tokens,dim,vocab", [("bf16", 5003, 136, 58001), ("f32", 2501, 68, 55003),
+                                                    ("bf16", 3, 8, 9000001), ("f32", 2, 5, 4300001)])
 def test_pieces_of_the_vocabulary(dtype, tokens, dim, vocab):
-    """Logits of more than 512 MB: the gradient takes the vocabulary in pieces.
-    The reference runs in float64 on the GPU."""
+    """Logits of more than 512 MB, or rows of them of more than 16 MB: the
+    gradient takes the vocabulary in pieces. The reference runs in float64 on the GPU."""
     import vision_mamba_selective_amd as vms
     say("case vocab pieces %s" % dtype)
     x, W, target, dloss = make(4, dtype, tokens, dim, vocab, False)

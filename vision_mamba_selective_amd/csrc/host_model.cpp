@@ -256,6 +256,9 @@ VocabPlan vocab_plan(bool grad, int64_t tokens, int64_t dim, int64_t vocab, int 
         // P of a piece takes up to 512 MB
         int64_t piece = (int64_t(1) << 29) / (tokens * static_cast<int64_t>(es)) / 256 * 256;
         piece = piece < 256 ? 256 : piece;
+        // 256 rows of P, also those past the last token, have offsets of 32 bits
+        const int64_t most = (int64_t(1) << 24) / static_cast<int64_t>(es);
+        piece = piece > most ? most : piece;
         p.pieces = ceil_div(vocab, piece);
         p.piece = ceil_div(ceil_div(vocab, p.pieces), 256) * 256;
         p.pieces = ceil_div(vocab, p.piece);

@@ -103,7 +103,7 @@ struct Operand {
     uint32_t off;            // this lane's first chunk
     int wave;
     // fragment reads
-    uint32_t at[OUTER ? 4 : 4];
+    uint32_t at[4];
 
     static __device__ __forceinline__ int turn(int line) {
         if constexpr (!OUTER) return (line >> 1) & 7;
@@ -136,8 +136,9 @@ struct Operand {
                                                             static_cast<int>(left < 0x7fffffff ? (left > 0 ? left : 0) : 0x7fffffff), 0x00020000);
 #pragma unroll
         for (int i = 0; i < kIters; ++i)
-            __builtin_amdgcn_raw_ptr_buffer_load_lds(rsrc, (lds_void*)(lds + (i * WAVES + wave) * 1024), 16, static_cast<int>(off),
-                                                     static_cast<int>(i * WAVES * kLines * ld), 0, 0);
+            // all of the offset in the lane's part, which the range check goes by
+            __builtin_amdgcn_raw_ptr_buffer_load_lds(rsrc, (lds_void*)(lds + (i * WAVES + wave) * 1024), 16,
+                                                     static_cast<int>(off + static_cast<uint32_t>(i * WAVES * kLines * ld)), 0, 0, 0);
     }
     // zeros for k >= n of a stage in LDS
     __device__ __forceinline__ void cut(char* lds, int n, int tid) const {
@@ -250,6 +251,12 @@ __device__ __forceinline__ void write_rows(const Lds& s, int wave, int lane, T* 
     wave_sync();
 }
 
+// a barrier that the copies to LDS this wave has asked for are behind
+__device__ __forceinline__ void landed() {
+    __builtin_amdgcn_s_waitcnt(0x0f70);              // vmcnt(0)
+    __syncthreads();
+}
+
 // One tile of a product, of the split `z` of its k.
 template <typename T, int BM, int BN, int WM, int WN, bool AO, bool BO, Epilogue EPI>
 __device__ __forceinline__ void gemm_tile(const GemmArgs& a, int tile, int z, const Lds& lds) {
@@ -306,11 +313,11 @@ __device__ __forceinline__ void gemm_tile(const GemmArgs& a, int tile, int z, co
 #pragma unroll
                 for (int j = 0; j < NF; ++j) Types<T>::mma(fa[s & 1][i], fb[s & 1][j], acc[i][j]);
         }
-        __syncthreads();
+        landed();
     };
     A.load(lds.a0, k_lo);
     B.load(lds.b0, k_lo);
-    __syncthreads();
+    landed();
     int k = k_lo;
     for (; k + OpA::kBk < k_hi; k += 2 * OpA::kBk) {
         A.load(lds.a1, k + OpA::kBk);
