@@ -143,6 +143,7 @@ const char* norm_problem(int64_t batch, int64_t dim, int64_t L, int& code) {
     return nullptr;
 }
 
+// a wave a row while it holds the row in 16 bytes a lane, then four, then sixteen
 NormForm norm_rows(int64_t dim, int dtype) {
     const int64_t lanes = dtype == VS_BF16 ? 8 : 4;     // entries of 16 bytes
     if (dim <= 64 * lanes) return kNormRow1;
@@ -216,7 +217,10 @@ int64_t tiles_of(int64_t m, int64_t n, int64_t tile) { return ceil_div(m, tile) 
 // Whether the logits take the larger tile: by rounds of tiles over the chip, one
 // larger tile or two smaller ones on a compute unit at a time. A round of smaller
 // ones takes 0.65 of a larger one's time in bf16, whose operands are read twice
-// as often, and half in fp32, which the matrix cores bound.
+// as often, and half in fp32, which the matrix cores bound. bf16: 197 x 768 x
+// 49,999 scored 26.7 us (smaller tile 30.7), 64 x 1,536 x 32,768 31.4 (larger 44.5),
+// the training step of 8,194 x 1,536 x 49,999 4,850 (smaller 5,240); fp32 500 x 768
+// x 10,000 scored 98.6 (larger 187).
 bool vocab_wide(int64_t m, int64_t n, int dtype) {
     const int64_t wide = ceil_div(tiles_of(m, n, 256), kNumCUs), narrow = ceil_div(tiles_of(m, n, 128), 2 * kNumCUs);
     return 20 * wide <= (dtype == VS_BF16 ? 13 : 10) * narrow;
@@ -253,7 +257,10 @@ VocabPlan vocab_plan(bool grad, int64_t tokens, int64_t dim, int64_t vocab, int 
         p.part = take(static_cast<size_t>(p.tiles) * static_cast<size_t>(tokens) * 2 * kF);
         p.logit = take(static_cast<size_t>(tokens) * kF);
     } else {
-        // P of a piece takes up to 512 MB
+        // P of a piece takes up to 512 MB: half of that lets P stay in the memory-side
+        // cache, but the products have fewer tiles to share out (bf16 8,194 x 1,536 x
+        // 49,999 5,230 us, with 256 MB 5,120; 8,194 x 768 x 32,768 2,045 and 2,211;
+        // 4,096 x 768 x 49,152 1,429 and 1,495; fp32 2,049 x 384 x 49,999 2,699 and 2,780)
         int64_t piece = (int64_t(1) << 29) / (tokens * static_cast<int64_t>(es)) / 256 * 256;
         piece = piece < 256 ? 256 : piece;
         // 256 rows of P, also those past the last token, have offsets of 32 bits
@@ -265,6 +272,8 @@ VocabPlan vocab_plan(bool grad, int64_t tokens, int64_t dim, int64_t vocab, int 
         const int64_t n = p.piece < vocab ? p.piece : vocab;
         p.prob_wide = vocab_wide(n, tokens, dtype);
         // a quarter of the larger tile's work costs the smaller one 1.3 (fp32: 1.05) quarters
+        // (bf16 8,194 x 1,536 x 49,999 4,850 us, with the smaller tile 5,300; 4,097 x 384 x
+        // 1,000 59.8, with the larger 72.8; fp32 394 x 384 x 32,768 412 and 545)
         const Splits wide = vocab_splits(dim, tokens, n, 256, dtype), narrow = vocab_splits(dim, tokens, n, 128, dtype);
         p.wide = 80 * wide.work <= (dtype == VS_BF16 ? 26 : 21) * narrow.work;
         p.dx_splits = p.wide ? wide.dx : narrow.dx;
