@@ -2,6 +2,7 @@
 together, in HIP graphs, on side streams and threads, with workspaces of exactly
 the stated size, on tensors that are written in place, at full size, with
 offsets past 32 bits; and what the Python layer refuses."""
+import gc
 import threading
 
 import pytest
@@ -73,6 +74,55 @@ def test_graph_replays(dtype):
         torch.cuda.synchronize()
         assert all(torch.equal(a, b) for a, b in zip(got, eager)), r
         assert all(torch.equal(a, b) for a, b in zip(m.step(), eager)), r
+
+
+def test_captured_backward_pass():
+    """A training step through the autograd forms, captured as torch asks: after
+    a run on a side stream, with no eager graph of the same leaves alive."""
+    import vision_mamba_selective_amd as vms
+    say("case model captured backward")
+    g = torch.Generator().manual_seed(9)
+    rnd = lambda *s: torch.randn(*s, generator=g).cuda().requires_grad_()            # noqa: E731
+    x, w, r, i, lam, W = rnd(2, 48, 130), rnd(48), rnd(2, 48, 130), rnd(2, 48, 130), rnd(48), rnd(300, 48)
+    leaves = [x, w, r, i, lam, W]
+    target = torch.randint(-20, 300, (260,), generator=g).cuda()
+    dloss = torch.ones(260).cuda()
+
+    def step():
+        y, _ = vms.rms_norm_autograd(x, w)
+        y, _ = vms.gated_scan_autograd(y, r, i, lam, z=r)
+        y, _ = vms.rms_norm_autograd(y, None, residual=x)
+        loss = vms.vocab_loss_autograd(y.transpose(1, 2).reshape(260, 48), W, target)
+        return [loss.detach()] + list(torch.autograd.grad(loss, leaves, grad_outputs=dloss))
+
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        eager = [v.clone() for v in step()]
+    torch.cuda.current_stream().wait_stream(side)
+    torch.cuda.synchronize()
+    # an eager graph of the same leaves: refused before anything is captured
+    for call in (lambda: vms.rms_norm_autograd(x, w)[0], lambda: vms.rms_norm_autograd(x.detach(), None, residual=x)[0],
+                 lambda: vms.gated_scan_autograd(x.detach(), r.detach(), i.detach(), lam)[0],
+                 lambda: vms.vocab_loss_autograd(x.detach()[0].t().contiguous(), W, target[:130])):
+        alive = call()
+        torch.cuda.synchronize()
+        with pytest.raises(RuntimeError, match="eager graph"):
+            with torch.cuda.graph(torch.cuda.CUDAGraph()):
+                call()
+        del alive
+    gc.collect()                     # the exceptions' frames hold the refused calls' graphs
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        got = step()
+    for k in range(3):
+        for v in got:
+            v.zero_()
+        graph.replay()
+        torch.cuda.synchronize()
+        assert all(torch.equal(a, b) for a, b in zip(got, eager)), k
+        assert all(torch.equal(a, b) for a, b in zip(step(), eager)), k
 
 
 def test_two_graphs_share_a_workspace():

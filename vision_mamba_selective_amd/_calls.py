@@ -45,3 +45,4 @@ rms_norm = _binding.rms_norm
 rms_norm_grad = _binding.rms_norm_grad
 vocab_loss = _binding.vocab_loss
 vocab_loss_grad = _binding.vocab_loss_grad
+capture_ready = _binding.capture_ready

@@ -17,10 +17,13 @@
 #include <ATen/ops/empty.h>
 #include <c10/core/DeviceGuard.h>
 #include <c10/hip/HIPFunctions.h>
+#include <c10/hip/HIPGraphsC10Utils.h>
 #include <c10/hip/HIPStream.h>
 #include <torch/csrc/DynamicTypes.h>
 #include <torch/csrc/Exceptions.h>
+#include <torch/csrc/autograd/function.h>
 #include <torch/csrc/autograd/python_variable.h>
+#include <torch/csrc/autograd/variable.h>
 
 #include <cstdarg>
 #include <initializer_list>
@@ -727,6 +730,27 @@ PyObject* reorder(PyObject* const* a) {
     return r;
 }
 
+// ---------------------------------------------------------------- autograd
+// inputs of a differentiable call. Where its stream is capturing, none of them may
+// be a leaf of an eager graph that is still alive: that graph's node for the
+// leaf's gradient belongs to the stream it was made on, and the captured backward
+// pass would make that stream wait inside the capture, which ends the process.
+PyObject* capture_ready(PyObject* const* a) {
+    if (!PyTuple_Check(a[0])) raise(PyExc_TypeError, "expected a tuple of tensors");
+    for (Py_ssize_t k = 0; k < PyTuple_GET_SIZE(a[0]); ++k) {
+        Maybe t = maybe("input", PyTuple_GET_ITEM(a[0], k));
+        if (!t || !t->is_cuda() || !t->requires_grad() || !t->is_leaf()) continue;
+        const c10::DeviceGuard guard(t->device());
+        if (c10::hip::currentStreamCaptureStatusMayInitCtx() == c10::hip::CaptureStatus::None) break;
+        const auto node = torch::autograd::impl::try_get_grad_accumulator(*t);
+        const auto made = node ? node->stream() : std::nullopt;
+        if (made && made->id() != c10::hip::getCurrentHIPStream(t->device().index()).unwrap().id())
+            raise(PyExc_RuntimeError, "a leaf of this call is part of an eager graph that is still alive: free it (its outputs and losses) before "
+                                      "its backward pass is captured");
+    }
+    Py_RETURN_NONE;
+}
+
 // ------------------------------------------------------------------ module
 // addresses of the library's functions by name, and what turns a status into an
 // exception; where one is missing, those bound before stay
@@ -773,6 +797,7 @@ PyMethodDef methods[] = {
     method<gated, 10>("gated_scan"), method<gated_saved, 11>("gated_scan_saved"), method<gated_grad, 12>("gated_scan_grad"),
     method<gated_step, 10>("gated_scan_step"), method<norm, 7>("rms_norm"), method<norm_grad, 7>("rms_norm_grad"),
     method<vocab_forward, 4>("vocab_loss"), method<vocab_grad, 6>("vocab_loss_grad"),
+    method<capture_ready, 1>("capture_ready"),
     {nullptr, nullptr, 0, nullptr}};
 
 PyModuleDef module_def = {PyModuleDef_HEAD_INIT, "_binding", nullptr, -1, methods, nullptr, nullptr, nullptr, nullptr};

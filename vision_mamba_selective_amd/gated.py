@@ -1,7 +1,12 @@
 """Torch-facing binding of the gated linear recurrence (include/vimscan.h, "The
 gated linear recurrence"): over prompts, for training and for single tokens on
 a pool of states. Layouts, strides, lengths, tensors written in place and what
-is differentiable (gated_scan_autograd only) are as in causal.py."""
+is differentiable (gated_scan_autograd only) are as in causal.py.
+
+gated_scan_autograd, rms_norm_autograd and vocab_loss_autograd may be captured in
+a HIP graph together with their backward pass, in torch's order: a run on a side
+stream first, and no eager graph of the same leaves alive (refused with a
+RuntimeError while capturing)."""
 from __future__ import annotations
 
 import torch
@@ -56,6 +61,7 @@ class GatedScanFunction(torch.autograd.Function):
 
     @staticmethod
     def forward(ctx, x, r, i, lam, z, h0, lengths, rate):
+        _calls.capture_ready((x, r, i, lam, z, h0))
         y, h, saved = gated_scan_saved(x, r, i, lam, z=z, h0=h0, lengths=lengths, rate=rate)
         ctx.save_for_backward(x, r, i, lam, z, h0, lengths, saved)
         ctx.rate = rate

@@ -42,6 +42,7 @@ class VocabLossFunction(torch.autograd.Function):
 
     @staticmethod
     def forward(ctx, x, W, target):
+        _calls.capture_ready((x, W))
         loss, lse = vocab_loss(x, W, target)
         ctx.save_for_backward(x, W, target, lse)
         return loss

@@ -44,6 +44,7 @@ class RmsNormFunction(torch.autograd.Function):
 
     @staticmethod
     def forward(ctx, x, w, residual, eps, lengths):
+        _calls.capture_ready((x, w, residual))
         y, s = rms_norm(x, w, residual=residual, eps=eps, lengths=lengths)
         ctx.save_for_backward(s, w, lengths)
         ctx.eps, ctx.added = eps, residual is not None
