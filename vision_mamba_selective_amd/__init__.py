@@ -1,10 +1,11 @@
 """MI355X (gfx950) selective scan for Vision Mamba and VMamba, and the causal
-form of it that a language model needs, with beam search over its states.
+form of it that a language model needs, with beam search over its states, a
+gated linear recurrence, the norm between mixers and the loss over a vocabulary.
 
 The scan itself lives in libvimscan.so (HIP kernels behind a C ABI,
 include/vimscan.h). This package holds the in-tree build step, the binding
-with the same entry-point names (ctypes; a compiled one for the causal mixer
-and beam search), and the seeded workload generator.
+with the same entry-point names (ctypes; a compiled one for the language model's
+operators), and the seeded workload generator.
 The binding is imported lazily so that the generator can be used without the
 library.
 """
