@@ -662,7 +662,9 @@ int gated_scan_step(int64_t batch, int64_t dim, int dtype, const void* x, const 
  *   lengths     as for the causal mixer: y and sum are zero at padding
  * L = 1 with channel stride 1 is one row of channels for each token, and
  * takes a form of its own. dim is at most 8192, eps finite and >= 0, batch x
- * ceil(L / 32) below 2^24. Sums are fp32. Outputs may overlap nothing else.
+ * ceil(L / 16) below 2^22; rows below 2^26 where 64 lanes of 16 bytes hold the
+ * channels, below 2^24 where 256 do, else below 2^22. Sums are fp32. Outputs
+ * may overlap nothing else.
  */
 int rms_norm(int64_t batch, int64_t dim, int64_t seqlen, int dtype, const void* x,
              const void* residual, const int64_t* strides, const float* w, float eps,
@@ -703,7 +705,8 @@ int rms_norm_grad(int64_t batch, int64_t dim, int64_t seqlen, int dtype, const v
  *   target      [tokens] integers of target_bits (32 or 64) bits
  *   loss, lse   [tokens] fp32
  *   workspace   vocab_workspace_bytes(VS_VOCAB_LOSS, ...), 16-byte aligned
- * dim is at most 65536, tokens and vocab below 2^24, tokens x vocab below 2^36.
+ * dim is at most 65536, tokens and vocab below 2^24, tokens x vocab below 2^36,
+ * tokens x dim and vocab x dim below 2^34.
  */
 enum { VS_VOCAB_LOSS = 0, VS_VOCAB_GRAD = 1 };
 size_t vocab_workspace_bytes(int op, int64_t tokens, int64_t dim, int64_t vocab, int dtype);

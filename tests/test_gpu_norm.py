@@ -92,6 +92,12 @@ CASES = [
     (2, 1700, 37, [5, 37], False),
     (5, 7, 500, [500, 499, 40, -3, 999], False),
     (1, 3500, 33, None, False),
+    (3, 400, 129, [129, 64, 128], True),
+    (2, 24, 72, [72, 65], False),
+    (2, 500, 73, None, True),
+    (3, 900, 68, [66, 68, 1], False),
+    (40, 100, 1001, None, False),
+    (36, 200, 961, [961 - 30 * k for k in range(36)], True),
 ]
 IDS = ["b%d-d%d-L%d-%s" % (c[0], c[1], c[2], "ragged" if c[3] else "full") for c in CASES]
 

@@ -68,7 +68,10 @@ def test_gated_step_refuses(kw, code):
 NORM = dict(batch=2, dim=8, L=33, dtype=nat.VS_BF16, x=at(0), res=at(1), strides=None, w=at(2), eps=1e-6, lengths=at(3), y=at(4), sum=at(5),
             stream=None)
 NORM_BAD = COMMON + [
-    (dict(dim=8193), UNSUP), (dict(batch=1 << 31, L=1), UNSUP), (dict(batch=1 << 24, L=1), UNSUP), (dict(batch=1 << 20, L=1024), UNSUP),
+    (dict(dim=8193), UNSUP), (dict(batch=1 << 31, L=1), UNSUP), (dict(batch=1 << 26, L=1), UNSUP), (dict(batch=1 << 20, L=1024), UNSUP),
+    # launches of 2^32 threads: a row form of four waves, of sixteen, rows that lie apart, tiles
+    (dict(batch=1 << 24, dim=2048, L=1), UNSUP), (dict(batch=1 << 22, dim=2056, L=1), UNSUP),
+    (dict(batch=1 << 22, L=1, strides=arr(16, 2, 16, 2, 16, 2)), UNSUP), (dict(batch=1 << 21, L=32), UNSUP),
     (dict(eps=-1.0), UNSUP), (dict(eps=NAN), UNSUP), (dict(eps=INF), UNSUP), (dict(x=None), NULL), (dict(y=None), NULL), (dict(x=at(0) + 1), ALIGN),
     (dict(w=at(2) + 2), ALIGN), (dict(lengths=at(3) + 2), ALIGN), (dict(y=at(4) + 1), ALIGN), (dict(y=at(0)), ALIAS), (dict(y=at(2)), ALIAS),
     (dict(strides=arr(-1, 33, 264, 33, 264, 33)), SHAPE), (dict(strides=arr(264, 1 << 27, 264, 33, 264, 33)), UNSUP)]
@@ -100,6 +103,7 @@ VOCAB = dict(tokens=5, dim=24, vocab=100, dtype=nat.VS_BF16, x=at(0), ldx=0, W=a
 VOCAB_BAD = [
     (dict(dtype=4), DTYPE), (dict(tokens=0), SHAPE), (dict(dim=0), SHAPE), (dict(vocab=-4), SHAPE), (dict(dim=65537), UNSUP),
     (dict(tokens=1 << 24), UNSUP), (dict(vocab=1 << 24), UNSUP), (dict(tokens=1 << 20, vocab=1 << 20), UNSUP), (dict(bits=16), UNSUP),
+    (dict(tokens=1 << 18, dim=1 << 16), UNSUP), (dict(vocab=1 << 18, dim=1 << 16), UNSUP),
     (dict(ldx=23), SHAPE), (dict(ldx=-1), SHAPE), (dict(ldx=1 << 28), UNSUP), (dict(x=None), NULL), (dict(W=None), NULL), (dict(target=None), NULL),
     (dict(x=at(0) + 1), ALIGN), (dict(W=at(1) + 2), ALIGN), (dict(target=at(2) + 4), ALIGN), (dict(ws=None), WS), (dict(ws_bytes=64), WS),
     (dict(ws=at(5) + 8), ALIGN), (dict(ws=at(1)), ALIAS)]

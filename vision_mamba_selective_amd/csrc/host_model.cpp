@@ -137,8 +137,9 @@ const char* norm_problem(int64_t batch, int64_t dim, int64_t L, int& code) {
     code = VS_ERR_UNSUPPORTED;
     if (dim > kNormMaxDim) return "dim above 8192 is not supported";
     if (L >= kCausalMaxL) return "sequences of 2^27 tokens or more are not supported";
-    if (batch >= (int64_t(1) << 31) || batch * ceil_div(L, kNormTile) >= kMaxGroups)
-        return "2^24 rows or tiles of 32 tokens or more are not supported";
+    // launches of fewer than 2^32 threads: up to 1,024 a tile, 64 or more a row
+    if (batch >= (int64_t(1) << 26) || (L > 1 && batch * ceil_div(L, 16) >= (int64_t(1) << 22)))
+        return "2^26 rows, or 2^22 tiles of 16 tokens, or more are not supported";
     if (!product_below(batch, dim, L, int64_t(1) << 40)) return "outputs of 2^40 elements or more are not supported";
     return nullptr;
 }
@@ -151,9 +152,19 @@ NormForm norm_rows(int64_t dim, int dtype) {
     return kNormRow16;
 }
 
+// Tokens of a tile, channel-major. The wider the piece of a row, the fewer lines are
+// shared with a neighbouring tile (bf16 8 x 768 x 4,097 with a residual 53.6 us in
+// pieces of 64 bytes, 44.3 in pieces of 128; training step of 8 x 384 x 4,097 62.3 and
+// 52.2), as long as six sweeps of sixteen waves (the gradient, which holds more:
+// eight), eight channels a wave, hold all channels (gradient of 8 x 768 x 4,097:
+// 106 us a step; with twelve sweeps 112, sixteen waves 108).
+int norm_tile(int64_t dim, bool grad, size_t es) {
+    return (dim <= (grad ? 384 : 768) ? kNormWide : kNormNarrow) / static_cast<int>(es);
+}
+
 // lines of dw's sums: one for each tile, or for each wave or workgroup that takes rows
-int64_t norm_parts(NormForm f, int64_t batch, int64_t L) {
-    if (f == kNormColumn) return batch * ceil_div(L, kNormTile);
+int64_t norm_parts(NormForm f, int64_t batch, int64_t L, int tile) {
+    if (f == kNormColumn) return batch * ceil_div(L, tile);
     const int64_t per = f == kNormRow1 ? 4 : 1, groups = ceil_div(batch, per);
     return (groups < kNormGroups ? groups : kNormGroups) * per;
 }
@@ -179,7 +190,11 @@ int prepare_norm(NormCall& c) {
         rows = rows && (c.st[k].d == 1 || c.dim == 1);
     }
     c.form = rows ? norm_rows(c.dim, c.dtype) : kNormColumn;
-    c.parts = norm_parts(c.form, c.batch, c.L);
+    const int64_t threads = c.form == kNormRow1 ? 64 : c.form == kNormRow4 ? 256 : 1024;
+    if (c.batch * ceil_div(c.L, 16) >= (int64_t(1) << 32) / threads)
+        return fail(VS_ERR_UNSUPPORTED, "rows of that many channels: launches of 2^32 threads or more are not supported");
+    c.tile = norm_tile(c.dim, c.grad, esize(c.dtype));
+    c.parts = norm_parts(c.form, c.batch, c.L, c.tile);
     const size_t es = esize(c.dtype), act = static_cast<size_t>(c.batch * c.dim * c.L) * es;
     const size_t par = static_cast<size_t>(c.dim) * kF, ws = c.dw ? static_cast<size_t>(c.parts) * par : 0;
     if (ws > 0 && (!c.ws || c.ws_bytes < ws)) return fail(VS_ERR_WORKSPACE, "workspace missing or smaller than norm_workspace_bytes()");
@@ -208,6 +223,8 @@ const char* vocab_problem(int64_t tokens, int64_t dim, int64_t vocab, int& code)
     code = VS_ERR_UNSUPPORTED;
     if (dim > 65536) return "dim above 65536 is not supported";
     if (tokens >= (int64_t(1) << 24) || vocab >= (int64_t(1) << 24)) return "2^24 tokens or vocabulary entries or more are not supported";
+    if (!product_below(tokens, dim, 1, int64_t(1) << 34) || !product_below(vocab, dim, 1, int64_t(1) << 34))
+        return "matrices of 2^34 entries or more are not supported";
     if (ceil_div(tokens, 128) * ceil_div(vocab, 128) >= (int64_t(1) << 22)) return "2^36 logits or more are not supported";
     return nullptr;
 }
@@ -336,9 +353,9 @@ size_t norm_workspace_bytes(int64_t batch, int64_t dim, int64_t seqlen) {
     int code;
     if (vs::norm_problem(batch, dim, seqlen, code)) return 0;
     // whichever form the strides and the type lead to
-    int64_t parts = vs::norm_parts(vs::kNormColumn, batch, seqlen);
+    int64_t parts = vs::norm_parts(vs::kNormColumn, batch, seqlen, vs::norm_tile(dim, true, 4));
     if (seqlen == 1) {
-        const int64_t rows = vs::norm_parts(vs::kNormRow1, batch, 1);
+        const int64_t rows = vs::norm_parts(vs::kNormRow1, batch, 1, 1);
         parts = parts > rows ? parts : rows;
     }
     return static_cast<size_t>(parts * dim) * vs::kF;

@@ -5,13 +5,13 @@
 //     ds = dsum + q (w dy) - s q^3 mean_d(w dy s),  dw = sum over tokens of dy s q
 // for channel-major prompts [batch][dim][L] and for rows [tokens][dim].
 //
-// Channel-major: a workgroup takes 32 tokens and all channels. A lane holds 16
-// bytes of tokens of one channel, a wave 16 channels (8 in fp32), and a sweep of
-// the workgroup 128 (64); the sweeps' s stay in registers between the sum of
-// squares and the scaling, so that every input is read once. Rows: a wave or a
-// workgroup takes a row, in the same way.
+// Channel-major: a workgroup takes a tile, 128 (64) bytes of tokens of all channels.
+// A lane holds 16 bytes of tokens of one channel, a wave 8 (16) channels; the
+// sweeps' s stay in registers between the sum of squares and the scaling, so that
+// every input is read once. Rows: a wave or a workgroup takes a row, in the same
+// way.
 //
-// dw is summed in a fixed order: per tile of 32 tokens (or per workgroup, which
+// dw is summed in a fixed order: per tile of tokens (or per workgroup, which
 // takes every n-th row) into the workspace, then over those.
 #include <hip/hip_runtime.h>
 
@@ -132,44 +132,46 @@ template <typename T>
 __device__ __forceinline__ const T* at(const void* p, int64_t off) { return static_cast<const T*>(p) + off; }
 
 // ------------------------------------------------------------ channel-major
-constexpr int kTile = vs::kNormTile;         // tokens
 
 // A lane's place in its workgroup's tile: N tokens from t on of one channel of
 // each sweep of W waves. It loads 16 bytes from `from` on, which is t except where
 // these would pass the row's end: there the entries are moved down afterwards,
 // and entries at and past the row's length become zeros. None of that is asked
 // for in a full tile, whose code is its own.
-template <typename T, int W>
+// TL lanes stand side by side along the tokens: a tile is TL times 16 bytes of each row.
+template <typename T, int W, int TL>
 struct Column {
-    static constexpr int N = Pack<T>::N, kTl = kTile / N, kCh = 64 / kTl;
+    static constexpr int N = Pack<T>::N, kTl = TL, kCh = 64 / kTl, kTile = kTl * N;
     static constexpr int kSweep = kCh * W;              // channels of a sweep
     int lane, wave, t, from, ch, len, L;
-    bool full, empty;        // the whole tile holds tokens, or none of it (the same for the workgroup)
+    bool full, empty, few;   // the whole tile holds tokens, or none of it, or the row has at most N there (the same for the workgroup)
     int64_t b;
     uint32_t tile;
-    __device__ __forceinline__ explicit Column(const NormArgs& a) {
+    // `tokens` of a tile, where that isn't this form's
+    __device__ __forceinline__ explicit Column(const NormArgs& a, int tokens = kTile) {
         // neighbouring tiles share the lines at their border: contiguous ranges of tiles to each XCD
         uint32_t zero;
         xcd_block(tile, zero);
         b = tile / a.tiles;
         lane = threadIdx.x & 63;
         wave = threadIdx.x >> 6;
-        const int t0 = static_cast<int>(tile - b * a.tiles) * kTile;
+        const int t0 = static_cast<int>(tile - b * a.tiles) * tokens;
         L = a.L;
         t = t0 + lane % kTl * N;
         from = min(t, L - N);
         ch = wave * kCh + lane / kTl;
         len = a.lengths ? __builtin_amdgcn_readfirstlane(min(max(a.lengths[b], 0), L)) : L;
-        full = t0 + kTile <= len;
+        full = t0 + tokens <= len;
         empty = t0 >= len;
+        few = L - t0 <= N;
     }
     template <bool FULL>
     __device__ __forceinline__ void load(Pack<T>& p, const T* row) const {
         if (FULL) {
             p.load(row + t);
-        } else if (L >= N && !empty) {
+        } else if (TL > 1 || L >= N) {
             p.load(row + from);
-        } else {             // rows shorter than a load
+        } else {             // rows shorter than a load have one tile, of few tokens
             p.zero();
 #pragma unroll 1
             for (int i = len - 1; i >= t; --i) p.up(ld_raw(row, i));
@@ -178,40 +180,52 @@ struct Column {
     // what load() gave, made zero past the row's length
     template <bool FULL>
     __device__ __forceinline__ void trim(Pack<T>& p) const {
-        if (!FULL) p.cut(L >= N ? t - from : 0, len - t);
+        if (!FULL) p.cut(TL > 1 || L >= N ? t - from : 0, len - t);
+    }
+    // a tile without tokens
+    __device__ __forceinline__ void clear(T* out, int dim) const {
+        Pack<T> none;
+        none.zero();
+        for (int c = ch; c < dim; c += kSweep) none.store(out + static_cast<int64_t>(c) * L, t, L);
     }
 };
 
+// A row's last tile of few tokens (one of 1,025 or 4,097) takes a channel a lane, in
+// fewer sweeps: as wide as the others it is the last to end, for its sweeps wait
+// for one another (bf16 training step of 8 x 768 x 4,097 126 -> 114 us).
+template <int HOLD, int TL>
+constexpr int kFew = (HOLD + TL - 1) / TL;
+
 // sums over the workgroup's channels of each lane's tokens
-template <typename T, int W>
-__device__ __forceinline__ void column_sum(const Column<T, W>& c, float (&v)[Pack<T>::N], float (*red)[kTile]) {
-    constexpr int N = Pack<T>::N, kTl = Column<T, W>::kTl;
+template <typename T, int W, int TL>
+__device__ __forceinline__ void column_sum(const Column<T, W, TL>& c, float (&v)[Pack<T>::N], float* red) {
+    constexpr int N = Pack<T>::N, kTl = TL;
 #pragma unroll
     for (int o = kTl; o < 64; o *= 2)
 #pragma unroll
         for (int i = 0; i < N; ++i) v[i] += __shfl_xor(v[i], o, 64);
     if (c.lane < kTl) {
 #pragma unroll
-        for (int i = 0; i < N; ++i) red[c.wave][c.lane * N + i] = v[i];
+        for (int i = 0; i < N; ++i) red[(c.wave * kTl + c.lane) * N + i] = v[i];
     }
     __syncthreads();
 #pragma unroll
     for (int i = 0; i < N; ++i) v[i] = 0.f;
-#pragma unroll
+#pragma unroll 4                        // of all waves' lines at once, the reads would take 128 registers
     for (int o = 0; o < W; ++o)
 #pragma unroll
-        for (int i = 0; i < N; ++i) v[i] += red[o][c.lane % kTl * N + i];
+        for (int i = 0; i < N; ++i) v[i] += red[(o * kTl + c.lane % kTl) * N + i];
 }
 
-template <typename T, int W, int HOLD, bool ADD, bool FULL>
-__device__ __forceinline__ void norm_column(const NormArgs& a, const Column<T, W>& c, float (*red)[kTile]) {
+template <typename T, int W, int HOLD, bool ADD, bool FULL, bool REST, int TL>
+__device__ __forceinline__ void norm_column(const NormArgs& a, const Column<T, W, TL>& c, float* red) {
     constexpr int N = Pack<T>::N;
     const T* x = at<T>(a.x, c.b * a.sx.b);
     const T* res = ADD ? at<T>(a.res, c.b * a.sres.b) : nullptr;
     const int64_t base = c.b * a.dim * static_cast<int64_t>(a.L);
     T *y = static_cast<T*>(a.y) + base, *sum = ADD ? static_cast<T*>(a.sum) + base : nullptr;
     Pack<T> held[HOLD], r[HOLD];
-    float ss[N];
+    float ss[N], hw[HOLD];
 #pragma unroll
     for (int i = 0; i < N; ++i) ss[i] = 0.f;
     // the loads of all sweeps are in flight before the first is waited for
@@ -235,15 +249,16 @@ __device__ __forceinline__ void norm_column(const NormArgs& a, const Column<T, W
     };
 #pragma unroll
     for (int k = 0; k < HOLD; ++k) {
-        const int ch = c.ch + k * (Column<T, W>::kSweep);
+        const int ch = c.ch + k * (Column<T, W, TL>::kSweep);
+        hw[k] = a.w && ch < a.dim ? a.w[ch] : 1.f;
         if (ch < a.dim) read(ch, held[k], r[k]);
     }
 #pragma unroll
     for (int k = 0; k < HOLD; ++k) {
-        const int ch = c.ch + k * (Column<T, W>::kSweep);
+        const int ch = c.ch + k * (Column<T, W, TL>::kSweep);
         if (ch < a.dim) take(ch, held[k], r[k]);
     }
-    for (int ch = c.ch + HOLD * (Column<T, W>::kSweep); ch < a.dim; ch += (Column<T, W>::kSweep)) {
+    for (int ch = c.ch + HOLD * (Column<T, W, TL>::kSweep); REST && ch < a.dim; ch += (Column<T, W, TL>::kSweep)) {
         Pack<T> s, q;
         read(ch, s, q);
         take(ch, s, q);
@@ -252,8 +267,7 @@ __device__ __forceinline__ void norm_column(const NormArgs& a, const Column<T, W
     float q[N];
 #pragma unroll
     for (int i = 0; i < N; ++i) q[i] = __builtin_amdgcn_rsqf(fmaf(ss[i], a.inv_dim, a.eps));
-    auto put = [&](int ch, const Pack<T>& s) VS_INLINE {
-        const float w = a.w ? a.w[ch] : 1.f;
+    auto put = [&](int ch, float w, const Pack<T>& s) VS_INLINE {
         float f[N];
 #pragma unroll
         for (int i = 0; i < N; ++i) f[i] = FULL || c.t + i < c.len ? s.get(i) * q[i] * w : 0.f;
@@ -263,11 +277,11 @@ __device__ __forceinline__ void norm_column(const NormArgs& a, const Column<T, W
     };
 #pragma unroll
     for (int k = 0; k < HOLD; ++k) {
-        const int ch = c.ch + k * (Column<T, W>::kSweep);
-        if (ch < a.dim) put(ch, held[k]);
+        const int ch = c.ch + k * (Column<T, W, TL>::kSweep);
+        if (ch < a.dim) put(ch, hw[k], held[k]);
     }
     // channels past what is held: read again (the lane's own entries of the sum, or x)
-    for (int ch = c.ch + HOLD * (Column<T, W>::kSweep); ch < a.dim; ch += (Column<T, W>::kSweep)) {
+    for (int ch = c.ch + HOLD * (Column<T, W, TL>::kSweep); REST && ch < a.dim; ch += (Column<T, W, TL>::kSweep)) {
         Pack<T> s;
         if constexpr (ADD) {
             s.load(sum + static_cast<int64_t>(ch) * a.L, c.t, a.L);
@@ -275,24 +289,34 @@ __device__ __forceinline__ void norm_column(const NormArgs& a, const Column<T, W
             c.template load<FULL>(s, x + ch * a.sx.d);
             c.template trim<FULL>(s);
         }
-        put(ch, s);
+        put(ch, a.w ? a.w[ch] : 1.f, s);
     }
 }
 
-// Bound by memory, in pieces of 64 bytes: 8 x 768 x 4,097 bf16 with a residual, four
-// streams of 50 MB, 57 us (3.5 TB/s), of 4,096 tokens, whose rows lie on whole
-// lines, 48.7; without a residual 22.8 us (4.4 TB/s).
-template <typename T, int W, int HOLD, bool ADD>
+// Bound by memory: 8 x 768 x 4,097 bf16 with a residual, four streams of 50 MB, 44.3
+// us, 4.5 TB/s
+template <typename T, int W, int HOLD, bool ADD, int TL>
 __global__ __launch_bounds__(64 * W) void norm_column_kernel(const NormArgs a) {
-    __shared__ float red[W][kTile];
-    const Column<T, W> c(a);
-    if (c.full) norm_column<T, W, HOLD, ADD, true>(a, c, red);
-    else norm_column<T, W, HOLD, ADD, false>(a, c, red);
+    typedef Column<T, W, TL> Col;
+    constexpr bool kRest = TL == 4;                  // else all channels are held
+    __shared__ float red[W * Col::kTile];
+    const Col c(a);
+    if (c.full) {
+        norm_column<T, W, HOLD, ADD, true, kRest>(a, c, red);
+    } else if (c.empty) {
+        const int64_t base = c.b * a.dim * static_cast<int64_t>(a.L);
+        c.clear(static_cast<T*>(a.y) + base, a.dim);
+        if constexpr (ADD) c.clear(static_cast<T*>(a.sum) + base, a.dim);
+    } else if (c.few) {
+        norm_column<T, W, kFew<HOLD, TL>, ADD, false, kRest>(a, Column<T, W, 1>(a, Col::kTile), red);
+    } else {
+        norm_column<T, W, HOLD, ADD, false, kRest>(a, c, red);
+    }
 }
 
-template <typename T, int W, int HOLD, bool FULL>
-__device__ __forceinline__ void norm_column_grad(const NormArgs& a, const Column<T, W>& c, float (*red)[W][kTile], uint4 (*held)[64 * W]) {
-    constexpr int N = Pack<T>::N, kTl = Column<T, W>::kTl;
+template <typename T, int W, int HOLD, bool FULL, bool REST, int TL>
+__device__ __forceinline__ void norm_column_grad(const NormArgs& a, const Column<T, W, TL>& c, float* red, uint4 (*held)[64 * W]) {
+    constexpr int N = Pack<T>::N, kTl = TL;
     const T *s = at<T>(a.x, c.b * a.sx.b), *dy = at<T>(a.dy, c.b * a.sdy.b);
     const T* dsum = a.dsum ? at<T>(a.dsum, c.b * a.sdsum.b) : nullptr;
     T* ds = static_cast<T*>(a.y) + c.b * a.dim * static_cast<int64_t>(a.L);
@@ -317,17 +341,17 @@ __device__ __forceinline__ void norm_column_grad(const NormArgs& a, const Column
     };
     {
         // two sweeps ahead: asked for all at once, the loads of a unit's two
-        // workgroups come in one burst (bf16 8 x 768 x 4,097 training step: 131 us,
-        // three ahead 126.5, two 126.1)
+        // workgroups come in one burst (bf16 8 x 768 x 4,097 training step, before
+        // the last tile's own form: 131 us, three ahead 126.5, two 126.1)
         Pack<T> hy[2];
 #pragma unroll
-        for (int k = 0; k < 2; ++k) {
-            const int ch = c.ch + k * (Column<T, W>::kSweep);
+        for (int k = 0; k < 2 && k < HOLD; ++k) {
+            const int ch = c.ch + k * (Column<T, W, TL>::kSweep);
             if (ch < a.dim) read(ch, hs[k], hy[k]);
         }
 #pragma unroll
         for (int k = 0; k < HOLD; ++k) {
-            const int ch = c.ch + k * (Column<T, W>::kSweep), next = ch + 2 * (Column<T, W>::kSweep);
+            const int ch = c.ch + k * (Column<T, W, TL>::kSweep), next = ch + 2 * (Column<T, W, TL>::kSweep);
             Pack<T>& py = hy[k % 2];
             if (ch < a.dim) take(ch, hs[k], py);
             hs[k].settle();
@@ -335,26 +359,33 @@ __device__ __forceinline__ void norm_column_grad(const NormArgs& a, const Column
             if (k + 2 < HOLD && next < a.dim) read(next, hs[k + 2], py);
         }
     }
-    for (int ch = c.ch + HOLD * (Column<T, W>::kSweep); ch < a.dim; ch += (Column<T, W>::kSweep)) {
+    for (int ch = c.ch + HOLD * (Column<T, W, TL>::kSweep); REST && ch < a.dim; ch += (Column<T, W, TL>::kSweep)) {
         Pack<T> ps, py;
         read(ch, ps, py);
         take(ch, ps, py);
     }
-    column_sum(c, ss, red[0]);
-    column_sum(c, sd, red[1]);
+    auto more = [&](int ch, Pack<T>& g) VS_INLINE {
+        if (dsum) c.template load<FULL>(g, dsum + ch * a.sdsum.d);
+    };
+    // dsum two sweeps ahead: its first loads are on their way while the waves meet,
+    // and none stands behind a sweep's stores (8 x 768 x 4,097: 108 -> 106 us a step)
+    Pack<T> hg[2];
+#pragma unroll
+    for (int k = 0; k < 2 && k < HOLD; ++k) {
+        const int ch = c.ch + k * (Column<T, W, TL>::kSweep);
+        if (ch < a.dim) more(ch, hg[k]);
+    }
+    column_sum(c, ss, red);
+    column_sum(c, sd, red + W * Column<T, W, TL>::kTile);
     float q[N], m[N];
 #pragma unroll
     for (int i = 0; i < N; ++i) {
         q[i] = __builtin_amdgcn_rsqf(fmaf(ss[i], a.inv_dim, a.eps));
         m[i] = q[i] * q[i] * (sd[i] * a.inv_dim);
     }
-    auto put = [&](int ch, const Pack<T>& ps, const Pack<T>& py) VS_INLINE {
+    auto put = [&](int ch, const Pack<T>& ps, const Pack<T>& py, Pack<T>& g) VS_INLINE {
         const float w = a.w ? a.w[ch] : 1.f;
-        Pack<T> g;
-        if (dsum) {
-            c.template load<FULL>(g, dsum + ch * a.sdsum.d);
-            c.template trim<FULL>(g);
-        }
+        if (dsum) c.template trim<FULL>(g);
         float f[N], dw = 0.f;
 #pragma unroll
         for (int i = 0; i < N; ++i) {
@@ -375,31 +406,46 @@ __device__ __forceinline__ void norm_column_grad(const NormArgs& a, const Column
     };
 #pragma unroll
     for (int k = 0; k < HOLD; ++k) {
-        const int ch = c.ch + k * (Column<T, W>::kSweep);
+        const int ch = c.ch + k * (Column<T, W, TL>::kSweep);
         const uint4 y = held[k][threadIdx.x];
         Pack<T> py;
         py.v[0] = y.x; py.v[1] = y.y; py.v[2] = y.z; py.v[3] = y.w;
-        if (ch < a.dim) put(ch, hs[k], py);
+        const int next = ch + 2 * (Column<T, W, TL>::kSweep);
+        if (ch < a.dim) put(ch, hs[k], py, hg[k % 2]);
+        if (k + 2 < HOLD && next < a.dim) more(next, hg[k % 2]);
     }
-    for (int ch = c.ch + HOLD * (Column<T, W>::kSweep); ch < a.dim; ch += (Column<T, W>::kSweep)) {
-        Pack<T> ps, py;
+    for (int ch = c.ch + HOLD * (Column<T, W, TL>::kSweep); REST && ch < a.dim; ch += (Column<T, W, TL>::kSweep)) {
+        Pack<T> ps, py, g;
         read(ch, ps, py);
+        more(ch, g);
         c.template trim<FULL>(ps);
         c.template trim<FULL>(py);
-        put(ch, ps, py);
+        put(ch, ps, py, g);
     }
 }
 
-// The same pieces, three streams read and one written: 66 us, 3.1 TB/s
-template <typename T, int W, int HOLD>
-__global__ __launch_bounds__(64 * W) void norm_column_grad_kernel(const NormArgs a) {
-    __shared__ float red[2][W][kTile];
+// Three streams read and one written, at 768 channels in pieces of 64 bytes: 57 us,
+// 3.5 TB/s
+template <typename T, int W, int HOLD, int TL>
+__global__ __launch_bounds__(64 * W, HOLD > 6 ? 2 : 4) void norm_column_grad_kernel(const NormArgs a) {
+    typedef Column<T, W, TL> Col;
+    constexpr bool kRest = TL == 4 && HOLD > 6;      // else all channels are held
+    __shared__ float red[2 * W * Col::kTile];
     // dy is held in LDS: in registers, s and dy together leave a compute unit one
     // workgroup, whose loads and stores then take turns
     __shared__ uint4 held[HOLD][64 * W];
-    const Column<T, W> c(a);
-    if (c.full) norm_column_grad<T, W, HOLD, true>(a, c, red, held);
-    else norm_column_grad<T, W, HOLD, false>(a, c, red, held);
+    const Col c(a);
+    if (c.full) {
+        norm_column_grad<T, W, HOLD, true, kRest>(a, c, red, held);
+    } else if (c.empty) {
+        c.clear(static_cast<T*>(a.y) + c.b * a.dim * static_cast<int64_t>(a.L), a.dim);
+        if (a.part)
+            for (int ch = threadIdx.x; ch < a.dim; ch += 64 * W) a.part[static_cast<size_t>(c.tile) * a.dim + ch] = 0.f;
+    } else if (c.few) {
+        norm_column_grad<T, W, kFew<HOLD, TL>, false, kRest>(a, Column<T, W, 1>(a, Col::kTile), red, held);
+    } else {
+        norm_column_grad<T, W, HOLD, false, kRest>(a, c, red, held);
+    }
 }
 
 // -------------------------------------------------------------------- rows
@@ -590,11 +636,11 @@ void launch_rows(const NormArgs& a, const vs::NormCall& c, hipStream_t s) {
     }
 }
 // the sweeps that are held: as few as the channels need
-template <typename T, bool ADD, int W, int HOLD, int... MORE>
+template <typename T, bool ADD, int TL, int W, int HOLD, int... MORE>
 void launch_column(const NormArgs& a, uint32_t tiles, hipStream_t s) {
     if constexpr (sizeof...(MORE) > 0)
-        if (a.dim > HOLD * Column<T, W>::kSweep) return launch_column<T, ADD, W, MORE...>(a, tiles, s);
-    norm_column_kernel<T, W, HOLD, ADD><<<tiles, 64 * W, 0, s>>>(a);
+        if (a.dim > HOLD * Column<T, W, TL>::kSweep) return launch_column<T, ADD, TL, W, MORE...>(a, tiles, s);
+    norm_column_kernel<T, W, HOLD, ADD, TL><<<tiles, 64 * W, 0, s>>>(a);
 }
 template <typename T, bool ADD>
 void launch_columns(const NormArgs& a, const vs::NormCall& c, hipStream_t s) {
@@ -603,21 +649,23 @@ void launch_columns(const NormArgs& a, const vs::NormCall& c, hipStream_t s) {
     // compute unit they halve what each wave waits for (fp32 8 x 384 x 1,025:
     // 12.6 -> 10.9 us), and past six sweeps of eight waves these would leave a unit
     // one workgroup (fp32 8 x 768 x 4,097 44.8 -> 39.7 us, bf16 4 x 1,536 x 4,097
-    // with a residual 60.6 -> 58.7). Else eight (bf16 8 x 768 x 4,097 with a
-    // residual: 56.7 us, with sixteen 60.1, with four 59.5).
-    if (tiles <= 512 || a.dim > 6 * Column<T, 8>::kSweep) launch_column<T, ADD, 16, 1, 3, 6>(a, tiles, s);
-    else launch_column<T, ADD, 8, 2, 6, 12>(a, tiles, s);
+    // with a residual 60.6 -> 58.7).
+    if (c.tile != vs::kNormWide / static_cast<int>(sizeof(T))) launch_column<T, ADD, 4, 16, 6>(a, tiles, s);
+    else if (tiles <= 512 || a.dim > 6 * Column<T, 8, 8>::kSweep) launch_column<T, ADD, 8, 16, 1, 3, 6>(a, tiles, s);
+    else launch_column<T, ADD, 8, 8, 2, 6>(a, tiles, s);
 }
-template <typename T, int W, int HOLD, int... MORE>
+template <typename T, int TL, int W, int HOLD, int... MORE>
 void launch_column_grad(const NormArgs& a, uint32_t tiles, hipStream_t s) {
     if constexpr (sizeof...(MORE) > 0)
-        if (a.dim > HOLD * Column<T, W>::kSweep) return launch_column_grad<T, W, MORE...>(a, tiles, s);
-    norm_column_grad_kernel<T, W, HOLD><<<tiles, 64 * W, 0, s>>>(a);
+        if (a.dim > HOLD * Column<T, W, TL>::kSweep) return launch_column_grad<T, TL, W, MORE...>(a, tiles, s);
+    norm_column_grad_kernel<T, W, HOLD, TL><<<tiles, 64 * W, 0, s>>>(a);
 }
 template <typename T>
 void launch_grad(const NormArgs& a, const vs::NormCall& c, hipStream_t s) {
     if (c.form == vs::kNormColumn) {
-        launch_column_grad<T, 8, 2, 6, 12>(a, static_cast<uint32_t>(c.batch * a.tiles), s);
+        const uint32_t tiles = static_cast<uint32_t>(c.batch * a.tiles);
+        if (c.tile == vs::kNormWide / static_cast<int>(sizeof(T))) launch_column_grad<T, 8, 8, 2, 6>(a, tiles, s);
+        else launch_column_grad<T, 4, 8, 6, 12>(a, tiles, s);
     } else {
         const dim3 grid(static_cast<uint32_t>(c.form == vs::kNormRow1 ? a.parts / 4 : a.parts));
         switch (c.form) {
@@ -637,7 +685,7 @@ int run(vs::NormCall& c) {
     a.w = c.w; a.eps = c.eps; a.inv_dim = 1.f / static_cast<float>(c.dim); a.lengths = c.lengths;
     a.y = c.y; a.sum = c.sum; a.part = c.dw ? static_cast<float*>(c.ws) : nullptr; a.dw = c.dw;
     a.rows = c.batch; a.dim = static_cast<int>(c.dim); a.L = static_cast<int>(c.L);
-    a.tiles = static_cast<int>((c.L + kTile - 1) / kTile);
+    a.tiles = static_cast<int>((c.L + c.tile - 1) / c.tile);
     a.parts = static_cast<int>(c.parts);
     const auto s = static_cast<hipStream_t>(c.stream);
     const bool bf16 = c.dtype == VS_BF16;

@@ -63,7 +63,9 @@ struct GatedStepCall {
 int prepare_gated_step(GatedStepCall& c);
 
 // ---- the norm (norm.hip)
-constexpr int kNormTile = 32;                        // tokens of a workgroup, channel-major
+// Bytes of each channel's row that a workgroup takes, channel-major: the wider
+// tile where six sweeps of its waves hold the channels
+constexpr int kNormWide = 128, kNormNarrow = 64;
 constexpr int64_t kNormMaxDim = 8192;
 constexpr int64_t kNormGroups = 1024;                // workgroups that take the rows of a gradient in turn
 // channel-major, or rows in 1, 4 or 16 waves: the channels a lane holds bound
@@ -85,6 +87,7 @@ struct NormCall {
     void* stream;
     bool grad = false;
     Strides st[3];                                   // x, residual; gradient: s, dy, dsum
+    int tile;                                        // tokens
     NormForm form;
     int64_t parts;                                   // gradient: lines of sums for dw
 };
