@@ -199,8 +199,9 @@ int prepare_norm(NormCall& c) {
     const size_t par = static_cast<size_t>(c.dim) * kF, ws = c.dw ? static_cast<size_t>(c.parts) * par : 0;
     if (ws > 0 && (!c.ws || c.ws_bytes < ws)) return fail(VS_ERR_WORKSPACE, "workspace missing or smaller than norm_workspace_bytes()");
     auto span = [&](int k) { return Span{ins[k], ins[k] ? span_bytes(c.batch, c.dim, c.L, c.st[k], es) : 0}; };
-    // the sum may be the residual itself
-    const bool inplace = !c.grad && c.sum && c.sum == c.residual && c.st[1].d == c.L && (c.st[1].b == c.dim * c.L || c.batch == 1);
+    // the sum may be the residual itself (a stride over one channel, or one row, says nothing)
+    const bool inplace = !c.grad && c.sum && c.sum == c.residual && (c.st[1].d == c.L || c.dim == 1) &&
+                         (c.st[1].b == c.dim * c.L || c.batch == 1);
     const Span in[] = {span(0), span(1), span(2), {c.w, par}, {c.lengths, static_cast<size_t>(c.batch) * 4}};
     const Span out[] = {{c.y, act}, {c.grad ? nullptr : c.sum, act}, {c.dw, par}, {c.dw ? c.ws : nullptr, ws}};
     if (int rc = check_aligned(in, 3, es, "activation pointer misaligned")) return rc;
