@@ -670,7 +670,9 @@ int rms_norm(int64_t batch, int64_t dim, int64_t seqlen, int dtype, const void* 
              const void* residual, const int64_t* strides, const float* w, float eps,
              const int32_t* lengths, void* y, void* sum, void* stream);
 
-/* Bytes of rms_norm_grad's workspace; 0 for sizes it refuses. */
+/* Bytes of rms_norm_grad's workspace; 0 for sizes it refuses. It does not grow
+ * with the batch past 4,096 lines of dim floats (dim above 512: 1,024), for L > 1
+ * past 64 MB of them: the rows are then taken in parts, one launch after another. */
 size_t norm_workspace_bytes(int64_t batch, int64_t dim, int64_t seqlen);
 
 /*

@@ -39,10 +39,39 @@ void in_place() {
     expect(vs::prepare_norm(c) == VS_ERR_ALIAS, "one channel, rows that lie apart");
 }
 
+// the workspace of the gradient's sums: what norm_workspace_bytes() says suffices for
+// any type and strides, no more lines for one token a row past 4,096 (past 512
+// channels 1,024), and 64 MB or that many lines for longer rows
+void norm_workspaces() {
+    const int64_t batches[] = {1, 2, 3, 700, 1023, 1025, 4097, 8194, 65536, 100000, (int64_t(1) << 22) - 1};
+    const int64_t lengths[] = {1, 2, 17, 32, 33, 100, 4097, 21845, 43712, 70000, 100000, (int64_t(1) << 27) - 1};
+    for (int64_t batch : batches)
+        for (int64_t dim : {1, 24, 384, 385, 512, 513, 768, 769, 1536, 4096, 8192})
+            for (int64_t L : lengths) {
+                const size_t bytes = norm_workspace_bytes(batch, dim, L);
+                if (bytes == 0) continue;                    // sizes that are refused
+                const int64_t strides[] = {dim, 1, dim, 1, dim, 1}, apart[] = {2 * dim * L, 2 * L, 2 * dim * L, 2 * L, 2 * dim * L, 2 * L};
+                for (int k = 0; k < 6; ++k) {
+                    vs::NormCall c = norm(batch, dim, L, k / 2 == 0 ? nullptr : k / 2 == 1 && L == 1 ? strides : apart);
+                    c.dtype = k % 2 ? VS_BF16 : VS_F32;
+                    c.grad = true; c.dy = at(3); c.dw = fp(4); c.ws = at(5); c.ws_bytes = bytes;
+                    expect(vs::prepare_norm(c) == VS_OK || vs::last_error()[0] != 'w', "a workspace of the stated size");
+                    if (c.form == vs::kNormColumn) {
+                        const int64_t tiles = (L + c.tile - 1) / c.tile;
+                        expect(c.slab >= 1 && c.slab <= batch && c.slab * tiles == c.parts, "a slab's tiles");
+                    }
+                }
+                const int64_t few = dim > 512 ? 1024 : 4096, lines = static_cast<int64_t>(bytes) / 4 / dim;
+                if (L == 1) expect(lines <= few, "rows of one token: a bounded workspace");
+                else expect(lines <= few || lines * dim * 4 <= 64 << 20 || lines <= (L + 15) / 16, "a bounded workspace");
+            }
+}
+
 }  // namespace
 
 int main() {
     in_place();
+    norm_workspaces();
     if (failures) return 1;
     std::puts("host model edges ok");
     return 0;

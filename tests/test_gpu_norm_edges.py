@@ -22,3 +22,32 @@ def test_stream_in_place_of_one_channel():
         stream = res.clone()
         y2, _ = vms.rms_norm(x, w, residual=stream, sum_out=stream)
         assert torch.equal(y, y2) and torch.equal(s, stream)
+
+
+# rows, dim, tokens, strided: launches that follow one another because the workspace holds the sums of a part of the rows
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16], ids=["f32", "bf16"])
+@pytest.mark.parametrize("batch,dim,L", [(9000, 40, 1), (3000, 520, 1), (2100, 8192, 2)], ids=str)
+def test_gradient_of_many_rows_in_parts(batch, dim, L, dtype):
+    """Rows whose channels lie apart (one token of longer prompts), and short
+    prompts of many channels, some of them empty; the workspace is exactly of the
+    stated size and shared by the launches."""
+    import vision_mamba_selective_amd as vms
+    say("case norm parts %s" % ((batch, dim, L),))
+    g = torch.Generator(device="cuda").manual_seed(dim)
+    rnd = lambda: torch.randn(batch, dim, L + (2 if L == 1 else 0), generator=g, device="cuda").to(dtype)    # noqa: E731
+    s, dy, dsum = ((v[:, :, 1:2] if L == 1 else v) for v in (rnd(), rnd(), rnd()))
+    w = 1 + 0.3 * torch.randn(dim, generator=g, device="cuda")
+    lengths = torch.randint(0, L + 1, (batch,), generator=g, device="cuda").to(torch.int32)
+    size = vms.norm_workspace_bytes(batch, dim, L)
+    whole = torch.full((size + 4096,), 0xA5, dtype=torch.uint8, device="cuda")
+    got = vms.rms_norm_grad(s, w, dy, dsum=dsum, eps=1e-5, lengths=lengths, workspace=whole[:size])
+    again = vms.rms_norm_grad(s, w, dy, dsum=dsum, eps=1e-5, lengths=lengths)
+    assert bool((whole[size:] == 0xA5).all())
+    assert torch.equal(got["dx"], again["dx"]) and torch.equal(got["dw"], again["dw"])
+    live = (torch.arange(L, device="cuda") < lengths[:, None])[:, None, :].double()
+    sd, yd, gd = (v.double() * live for v in (s, dy, dsum))
+    q = 1 / torch.sqrt(sd.square().mean(1, keepdim=True) + 1e-5)
+    wy = w.double()[:, None] * yd
+    want = (gd + q * wy - sd * q ** 3 * (wy * sd).mean(1, keepdim=True)) * live
+    close(got["dx"], want.cpu(), "dx")
+    close(got["dw"], (yd * sd * q).sum((0, 2)).cpu(), "dw")

@@ -162,9 +162,20 @@ int norm_tile(int64_t dim, bool grad, size_t es) {
     return (dim <= (grad ? 384 : 768) ? kNormWide : kNormNarrow) / static_cast<int>(es);
 }
 
-// lines of dw's sums: one for each tile, or for each wave or workgroup that takes rows
-int64_t norm_parts(NormForm f, int64_t batch, int64_t L, int tile) {
-    if (f == kNormColumn) return batch * ceil_div(L, tile);
+// Batch rows that a channel-major gradient takes in one launch: each tile leaves a
+// line of dw's sums, 4 bytes a channel, and rows of one token would leave twice
+// what a bf16 activation holds (65,536 x 4,096: 1 GB). One token: as many lines as
+// the rows' form has; more: 64 MB of lines, or 4,096. What is past that goes into dw
+// launch by launch.
+int64_t norm_slab(int64_t batch, int64_t dim, int64_t L, int tile) {
+    const int64_t few = dim > 512 ? kNormGroups : 4 * kNormGroups, fit = (int64_t(1) << 24) / dim, tiles = ceil_div(L, tile);
+    const int64_t rows = (L == 1 || fit < few ? few : fit) / tiles;
+    return rows < 1 ? 1 : rows < batch ? rows : batch;
+}
+
+// lines of dw's sums: one for each tile of a launch, or for each wave or workgroup that takes rows
+int64_t norm_parts(NormForm f, int64_t batch, int64_t dim, int64_t L, int tile) {
+    if (f == kNormColumn) return norm_slab(batch, dim, L, tile) * ceil_div(L, tile);
     const int64_t per = f == kNormRow1 ? 4 : 1, groups = ceil_div(batch, per);
     return (groups < kNormGroups ? groups : kNormGroups) * per;
 }
@@ -194,7 +205,8 @@ int prepare_norm(NormCall& c) {
     if (c.batch * ceil_div(c.L, 16) >= (int64_t(1) << 32) / threads)
         return fail(VS_ERR_UNSUPPORTED, "rows of that many channels: launches of 2^32 threads or more are not supported");
     c.tile = norm_tile(c.dim, c.grad, esize(c.dtype));
-    c.parts = norm_parts(c.form, c.batch, c.L, c.tile);
+    c.slab = c.grad && c.dw && c.form == kNormColumn ? norm_slab(c.batch, c.dim, c.L, c.tile) : c.batch;
+    c.parts = norm_parts(c.form, c.batch, c.dim, c.L, c.tile);
     const size_t es = esize(c.dtype), act = static_cast<size_t>(c.batch * c.dim * c.L) * es;
     const size_t par = static_cast<size_t>(c.dim) * kF, ws = c.dw ? static_cast<size_t>(c.parts) * par : 0;
     if (ws > 0 && (!c.ws || c.ws_bytes < ws)) return fail(VS_ERR_WORKSPACE, "workspace missing or smaller than norm_workspace_bytes()");
@@ -354,11 +366,14 @@ size_t norm_workspace_bytes(int64_t batch, int64_t dim, int64_t seqlen) {
     int code;
     if (vs::norm_problem(batch, dim, seqlen, code)) return 0;
     // whichever form the strides and the type lead to
-    int64_t parts = vs::norm_parts(vs::kNormColumn, batch, seqlen, vs::norm_tile(dim, true, 4));
-    if (seqlen == 1) {
-        const int64_t rows = vs::norm_parts(vs::kNormRow1, batch, 1, 1);
-        parts = parts > rows ? parts : rows;
-    }
+    int64_t parts = 0;
+    auto most = [&](vs::NormForm f, int tile) {
+        const int64_t n = vs::norm_parts(f, batch, dim, seqlen, tile);
+        parts = n > parts ? n : parts;
+    };
+    for (size_t es : {2, 4}) most(vs::kNormColumn, vs::norm_tile(dim, true, es));
+    // past 512 channels a row has four waves or more in either type
+    if (seqlen == 1) most(dim > 512 ? vs::kNormRow4 : vs::kNormRow1, 1);
     return static_cast<size_t>(parts * dim) * vs::kF;
 }
 

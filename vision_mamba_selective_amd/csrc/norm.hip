@@ -126,6 +126,7 @@ struct NormArgs {
     int64_t rows;                           // the batch
     int dim, L, tiles;                      // tiles of a batch row
     int parts;
+    int add;                                // dw already holds the sums of other rows
 };
 
 template <typename T>
@@ -630,7 +631,7 @@ __global__ __launch_bounds__(kDwCh* kDwLines) void norm_dw_kernel(const NormArgs
     red[line][threadIdx.x % kDwCh] = s;
     __syncthreads();
     if (threadIdx.x < kDwCh && ch < a.dim) {
-        s = 0.f;
+        s = a.add ? a.dw[ch] : 0.f;
         for (int o = 0; o < kDwLines; ++o) s += red[o][threadIdx.x];
         a.dw[ch] = s;
     }
@@ -674,12 +675,29 @@ void launch_column_grad(const NormArgs& a, uint32_t tiles, hipStream_t s) {
         if (a.dim > HOLD * Column<T, W, TL>::kSweep) return launch_column_grad<T, TL, W, MORE...>(a, tiles, s);
     norm_column_grad_kernel<T, W, HOLD, TL><<<tiles, 64 * W, 0, s>>>(a);
 }
+void launch_dw(const NormArgs& a, hipStream_t s) {
+    if (a.dw) norm_dw_kernel<<<dim3((a.dim + kDwCh - 1) / kDwCh), kDwCh * kDwLines, 0, s>>>(a);
+}
 template <typename T>
 void launch_grad(const NormArgs& a, const vs::NormCall& c, hipStream_t s) {
     if (c.form == vs::kNormColumn) {
-        const uint32_t tiles = static_cast<uint32_t>(c.batch * a.tiles);
-        if (c.tile == vs::kNormWide / static_cast<int>(sizeof(T))) launch_column_grad<T, 8, 8, 2, 6>(a, tiles, s);
-        else launch_column_grad<T, 4, 8, 6, 12>(a, tiles, s);
+        // the batch rows whose lines of dw the workspace holds, one such slab after another
+        for (int64_t b = 0; b < c.batch; b += c.slab) {
+            const int64_t rows = c.batch - b < c.slab ? c.batch - b : c.slab;
+            NormArgs p = a;
+            p.x = static_cast<const T*>(a.x) + b * a.sx.b;
+            p.dy = static_cast<const T*>(a.dy) + b * a.sdy.b;
+            if (a.dsum) p.dsum = static_cast<const T*>(a.dsum) + b * a.sdsum.b;
+            if (a.lengths) p.lengths = a.lengths + b;
+            p.y = static_cast<T*>(a.y) + b * a.dim * a.L;
+            p.rows = rows;
+            p.add = b > 0;
+            const uint32_t tiles = static_cast<uint32_t>(rows * a.tiles);
+            p.parts = static_cast<int>(tiles);
+            if (c.tile == vs::kNormWide / static_cast<int>(sizeof(T))) launch_column_grad<T, 8, 8, 2, 6>(p, tiles, s);
+            else launch_column_grad<T, 4, 8, 6, 12>(p, tiles, s);
+            launch_dw(p, s);
+        }
     } else {
         const dim3 grid(static_cast<uint32_t>(c.form == vs::kNormRow1 ? a.parts / 4 : a.parts));
         switch (c.form) {
@@ -687,8 +705,8 @@ void launch_grad(const NormArgs& a, const vs::NormCall& c, hipStream_t s) {
             case vs::kNormRow4: norm_row_grad_kernel<T, 4, 1><<<grid, 256, 0, s>>>(a); break;
             default: norm_row_grad_kernel<T, 16, kRowHold<T>><<<grid, 1024, 0, s>>>(a); break;
         }
+        launch_dw(a, s);
     }
-    if (a.dw) norm_dw_kernel<<<dim3((a.dim + kDwCh - 1) / kDwCh), kDwCh * kDwLines, 0, s>>>(a);
 }
 
 int run(vs::NormCall& c) {

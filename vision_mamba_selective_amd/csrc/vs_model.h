@@ -92,6 +92,7 @@ struct NormCall {
     int tile;                                        // tokens
     NormForm form;
     int64_t parts;                                   // gradient: lines of sums for dw
+    int64_t slab;                                    // batch rows of a launch
 };
 int prepare_norm(NormCall& c);
 
