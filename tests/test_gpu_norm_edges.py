@@ -51,3 +51,17 @@ def test_gradient_of_many_rows_in_parts(batch, dim, L, dtype):
     want = (gd + q * wy - sd * q ** 3 * (wy * sd).mean(1, keepdim=True)) * live
     close(got["dx"], want.cpu(), "dx")
     close(got["dw"], (yd * sd * q).sum((0, 2)).cpu(), "dw")
+
+
+@pytest.mark.parametrize("shape,value", [(((1 << 22) - 1, 1, 2), 1.1), ((1 << 25, 1), 1.2)], ids=["tiles", "rows"])
+def test_weight_gradient_of_many_equal_terms(shape, value):
+    """Where all terms of dw agree, roundings of an fp32 sum lean to one side: 65,536
+    (8,192) of them one after another are off by 7e-4 (8e-5) of the sum. In steps of 64
+    and in 64 bits fewer than 400 roundings of 2^-24 are left, close()'s bound."""
+    import vision_mamba_selective_amd as vms
+    say("case norm many equal terms %s" % (shape,))
+    s = torch.ones(shape, device="cuda")
+    dy = torch.full_like(s, value)
+    g = vms.rms_norm_grad(s, torch.ones(1, device="cuda"), dy, eps=0.0)
+    close(g["dw"], dy.flatten()[:1].cpu().double() * s.numel(), "dw")
+    assert float(g["dx"].abs().max()) <= 8 * 2.0 ** -24

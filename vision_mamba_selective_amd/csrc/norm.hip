@@ -12,7 +12,7 @@
 // way.
 //
 // dw is summed in a fixed order: per tile of tokens (or per workgroup, which
-// takes every n-th row) into the workspace, then over those.
+// takes every n-th row) into the workspace, then over those in 64 bits.
 #include <hip/hip_runtime.h>
 
 #include <cstdint>
@@ -540,11 +540,11 @@ __global__ __launch_bounds__(W == 1 ? 256 : 64 * W) void norm_row_grad_kernel(co
     constexpr int N = Pack<T>::N, kStep = 64 * W * N;
     __shared__ float red[2][W][2];
     const RowOf<W> r;
-    float dw[HOLD][N];
+    float dw[HOLD][N], before[HOLD][N];
 #pragma unroll
     for (int k = 0; k < HOLD; ++k)
 #pragma unroll
-        for (int i = 0; i < N; ++i) dw[k][i] = 0.f;
+        for (int i = 0; i < N; ++i) dw[k][i] = before[k][i] = 0.f;
     const int64_t first = W == 1 ? static_cast<int64_t>(blockIdx.x) * 4 + r.wave : blockIdx.x;
     const int64_t step = static_cast<int64_t>(gridDim.x) * (W == 1 ? 4 : 1);
     // the next row is read while this one is worked on
@@ -563,7 +563,7 @@ __global__ __launch_bounds__(W == 1 ? 256 : 64 * W) void norm_row_grad_kernel(co
         }
     };
     if (first < a.rows) read(first);
-    int odd = 0;
+    int odd = 0, left = 64;
     for (int64_t b = first; b < a.rows; b += step, odd ^= 1) {
         T* ds = static_cast<T*>(a.y) + b * a.dim;
         const bool real = n != 0;
@@ -607,6 +607,18 @@ __global__ __launch_bounds__(W == 1 ? 256 : 64 * W) void norm_row_grad_kernel(co
             o.set(f);
             o.store(ds, i0, a.dim);
         }
+        // 64 rows at a time: a lane may take 16,384, whose terms one after another
+        // would be off by 1.7e-4 of their sum
+        if (--left == 0) {
+            left = 64;
+#pragma unroll
+            for (int k = 0; k < HOLD; ++k)
+#pragma unroll
+                for (int i = 0; i < N; ++i) {
+                    before[k][i] += dw[k][i];
+                    dw[k][i] = 0.f;
+                }
+        }
     }
     if (!a.part) return;
     float* part = a.part + static_cast<size_t>(W == 1 ? blockIdx.x * 4 + r.wave : blockIdx.x) * a.dim;
@@ -615,16 +627,19 @@ __global__ __launch_bounds__(W == 1 ? 256 : 64 * W) void norm_row_grad_kernel(co
 #pragma unroll
         for (int i = 0; i < N; ++i) {
             const int at_ = k * kStep + r.tid * N + i;
-            if (at_ < a.dim) part[at_] = dw[k][i];
+            if (at_ < a.dim) part[at_] = before[k][i] + dw[k][i];
         }
 }
 
-// dw from the parts: 16 channels a workgroup, 64 lines of parts side by side
+// dw from the parts: 16 channels a workgroup, 64 lines of parts side by side. In 64
+// bits: a call may have 4 million parts, 65,536 for each thread, whose sum in 32 would
+// be off by 7e-4 where they agree in sign. 5 us for 1,032 parts of 768 channels, a
+// chain of reads; few channels with many parts leave most compute units idle.
 constexpr int kDwCh = 16, kDwLines = 64;
 __global__ __launch_bounds__(kDwCh* kDwLines) void norm_dw_kernel(const NormArgs a) {
-    __shared__ float red[kDwLines][kDwCh + 1];
+    __shared__ double red[kDwLines][kDwCh + 1];
     const int ch = blockIdx.x * kDwCh + threadIdx.x % kDwCh, line = threadIdx.x / kDwCh;
-    float s = 0.f;
+    double s = 0;
     if (ch < a.dim)
 #pragma unroll 8
         for (int p = line; p < a.parts; p += kDwLines) s += a.part[static_cast<size_t>(p) * a.dim + ch];
@@ -633,7 +648,7 @@ __global__ __launch_bounds__(kDwCh* kDwLines) void norm_dw_kernel(const NormArgs
     if (threadIdx.x < kDwCh && ch < a.dim) {
         s = a.add ? a.dw[ch] : 0.f;
         for (int o = 0; o < kDwLines; ++o) s += red[o][threadIdx.x];
-        a.dw[ch] = s;
+        a.dw[ch] = static_cast<float>(s);
     }
 }
 
