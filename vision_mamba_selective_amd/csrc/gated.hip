@@ -386,7 +386,10 @@ __global__ __launch_bounds__(NW > 4 ? 64 * NW : 256) void gated_grad_kernel(cons
     const float k2 = a.rate * softplus_f(a.lam[w.d]) * kLog2e;
     const bool slow = __ballot(!(k2 < kSlow)) == 0;
     float mu = a.dh_out ? a.dh_out[w.row] : 0.f;
-    float sum = 0.f;
+    // dlam's sum, a block's tokens in 32 bits and the blocks in 64: a row of 2^24
+    // tokens has 32,768 for each lane, which in 32 bits were off by 3e-4 of their sum.
+    // Rows of 16 lanes have at most three blocks.
+    std::conditional_t<G == 16, float, double> total = 0;
 
     auto block = [&](auto vec, auto is_slow, auto is_part, auto& tx, auto& tr, auto& ti, auto& tz, auto& ty, float& first, int t, int c,
                      auto&& next) VS_INLINE {
@@ -438,7 +441,7 @@ __global__ __launch_bounds__(NW > 4 ? 64 * NW : 256) void gated_grad_kernel(cons
         float Pl, Ml;
         later_and_all<G>(P, M, w.lane, Pl, Ml, Pa, Ha);
         const float from = pass_on<NW, true>(ex, c & 1, w.wave, w.lane, Pa, Ha, mu);
-        float back = fmaf(Pl, from, Ml), fx[V], fr[V], fi[V];
+        float back = fmaf(Pl, from, Ml), sum = 0.f, fx[V], fr[V], fi[V];
 #pragma unroll
         for (int j = V - 1; j >= 0; --j) {
             const bool on = !PART || t + j < w.len;
@@ -451,6 +454,7 @@ __global__ __launch_bounds__(NW > 4 ? 64 * NW : 256) void gated_grad_kernel(cons
             fr[j] = gs * fmaf(-sr[j], kLn2, kLn2);
             sum += gs;
         }
+        total += sum;
         store_tokens<PART>(dx, t, w.L, fx);
         store_tokens<PART>(dr, t, w.L, fr);
         store_tokens<PART>(di, t, w.L, fi);
@@ -518,7 +522,8 @@ __global__ __launch_bounds__(NW > 4 ? 64 * NW : 256) void gated_grad_kernel(cons
     if (a.dh0 && w.lane == 0 && w.wave == 0 && w.L > 0) a.dh0[w.row] = mu;
     // the row's part of dlam: lanes, then waves, in a fixed order
 #pragma unroll
-    for (int o = 1; o < G; o *= 2) sum += __shfl_xor(sum, o, 64);
+    for (int o = 1; o < G; o *= 2) total += __shfl_xor(total, o, 64);
+    float sum = static_cast<float>(total);
     if constexpr (NW > 1) {
         __syncthreads();
         if (w.lane == 0) ex.P[0][w.wave] = sum;
@@ -531,7 +536,8 @@ __global__ __launch_bounds__(NW > 4 ? 64 * NW : 256) void gated_grad_kernel(cons
 }
 
 // dlam: the rows of each channel, in 64 bits (their terms have either sign). One
-// short chain of reads: 5 us, a launch of its own because it needs every row.
+// chain of reads for each channel, eight rows at a time: 4 us for a batch of 8, 16 of
+// 64, 122 of 512 (384 channels). A launch of its own because it needs every row.
 __global__ __launch_bounds__(256) void gated_lam_kernel(const GatedArgs a) {
     const uint32_t d = blockIdx.x * 256 + threadIdx.x;
     if (d >= a.dim) return;
