@@ -67,11 +67,27 @@ void norm_workspaces() {
             }
 }
 
+// Operands are read by words: rows whose length is no whole number of them are
+// packed, also where their stride is one, for the last row may end the caller's memory.
+void odd_rows() {
+    for (int64_t dim : {1, 24, 25, 26, 63})
+        for (int64_t ldx : {dim, dim + 1, dim + 2, int64_t(70000)})
+            for (int dtype : {VS_F32, VS_BF16}) {
+                vs::VocabCall c{};
+                c.tokens = 5; c.dim = dim; c.vocab = 100; c.dtype = dtype; c.x = at(0); c.ldx = ldx; c.W = at(1); c.target = at(2);
+                c.target_bits = 64; c.loss = fp(4); c.lse = fp(5); c.ws = at(3); c.ws_bytes = size_t(1) << 43;
+                expect(vs::prepare_vocab(c) == VS_OK, "a loss");
+                const bool odd = dtype == VS_BF16 && (dim % 2 || ldx % 2);
+                expect(c.plan.pack_x == (odd || ldx > 65536) && c.plan.pack_w == (dtype == VS_BF16 && dim % 2), "rows that are packed");
+            }
+}
+
 }  // namespace
 
 int main() {
     in_place();
     norm_workspaces();
+    odd_rows();
     if (failures) return 1;
     std::puts("host model edges ok");
     return 0;

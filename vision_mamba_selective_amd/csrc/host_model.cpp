@@ -276,7 +276,7 @@ VocabPlan vocab_plan(bool grad, int64_t tokens, int64_t dim, int64_t vocab, int 
     VocabPlan p{};
     const size_t es = esize(dtype);
     p.dp = ceil_div(dim, 8) * 8;
-    p.pack_w = dim * static_cast<int64_t>(es) % 4 != 0;         // a row starts between words
+    p.pack_w = dim * static_cast<int64_t>(es) % 4 != 0;         // a row starts or ends between words
     size_t off = 0;
     auto take = [&](size_t n) { const size_t at = off; off += al256(n); return at; };
     p.x = take(static_cast<size_t>(tokens * p.dp) * es);
@@ -333,7 +333,8 @@ int prepare_vocab(VocabCall& c) {
     c.plan = vocab_plan(c.grad, c.tokens, c.dim, c.vocab, c.dtype);
     const size_t es = esize(c.dtype);
     if (!c.ws || c.ws_bytes < c.plan.bytes) return fail(VS_ERR_WORKSPACE, "workspace missing or smaller than vocab_workspace_bytes()");
-    c.plan.pack_x = !aligned(c.x, 4) || c.ldx * static_cast<int64_t>(es) % 4 != 0 || c.ldx > 65536;
+    // reads go by words: x starts, steps and ends on one, or is packed
+    c.plan.pack_x = !aligned(c.x, 4) || c.ldx * static_cast<int64_t>(es) % 4 != 0 || c.plan.pack_w || c.ldx > 65536;
     const size_t xs = (static_cast<size_t>((c.tokens - 1) * c.ldx) + static_cast<size_t>(c.dim)) * es, ws = static_cast<size_t>(c.vocab * c.dim) * es;
     const size_t row = static_cast<size_t>(c.tokens) * kF;
     const Span ins[] = {{c.x, xs}, {c.W, ws}, {c.target, static_cast<size_t>(c.tokens) * (c.target64 ? 8 : 4)},
