@@ -20,3 +20,31 @@ def test_rows_of_odd_length_at_even_strides(dim, stride):
     rows = memory.as_strided((133, dim), (stride, 1))
     rows.copy_(x)
     check(rows, W, target, dloss)
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("vocab", [64, 700, 40000])
+@pytest.mark.parametrize("base", [64.0, -64.0, 8.0])
+def test_loss_far_from_zero(base, vocab, dtype):
+    """Logits around +-4,096 (and 64) that fp32 holds exactly: 64 x base, and steps of
+    1/512 up to 1/2 added. The loss goes by their differences, so what bounds it is a
+    maximum's distance (exact), an exponential, sums of positive terms and a logarithm:
+    32 roundings of 2^-24, relative to 1 + the loss. lse itself is rounded at
+    its size."""
+    import vision_mamba_selective_amd as vms
+    say("case vocab far from zero %s %d %s" % (base, vocab, dtype))
+    dt = torch.float32 if dtype == "f32" else torch.bfloat16
+    g = torch.Generator().manual_seed(vocab)
+    tokens = 200
+    x = torch.zeros(tokens, 8)
+    x[:, 0], x[:, 3] = 64, 2.0 ** torch.randint(-1, 2, (tokens,), generator=g)
+    W = torch.zeros(vocab, 8)
+    W[:, 0], W[:, 3] = base, torch.randint(0, 128, (vocab,), generator=g) / 256.0
+    target = torch.randint(0, vocab, (tokens,), generator=g)
+    loss, lse = vms.vocab_loss(x.to(dt).cuda(), W.to(dt).cuda(), target.cuda())
+    l = x.double() @ W.double().T
+    assert torch.equal(l, l.float().double()) and torch.equal(x, x.to(dt).float()) and torch.equal(W, W.to(dt).float())
+    ref = torch.logsumexp(l, dim=1)
+    want = torch.logsumexp(l - l.gather(1, target[:, None]), dim=1)
+    assert bool(((loss.cpu().double() - want).abs() <= 32 * 2.0 ** -24 * (1 + want)).all()), float((loss.cpu().double() - want).abs().max())
+    assert bool(((lse.cpu().double() - ref).abs() <= 2.0 ** -24 * ref.abs() + 32 * 2.0 ** -24 * (1 + want)).all())

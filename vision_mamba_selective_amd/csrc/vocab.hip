@@ -354,13 +354,15 @@ __device__ __forceinline__ void gemm_tile(const GemmArgs& a, int tile, int z, co
 #pragma unroll
                 for (int r = 0; r < 16; ++r) mx = fmaxf(mx, acc[i][j][r]);
             mx = fmaxf(mx, __shfl_xor(mx, 32, 64));
-            const float from = (mx == -INFINITY ? 0.f : mx) * kLog2e;
+            const float top = mx == -INFINITY ? 0.f : mx, from = top * kLog2e;
             float sum = 0.f;
 #pragma unroll
             for (int i = 0; i < MF; ++i)
 #pragma unroll
                 for (int r = 0; r < 16; ++r) sum += __builtin_amdgcn_exp2f(fmaf(acc[i][j][r], kLog2e, -from));
             sum += __shfl_xor(sum, 32, 64);
+            // what rounding `from` took off each exponent: 2.4e-4 where logits are near 4,096
+            sum *= __builtin_amdgcn_exp2f(fmaf(-top, kLog2e, from));
             if (lane < 32) {
                 red[wm * BN + n - n0] = mx;
                 red[(WM + wm) * BN + n - n0] = sum;
@@ -559,10 +561,11 @@ __global__ __launch_bounds__(256) void vocab_lse_kernel(const LseArgs a) {
     sum = 0.f;
 #pragma unroll
     for (int o = 0; o < 16; ++o) sum += red[1][o][c] * __builtin_amdgcn_exp2f((red[0][o][c] - safe) * kLog2e);
-    const float lse = safe + logf(sum);
-    a.lse[t] = lse;
+    // the loss from differences: of lse, rounded at the logits' size, it would lose what they are away from zero
+    const float rest = logf(sum);
+    a.lse[t] = safe + rest;
     const int64_t g = a.target64 ? static_cast<const int64_t*>(a.target)[t] : static_cast<const int32_t*>(a.target)[t];
-    a.loss[t] = g >= 0 && g < a.vocab ? lse - a.target_logit[t] : 0.f;
+    a.loss[t] = g >= 0 && g < a.vocab ? (safe - a.target_logit[t]) + rest : 0.f;
 }
 
 // the splits of a product, in order
