@@ -48,3 +48,40 @@ def test_loss_far_from_zero(base, vocab, dtype):
     want = torch.logsumexp(l - l.gather(1, target[:, None]), dim=1)
     assert bool(((loss.cpu().double() - want).abs() <= 32 * 2.0 ** -24 * (1 + want)).all()), float((loss.cpu().double() - want).abs().max())
     assert bool(((lse.cpu().double() - ref).abs() <= 2.0 ** -24 * ref.abs() + 32 * 2.0 ** -24 * (1 + want)).all())
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("dim", [8, 131])
+def test_gradient_far_from_zero(dim, dtype):
+    """Logits of up to 7,936, of which one is 2,112 or more above the others: lse is that
+    one, exactly, its entry of P is 0 or dloss and the target's 0 or -dloss. An
+    exponential of zero and the products: 8 roundings of 2^-24 and those of a sum (bf16
+    adds P's and the result's). What rounding lse log2(e) takes off the exponent would be 3e-4 here."""
+    import vision_mamba_selective_amd as vms
+    say("case vocab gradient far from zero %d %s" % (dim, dtype))
+    dt = torch.float32 if dtype == "f32" else torch.bfloat16
+    tokens, vocab = 150, 300
+    g = torch.Generator().manual_seed(dim)
+    x = torch.zeros(tokens, dim)
+    x[:, 0] = torch.arange(tokens) % 30 + 33.0
+    W = torch.randn(vocab, dim, generator=g).to(dt).float()
+    W[:, 0] = 64.0
+    W[7, 0] = 128.0
+    target = torch.where(torch.arange(tokens) % 3 == 0, torch.arange(tokens) + 8, torch.tensor(7))
+    dloss = torch.randn(tokens, generator=g)
+    x, W, target, dloss = x.to(dt).cuda(), W.to(dt).cuda(), target.cuda(), dloss.cuda()
+    _, lse = vms.vocab_loss(x, W, target)
+    assert torch.equal(lse, 128.0 * x[:, 0].float())
+    got = vms.vocab_loss_grad(x, W, target, lse, dloss)
+    P, size = (torch.zeros(tokens, vocab, dtype=torch.float64, device="cuda") for _ in range(2))
+    rows = torch.arange(tokens, device="cuda")
+    P[:, 7] += dloss
+    P[rows, target] -= dloss
+    size[:, 7] = size[rows, target] = dloss.abs().double()
+    E = 2.0 ** -24
+    half = 2.0 ** -8 if dtype == "bf16" else 0.0              # P's rounding, and the result's
+    for name, want, big in (("dx", P @ W.double(), size @ W.double().abs()), ("dW", P.T @ x.double(), size.T @ x.double().abs())):
+        exact = P.abs() @ W.double().abs() if name == "dx" else P.abs().T @ x.double().abs()
+        tol = (8 + 4 * math.sqrt(tokens)) * E * big + half * (exact + want.abs())
+        off = (got[name].double() - want).abs()
+        assert bool((off <= tol).all()), (name, float((off / (tol + 1e-300)).max()))

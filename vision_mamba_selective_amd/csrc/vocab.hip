@@ -396,16 +396,17 @@ __device__ __forceinline__ void gemm_tile(const GemmArgs& a, int tile, int z, co
             const int n = nw + 32 * j, nc = min(n, a.N - 1);
             const int64_t t = target_of(a, nc);
             const bool on = t >= 0 && t < a.vocab;
-            const float lse = a.lse[nc] * kLog2e, g = on ? a.dloss[nc] : 0.f;
+            const float lse = a.lse[nc], shift = lse * kLog2e, g = on ? a.dloss[nc] : 0.f;
+            // with what rounding `shift` took off each exponent
+            const float gp = g * __builtin_amdgcn_exp2f(fmaf(-lse, kLog2e, shift));
             // the target's place among this lane's rows
             const int64_t hot = t - a.v0 - mw;
             const int first = n0 + wn * (BN / WN) + 32 * j, mf = m0 + wm * (BM / WM);
             write_rows<T, BM, WM>(lds, wave, lane, static_cast<T*>(a.P) + static_cast<int64_t>(first) * a.ldp + mf, a.ldp, a.N - first, a.ldp - mf,
                                   [&](int i, int r) VS_INLINE {
                                       const int m = 32 * i + 8 * (r / 4) + r % 4;
-                                      float p = __builtin_amdgcn_exp2f(fmaf(acc[i][j][r], kLog2e, -lse));
-                                      if (hot == m) p -= 1.f;
-                                      return on && mw + m < a.M ? p * g : 0.f;
+                                      const float p = __builtin_amdgcn_exp2f(fmaf(acc[i][j][r], kLog2e, -shift));
+                                      return on && mw + m < a.M ? fmaf(p, gp, hot == m ? -g : 0.f) : 0.f;
                                   });
         }
     } else {
