@@ -85,3 +85,34 @@ def test_gradient_far_from_zero(dim, dtype):
         tol = (8 + 4 * math.sqrt(tokens)) * E * big + half * (exact + want.abs())
         off = (got[name].double() - want).abs()
         assert bool((off <= tol).all()), (name, float((off / (tol + 1e-300)).max()))
+
+
+# one tile, a product cut into parts, pieces of the vocabulary
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("tokens,dim,vocab", [(300, 72, 900), (40, 300, 30001), (3, 8, 9000001)], ids=str)
+def test_left_out_tokens_have_zero_gradients_whatever_the_head_holds(tokens, dim, vocab, dtype):
+    """Entries of the head with a -inf (no token's logit there is above -inf) or a NaN
+    and a +inf: the left-out tokens' loss and dx are zero all the same. With the -inf, dW
+    of every other entry keeps its bits: that entry's part of P is zero."""
+    import vision_mamba_selective_amd as vms
+    say("case vocab left out, head %s %s" % ((tokens, dim, vocab), dtype))
+    x, W, target, dloss = make(5, dtype, tokens, dim, vocab, False)
+    x = x.abs()
+    left = (target < 0) | (target >= vocab)
+    bad = vocab // 2
+    target = torch.where(target == bad, bad + 1, target)
+    W[bad] = 0
+    W[bad, 0] = -1e30
+    _, lse = vms.vocab_loss(x, W, target)
+    clean = vms.vocab_loss_grad(x, W, target, lse, dloss)
+    W[bad, 0] = -math.inf
+    loss, lse2 = vms.vocab_loss(x, W, target)
+    got = vms.vocab_loss_grad(x, W, target, lse2, dloss)
+    assert torch.equal(lse, lse2) and float(loss[left].abs().sum()) == 0
+    assert float(got["dx"][left].float().abs().sum()) == 0
+    same = torch.arange(vocab, device="cuda") != bad
+    assert torch.equal(got["dW"][same], clean["dW"][same]) and float(got["dW"][bad].float().abs().sum()) == 0
+    W[bad, 0], W[bad, dim - 1] = math.nan, math.inf
+    loss, lse2 = vms.vocab_loss(x, W, target)
+    got = vms.vocab_loss_grad(x, W, target, lse2, dloss)
+    assert float(loss[left].abs().sum()) == 0 and float(got["dx"][left].float().abs().sum()) == 0

@@ -50,7 +50,7 @@ struct GemmArgs {
     int M, N, K;
     int tiles_m, tiles_n;
     int k_split;                    // k of one split (a multiple of a stage's)
-    // logits
+    // logits, dx
     const void* target;
     int target64;
     int v0, vocab;                  // the vocabulary entry of m = 0; entries in all
@@ -182,6 +182,8 @@ struct Operand {
 __device__ __forceinline__ int64_t target_of(const GemmArgs& a, int t) {
     return a.target64 ? static_cast<const int64_t*>(a.target)[t] : static_cast<const int32_t*>(a.target)[t];
 }
+// whether a token's target is an entry of the vocabulary
+__device__ __forceinline__ bool kept(const GemmArgs& a, int64_t target) { return target >= 0 && target < a.vocab; }
 
 // four consecutive entries of a row of n
 __device__ __forceinline__ void put_four(float* p, int at, int n, const float (&f)[4]) {
@@ -395,7 +397,7 @@ __device__ __forceinline__ void gemm_tile(const GemmArgs& a, int tile, int z, co
         for (int j = 0; j < NF; ++j) {
             const int n = nw + 32 * j, nc = min(n, a.N - 1);
             const int64_t t = target_of(a, nc);
-            const bool on = t >= 0 && t < a.vocab;
+            const bool on = kept(a, t);
             const float lse = a.lse[nc], shift = lse * kLog2e, g = on ? a.dloss[nc] : 0.f;
             // with what rounding `shift` took off each exponent
             const float gp = g * __builtin_amdgcn_exp2f(fmaf(-lse, kLog2e, shift));
@@ -415,11 +417,13 @@ __device__ __forceinline__ void gemm_tile(const GemmArgs& a, int tile, int z, co
         for (int j = 0; j < NF; ++j) {
             const int n = nw + 32 * j, first = n0 + wn * (BN / WN) + 32 * j, mf = m0 + wm * (BM / WM);
             float* sum = a.sum ? a.sum + (static_cast<int64_t>(split ? z : 0) * a.N + min(n, a.N - 1)) * a.M : nullptr;
+            // a token that is left out: its row of P is zeros, but an infinity in W would make NaN of them
+            const bool on = BO || kept(a, target_of(a, min(n, a.N - 1)));
             if (a.out && !split) {
                 write_rows<T, BM, WM>(lds, wave, lane, static_cast<T*>(a.out) + static_cast<int64_t>(first) * a.ldo + mf, a.ldo, a.N - first,
                                       a.M - mf, [&](int i, int r) VS_INLINE {
                                           const int m = mw + 32 * i + 8 * (r / 4) + r % 4;
-                                          return acc[i][j][r] + (a.add && m < a.M ? sum[m] : 0.f);
+                                          return on ? acc[i][j][r] + (a.add && m < a.M ? sum[m] : 0.f) : 0.f;
                                       });
                 continue;
             }
@@ -432,7 +436,7 @@ __device__ __forceinline__ void gemm_tile(const GemmArgs& a, int tile, int z, co
                     if (m >= a.M) continue;
                     float f[4];
 #pragma unroll
-                    for (int r = 0; r < 4; ++r) f[r] = acc[i][j][4 * q + r] + (a.add && !split && m + r < a.M ? sum[m + r] : 0.f);
+                    for (int r = 0; r < 4; ++r) f[r] = on ? acc[i][j][4 * q + r] + (a.add && !split && m + r < a.M ? sum[m + r] : 0.f) : 0.f;
                     put_four(sum, m, a.M, f);
                 }
         }
@@ -686,6 +690,7 @@ int launch(const vs::VocabCall& c) {
             GemmArgs dx{}, dw{};
             dx.A = W + v0 * ldw; dx.lda = ldw; dx.B = l.P; dx.ldb = l.ldp;
             dx.M = static_cast<int>(c.dim); dx.N = static_cast<int>(c.tokens); dx.K = n;
+            dx.target = c.target; dx.target64 = c.target64; dx.vocab = l.vocab;
             dx.add = v0 > 0; dx.sum = p.pieces > 1 ? sum : nullptr;
             dx.out = last ? c.dx : nullptr; dx.ldo = c.dim;
             dw.A = x; dw.lda = ldx; dw.B = l.P; dw.ldb = l.ldp;
