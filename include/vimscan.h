@@ -720,7 +720,9 @@ int vocab_loss(int64_t tokens, int64_t dim, int64_t vocab, int dtype, const void
  * Gradient of sum_t dloss_t loss_t, with the lse of a vocab_loss call on the
  * same inputs (not checked). The vocabulary is taken in pieces: of each the
  * logits again, P = (exp(l - lse) - [v = target]) dloss, rounded to dtype for
- * the two products that follow, and sums in fp32.
+ * the two products that follow (what that takes off the target's entry, which
+ * outweighs the others, comes to both in a term of its own), and sums in fp32.
+ * lse being rounded, P is off by 2^-24 |lse| of exp(l - lse) dloss.
  *   dloss       [tokens] fp32; not used where the target leaves the token out
  *   dx          [tokens][dim], dW [vocab][dim], dtype; both repeat bit for bit
  *   workspace   vocab_workspace_bytes(VS_VOCAB_GRAD, ...)

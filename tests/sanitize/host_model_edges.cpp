@@ -82,12 +82,23 @@ void odd_rows() {
             }
 }
 
+// bf16: a gradient's workspace ends with what rounding took off the targets' entries, a token each
+void rests() {
+    for (int64_t t : {1, 33, 500, 4097, 8194})
+        for (int64_t d : {1, 24, 1536})
+            for (int64_t v : {1, 257, 49999, 1000000}) {
+                const vs::VocabPlan g = vs::vocab_plan(true, t, d, v, VS_BF16);
+                expect(g.rest >= g.sum + (g.pieces > 1 ? size_t(t * d) * 4 : 0) && g.rest + size_t(t) * 4 <= g.bytes, "their place");
+            }
+}
+
 }  // namespace
 
 int main() {
     in_place();
     norm_workspaces();
     odd_rows();
+    rests();
     if (failures) return 1;
     std::puts("host model edges ok");
     return 0;

@@ -116,3 +116,60 @@ def test_left_out_tokens_have_zero_gradients_whatever_the_head_holds(tokens, dim
     loss, lse2 = vms.vocab_loss(x, W, target)
     got = vms.vocab_loss_grad(x, W, target, lse2, dloss)
     assert float(loss[left].abs().sum()) == 0 and float(got["dx"][left].float().abs().sum()) == 0
+
+
+def tight(x, W, target, dloss):
+    """dx and dW in float64 with the bounds of test_gpu_vocab.py, but of the target's entry of
+    P only what its two parts in bf16 leave: 2^-16 of itself (each is off by at most 2^-8
+    of what it stands for)."""
+    kept = (target >= 0) & (target < W.shape[0])
+    E, xd, Wd = 2.0 ** -24, torch.where(kept[:, None], x, 0).double(), W.double()
+    l = xd @ Wd.T
+    g = torch.where(kept, dloss.double(), 0.0)[:, None]
+    p = torch.softmax(l, dim=1)
+    hot = torch.zeros_like(p).scatter_(1, torch.where(kept, target, 0).long()[:, None], 1.0)
+    P = (p - hot) * g
+    delta = 4 * E * math.sqrt(x.shape[1]) * float(xd.norm(dim=1).max()) * float(Wd.norm(dim=1).max()) + 16 * E
+    off = torch.where(hot > 0, 2.0 ** -16 * P.abs(), 2.0 ** -8 * P.abs()) + delta * p * g.abs()
+    mag, out = (p + hot) * g.abs(), {}
+    for name, left, right, size, terms in (("dx", P, Wd, (off, mag), W.shape[0]), ("dW", P.T, xd, (off.T, mag.T), x.shape[0])):
+        want = left @ right
+        out[name] = want, size[0] @ right.abs() + (16 + 4 * math.sqrt(terms)) * E * (size[1] @ right.abs()) + 2.0 ** -8 * want.abs()
+    return out
+
+
+# tokens, dim, vocab, distinct targets (0: any): few and many tokens for a tile of dW, both tile sizes, tails, products cut
+# into parts, rows of odd length, one target for all (more than a pass's list), pieces of the vocabulary
+@pytest.mark.parametrize("tokens,dim,vocab,targets", [
+    (1, 1, 1, 0), (5, 7, 33, 0), (129, 100, 257, 0), (300, 30, 2500, 0), (1000, 130, 40, 0), (2100, 33, 700, 1), (40, 1536, 3001, 0),
+    (9000, 24, 5000, 1), (9000, 264, 5000, 3), (4097, 520, 9000, 0), (3, 8, 9000001, 2), (5003, 136, 58001, 0), (20000, 8, 300, 2)], ids=str)
+def test_rounding_of_the_targets_entries(tokens, dim, vocab, targets):
+    import vision_mamba_selective_amd as vms
+    say("case vocab targets' entries %s" % ((tokens, dim, vocab, targets),))
+    x, W, target, dloss = make(7, "bf16", tokens, dim, vocab, False)
+    W = (W.float() / 4).bfloat16()                             # other entries stay small
+    if targets:
+        kept = (target >= 0) & (target < vocab)
+        target = torch.where(kept, (target % targets) * (vocab // 2) % vocab, target)
+    _, lse = vms.vocab_loss(x, W, target)
+    got = vms.vocab_loss_grad(x, W, target, lse, dloss)
+    again = vms.vocab_loss_grad(x, W, target, lse, dloss)
+    for name, (want, tol) in tight(x, W, target, dloss).items():
+        off = (got[name].double() - want).abs() / (tol + 1e-300)
+        assert bool(torch.isfinite(off).all()) and float(off.max()) <= 1, (name, float(off.max()))
+        assert torch.equal(got[name], again[name])
+
+
+def test_bf16_gradients_are_as_good_as_their_last_rounding():
+    """With the softmax spread over 5,000 entries the root of its squares' sum is about
+    0.1, so that rounding its entries adds less than 1 % (in squares) to the
+    results' own rounding; the target's entry, rounded once, would add as much as that."""
+    import vision_mamba_selective_amd as vms
+    say("case vocab bf16 gradients")
+    x, W, target, _ = make(12, "bf16", 1500, 256, 5000, False)
+    dloss = 0.5 + torch.rand(1500, generator=torch.Generator().manual_seed(3)).cuda()
+    _, lse = vms.vocab_loss(x, W, target)
+    got = vms.vocab_loss_grad(x, W, target, lse, dloss)
+    for name, (want, _) in tight(x, W, target, dloss).items():
+        least = float((want.bfloat16().double() - want).norm())
+        assert float((got[name].double() - want).norm()) <= 1.05 * least, (name, float((got[name].double() - want).norm()) / least)

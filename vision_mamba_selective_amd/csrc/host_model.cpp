@@ -312,6 +312,7 @@ VocabPlan vocab_plan(bool grad, int64_t tokens, int64_t dim, int64_t vocab, int 
         p.part_dx = take(p.dx_splits > 1 ? static_cast<size_t>(p.dx_splits * tokens * dim) * kF : 0);
         p.part_dw = take(p.dw_splits > 1 ? static_cast<size_t>(p.dw_splits * n * dim) * kF : 0);
         p.sum = take(p.pieces > 1 ? static_cast<size_t>(tokens * dim) * kF : 0);
+        p.rest = take(dtype == VS_BF16 ? static_cast<size_t>(tokens) * kF : 0);
     }
     p.bytes = off;
     return p;

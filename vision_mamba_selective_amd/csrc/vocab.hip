@@ -22,7 +22,10 @@
 // The forward pass leaves a maximum and a sum for each token and tile of the
 // vocabulary, 8 bytes for 256 logits. The gradient takes the vocabulary in
 // pieces: logits again, P of the piece into the workspace, then both products
-// that read it.
+// that read it. P is held in the operands' type, as the matrix cores take it. In bf16
+// its entries are off by half a step, at random, which a sum of many averages out; but
+// a token's largest is its target's, -dloss less a little, so what rounding took
+// off that one is kept in fp32 and added to both products.
 #include <hip/hip_runtime.h>
 
 #include <cstdint>
@@ -58,6 +61,8 @@ struct GemmArgs {
     const float *lse, *dloss;       // kProb
     void* P;                        // [N][ldp]
     int ldp;
+    float* rest;                    // bf16: what rounding took off the targets' entries of P, [tokens]; a product that has it adds it
+    const void* rows;               // dx: W from entry 0
     // kSum: sum[n][m] = (add ? sum : 0) + product, or out in the operands' type
     void* out;
     int64_t ldo;
@@ -140,6 +145,24 @@ struct Operand {
             __builtin_amdgcn_raw_ptr_buffer_load_lds(rsrc, (lds_void*)(lds + (i * WAVES + wave) * 1024), 16,
                                                      static_cast<int>(off + static_cast<uint32_t>(i * WAVES * kLines * ld)), 0, 0, 0);
     }
+    // where entry `at` of a line of LDS stands
+    static __device__ __forceinline__ int place(int line, int at) { return line * kLine + ((at * kEs / 16) ^ turn(line)) * 16 + at * kEs % 16; }
+    // a stage of rows from k on, those of list[0..n-1] (its low 16 bits, from k); zeros behind them
+    __device__ __forceinline__ void pick(char* lds, int k, const int* list, int n, int lane) const {
+        static_assert(OUTER, "a row of the operand is a line");
+        const int64_t left = bytes - k * ld;
+        const auto rsrc = __builtin_amdgcn_make_buffer_rsrc(const_cast<char*>(base + k * ld), 0,
+                                                            static_cast<int>(left < 0x7fffffff ? left : 0x7fffffff), 0x00020000);
+#pragma unroll
+        for (int i = 0; i < kIters; ++i) {
+            const int line = (i * WAVES + wave) * kLines + lane / kLanes;
+            const uint32_t at_ = line < n ? static_cast<uint32_t>((list[line] & 0xffff) * ld) + (lane % kLanes ^ turn(line)) * 16 : 0x80000000u;
+            __builtin_amdgcn_raw_ptr_buffer_load_lds(rsrc, (lds_void*)(lds + (i * WAVES + wave) * 1024), 16, static_cast<int>(at_), 0, 0, 0);
+        }
+    }
+    static __device__ __forceinline__ void clear(char* lds, int tid) {
+        for (int i = tid * 16; i < kBytes; i += WAVES * 64 * 16) *reinterpret_cast<f32x4*>(lds + i) = f32x4{0.f, 0.f, 0.f, 0.f};
+    }
     // zeros for k >= n of a stage in LDS
     __device__ __forceinline__ void cut(char* lds, int n, int tid) const {
         if constexpr (OUTER) {
@@ -147,7 +170,7 @@ struct Operand {
         } else {
             for (int i = tid; i < R * kBk; i += WAVES * 64) {
                 const int row = i / kBk, k = i % kBk;
-                if (k >= n) *reinterpret_cast<T*>(lds + row * kStage + ((k * kEs / 16) ^ turn(row)) * 16 + k * kEs % 16) = 0;
+                if (k >= n) *reinterpret_cast<T*>(lds + place(row, k)) = 0;
             }
         }
     }
@@ -202,10 +225,19 @@ __device__ __forceinline__ void put_four(uint16_t* p, int at, int n, const float
             if (at + i < n) p[at + i] = b[i];
 }
 
+// Of a run of tokens those whose targets are entries of a tile of dW, in order: token
+// (16 bits) and entry, and the rest of its entry of P
+constexpr int kHits = 2048;
+struct Hits {
+    int list[kHits];
+    uint16_t rest[kHits];
+    int count[8];
+};
 // A workgroup's LDS: two stages of both operands, in arrays of their own, so
 // that a stage's reads do not wait for the next one's loads.
 struct Lds {
     char *a0, *a1, *b0, *b1;
+    Hits* hits;
 };
 
 // what a wave has written to its part of LDS is there for its other lanes
@@ -292,12 +324,7 @@ __device__ __forceinline__ void gemm_tile(const GemmArgs& a, int tile, int z, co
 #pragma unroll
             for (int r = 0; r < 16; ++r) acc[i][j][r] = 0.f;
 
-    auto stage = [&](char* pa, char* pb, int k) VS_INLINE {
-        if (k + OpA::kBk > k_hi) {
-            A.cut(pa, k_hi - k, tid);
-            B.cut(pb, k_hi - k, tid);
-            __syncthreads();
-        }
+    auto multiply = [&](char* pa, char* pb) VS_INLINE {
         // a step's fragments are read while the matrix cores work on the last one's
         typename Types<T>::Frag fa[2][MF], fb[2][NF];
         auto read = [&](int s) VS_INLINE {
@@ -317,6 +344,14 @@ __device__ __forceinline__ void gemm_tile(const GemmArgs& a, int tile, int z, co
         }
         landed();
     };
+    auto stage = [&](char* pa, char* pb, int k) VS_INLINE {
+        if (k + OpA::kBk > k_hi) {
+            A.cut(pa, k_hi - k, tid);
+            B.cut(pb, k_hi - k, tid);
+            __syncthreads();
+        }
+        multiply(pa, pb);
+    };
     A.load(lds.a0, k_lo);
     B.load(lds.b0, k_lo);
     landed();
@@ -332,6 +367,76 @@ __device__ __forceinline__ void gemm_tile(const GemmArgs& a, int tile, int z, co
         stage(lds.a1, lds.b1, k + OpA::kBk);
     }
     if (k < k_hi) stage(lds.a0, lds.b0, k);
+
+    // The targets' entries of P, near -dloss, outweigh the others, so that what their
+    // rounding took off would add to a result's own in full (bf16 8,194 x 1,536 x 49,999: off
+    // by 0.0023 of dx and dW where 0.0017 is the last rounding). dW: in stages of their
+    // own, those of the split's tokens whose targets are entries of the tile (one or two
+    // behind 128; as many again where the vocabulary is one tile).
+    if constexpr (EPI == kSum && BO && sizeof(T) == 2) {
+        if (a.rest) {
+            constexpr int kThreads = 64 * kWaves;
+            Hits& hits = *lds.hits;
+            auto entry = [&](int t) VS_INLINE {
+                const int64_t v = t < k_hi ? target_of(a, t) : -1, in = v - a.v0 - n0;
+                return kept(a, v) && in >= 0 && in < BN && n0 + in < a.N ? static_cast<int>(in) : -1;
+            };
+            int set0 = -1, set1 = -1;                                // what a lane has set in its line of b0 and b1
+            bool clear = false;
+            for (int t0 = k_lo; t0 < k_hi; t0 += kHits) {
+                const int per = (min(kHits, k_hi - t0) + kThreads - 1) / kThreads, mine = t0 + tid * per;
+                uint32_t found = 0;
+#pragma unroll 4
+                for (int j = 0; j < per; ++j) found |= (entry(mine + j) >= 0 ? 1u : 0u) << j;
+                // this thread's place in the list: tokens stay in order
+                int before = __builtin_popcount(found), all = 0;
+                const int own = before;
+#pragma unroll
+                for (int o = 1; o < 64; o *= 2) {
+                    const int up = __shfl_up(before, o, 64);
+                    before += lane >= o ? up : 0;
+                }
+                if (lane == 63) hits.count[wave] = before;
+                __syncthreads();
+                before -= own;
+                for (int w = 0; w < kWaves; ++w) {
+                    const int n = hits.count[w];
+                    before += w < wave ? n : 0;
+                    all += n;
+                }
+                for (; found; found &= found - 1, ++before) {
+                    const int t = mine + __builtin_ctz(found);
+                    hits.list[before] = (t - t0) | entry(t) << 16;
+                    st(hits.rest, before, a.rest[t]);
+                }
+                if (all > 0 && !clear) {
+                    OpB::clear(lds.b0, tid);
+                    OpB::clear(lds.b1, tid);
+                    clear = true;
+                }
+                __syncthreads();
+                auto fill = [&](char* pa, char* pb, int s, int& set) VS_INLINE {
+                    A.pick(pa, t0, hits.list + s, all - s, lane);
+                    if (tid < OpA::kBk) {
+                        T* line = reinterpret_cast<T*>(pb);
+                        if (set >= 0) line[set] = 0;
+                        set = s + tid < all ? OpB::place(tid, hits.list[s + tid] >> 16) / OpB::kEs : -1;
+                        if (set >= 0) line[set] = hits.rest[s + tid];
+                    }
+                };
+                if (all > 0) {
+                    fill(lds.a0, lds.b0, 0, set0);
+                    landed();
+                }
+                for (int s = 0; s < all; s += 2 * OpA::kBk) {
+                    if (s + OpA::kBk < all) fill(lds.a1, lds.b1, s + OpA::kBk, set1);
+                    multiply(lds.a0, lds.b0);
+                    if (s + 2 * OpA::kBk < all) fill(lds.a0, lds.b0, s + 2 * OpA::kBk, set0);
+                    if (s + OpA::kBk < all) multiply(lds.a1, lds.b1);
+                }
+            }
+        }
+    }
 
     // acc[i][j][r] of a lane: row m0 + wm BM / WM + 32 i + 8 (r / 4) + 4 (lane / 32) + r % 4, column n0 + wn BN / WN + 32 j + lane % 32
     const int mw = m0 + wm * (BM / WM) + 4 * (lane >> 5), nw = n0 + wn * (BN / WN) + (lane & 31);
@@ -401,18 +506,55 @@ __device__ __forceinline__ void gemm_tile(const GemmArgs& a, int tile, int z, co
             const float lse = a.lse[nc], shift = lse * kLog2e, g = on ? a.dloss[nc] : 0.f;
             // with what rounding `shift` took off each exponent
             const float gp = g * __builtin_amdgcn_exp2f(fmaf(-lse, kLog2e, shift));
-            // the target's place among this lane's rows
+            // the target's place among this lane's rows, and its entry
             const int64_t hot = t - a.v0 - mw;
+            float top = 0.f;
             const int first = n0 + wn * (BN / WN) + 32 * j, mf = m0 + wm * (BM / WM);
             write_rows<T, BM, WM>(lds, wave, lane, static_cast<T*>(a.P) + static_cast<int64_t>(first) * a.ldp + mf, a.ldp, a.N - first, a.ldp - mf,
                                   [&](int i, int r) VS_INLINE {
                                       const int m = 32 * i + 8 * (r / 4) + r % 4;
                                       const float p = __builtin_amdgcn_exp2f(fmaf(acc[i][j][r], kLog2e, -shift));
-                                      return on && mw + m < a.M ? fmaf(p, gp, hot == m ? -g : 0.f) : 0.f;
+                                      const float e = on && mw + m < a.M ? fmaf(p, gp, hot == m ? -g : 0.f) : 0.f;
+                                      if constexpr (sizeof(T) == 2) top = hot == m ? e : top;
+                                      return e;
                                   });
+            if constexpr (sizeof(T) == 2) {
+                // this lane's rows are 4 of every 8, from its mw on
+                if (hot >= 0 && hot < BM / WM && (hot & 4) == 0 && mw + hot < a.M && n < a.N && on) {
+                    const float kept_part = static_cast<float>(static_cast<__bf16>(top));
+                    a.rest[n] = __builtin_isfinite(kept_part) ? top - kept_part : 0.f;
+                }
+            }
         }
     } else {
         const bool split = a.k_split < a.K;
+        // dx: the rest of the target's entry times its row of W
+        if constexpr (!BO && sizeof(T) == 2) {
+            if (a.rest && z == 0) {
+#pragma unroll
+                for (int j = 0; j < NF; ++j) {
+                    const int n = nw + 32 * j;
+                    const int64_t v = target_of(a, min(n, a.N - 1));
+                    if (n >= a.N || !kept(a, v)) continue;
+                    const float rest = a.rest[n];
+                    const T* row = static_cast<const T*>(a.rows) + v * a.lda;
+#pragma unroll
+                    for (int i = 0; i < MF; ++i)
+#pragma unroll
+                        for (int q = 0; q < 4; ++q) {
+                            const int m = mw + 32 * i + 8 * q;
+                            T w[4] = {};
+                            if (m + 4 <= a.M) __builtin_memcpy(w, row + m, sizeof(w));
+                            else
+#pragma unroll
+                                for (int r = 0; r < 4; ++r)
+                                    if (m + r < a.M) w[r] = row[m + r];
+#pragma unroll
+                            for (int r = 0; r < 4; ++r) acc[i][j][4 * q + r] = fmaf(rest, ld(w, r), acc[i][j][4 * q + r]);
+                        }
+                }
+            }
+        }
 #pragma unroll
         for (int j = 0; j < NF; ++j) {
             const int n = nw + 32 * j, first = n0 + wn * (BN / WN) + 32 * j, mf = m0 + wm * (BM / WM);
@@ -456,7 +598,7 @@ __device__ __forceinline__ Range xcd_range(int n, int x) {
     __shared__ __attribute__((aligned(1024))) char sA1[Operand<T, AO, BM, WM * WN>::kBytes];            \
     __shared__ __attribute__((aligned(1024))) char sB0[Operand<T, BO, BN, WM * WN>::kBytes];            \
     __shared__ __attribute__((aligned(1024))) char sB1[Operand<T, BO, BN, WM * WN>::kBytes];            \
-    const Lds lds{sA0, sA1, sB0, sB1};
+    Lds lds{sA0, sA1, sB0, sB1, nullptr};
 
 // Bound by the matrix cores: 8,194 x 1,536 x 49,999 bf16 scored in 1,140 us, 1.10
 // PFLOP/s (59 % of their cycles; the library's product of these sizes alone, which
@@ -479,6 +621,10 @@ __global__ __launch_bounds__(64 * WM * WN) void vocab_logits_kernel(const GemmAr
 template <typename T, int BM, int BN, int WM, int WN>
 __global__ __launch_bounds__(64 * WM * WN) void vocab_grads_kernel(const GemmArgs dx, const GemmArgs dw, int n_dx) {
     VS_GEMM_LDS(T, true, true)
+    if constexpr (sizeof(T) == 2) {
+        __shared__ Hits hits;
+        lds.hits = &hits;
+    }
     const int x = blockIdx.x % kXcds, k = blockIdx.x / kXcds;
     const Range all = xcd_range(gridDim.x, x), one = xcd_range(n_dx, x);
     if (k < one.count) {
@@ -685,12 +831,14 @@ int launch(const vs::VocabCall& c) {
             const bool last = v0 + n == c.vocab;
             l.A = W + v0 * ldw; l.M = n; l.v0 = static_cast<int>(v0);
             l.lse = c.lse_in; l.dloss = c.dloss; l.P = ws + p.P;
+            if (sizeof(T) == 2) l.rest = reinterpret_cast<float*>(ws + p.rest);
             l.ldp = ceil_div(n, 8) * 8;                 // rows of whole 16 bytes
             logits<T, kProb>(l, p.prob_wide, s);
             GemmArgs dx{}, dw{};
             dx.A = W + v0 * ldw; dx.lda = ldw; dx.B = l.P; dx.ldb = l.ldp;
             dx.M = static_cast<int>(c.dim); dx.N = static_cast<int>(c.tokens); dx.K = n;
-            dx.target = c.target; dx.target64 = c.target64; dx.vocab = l.vocab;
+            dx.target = dw.target = c.target; dx.target64 = dw.target64 = c.target64; dx.vocab = dw.vocab = l.vocab; dw.v0 = l.v0;
+            dx.rest = last ? l.rest : nullptr; dx.rows = W; dw.rest = l.rest;    // dx: every piece's, once all are there
             dx.add = v0 > 0; dx.sum = p.pieces > 1 ? sum : nullptr;
             dx.out = last ? c.dx : nullptr; dx.ldo = c.dim;
             dw.A = x; dw.lda = ldx; dw.B = l.P; dw.ldb = l.ldp;

@@ -109,7 +109,7 @@ struct VocabPlan {
     int dx_splits, dw_splits;
     int64_t piece;                                   // vocabulary entries of a piece of the gradient
     int64_t pieces;
-    size_t x, w, part, logit, P, part_dx, part_dw, sum, bytes;    // offsets in the workspace, and its size
+    size_t x, w, part, logit, P, part_dx, part_dw, sum, rest, bytes;    // offsets in the workspace, and its size
 };
 struct VocabCall {
     int64_t tokens, dim, vocab;
