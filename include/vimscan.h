@@ -663,8 +663,10 @@ int gated_scan_step(int64_t batch, int64_t dim, int dtype, const void* x, const 
  * L = 1 with channel stride 1 is one row of channels for each token, and
  * takes a form of its own. dim is at most 8192, eps finite and >= 0, batch x
  * ceil(L / 16) below 2^22; rows below 2^26 where 64 lanes of 16 bytes hold the
- * channels, below 2^24 where 256 do, else below 2^22. Sums are fp32. Outputs
- * may overlap nothing else.
+ * channels, below 2^24 where 256 do, else below 2^22. Sums are fp32: where eps
+ * is 0, a token whose mean square is below 2^-126 loses digits as subnormal
+ * numbers do, and one whose squares vanish is divided by zero. Outputs may
+ * overlap nothing else.
  */
 int rms_norm(int64_t batch, int64_t dim, int64_t seqlen, int dtype, const void* x,
              const void* residual, const int64_t* strides, const float* w, float eps,

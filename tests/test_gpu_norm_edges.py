@@ -65,3 +65,36 @@ def test_weight_gradient_of_many_equal_terms(shape, value):
     g = vms.rms_norm_grad(s, torch.ones(1, device="cuda"), dy, eps=0.0)
     close(g["dw"], dy.flatten()[:1].cpu().double() * s.numel(), "dw")
     assert float(g["dx"].abs().max()) <= 8 * 2.0 ** -24
+
+
+@pytest.mark.parametrize("scale", [2.0 ** -62, 2.0 ** -64, 2.0 ** -66])
+@pytest.mark.parametrize("shape", [(5, 64), (3, 700), (2, 64, 40), (2, 500, 37)], ids=str)
+def test_tokens_whose_mean_square_is_subnormal(shape, scale):
+    """Without eps tokens of 2^-66 are normed like others. Their mean square, 2^-132, has
+    17 significant bits, and sums of such squares lose half a unit of 2^-149 at each
+    addition: 2^-18 sqrt(channels / 64) relative, of which q has half and its cube three
+    halves; close() allows 2^-15.4. The other half of the tokens is 2^3 larger, so that some
+    mean squares are normal numbers."""
+    import vision_mamba_selective_amd as vms
+    say("case norm subnormal squares %s %g" % (shape, scale))
+    g = torch.Generator().manual_seed(9)
+    rnd = lambda *v: torch.randn(*v, generator=g).cuda()                              # noqa: E731
+    s, dy, w = rnd(*shape) * scale, rnd(*shape), 1 + 0.3 * rnd(shape[1])
+    if len(shape) == 3:
+        s[:, :, ::2] *= 8
+    else:
+        s[::2] *= 8
+    lengths = None if len(shape) == 2 else torch.tensor([shape[2], shape[2] - 5], dtype=torch.int32).cuda()
+    y, _ = vms.rms_norm(s, w, eps=0.0, lengths=lengths)
+    got = vms.rms_norm_grad(s, w, dy, eps=0.0, lengths=lengths)
+    wide = [v.view(shape[0], shape[1], -1) for v in (s, dy)]
+    leaf, lw = ref.f64(wide[0] / scale).requires_grad_(), ref.f64(w).requires_grad_()
+    keep = torch.ones(shape[0], 1, 1, dtype=torch.float64)
+    if lengths is not None:                                    # ones stand at padding, where the reference would divide by zero
+        keep = (torch.arange(shape[2]) < lengths.cpu()[:, None])[:, None].double()
+        leaf = (leaf.detach() * keep + (1 - keep)).requires_grad_()
+    want = ref.norm(leaf, lw, None, None, 0.0, torch.float32)[0] * keep
+    dx, dw = ref.gradients([want], [ref.f64(wide[1])], [leaf, lw])
+    close(y.view_as(wide[0]), want.detach(), "y")
+    close(got["dx"].view_as(wide[0]) * scale, dx, "dx")
+    close(got["dw"], dw, "dw")

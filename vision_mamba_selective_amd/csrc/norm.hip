@@ -104,6 +104,15 @@ struct Pack {
     }
 };
 
+// 1 / sqrt(v) by the hardware's approximation, off by one unit in the last place (an exact
+// root and division would leave results off by 5.0e-8 instead of 6.0e-8 of their size).
+// It takes subnormal numbers for zeros: they are scaled up first.
+__device__ __forceinline__ float inverse_root(float v) {
+    const bool low = v < 0x1p-100f;
+    const float r = __builtin_amdgcn_rsqf(low ? v * 0x1p64f : v);
+    return low ? r * 0x1p32f : r;
+}
+
 // weights first .. first + N - 1, ones without weights and past the last
 template <int N>
 __device__ __forceinline__ void weights(const float* w, int first, int n, float (&f)[N]) {
@@ -267,7 +276,7 @@ __device__ __forceinline__ void norm_column(const NormArgs& a, const Column<T, W
     column_sum(c, ss, red);
     float q[N];
 #pragma unroll
-    for (int i = 0; i < N; ++i) q[i] = __builtin_amdgcn_rsqf(fmaf(ss[i], a.inv_dim, a.eps));
+    for (int i = 0; i < N; ++i) q[i] = inverse_root(fmaf(ss[i], a.inv_dim, a.eps));
     auto put = [&](int ch, float w, const Pack<T>& s) VS_INLINE {
         float f[N];
 #pragma unroll
@@ -381,8 +390,8 @@ __device__ __forceinline__ void norm_column_grad(const NormArgs& a, const Column
     float q[N], m[N];
 #pragma unroll
     for (int i = 0; i < N; ++i) {
-        q[i] = __builtin_amdgcn_rsqf(fmaf(ss[i], a.inv_dim, a.eps));
-        m[i] = q[i] * q[i] * (sd[i] * a.inv_dim);
+        q[i] = inverse_root(fmaf(ss[i], a.inv_dim, a.eps));
+        m[i] = q[i] * (sd[i] * a.inv_dim);
     }
     auto put = [&](int ch, const Pack<T>& ps, const Pack<T>& py, Pack<T>& g) VS_INLINE {
         const float w = a.w ? a.w[ch] : 1.f;
@@ -390,11 +399,12 @@ __device__ __forceinline__ void norm_column_grad(const NormArgs& a, const Column
         float f[N], dw = 0.f;
 #pragma unroll
         for (int i = 0; i < N; ++i) {
-            const float sv = ps.get(i), yv = py.get(i);
-            const float d = q[i] * (w * yv - sv * m[i]);
+            // by the normed value u: the square of q alone may be infinite
+            const float u = ps.get(i) * q[i], yv = py.get(i);
+            const float d = q[i] * (w * yv - u * m[i]);
             const bool on = FULL || c.t + i < c.len;
             f[i] = on ? (dsum ? g.get(i) + d : d) : 0.f;
-            dw = fmaf(on ? yv * q[i] : 0.f, sv, dw);
+            dw = on ? fmaf(yv, u, dw) : dw;
         }
         Pack<T> o;
         o.set(f);
@@ -519,7 +529,7 @@ __global__ __launch_bounds__(W == 1 ? 256 : 64 * W) void norm_row_kernel(const N
 #pragma unroll
         for (int i = 0; i < N; ++i) ss = fmaf(s[k].get(i), s[k].get(i), ss);
     }
-    const float q = __builtin_amdgcn_rsqf(fmaf(r.sum(ss, red), a.inv_dim, a.eps));
+    const float q = inverse_root(fmaf(r.sum(ss, red), a.inv_dim, a.eps));
 #pragma unroll
     for (int k = 0; k < HOLD; ++k) {
         const int i0 = k * kStep + r.tid * N;
@@ -589,7 +599,7 @@ __global__ __launch_bounds__(W == 1 ? 256 : 64 * W) void norm_row_grad_kernel(co
             }
         }
         r.sums(ss, sd, red[odd]);
-        const float q = __builtin_amdgcn_rsqf(fmaf(ss, a.inv_dim, a.eps)), m = q * q * (sd * a.inv_dim);
+        const float q = inverse_root(fmaf(ss, a.inv_dim, a.eps)), m = q * (sd * a.inv_dim);
 #pragma unroll
         for (int k = 0; k < HOLD; ++k) {
             const int i0 = k * kStep + r.tid * N;
@@ -598,10 +608,10 @@ __global__ __launch_bounds__(W == 1 ? 256 : 64 * W) void norm_row_grad_kernel(co
             weights(a.w, i0, a.dim, w);
 #pragma unroll
             for (int i = 0; i < N; ++i) {
-                const float sv = hs[k].get(i), yv = hy[k].get(i);
-                const float d = q * (w[i] * yv - sv * m);
+                const float u = hs[k].get(i) * q, yv = hy[k].get(i);
+                const float d = q * (w[i] * yv - u * m);
                 f[i] = real ? (a.dsum ? hg[k].get(i) + d : d) : 0.f;
-                if (real) dw[k][i] = fmaf(yv * q, sv, dw[k][i]);
+                if (real) dw[k][i] = fmaf(yv, u, dw[k][i]);
             }
             Pack<T> o;
             o.set(f);
