@@ -1,0 +1,67 @@
+"""Which differentiable calls may be captured in a HIP graph: those that a
+captured backward pass could not be made of are refused before anything is
+captured, the others are not."""
+import gc
+
+import pytest
+import torch
+
+from gpu_util import say
+
+pytestmark = pytest.mark.gpu
+
+
+@pytest.fixture
+def leaves():
+    """Leaves of both mixers, the norm and the loss, and a training step of them all."""
+    import vision_mamba_selective_amd as vms
+    g = torch.Generator().manual_seed(9)
+    rnd = lambda *s: torch.randn(*s, generator=g).cuda().requires_grad_()            # noqa: E731
+    p = dict(x=rnd(2, 48, 130), w=rnd(48), r=rnd(2, 48, 130), i=rnd(2, 48, 130), lam=rnd(48), W=rnd(300, 48), taps=rnd(48, 4), bias=rnd(48),
+             B=rnd(2, 16, 130), C=rnd(2, 16, 130), A=(-torch.rand(48, 16, generator=g) - 0.1).cuda().requires_grad_(), D=rnd(48), dt=rnd(48))
+    target = torch.randint(-20, 300, (260,), generator=g).cuda()
+
+    def step():
+        y, _ = vms.rms_norm_autograd(p["x"], p["w"])
+        u, _ = vms.s6_causal_conv_autograd(y, p["taps"], p["bias"])
+        y, _ = vms.gated_scan_autograd(u, p["r"], p["i"], p["lam"], z=p["r"])
+        y, _ = vms.s6_causal_scan_autograd(y, p["r"], p["i"], p["B"], p["C"], p["A"], p["D"], p["dt"])
+        y, _ = vms.rms_norm_autograd(y, None, residual=p["x"])
+        return vms.vocab_loss_autograd(y.transpose(1, 2).reshape(260, 48), p["W"], target)
+    return p, step, target
+
+
+def settle():
+    gc.collect()                     # an exception's frames hold the refused call's graph
+    torch.cuda.synchronize()
+
+
+def replays(graph, got, eager):
+    for k in range(3):
+        for v in got:
+            v.zero_()
+        graph.replay()
+        torch.cuda.synchronize()
+        assert all(torch.equal(a, b) for a, b in zip(got, eager)), k
+
+
+def test_without_gradients_a_living_eager_graph_does_not_matter(leaves):
+    """Captured under no_grad the calls record no graph: nothing is refused."""
+    import vision_mamba_selective_amd as vms
+    say("case capture no_grad")
+    p, step, target = leaves
+    alive = step()
+    torch.cuda.synchronize()
+
+    def calls():
+        y, _ = vms.rms_norm_autograd(p["x"], p["w"])
+        z, h = vms.gated_scan_autograd(y, p["r"], p["i"], p["lam"])
+        return y, z, h, vms.vocab_loss_autograd(z.transpose(1, 2).reshape(260, 48), p["W"], target)
+    with torch.no_grad():
+        eager = [v.clone() for v in calls()]
+        torch.cuda.synchronize()
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph):
+            got = calls()
+    replays(graph, got, eager)
+    assert alive.requires_grad

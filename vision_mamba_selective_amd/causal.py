@@ -108,6 +108,17 @@ def _rows(g, like):
     return g if g.stride(-1) == 1 and min(g.stride()) >= 0 else g.contiguous()
 
 
+class CapturableFunction(torch.autograd.Function):
+    """A call that may be captured in a HIP graph together with its backward
+    pass: while capturing and recording gradients it refuses a leaf of an eager
+    graph that is still alive."""
+
+    @classmethod
+    def apply(cls, *args):
+        _calls.capture_ready(args)
+        return super().apply(*args)
+
+
 class CausalConvFunction(torch.autograd.Function):
     """s6_causal_conv for autograd; both outputs are differentiable, once: a
     gradient of the gradient is refused."""

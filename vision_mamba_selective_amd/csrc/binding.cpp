@@ -731,14 +731,16 @@ PyObject* reorder(PyObject* const* a) {
 }
 
 // ---------------------------------------------------------------- autograd
-// inputs of a differentiable call. Where its stream is capturing, none of them may
-// be a leaf of an eager graph that is still alive: that graph's node for the
+// A differentiable call's arguments, before it is made. Where its stream is
+// capturing and gradients are recorded, none of them may be a leaf of an eager graph that is still alive: that graph's node for the
 // leaf's gradient belongs to the stream it was made on, and the captured backward
 // pass would make that stream wait inside the capture, which ends the process.
 PyObject* capture_ready(PyObject* const* a) {
-    if (!PyTuple_Check(a[0])) raise(PyExc_TypeError, "expected a tuple of tensors");
+    if (!PyTuple_Check(a[0])) raise(PyExc_TypeError, "expected a tuple of arguments");
+    if (!at::GradMode::is_enabled()) Py_RETURN_NONE;
     for (Py_ssize_t k = 0; k < PyTuple_GET_SIZE(a[0]); ++k) {
-        Maybe t = maybe("input", PyTuple_GET_ITEM(a[0], k));
+        PyObject* o = PyTuple_GET_ITEM(a[0], k);
+        Maybe t = THPVariable_Check(o) ? &THPVariable_Unpack(o) : nullptr;
         if (!t || !t->is_cuda() || !t->requires_grad() || !t->is_leaf()) continue;
         const c10::DeviceGuard guard(t->device());
         if (c10::hip::currentStreamCaptureStatusMayInitCtx() == c10::hip::CaptureStatus::None) break;

@@ -9,12 +9,11 @@ stream first, and no eager graph of the same leaves alive (refused with a
 RuntimeError while capturing)."""
 from __future__ import annotations
 
-import torch
 from torch.autograd.function import once_differentiable
 
 from . import _calls
 from . import _native as nat
-from .causal import _rows
+from .causal import CapturableFunction, _rows
 
 
 def gated_workspace_bytes(op: int, batch: int, dim: int, seqlen: int) -> int:
@@ -55,13 +54,12 @@ def gated_scan_step(x, r, i, lam, h, z=None, slot_in=None, slot_out=None, rate=8
     return _calls.gated_scan_step(x, r, i, lam, h, z, slot_in, slot_out, rate, out)
 
 
-class GatedScanFunction(torch.autograd.Function):
+class GatedScanFunction(CapturableFunction):
     """gated_scan for autograd; y and h are differentiable, once: a gradient of
     the gradient is refused."""
 
     @staticmethod
     def forward(ctx, x, r, i, lam, z, h0, lengths, rate):
-        _calls.capture_ready((x, r, i, lam, z, h0))
         y, h, saved = gated_scan_saved(x, r, i, lam, z=z, h0=h0, lengths=lengths, rate=rate)
         ctx.save_for_backward(x, r, i, lam, z, h0, lengths, saved)
         ctx.rate = rate

@@ -8,6 +8,7 @@ from torch.autograd.function import once_differentiable
 
 from . import _calls
 from . import _native as nat
+from .causal import CapturableFunction
 
 
 def vocab_workspace_bytes(op: int, tokens: int, dim: int, vocab: int, dtype: torch.dtype) -> int:
@@ -36,13 +37,12 @@ def vocab_loss_grad(x, W, target, lse, dloss, workspace=None):
     return _calls.vocab_loss_grad(x, W, target, lse, dloss, workspace)
 
 
-class VocabLossFunction(torch.autograd.Function):
+class VocabLossFunction(CapturableFunction):
     """vocab_loss for autograd; the loss is differentiable once: a gradient of
     the gradient is refused."""
 
     @staticmethod
     def forward(ctx, x, W, target):
-        _calls.capture_ready((x, W))
         loss, lse = vocab_loss(x, W, target)
         ctx.save_for_backward(x, W, target, lse)
         return loss

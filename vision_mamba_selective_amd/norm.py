@@ -4,12 +4,11 @@ norm between the mixers"): prompts [batch, dim, L], normed over dim, and rows
 differentiable (rms_norm_autograd only) are as in causal.py."""
 from __future__ import annotations
 
-import torch
 from torch.autograd.function import once_differentiable
 
 from . import _calls
 from . import _native as nat
-from .causal import _rows
+from .causal import CapturableFunction, _rows
 
 
 def norm_workspace_bytes(batch: int, dim: int, seqlen: int) -> int:
@@ -38,13 +37,12 @@ def rms_norm_grad(s, w, dy, dsum=None, eps=1e-6, lengths=None, workspace=None):
     return _calls.rms_norm_grad(s, w, dy, dsum, eps, lengths, workspace)
 
 
-class RmsNormFunction(torch.autograd.Function):
+class RmsNormFunction(CapturableFunction):
     """rms_norm for autograd; y and s are differentiable, once: a gradient of
     the gradient is refused."""
 
     @staticmethod
     def forward(ctx, x, w, residual, eps, lengths):
-        _calls.capture_ready((x, w, residual))
         y, s = rms_norm(x, w, residual=residual, eps=eps, lengths=lengths)
         ctx.save_for_backward(s, w, lengths)
         ctx.eps, ctx.added = eps, residual is not None
