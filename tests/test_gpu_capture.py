@@ -65,3 +65,27 @@ def test_without_gradients_a_living_eager_graph_does_not_matter(leaves):
             got = calls()
     replays(graph, got, eager)
     assert alive.requires_grad
+
+
+def test_streams_that_are_captured_together(leaves):
+    """A leaf whose gradient node was made on another stream of the same capture is no eager graph's."""
+    import vision_mamba_selective_amd as vms
+    say("case capture two streams")
+    p, _, _ = leaves
+    side = torch.cuda.Stream()
+
+    def calls():
+        main = torch.cuda.current_stream()
+        side.wait_stream(main)
+        with torch.cuda.stream(side):
+            a, _ = vms.rms_norm_autograd(p["x"], p["w"])
+        main.wait_stream(side)
+        b, _ = vms.rms_norm_autograd(p["r"], p["w"])
+        return a, b
+    eager = [v.detach().clone() for v in calls()]
+    settle()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        got = calls()
+    with torch.no_grad():
+        replays(graph, got, eager)

@@ -731,6 +731,16 @@ PyObject* reorder(PyObject* const* a) {
 }
 
 // ---------------------------------------------------------------- autograd
+// whether a node was made on a stream that is neither the current one nor being captured with it
+bool elsewhere(const c10::Stream& made) {
+    if (made.id() == c10::hip::getCurrentHIPStream(made.device_index()).unwrap().id()) return false;
+    const hipStream_t s = c10::hip::HIPStream(c10::hip::HIPStream::UNCHECKED, made).stream();
+    if (!s) return true;                                     // the null stream cannot be captured
+    hipStreamCaptureStatus status = hipStreamCaptureStatusNone;
+    if (hipStreamIsCapturing(s, &status) != hipSuccess) (void)hipGetLastError();
+    return status == hipStreamCaptureStatusNone;
+}
+
 // A differentiable call's arguments, before it is made. Where its stream is
 // capturing and gradients are recorded, none of them may be a leaf of an eager graph that is still alive: that graph's node for the
 // leaf's gradient belongs to the stream it was made on, and the captured backward
@@ -746,7 +756,7 @@ PyObject* capture_ready(PyObject* const* a) {
         if (c10::hip::currentStreamCaptureStatusMayInitCtx() == c10::hip::CaptureStatus::None) break;
         const auto node = torch::autograd::impl::try_get_grad_accumulator(*t);
         const auto made = node ? node->stream() : std::nullopt;
-        if (made && made->id() != c10::hip::getCurrentHIPStream(t->device().index()).unwrap().id())
+        if (made && elsewhere(*made))
             raise(PyExc_RuntimeError, "a leaf of this call is part of an eager graph that is still alive: free it (its outputs and losses) before "
                                       "its backward pass is captured");
     }
