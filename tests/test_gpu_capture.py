@@ -89,3 +89,82 @@ def test_streams_that_are_captured_together(leaves):
         got = calls()
     with torch.no_grad():
         replays(graph, got, eager)
+
+
+def refused(call):
+    """The call is refused while capturing, before it launches anything, for an eager graph that is alive."""
+    with pytest.raises(RuntimeError, match="eager graph"):
+        with torch.cuda.graph(torch.cuda.CUDAGraph()):
+            call()
+    settle()
+
+
+def test_leaves_behind_other_operations_are_seen(leaves):
+    """Leaves that enter through torch's operations, the causal mixer's, or both, of a
+    living eager graph; an eager graph that leads to an input itself; and the causal
+    mixer's own calls. Freed, the eager graph is in no one's way."""
+    import vision_mamba_selective_amd as vms
+    say("case capture leaves behind operations")
+    p, _, target = leaves
+    x, w, r, i, lam, taps, bias, W = (p[k] for k in ("x", "w", "r", "i", "lam", "taps", "bias", "W"))
+    plain = {k: v.detach() for k, v in p.items()}
+    fixed = plain["x"]
+
+    def conv():
+        return vms.s6_causal_conv_autograd(fixed, taps, bias)[0]
+
+    def scan():
+        return vms.s6_causal_scan_autograd(fixed, plain["r"], plain["i"], plain["B"], plain["C"], p["A"], plain["D"], plain["dt"])[0]
+    calls = {
+        "torch operation, norm": lambda: vms.rms_norm_autograd(x * 2, plain["w"])[0],
+        "torch operation, weight": lambda: vms.rms_norm_autograd(fixed, w.exp())[0],
+        "torch operation, residual": lambda: vms.rms_norm_autograd(fixed, None, residual=x + 1)[0],
+        "torch operations, recurrence": lambda: vms.gated_scan_autograd(fixed, (r * 2).tanh(), plain["i"], plain["lam"])[0],
+        "torch operation, loss": lambda: vms.vocab_loss_autograd(fixed[0].t().contiguous(), W * 2, target[:130]),
+        "convolution": conv,
+        "scan": scan,
+        "convolution, recurrence": lambda: vms.gated_scan_autograd(conv(), plain["r"], plain["i"], plain["lam"])[0],
+    }
+    for name, call in calls.items():
+        say("case capture %s" % name)
+        alive = call()
+        torch.cuda.synchronize()
+        refused(call)
+        del alive
+        settle()
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph):
+            got = call()
+        eager = call().detach().clone()
+        with torch.no_grad():
+            replays(graph, [got], [eager])
+        del got, graph
+        settle()
+    made = x * 2                                               # an eager graph of its own
+    torch.cuda.synchronize()
+    refused(lambda: vms.rms_norm_autograd(made, plain["w"])[0])
+    del made
+    settle()
+
+
+def test_captured_step_of_both_mixers(leaves):
+    """A whole training step, both mixers' forward and backward passes among it,
+    captured as torch asks: every replay equals the eager result."""
+    say("case capture whole step")
+    p, step, _ = leaves
+    names = [k for k in p]
+    dloss = torch.ones(260).cuda()
+
+    def whole():
+        loss = step()
+        return [loss.detach()] + list(torch.autograd.grad(loss, [p[k] for k in names], grad_outputs=dloss))
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        eager = [v.clone() for v in whole()]
+    torch.cuda.current_stream().wait_stream(side)
+    settle()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        got = whole()
+    replays(graph, got, eager)

@@ -110,8 +110,8 @@ def _rows(g, like):
 
 class CapturableFunction(torch.autograd.Function):
     """A call that may be captured in a HIP graph together with its backward
-    pass: while capturing and recording gradients it refuses a leaf of an eager
-    graph that is still alive."""
+    pass: while capturing and recording gradients it refuses inputs that an eager
+    graph leads to, or that were made of a leaf of one, while that graph is alive."""
 
     @classmethod
     def apply(cls, *args):
@@ -119,7 +119,7 @@ class CapturableFunction(torch.autograd.Function):
         return super().apply(*args)
 
 
-class CausalConvFunction(torch.autograd.Function):
+class CausalConvFunction(CapturableFunction):
     """s6_causal_conv for autograd; both outputs are differentiable, once: a
     gradient of the gradient is refused."""
 
@@ -146,7 +146,7 @@ def s6_causal_conv_autograd(x, w, bias=None, window=None, lengths=None, silu=Tru
     return CausalConvFunction.apply(x, w, bias, window, lengths, silu)
 
 
-class CausalScanFunction(torch.autograd.Function):
+class CausalScanFunction(CapturableFunction):
     """s6_causal_scan for autograd: the forward keeps the saved buffer for the
     backward; y and h are differentiable, once: a gradient of the gradient is
     refused. The gradients of B and C come back in their dtype (the library sums

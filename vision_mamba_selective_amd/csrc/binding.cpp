@@ -27,7 +27,10 @@
 
 #include <cstdarg>
 #include <initializer_list>
+#include <memory>
 #include <string>
+#include <unordered_set>
+#include <vector>
 
 #include "vimscan.h"
 
@@ -741,24 +744,39 @@ bool elsewhere(const c10::Stream& made) {
     return status == hipStreamCaptureStatusNone;
 }
 
-// A differentiable call's arguments, before it is made. Where its stream is
-// capturing and gradients are recorded, none of them may be a leaf of an eager graph that is still alive: that graph's node for the
-// leaf's gradient belongs to the stream it was made on, and the captured backward
-// pass would make that stream wait inside the capture, which ends the process.
+// A differentiable call's arguments, before it is made. Where their stream is
+// capturing and gradients are recorded, no graph that leads to one of them may have
+// a node of an eager graph that is still alive, a leaf's among them: that node
+// belongs to the stream it was made on, and the captured backward pass would
+// make that stream wait inside the capture, which ends the process.
 PyObject* capture_ready(PyObject* const* a) {
+    using torch::autograd::Node;
     if (!PyTuple_Check(a[0])) raise(PyExc_TypeError, "expected a tuple of arguments");
     if (!at::GradMode::is_enabled()) Py_RETURN_NONE;
+    std::vector<std::shared_ptr<Node>> todo;
+    bool capturing = false;
     for (Py_ssize_t k = 0; k < PyTuple_GET_SIZE(a[0]); ++k) {
         PyObject* o = PyTuple_GET_ITEM(a[0], k);
-        Maybe t = THPVariable_Check(o) ? &THPVariable_Unpack(o) : nullptr;
-        if (!t || !t->is_cuda() || !t->requires_grad() || !t->is_leaf()) continue;
-        const c10::DeviceGuard guard(t->device());
-        if (c10::hip::currentStreamCaptureStatusMayInitCtx() == c10::hip::CaptureStatus::None) break;
-        const auto node = torch::autograd::impl::try_get_grad_accumulator(*t);
-        const auto made = node ? node->stream() : std::nullopt;
+        if (!THPVariable_Check(o)) continue;
+        const at::Tensor& t = THPVariable_Unpack(o);
+        if (!t.is_cuda() || !t.requires_grad()) continue;
+        if (!capturing) {
+            const c10::DeviceGuard guard(t.device());
+            if (c10::hip::currentStreamCaptureStatusMayInitCtx() == c10::hip::CaptureStatus::None) Py_RETURN_NONE;
+            capturing = true;
+        }
+        todo.push_back(t.is_leaf() ? torch::autograd::impl::try_get_grad_accumulator(t) : t.grad_fn());
+    }
+    std::unordered_set<const Node*> seen;
+    while (!todo.empty()) {
+        const std::shared_ptr<Node> node = std::move(todo.back());
+        todo.pop_back();
+        if (!node || !seen.insert(node.get()).second) continue;
+        const auto made = node->stream();
         if (made && elsewhere(*made))
-            raise(PyExc_RuntimeError, "a leaf of this call is part of an eager graph that is still alive: free it (its outputs and losses) before "
-                                      "its backward pass is captured");
+            raise(PyExc_RuntimeError, "an eager graph that is still alive leads to this call or shares a leaf with it: free it (its outputs and losses) "
+                                      "before its backward pass is captured");
+        for (const auto& edge : node->next_edges()) todo.push_back(edge.function);
     }
     Py_RETURN_NONE;
 }

@@ -1,12 +1,8 @@
 """Torch-facing binding of the gated linear recurrence (include/vimscan.h, "The
 gated linear recurrence"): over prompts, for training and for single tokens on
-a pool of states. Layouts, strides, lengths, tensors written in place and what
-is differentiable (gated_scan_autograd only) are as in causal.py.
-
-gated_scan_autograd, rms_norm_autograd and vocab_loss_autograd may be captured in
-a HIP graph together with their backward pass, in torch's order: a run on a side
-stream first, and no eager graph of the same leaves alive (refused with a
-RuntimeError while capturing)."""
+a pool of states. Layouts, strides, lengths, tensors written in place, what is
+differentiable (gated_scan_autograd only) and what may be captured are as in
+causal.py."""
 from __future__ import annotations
 
 from torch.autograd.function import once_differentiable
