@@ -215,15 +215,6 @@ __device__ __forceinline__ void put_four(float* p, int at, int n, const float (&
         for (int i = 0; i < 4; ++i)
             if (at + i < n) p[at + i] = f[i];
 }
-__device__ __forceinline__ void put_four(uint16_t* p, int at, int n, const float (&f)[4]) {
-    uint16_t b[4];
-#pragma unroll
-    for (int i = 0; i < 4; ++i) st(b, i, f[i]);
-    if (at + 4 <= n) __builtin_memcpy(p + at, b, 8);
-    else
-        for (int i = 0; i < 4; ++i)
-            if (at + i < n) p[at + i] = b[i];
-}
 
 // Of a run of tokens those whose targets are entries of a tile of dW, in order: token
 // (16 bits) and entry, and the rest of its entry of P
