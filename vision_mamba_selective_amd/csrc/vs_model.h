@@ -67,8 +67,11 @@ int prepare_gated_step(GatedStepCall& c);
 // tile where six sweeps of its waves hold the channels
 constexpr int kNormWide = 128, kNormNarrow = 64;
 constexpr int64_t kNormMaxDim = 8192;
-// workgroups that take the rows of a gradient in turn (bf16 8,194 x 1,536 training
-// step 36.4 us; of 1,536 37.2, of 2,048 40.8, with as many more lines of dw to add up)
+// workgroups that take the rows of a gradient in turn. The more there are, the more lines
+// of dw there are to add up, and the fewer, the fewer loads are in flight; training steps with
+// 1,024, 1,536 and 2,048 of them: bf16 8,194 x 1,536 36.4, 37.2 and 40.8 us, fp32 109.9, 113.5
+// and 117.3, bf16 with a residual 8,194 x 1,536 51.9, 51.0 and 57.6, x 768 39.0, 35.3 and 41.4, x
+// 384 27.6, 31.7 and 37.7: the best count goes with the bytes of a row, by up to 10 %.
 constexpr int64_t kNormGroups = 1024;
 // channel-major, or rows in 1, 4 or 16 waves: the channels a lane holds bound
 // the row's length
