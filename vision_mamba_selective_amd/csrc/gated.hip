@@ -370,8 +370,8 @@ __global__ __launch_bounds__(NW > 4 ? 64 * NW : 256) void gated_scan_kernel(cons
 // sum G sigmoid(lam) / softplus(lam), which tends to sum G for small lam.
 __device__ __forceinline__ float lam_slope(float lam) { return lam < -20.f ? 1.f : sigmoid_f(lam) / softplus_f(lam); }
 
-// Nine streams (five read, four written), so memory again: 8 x 768 x 4,097 bf16 96 us,
-// 472 MB at 4.9 TB/s, VALU issue 66 %. The states are made again from the saved
+// Nine streams (five read, four written), so memory again: 8 x 768 x 4,097 bf16 93 us,
+// 472 MB at 5.1 TB/s, VALU issue 67 %. The states are made again from the saved
 // ones: keeping them all would be a tenth stream in fp32. A block's inputs are read
 // in two parts, as the registers of the former's become free.
 template <typename T, int G, int NW, bool GATED>

@@ -591,13 +591,13 @@ __device__ __forceinline__ Range xcd_range(int n, int x) {
     __shared__ __attribute__((aligned(1024))) char sB1[Operand<T, BO, BN, WM * WN>::kBytes];            \
     Lds lds{sA0, sA1, sB0, sB1, nullptr};
 
-// Bound by the matrix cores: 8,194 x 1,536 x 49,999 bf16 scored in 1,140 us, 1.10
-// PFLOP/s (59 % of their cycles; the library's product of these sizes alone, which
-// writes its logits, 1,083 us). With P half of the vocabulary takes 723 us for 557 of
-// product: a tile's 131 KB are written with no other tile on the compute unit to
-// work meanwhile. 197 x 768 x 49,999: 25 us for 77 MB of W, 196 of 256 units busy.
-// fp32 394 x 384 x 32,768: 109 us, matrix cores 72 %, and 394 tokens fill 77 % of
-// two tiles.
+// Bound by the matrix cores and by what they wait for: 8,194 x 1,536 x 49,999 bf16 scored
+// in 1,080 us (up to 1,160 on other cards), 1.17 PFLOP/s (59 % of their cycles; the
+// library's product of these sizes alone, which writes its logits, 1,083 us). With P
+// half of the vocabulary takes 680 us for 540 of product: a tile's 131 KB are written
+// with no other tile on the compute unit to work meanwhile. 197 x 768 x 49,999: 25 us
+// for 77 MB of W, 196 of 256 units busy. fp32 394 x 384 x 32,768: 100 us, matrix cores
+// 80 %, and 394 tokens fill 77 % of two tiles.
 template <typename T, int BM, int BN, int WM, int WN, Epilogue EPI>
 __global__ __launch_bounds__(64 * WM * WN) void vocab_logits_kernel(const GemmArgs a) {
     VS_GEMM_LDS(T, false, false)
@@ -607,8 +607,8 @@ __global__ __launch_bounds__(64 * WM * WN) void vocab_logits_kernel(const GemmAr
 
 // dx and dW of a piece in one launch: the tiles of dx, whose k is the longer one
 // with large pieces, first, and those of dW in the room that they leave. Bound by
-// the matrix cores: half of 8,194 x 1,536 x 49,999 bf16 1,250 us, 1.01 PFLOP/s;
-// fp32 394 x 384 x 32,768 211 us, 94 TFLOP/s of the useful products (busy 73 %).
+// the matrix cores: half of 8,194 x 1,536 x 49,999 bf16 1,280 us, 0.98 PFLOP/s (47 % of
+// their cycles); fp32 394 x 384 x 32,768 202 us, 98 TFLOP/s of the useful products (73 %).
 template <typename T, int BM, int BN, int WM, int WN>
 __global__ __launch_bounds__(64 * WM * WN) void vocab_grads_kernel(const GemmArgs dx, const GemmArgs dw, int n_dx) {
     VS_GEMM_LDS(T, true, true)
