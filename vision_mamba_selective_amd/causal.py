@@ -13,6 +13,15 @@ what every other function returns is outside any graph, also where an input
 requires a gradient. A tensor that a call writes in place (a pool, a given
 output or buffer) gets a new version, as after torch's in-place operations, and
 is refused if it requires a gradient while gradients are recorded.
+
+The differentiable functions here, in gated.py, norm.py and loss.py may be captured
+in a HIP graph together with their backward pass, in torch's order: a run on a
+side stream first, and no eager graph alive that has leaves in common with what
+is captured. Such a graph of another stream, whose backward nodes would end the
+process, is refused with a RuntimeError while capturing and recording gradients,
+as far as it leads to the call's inputs; what enters a captured graph by torch's
+own operations alone is not seen. A forward pass by itself is captured under
+torch.no_grad().
 """
 from __future__ import annotations
 

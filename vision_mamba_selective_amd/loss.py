@@ -1,6 +1,7 @@
 """Torch-facing binding of the loss over a vocabulary (include/vimscan.h, "The
 loss over a vocabulary"): softmax cross entropy of a linear head, without
-keeping the logits. Only vocab_loss_autograd is differentiable."""
+keeping the logits. Only vocab_loss_autograd is differentiable; what may be
+captured is as in causal.py."""
 from __future__ import annotations
 
 import torch

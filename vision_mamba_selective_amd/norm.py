@@ -1,7 +1,8 @@
 """Torch-facing binding of the norm between the mixers (include/vimscan.h, "The
 norm between the mixers"): prompts [batch, dim, L], normed over dim, and rows
-[rows, dim]. Strides, lengths, tensors written in place and what is
-differentiable (rms_norm_autograd only) are as in causal.py."""
+[rows, dim]. Strides, lengths, tensors written in place, what is
+differentiable (rms_norm_autograd only) and what may be captured are as in
+causal.py."""
 from __future__ import annotations
 
 from torch.autograd.function import once_differentiable
